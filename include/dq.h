@@ -2,8 +2,9 @@
  * dq.h -- C ABI of libdq: the single-token (M = 1) decode hot path of an LLM on
  * one NVIDIA GB300 (sm_103a): RMSNorm / LayerNorm, matrix-vector products over
  * bf16, Q4_K and Q6_K weights dequantised in registers, grouped-query decode
- * attention over an fp16 KV cache, and a whole decode token over a
- * Qwen3-8B-shaped layer stack.
+ * attention over an fp16 KV cache, a whole decode token over a
+ * Qwen3-8B-shaped layer stack; and for prompts and batches the attention of
+ * packed sequences and a paged 4-bit cache with its attention.
  *
  * Conventions (every entry point):
  *   - Returns a dq_status: 0 (DQ_OK) or a negative code.  Arguments are checked
@@ -299,6 +300,146 @@ DQ_API int dq_attention_decode_rope(const float* q, const float* k_new, void* k_
                                     const float* q_norm, const float* k_norm, const float* rope_table, float eps,
                                     int n_q, int n_kv, int head_dim, int max_ctx, int n_keys, void* workspace,
                                     size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------- prompts, packed rows, 4-bit caches
+ * What a prompt and a batch of sequences need next to the single-token calls
+ * above; the pages have no counterpart.  "Rows" are tokens, those of several
+ * sequences back to back.  Element types of the calls below: */
+#define DQ_TYPE_F32 0
+#define DQ_TYPE_F16 1
+#define DQ_TYPE_BF16 2
+
+/* The attention's inputs from the projections of many rows, for the Qwen3 family
+ * as dq_attention_decode_rope takes them one token at a time.  qkv: fp32, row r at
+ * qkv + r * row_stride holds n_q query heads, then n_kv key heads, then n_kv value
+ * heads of 128 (dq_matmul_q4k's output for a q | k | v table).  For row r:
+ *   q_out[r][h] = rope(head_rmsnorm(q_h, q_norm), positions[r])
+ *   k_out[r][g] = rope(head_rmsnorm(k_g, k_norm), positions[r])
+ *   v_out[r][g] = v_g
+ * each rounded once from fp32 to `type` (DQ_TYPE_*).  q_norm and k_norm both
+ * NULL: no head norm, the rotation alone.  positions: int32 [rows] (device); a row
+ * whose position is negative is padding, its output rows are left as they were;
+ * a position >= max_ctx leaves them as well and sets the bad-argument bit of the
+ * device's error flag.  rope_table: fp32 [max_ctx][64][2] as dq_rope_table fills it
+ * for head_dim 128.  Outputs contiguous [rows][n_q or n_kv][128]; they must not
+ * overlap qkv.  All pointers 16-byte aligned, row_stride a multiple of 4.
+ * Errors: NULL -> DQ_ERR_NULL (also one of q_norm, k_norm alone); rows, n_q, n_kv or
+ * max_ctx < 1, row_stride < (n_q + 2 n_kv) * 128, eps as for the norms, an unknown
+ * type -> DQ_ERR_SHAPE; head_dim != 128 -> DQ_ERR_UNSUPPORTED; DQ_ERR_ALIGN. */
+DQ_API int dq_qkv_rope(const float* qkv, long long row_stride, const int* positions, const float* q_norm,
+                       const float* k_norm, const float* rope_table, float eps, int rows, int n_q, int n_kv,
+                       int head_dim, int max_ctx, int type, void* q_out, void* k_out, void* v_out, void* stream);
+
+/* Causal attention of whole prompts, or of later pieces of them, packed back to
+ * back.  Sequence s owns query rows cu_q[s] .. cu_q[s+1]-1 and key rows
+ * cu_k[s] .. cu_k[s+1]-1 (int32 [n_seq + 1] each, device; cu_k NULL: the same as
+ * cu_q).  With Lq and Lk rows, its query i sees its keys j <= i + Lk - Lq: the last
+ * query sees every key, so Lk > Lq continues a cached prefix and Lk < Lq leaves the
+ * first rows without keys (their outputs are zero).  Head h reads KV head
+ * h / (n_q / n_kv):
+ *   out[i][h] = sum_j softmax_j(q_i . k_j / sqrt(128)) v_j
+ * q, k, v and out hold fp16 or bf16 (`type`) rows of 128 contiguous elements at
+ * row * X_row_stride + head * X_head_stride elements: three slices of one projected
+ * row, or a layer's cache planes (row stride 128, head stride max_ctx * 128), need
+ * no copy.  total_q and total_k are the rows that q / out and k / v have; no other
+ * row is read or written, and output rows of no sequence are left as they were.
+ * Scores and sums are fp32; the probabilities are rounded to `type` for the product
+ * with v, as the operands of the tensor cores are.  A masked key or value takes no
+ * part whatever it holds, infinities and NaN included.  An offset array that
+ * decreases or leaves its total sets the bad-argument bit of the device's error
+ * flag and its sequence is left out.
+ * Strides are multiples of 8, the base pointers 16-byte aligned; out must not
+ * overlap the inputs.
+ * workspace: device scratch of dq_attention_prompt_workspace_bytes(...) bytes (NULL
+ * where that is 0), 16-byte aligned, its content before and after the call of no
+ * meaning; calls that share one must not overlap in time.
+ * Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, a stride < 128 or not matched to its neighbours
+ * (a type other than fp16 or bf16, a workspace too small) -> DQ_ERR_SHAPE;
+ * head_dim != 128, n_q / n_kv > 128, totals above 2^30 -> DQ_ERR_UNSUPPORTED;
+ * DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    long long q_row_stride, q_head_stride, k_row_stride, k_head_stride; /* elements */
+    long long v_row_stride, v_head_stride, out_row_stride, out_head_stride;
+    const int* cu_q;
+    const int* cu_k;
+    int type, n_seq, total_q, total_k, n_q, n_kv, head_dim;
+    void* workspace;
+    size_t workspace_bytes;
+} dq_prompt;
+DQ_API size_t dq_attention_prompt_workspace_bytes(int n_seq, int total_q, int total_k, int n_q, int n_kv);
+DQ_API int dq_attention_prompt(const dq_prompt* p, void* stream);
+
+/* A paged key/value cache in 4 bits.  pool: n_pages pages of page_size rows (a
+ * multiple of 16) for n_kv heads of 128, uint8 [n_pages][n_kv][page_size / 16]
+ * [DQ_KV4_BLOCK_BYTES]; a block holds 16 consecutive rows of one head, keys and
+ * values (5 bits a value, scales included):
+ *   [0,1024)    key codes: row j at 64 j; its 32-bit word 4 t + g (t, g = 0..3) holds
+ *               dims 32 g + 8 t + e (e = 0..7): even e = 2 i at bits 4 i .. 4 i + 3,
+ *               odd e = 2 i + 1 at bits 16 + 4 i .. 19 + 4 i
+ *   [1024,2048) value codes: half (j & 1) of the 32-bit word at 512 (j >> 3) +
+ *               16 (4 r + ((j >> 1) & 3)) + 4 g holds dims 32 g + 4 r + i (r = 0..7,
+ *               i = 0..3) at bits 4 i .. 4 i + 3
+ *   [2048,2304) key scales, [2304,2560) value scales: at 32 (j >> 1) + 8 g the four
+ *               binary16 numbers d of the even row, d of the odd row, z of the even
+ *               and z of the odd row, for dims 32 g .. 32 g + 31
+ *   value = d * (c - 8) + z
+ * (the words are the operands' registers of the attention's matrix instructions).
+ * A group of 32 dims x is stored as d = fp16(fp32(max - min) / 15),
+ * z = fp16(min + 8 d), c = min(15, max(0, rint((x - z) / d) + 8)), every step one
+ * IEEE fp32 operation, halves to even; c = 8 where d is 0.  A group with an
+ * infinity or NaN, or whose d or z passes the fp16 range, is stored as NaN.
+ * A row's slot is page * page_size + its offset in the page.  The caller decides
+ * which pages a sequence has; a page that several sequences share is held once. */
+#define DQ_KV4_BLOCK_ROWS 16
+#define DQ_KV4_BLOCK_BYTES 2560
+
+/* Stores rows: k[r], v[r] (type DQ_TYPE_*; 128 contiguous elements at r * X_row_stride
+ * + g * X_head_stride) into slots[r] (int32 [rows], device).  A negative slot is
+ * padding and skipped; one past the pool is skipped and sets the bad-argument bit
+ * of the device's error flag.  Slots of one call must differ from one another.
+ * Strides are multiples of 8 elements (fp32: 4), pointers 16-byte aligned.
+ * Errors: NULL -> DQ_ERR_NULL; a count < 1, page_size not a multiple of 16, a stride
+ * < 128 where its count exceeds 1, an unknown type -> DQ_ERR_SHAPE; head_dim != 128,
+ * n_pages * page_size >= 2^31 -> DQ_ERR_UNSUPPORTED; DQ_ERR_ALIGN. */
+DQ_API int dq_kv4_append(const void* k, const void* v, int type, long long k_row_stride, long long k_head_stride,
+                         long long v_row_stride, long long v_head_stride, const int* slots, void* pool, int rows,
+                         int n_kv, int head_dim, int n_pages, int page_size, void* stream);
+
+/* Reads rows back: k_out[r][g], v_out[r][g] (contiguous [rows][n_kv][128] of `type`,
+ * d * (c - 8) + z rounded once) from slots[r], for instance as the keys and values of
+ * dq_attention_prompt.  A slot may occur more than once; a negative one leaves its
+ * output row as it was, one past the pool too, with the bad-argument bit.  Errors as
+ * dq_kv4_append. */
+DQ_API int dq_kv4_read(const void* pool, const int* slots, int type, void* k_out, void* v_out, int rows, int n_kv,
+                       int head_dim, int n_pages, int page_size, void* stream);
+
+/* One token of each of n_seq sequences over the 4-bit cache: for sequence s and its
+ * keys j < n_keys[s], row j in page pages[s][j / page_size] at offset j % page_size,
+ *   out[s][h] = sum_j softmax_j(q[s][h] . k_j / sqrt(128)) v_j
+ * with KV head h / (n_q / n_kv).  q, out: contiguous [n_seq][n_q][128] of `type`
+ * (DQ_TYPE_*); out may equal q.  pages: int32 [n_seq][max_pages], entries past a
+ * sequence's last page are not looked at.  n_keys: int32 [n_seq] (device); 0 gives
+ * a zero output; a negative count, one above max_keys, or a page outside the pool
+ * sets the bad-argument bit of the device's error flag (the sequence's output is
+ * then zero, a bad page's keys take no part).  max_keys: a bound on every n_keys,
+ * known to the host (it sets the split), at most max_pages * page_size.  Scores,
+ * softmax and sums are fp32; queries and probabilities enter the matrix
+ * instructions as two fp16 parts each (relative error about 2^-22).
+ * workspace: dq_attention_decode_kv4_workspace_bytes(...) bytes of device scratch
+ * (NULL where that is 0), 16-byte aligned, its content before and after the call
+ * of no meaning; calls that share one must not overlap in time.
+ * Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, page_size not a multiple of
+ * 16, max_keys out of range, an unknown type, a workspace too small -> DQ_ERR_SHAPE;
+ * head_dim != 128, n_q / n_kv > 8, n_pages * page_size >= 2^31 ->
+ * DQ_ERR_UNSUPPORTED; misaligned -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
+DQ_API size_t dq_attention_decode_kv4_workspace_bytes(int n_seq, int n_q, int n_kv, int max_keys);
+DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, const int* pages, const int* n_keys,
+                                   void* out, int n_seq, int n_q, int n_kv, int head_dim, int n_pages, int page_size,
+                                   int max_pages, int max_keys, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------ M-token sweep
  * "The roofline holds on a second GPU", section "The Math": M tokens share one

@@ -1,0 +1,62 @@
+// dq_types.cuh -- the element types of the row operators: four consecutive
+// elements to and from fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "dq_common.cuh"
+
+namespace dq {
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __half* p)
+{
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p)
+{
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+}
+
+// Two fp32 as one register of the type's pairs, each rounded once to nearest.
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __half*)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v)
+{
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v.x, v.y, p), pack2(v.z, v.w, p));
+}
+
+}  // namespace dq
+
+namespace dqhost {
+
+inline bool valid_type(int t) { return t == DQ_TYPE_F32 || t == DQ_TYPE_F16 || t == DQ_TYPE_BF16; }
+inline int type_bytes(int t) { return t == DQ_TYPE_F32 ? 4 : 2; }
+
+// f(pointer of the type) for one of the three element types.
+template <typename F>
+cudaError_t with_type(int type, F f)
+{
+    if (type == DQ_TYPE_F32)
+        return f(static_cast<float*>(nullptr));
+    if (type == DQ_TYPE_F16)
+        return f(static_cast<__half*>(nullptr));
+    return f(static_cast<__nv_bfloat16*>(nullptr));
+}
+
+}  // namespace dqhost

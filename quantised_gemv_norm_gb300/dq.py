@@ -47,6 +47,13 @@ SIGNATURES = {
     "dq_attention_decode_static": (I, [P, P, P, P, I, I, I, I, I, P]),
     "dq_rope_table": (I, [P, I, I, D, P]),
     "dq_attention_decode_rope": (I, [P, P, P, P, P, P, P, P, F, I, I, I, I, I, P, SZ, P]),
+    "dq_qkv_rope": (I, [P, LL, P, P, P, P, F, I, I, I, I, I, I, P, P, P, P]),
+    "dq_attention_prompt_workspace_bytes": (SZ, [I, I, I, I, I]),
+    "dq_attention_prompt": (I, [P, P]),
+    "dq_kv4_append": (I, [P, P, I, LL, LL, LL, LL, P, P, I, I, I, I, I, P]),
+    "dq_kv4_read": (I, [P, P, I, P, P, I, I, I, I, I, P]),
+    "dq_attention_decode_kv4_workspace_bytes": (SZ, [I, I, I, I]),
+    "dq_attention_decode_kv4": (I, [P, I, P, P, P, P, I, I, I, I, I, I, I, I, P, SZ, P]),
     "dq_matmul_q4k": (I, [P, P, P, I, I, I, P]),
     "dq_matmul_q4k_path": (I, [P, P, P, I, I, I, I, P]),
     "dq_matmul_q4k_split": (I, [P, P, P, I, I, I, P, LL, P]),
@@ -330,6 +337,212 @@ def attention_decode_rope(q: torch.Tensor, k_new: torch.Tensor, k_plane: torch.T
                                       _ptr(k_norm), _ptr(rope), float(eps), n_q, n_kv, hd, max_ctx, int(n_keys),
                                       _ptr(ws), ws.numel(), _stream())
     _check("dq_attention_decode_rope", st)
+    return out
+
+
+# ------------------------------------- prompts, packed rows, 4-bit caches
+
+TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2
+_TYPES = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+KV4_BLOCK_ROWS, KV4_BLOCK_BYTES = 16, 2560
+
+
+def _type(dtype) -> int:
+    t = _TYPES.get(dtype)
+    if t is None:
+        raise ValueError("no library type for %s" % dtype)
+    return t
+
+
+def _on_device(*tensors):
+    """The tensors' addresses; all on the current CUDA device, which the library launches on."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if not t.is_cuda or t.device.index != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+    return [t.data_ptr() for t in tensors]
+
+
+def _int32(name, t, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
+
+
+def _rows(name, t, dtype=None):
+    """Row and head stride (elements) of a [rows, heads, 128] tensor with contiguous heads of 128."""
+    if t.dim() != 3 or t.shape[2] != 128 or (t.stride(2) != 1) or (dtype is not None and t.dtype != dtype):
+        raise ValueError("%s must be [rows, heads, 128]%s with contiguous 128" % (name, " %s" % dtype if dtype else ""))
+    heads = t.shape[1]
+    head = t.stride(1) if heads > 1 else 128
+    return (t.stride(0) if t.shape[0] > 1 else max(head * heads, 128)), head
+
+
+def _out(name, t, like_shape, dtype, device):
+    if t is None:
+        return torch.empty(like_shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(like_shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(like_shape)))
+    return t
+
+
+def qkv_rope(qkv: torch.Tensor, positions: torch.Tensor, rope: torch.Tensor, n_q: int, n_kv: int, q_norm=None,
+             k_norm=None, eps: float = 1e-6, dtype=torch.float16, out=None):
+    """qkv: fp32 [rows, >= (n_q + 2 n_kv) 128] (a row stride is fine), positions int32 [rows] (negative: a padding
+    row, left as it was), rope from rope_table -> (q [rows, n_q, 128], k, v [rows, n_kv, 128]) of ``dtype``."""
+    lib = load()
+    if qkv.dim() != 2 or qkv.dtype != torch.float32 or (qkv.stride(1) != 1 and qkv.shape[1] > 1):
+        raise ValueError("qkv must be a 2-D fp32 tensor with contiguous rows")
+    rows, width = qkv.shape
+    if width < (n_q + 2 * n_kv) * 128:
+        raise ValueError("qkv has %d columns, %d heads of 128 are wanted" % (width, n_q + 2 * n_kv))
+    if rope.dtype != torch.float32 or tuple(rope.shape[1:]) != (64, 2) or not rope.is_contiguous():
+        raise ValueError("rope must be a contiguous fp32 [max_ctx, 64, 2] table")
+    _int32("positions", positions, (rows,))
+    for w in (q_norm, k_norm):
+        if w is not None and (w.dtype != torch.float32 or w.numel() != 128 or not w.is_contiguous()):
+            raise ValueError("a head norm's weight must be fp32 [128]")
+    t = _type(dtype)
+    q, k, v = out if out is not None else (None, None, None)
+    dev = qkv.device
+    q = _out("q", q, (rows, n_q, 128), dtype, dev)
+    k, v = _out("k", k, (rows, n_kv, 128), dtype, dev), _out("v", v, (rows, n_kv, 128), dtype, dev)
+    px, pp, pr, pq, pk, pv = _on_device(qkv, positions, rope, q, k, v)
+    wq, wk = (None if w is None else _on_device(w)[0] for w in (q_norm, k_norm))
+    stride = qkv.stride(0) if rows > 1 else -(-width // 4) * 4
+    _check("dq_qkv_rope", lib.dq_qkv_rope(px, stride, pp, wq, wk, pr, eps, rows, n_q, n_kv, 128, rope.shape[0], t,
+                                          pq, pk, pv, _stream()))
+    return q, k, v
+
+
+class _Prompt(ctypes.Structure):
+    _fields_ = ([(n, P) for n in ("q", "k", "v", "out")]
+                + [(n, LL) for n in ("q_row_stride", "q_head_stride", "k_row_stride", "k_head_stride",
+                                     "v_row_stride", "v_head_stride", "out_row_stride", "out_head_stride")]
+                + [("cu_q", P), ("cu_k", P)]
+                + [(n, I) for n in ("type", "n_seq", "total_q", "total_k", "n_q", "n_kv", "head_dim")]
+                + [("workspace", P), ("workspace_bytes", SZ)])
+
+
+def attention_prompt_workspace(n_seq: int, total_q: int, total_k: int, n_q: int, n_kv: int, device=None):
+    """Scratch for attention_prompt calls of at most these sizes (None where none is needed)."""
+    n = load().dq_attention_prompt_workspace_bytes(n_seq, total_q, total_k, n_q, n_kv)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
+
+
+def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k=None, out=None,
+                     workspace=None):
+    """Causal attention of packed sequences: q [total_q, n_q, 128], k and v [total_k, n_kv, 128], fp16 or bf16, any
+    row and head strides (slices of one projection, a cache plane transposed); cu_q, cu_k int32 [n_seq + 1].
+    Query i of a sequence sees keys j <= i + Lk - Lq.  Rows of no sequence are left as they were (uninitialised
+    where ``out`` is not given)."""
+    lib = load()
+    q_row, q_head = _rows("q", q)
+    k_row, k_head = _rows("k", k, q.dtype)
+    v_row, v_head = _rows("v", v, q.dtype)
+    total_q, n_q, _ = q.shape
+    total_k, n_kv, _ = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    n_seq = cu_q.numel() - 1
+    _int32("cu_q", cu_q, (n_seq + 1,))
+    if cu_k is not None:
+        _int32("cu_k", cu_k, (n_seq + 1,))
+    if out is None:
+        out = torch.empty((total_q, n_q, 128), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    o_row, o_head = _rows("out", out, q.dtype)
+    if workspace is None:
+        n = lib.dq_attention_prompt_workspace_bytes(n_seq, total_q, total_k, n_q, n_kv)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    pq, pk, pv, po, pc = _on_device(q, k, v, out, cu_q)
+    pck = None if cu_k is None else _on_device(cu_k)[0]
+    pw, nw = (None, 0) if workspace is None else (_on_device(workspace)[0], workspace.numel() * workspace.element_size())
+    d = _Prompt(pq, pk, pv, po, q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head, pc, pck, _type(q.dtype),
+                n_seq, total_q, total_k, n_q, n_kv, 128, pw, nw)
+    _check("dq_attention_prompt", lib.dq_attention_prompt(ctypes.byref(d), _stream()))
+    return out
+
+
+def kv4_pool(n_pages: int, n_kv: int, page_size: int, device=None) -> torch.Tensor:
+    """A zero-filled 4-bit cache pool: uint8 [n_pages, n_kv, page_size / 16, 2560] (see include/dq.h)."""
+    if page_size < 1 or page_size % KV4_BLOCK_ROWS:
+        raise ValueError("page_size must be a multiple of %d" % KV4_BLOCK_ROWS)
+    return torch.zeros((n_pages, n_kv, page_size // KV4_BLOCK_ROWS, KV4_BLOCK_BYTES), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def _pool(pool):
+    if pool.dim() != 4 or pool.dtype != torch.uint8 or pool.shape[3] != KV4_BLOCK_BYTES or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous uint8 [n_pages, n_kv, page_size / 16, %d] tensor" % KV4_BLOCK_BYTES)
+    return pool.shape[0], pool.shape[1], pool.shape[2] * KV4_BLOCK_ROWS
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor):
+    """Store k and v [rows, n_kv, 128] (fp32, fp16 or bf16, any row and head strides) at slots (int32 [rows]: page *
+    page_size + offset, negative to skip a row; all different) of the pool."""
+    lib = load()
+    n_pages, n_kv, page = _pool(pool)
+    k_row, k_head = _rows("k", k)
+    v_row, v_head = _rows("v", v, k.dtype)
+    rows = k.shape[0]
+    if v.shape != k.shape or k.shape[1] != n_kv:
+        raise ValueError("k and v must both be [rows, %d, 128]" % n_kv)
+    _int32("slots", slots, (rows,))
+    t = _type(k.dtype)
+    pk, pv, ps, pp = _on_device(k, v, slots, pool)
+    _check("dq_kv4_append", lib.dq_kv4_append(pk, pv, t, k_row, k_head, v_row, v_head, ps, pp, rows, n_kv,
+                                              128, n_pages, page, _stream()))
+
+
+def kv4_read(pool: torch.Tensor, slots: torch.Tensor, dtype=torch.float16, out=None):
+    """The rows at ``slots`` (int32 [rows]) as values: (k, v), each [rows, n_kv, 128] of ``dtype``."""
+    lib = load()
+    n_pages, n_kv, page = _pool(pool)
+    rows = slots.numel()
+    _int32("slots", slots, (rows,))
+    t = _type(dtype)
+    k, v = out if out is not None else (None, None)
+    k, v = (_out("out", x, (rows, n_kv, 128), dtype, pool.device) for x in (k, v))
+    pp, ps, pk, pv = _on_device(pool, slots, k, v)
+    _check("dq_kv4_read", lib.dq_kv4_read(pp, ps, t, pk, pv, rows, n_kv, 128, n_pages, page, _stream()))
+    return k, v
+
+
+def attention_decode_kv4_workspace(n_seq: int, n_q: int, n_kv: int, max_keys: int, device=None):
+    """Scratch for attention_decode_kv4 calls of these sizes (None where none is needed)."""
+    n = load().dq_attention_decode_kv4_workspace_bytes(n_seq, n_q, n_kv, max_keys)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
+
+
+def attention_decode_kv4(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tensor, n_keys: torch.Tensor,
+                         max_keys: int | None = None, workspace=None, out=None):
+    """One token a sequence over the 4-bit cache: q [n_seq, n_q, 128] (fp32, fp16 or bf16), pages int32 [n_seq,
+    max_pages], n_keys int32 [n_seq] -> [n_seq, n_q, 128] of q's type.  ``max_keys``: a bound on n_keys known to the
+    host (the work is split by it); all the table's pages where it is not given."""
+    lib = load()
+    n_pages, n_kv, page = _pool(pool)
+    if q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [n_seq, n_q, 128] tensor")
+    n_seq, n_q, _ = q.shape
+    if pages.dim() != 2:
+        raise ValueError("pages must be [n_seq, max_pages]")
+    max_pages = pages.shape[1]
+    _int32("pages", pages, (n_seq, max_pages))
+    _int32("n_keys", n_keys, (n_seq,))
+    if max_keys is None:
+        max_keys = max_pages * page
+    out = _out("out", out, q.shape, q.dtype, q.device)
+    if workspace is None:
+        n = lib.dq_attention_decode_kv4_workspace_bytes(n_seq, n_q, n_kv, max_keys)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    pq, pp, pt, pn, po = _on_device(q, pool, pages, n_keys, out)
+    pw, nw = (None, 0) if workspace is None else (_on_device(workspace)[0], workspace.numel() * workspace.element_size())
+    _check("dq_attention_decode_kv4",
+           lib.dq_attention_decode_kv4(pq, _type(q.dtype), pp, pt, pn, po, n_seq, n_q, n_kv, 128, n_pages, page,
+                                       max_pages, max_keys, pw, nw, _stream()))
     return out
 
 
