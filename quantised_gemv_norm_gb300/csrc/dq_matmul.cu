@@ -26,13 +26,11 @@
 // fp16 and not bf16 operands: a dequantised Q4_K weight d sc q - dmin m has up
 // to 21 significant bits; fp16 keeps 11 (relative error 2^-12 per weight,
 // about 1e-4 normwise on a row), bf16 only 8 (about 1e-3, half the tolerance).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
 #include "dq_gemv_host.h"
 #include "dq_tc.cuh"
+#include "dq_tma_host.h"
 
 namespace dq {
 
@@ -650,9 +648,7 @@ namespace dqhost {
 
 static int mm_nt(int M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
 
-using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
-
-static EncodeTiled encode_tiled()
+EncodeTiled encode_tiled()
 {
     static std::once_flag once;
     static EncodeTiled fn = nullptr;

@@ -1,76 +1,547 @@
-// dq_prompt.cu -- causal attention of packed prompts (dq_attention_prompt).
+// dq_prompt.cu -- causal attention of packed prompts (dq_attention_prompt) on the
+// 5th-generation tensor cores.
 //
-// One warp takes one query row of one head and walks the keys it sees with a
-// running maximum and sum, four dims a lane.
-#include "dq_attn.cuh"
+// A block takes two tiles of 128 query rows of one sequence and one KV head.  A
+// tile's rows are floor(128 / group) tokens times the `group` query heads that share
+// the KV head, so the heads of a group read each key and value tile once.  Per tile
+// of 128 keys, for each query tile:
+//   S = Q K^T     tcgen05.mma, 128 x 128 fp32 in tensor memory, operands in shared
+//                 memory (TMA, 128-byte swizzle);
+//   P = 2^(c S - c m), c = log2(e) / sqrt(128), by four warps, one row a thread, with
+//                 the row's running maximum m and sum l in fp32 registers; P goes
+//                 back into tensor memory over S as 16-bit pairs;
+//   O += P V      tcgen05.mma, P from tensor memory, V N-major from shared memory,
+//                 128 x 128 fp32 in tensor memory.
+// While the tensor cores work on one query tile, the other tile's warps do their
+// exponentials.  m follows the true maximum only when that has grown by more than
+// 2^8 (then l and O are scaled): the ratio P / l does not depend on which m is
+// used, P stays below 2^8 in fp16 and every sum is fp32, and the scaling of O,
+// which would wait for the last product, is rare after the first tiles.
+//
+// Key tiles that hold masked keys for some row (the diagonal's and a sequence's end)
+// have their infinities and NaNs in V replaced by zero before the product, since a
+// probability of 0 would not stop them; where such a key is seen by some row, the
+// epilogue adds the values themselves to the rows that see them.
+#include <mutex>
+
+#include "dq_tc.cuh"
+#include "dq_tma_host.h"
 #include "dq_types.cuh"
 
 namespace dq {
 
+constexpr int PR_HD = 128;
+constexpr int PR_KEYS = 128;                  // keys a tile
+constexpr int PR_STAGES = 5;                  // ring of key and value tiles, in turn
+constexpr int PR_TILE = PR_KEYS * PR_HD * 2;  // bytes of a key, value or query tile
+constexpr int PR_PANEL = PR_TILE / 2;         // 64 dims of it
+constexpr int PR_MMA_WARP = 8, PR_TMA_WARP = 9, PR_CLEAN_WARP = 10;
+constexpr int PR_THREADS = 384;
+// A block's rows end within 256 keys of one another: at most this many key tiles
+// are seen by some rows in part.
+constexpr int PR_CLEAN = 3;
+constexpr int PR_SMEM = (2 + PR_STAGES) * PR_TILE + 1024 /* alignment */ + 512;
+constexpr uint32_t PR_S0 = 0, PR_O0 = 256, PR_TCOLS = 512;  // tensor memory columns: S0 S1 O0 O1
+constexpr float PR_C = 0.08838834764831845f * 1.4426950408889634f;
+constexpr float PR_GROW = 8.0f;  // log2 of the growth of the maximum that is let pass
+
 struct PromptArgs {
-    const void* q;
-    const void* k;
+    CUtensorMap tq, tk, tv;
     const void* v;
     void* out;
-    long long q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head;
+    long long v_row, v_head, o_row, o_head;
     const int* cu_q;
     const int* cu_k;
-    int n_seq, total_q, total_k, n_q, group;
+    int n_seq, total_q, total_k, n_kv, group, tq_tokens;  // tokens a query tile
     int* err;
 };
 
-// Rows [a, b) of sequence s: false (and the error bit) where the offsets do not
-// ascend within their total.
-__device__ __forceinline__ bool prompt_range(const int* cu, int s, int total, int& a, int& b)
+// One block's share: query tokens [t0, ...) of a sequence, its rows and keys.
+struct PromptTile {
+    int q0, k0, lq, lk, t0, live;
+};
+
+// Rows of sequence s; false where the offsets do not ascend within their totals.
+__device__ __forceinline__ bool prompt_seq(const PromptArgs& a, int s, int& q0, int& lq, int& k0, int& lk)
 {
-    a = cu[s];
-    b = cu[s + 1];
-    return a >= 0 && a <= b && b <= total;
+    const int qa = __ldg(a.cu_q + s), qb = __ldg(a.cu_q + s + 1);
+    const int ka = __ldg(a.cu_k + s), kb = __ldg(a.cu_k + s + 1);
+    q0 = qa;
+    k0 = ka;
+    const bool ok = qa >= 0 && qa <= qb && qb <= a.total_q && ka >= 0 && ka <= kb && kb <= a.total_k;
+    lq = ok ? qb - qa : 0;
+    lk = ok ? kb - ka : 0;
+    return ok;
 }
 
-constexpr int PROMPT_WARPS = 4;
+// Block tile `idx`, counted from the last sequence's last tile (a causal sequence's
+// later tiles see more keys: they start first).  By one warp; `span` tokens a block.
+__device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, int span, int lane)
+{
+    PromptTile t{0, 0, 0, 0, 0, 0};
+    int total = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
+        int q0, lq = 0, k0, lk;
+        if (s0 + lane < a.n_seq && !prompt_seq(a, s0 + lane, q0, lq, k0, lk) && idx == 0)
+            set_error(a.err, DEVERR_BAD_ARG);
+        total += __reduce_add_sync(0xffffffffu, (lq + span - 1) / span);
+    }
+    const int want = total - 1 - idx;
+    if (want < 0)
+        return t;
+    int before = 0;
+    for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
+        int q0 = 0, lq = 0, k0 = 0, lk = 0;
+        if (s0 + lane < a.n_seq)
+            prompt_seq(a, s0 + lane, q0, lq, k0, lk);
+        const int n = (lq + span - 1) / span;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += x;
+        }
+        const int mine = want - before - (incl - n);
+        const unsigned hit = __ballot_sync(0xffffffffu, mine >= 0 && mine < n);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            t.q0 = __shfl_sync(0xffffffffu, q0, src);
+            t.k0 = __shfl_sync(0xffffffffu, k0, src);
+            t.lq = __shfl_sync(0xffffffffu, lq, src);
+            t.lk = __shfl_sync(0xffffffffu, lk, src);
+            t.t0 = __shfl_sync(0xffffffffu, mine, src) * span;
+            t.live = 1;
+            return t;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return t;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Bits 15 and 31 set where the low and the high 16-bit value is an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t non_finite2(uint32_t w)
+{
+    constexpr bool half = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t mask = half ? 0x7C007C00u : 0x7F807F80u, one = half ? 0x04000400u : 0x00800080u;
+    return ((w & mask) + one) & 0x80008000u;
+}
 
 template <typename T>
-__global__ void __launch_bounds__(32 * PROMPT_WARPS) prompt_kernel(PromptArgs a)
+__device__ __forceinline__ float one16(uint32_t bits)
 {
-    const int lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * PROMPT_WARPS + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(a.total_q) * a.n_q)
-        return;
-    const int row = static_cast<int>(item / a.n_q), h = static_cast<int>(item % a.n_q), g = h / a.group;
-    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-    bool found = false;
-    for (int s = 0; s < a.n_seq && !found; ++s) {
-        const bool ok = prompt_range(a.cu_q, s, a.total_q, q0, q1) && prompt_range(a.cu_k, s, a.total_k, k0, k1);
-        if (!ok && lane == 0)
-            set_error(a.err, DEVERR_BAD_ARG);
-        found = ok && row >= q0 && row < q1;
+    if (std::is_same<T, __nv_bfloat16>::value)
+        return bf16lo(bits);
+    return half_bits_to_float(bits);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_constant__ PromptArgs a)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    uint8_t* qs = sm;                    // two query tiles
+    uint8_t* ring = sm + 2 * PR_TILE;    // PR_STAGES key and value tiles
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + PR_STAGES * PR_TILE);  // [2]
+    uint64_t* full = q_full + 2;             // [PR_STAGES] a ring tile landed
+    uint64_t* freed = full + PR_STAGES;      // [PR_STAGES] its products are done
+    // value tiles with masked keys, each with barriers of its own, used once: the ring's
+    // phases go on without the warps that clean them
+    uint64_t* v_full = freed + PR_STAGES;    // [PR_CLEAN] landed
+    uint64_t* cleaned = v_full + PR_CLEAN;   // [PR_CLEAN] infinities and NaNs are out
+    uint64_t* s_full = cleaned + PR_CLEAN;   // [2] S of a query tile written
+    uint64_t* p_full = s_full + 2;           // [2] P written
+    uint64_t* o_full = p_full + 2;           // [2] a product P V done
+    uint64_t* drain = o_full + 2;
+    PromptTile* shared_tile = reinterpret_cast<PromptTile*>(drain + 1);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(shared_tile + 1);
+    volatile int* fail = reinterpret_cast<volatile int*>(tslot + 1);
+    volatile int* poison = fail + 1;  // a seen value is an infinity or NaN
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = blockIdx.x % a.n_kv;
+    const int rows = a.tq_tokens * a.group;
+    if (warp == 0) {
+        const PromptTile t = prompt_find(a, blockIdx.x / a.n_kv, 2 * a.tq_tokens, lane);
+        if (lane == 0)
+            *shared_tile = t;
+    } else if (warp == PR_MMA_WARP) {
+        tmem_alloc(tslot, PR_TCOLS);
+    } else if (warp == PR_TMA_WARP && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tq)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tk)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tv)) : "memory");
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < PR_STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&freed[i], 1);
+        }
+        for (int i = 0; i < PR_CLEAN; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&cleaned[i], 2);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        *fail = 0;
+        *poison = 0;
     }
-    if (!found)
-        return;
-    const int n = min(k1 - k0, row - q0 + (k1 - k0) - (q1 - q0) + 1);
-    const float4 q = load4(static_cast<const T*>(a.q) + row * a.q_row + h * a.q_head + 4 * lane);
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j = 0; j < n; ++j) {
-        const float4 k = load4(static_cast<const T*>(a.k) + (k0 + j) * a.k_row + g * a.k_head + 4 * lane);
-        const float4 v = load4(static_cast<const T*>(a.v) + (k0 + j) * a.v_row + g * a.v_head + 4 * lane);
-        const float s = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w) * 0.08838834764831845f;
-        const float mn = fmaxf(m, s);
-        const float corr = expf(m - mn), e = expf(s - mn);
-        m = mn;
-        l = l * corr + e;
-        o.x = o.x * corr + e * v.x;
-        o.y = o.y * corr + e * v.y;
-        o.z = o.z * corr + e * v.z;
-        o.w = o.w * corr + e * v.w;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const PromptTile tile = *shared_tile;
+    const uint32_t tbase = *tslot;
+
+    // tokens, key tiles and the keys that every row of the tile sees, per query tile
+    int ntok[2], end[2], open = 0x7fffffff;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int ts = tile.t0 + t * a.tq_tokens;
+        ntok[t] = max(0, min(a.tq_tokens, tile.lq - ts));
+        const int hi = min(tile.lk, max(0, ts + ntok[t] + tile.lk - tile.lq));
+        end[t] = ntok[t] ? (hi + PR_KEYS - 1) / PR_KEYS : 0;
+        if (ntok[t])
+            open = min(open, min(tile.lk, max(0, ts + 1 + tile.lk - tile.lq)));
     }
-    const float inv = n < 1 ? 0.f : 1.0f / l;
-    store4(static_cast<T*>(a.out) + row * a.o_row + h * a.o_head + 4 * lane,
-           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    const int jmax = max(end[0], end[1]);
+    const int jclean = open / PR_KEYS;  // the first key tile with a masked key for some row
+
+    auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (*fail)
+            return false;
+        if (!mbar_wait(bar, parity)) {
+            *fail = 1;
+            set_error(a.err, code);
+            return false;
+        }
+        return true;
+    };
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
+        return __all_sync(0xffffffffu, wait(bar, parity, code)) != 0;
+    };
+
+    if (tile.live && warp == PR_TMA_WARP) {
+        if (lane == 0 && jmax > 0) {
+            for (int t = 0; t < 2; ++t) {
+                if (!end[t])
+                    continue;
+                mbar_arrive_expect_tx(&q_full[t], static_cast<uint32_t>(2 * rows * 128));
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(qs + t * PR_TILE + p * PR_PANEL, &a.tq, 64 * p, g * a.group,
+                                tile.q0 + tile.t0 + t * a.tq_tokens, &q_full[t]);
+            }
+            int issued = 0, cleans = 0;
+            for (; issued < 2 * jmax; ++issued) {  // key tile 0, value tile 0, key tile 1, ...
+                const int s = issued % PR_STAGES;
+                if (issued >= PR_STAGES && !wait(&freed[s], ((issued / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
+                    break;
+                const int j = issued >> 1;
+                const bool clean = (issued & 1) && j >= jclean;
+                uint64_t* bar = clean ? &v_full[j - jclean] : &full[s];
+                mbar_arrive_expect_tx(bar, PR_TILE);
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(ring + s * PR_TILE + p * PR_PANEL, (issued & 1) ? &a.tv : &a.tk, 64 * p,
+                                tile.k0 + j * PR_KEYS, g, bar);
+                if (clean) {
+                    mbar_arrive(&full[s]);  // the slot's phase goes on
+                    ++cleans;
+                }
+            }
+            // every copy has landed before the block ends
+            for (int i = max(0, issued - PR_STAGES); i < issued; ++i)
+                if (!mbar_wait(&full[i % PR_STAGES], (i / PR_STAGES) & 1))
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+            for (int i = 0; i < cleans; ++i)
+                if (!mbar_wait(&v_full[i], 0))
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+            for (int t = 0; t < 2; ++t)
+                if (end[t] && !mbar_wait(&q_full[t], 0))
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+        }
+        __syncwarp();
+    } else if (tile.live && warp == PR_MMA_WARP) {
+        if (lane == 0 && jmax > 0) {
+            constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+            constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
+            constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
+            bool ok = true;
+            auto qk = [&](int t, int j) {  // S_t = Q_t K_j^T: eight steps of 16 dims, four a panel
+                const uint32_t kb = smem_addr(ring + (2 * j % PR_STAGES) * PR_TILE);
+                const uint64_t ad = umma_desc_sw128(smem_addr(qs + t * PR_TILE), 16, 1024);
+                const uint64_t bd = umma_desc_sw128(kb, 16, 1024);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint64_t step = ((s >> 2) * PR_PANEL + (s & 3) * 32) >> 4;
+                    umma_f16(tbase + PR_S0 + 128 * t, ad + step, bd + step, id_qk, s > 0);
+                }
+                umma_commit(&s_full[t]);
+            };
+            auto pv = [&](int t, int j) {  // O_t += P_t V_j: eight steps of 16 keys
+                const uint64_t bd = umma_desc_sw128(smem_addr(ring + ((2 * j + 1) % PR_STAGES) * PR_TILE), PR_PANEL, 1024);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    umma_f16_ta(tbase + PR_O0 + 128 * t, tbase + PR_S0 + 128 * t + 8 * s,
+                                bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, j > 0 || s > 0);
+                umma_commit(&o_full[t]);
+            };
+            ok = wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
+            for (int t = 0; ok && t < 2; ++t)
+                if (end[t] && (ok = wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
+                    qk(t, 0);
+            umma_commit(&freed[0]);
+            for (int j = 0; ok && j < jmax; ++j) {
+                const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
+                ok = j >= jclean ? wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
+                                 : wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
+                if (ok && j + 1 < jmax)
+                    ok = wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
+                for (int t = 0; ok && t < 2; ++t) {
+                    if (j >= end[t])
+                        continue;
+                    if (!(ok = wait(&p_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
+                        break;
+                    tc_fence_after_sync();
+                    pv(t, j);
+                    if (j + 1 < end[t])
+                        qk(t, j + 1);
+                }
+                umma_commit(&freed[sv]);
+                if (j + 1 < jmax)
+                    umma_commit(&freed[sk]);
+            }
+            umma_commit(drain);  // every product is done before the block ends
+            if (!mbar_wait(drain, 0))
+                set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+        }
+        __syncwarp();
+    } else if (tile.live && warp >= PR_CLEAN_WARP) {
+        // infinities and NaNs of the value tiles with masked keys become zero
+        const int ct = tid - 32 * PR_CLEAN_WARP;
+        for (int j = jclean; j < jmax; ++j) {
+            if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
+                break;
+            uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
+            bool seen = false;
+            for (int i = ct; i < PR_TILE / 16; i += 64) {
+                uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
+                const uint32_t nx = non_finite2<T>(w.x), ny = non_finite2<T>(w.y), nz = non_finite2<T>(w.z),
+                               nw = non_finite2<T>(w.w);
+                if (nx | ny | nz | nw) {
+                    // 0x8000 -> 0xffff per half: the halves to clear
+                    w.x &= ~((nx >> 15) * 0xffffu);
+                    w.y &= ~((ny >> 15) * 0xffffu);
+                    w.z &= ~((nz >> 15) * 0xffffu);
+                    w.w &= ~((nw >> 15) * 0xffffu);
+                    *reinterpret_cast<uint4*>(vt + 16 * i) = w;
+                    seen |= j * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
+                }
+            }
+            if (seen)
+                *poison = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&cleaned[j - jclean]);
+        }
+    } else if (tile.live) {
+        // ---- softmax and epilogue: warps 4 t .. 4 t + 3, thread r of them owns row r
+        const int t = warp >> 2, r = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tbase + lanes + PR_S0 + 128 * t, to = tbase + lanes + PR_O0 + 128 * t;
+        const int tok = tile.t0 + t * a.tq_tokens + r / a.group;  // within the sequence
+        const bool mine = r / a.group < ntok[t];
+        const int lim = min(tile.lk, max(0, tok + 1 + tile.lk - tile.lq));  // keys this row sees
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < end[t]; ++j) {
+            if (!(ok = warp_wait(&s_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
+                break;
+            tc_fence_after_sync();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tmem_ld32(ts + 32 * c, s + 32 * c);
+            tmem_ld_wait();
+            if (j >= jclean) {
+                const int left = lim - j * PR_KEYS;
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c >= left)
+                        s[c] = 0xff800000u;  // -infinity
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+                top = fmaxf(top, __uint_as_float(s[c]));
+            const bool grow = (top - m) * PR_C > PR_GROW;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float mn = grow ? top : m;
+                const float alpha = grow ? ex2((m - mn) * PR_C) : 1.0f;  // 0 from -infinity
+                m = mn;
+                l *= alpha;
+                if (j > 0) {
+                    if (!(ok = warp_wait(&o_full[t], (j - 1) & 1, DEVERR_TIMEOUT_FULL)))
+                        break;
+                    tc_fence_after_sync();
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st32(to + 32 * c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m * PR_C;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float x = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i]), PR_C, -base));
+                    const float y = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]), PR_C, -base));
+                    sum0 += x;
+                    sum1 += y;
+                    p[i] = pack2(x, y, static_cast<const T*>(nullptr));
+                }
+                tmem_st32(ts + 32 * c, p);
+            }
+            l += sum0 + sum1;
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&p_full[t]);
+        }
+        if (ok && end[t])
+            ok = warp_wait(&o_full[t], (end[t] - 1) & 1, DEVERR_TIMEOUT_FULL);
+        tc_fence_after_sync();
+        if (ok && ntok[t]) {
+            // a row that sees no key is zero, one whose scores are all -infinity NaN (0 / 0)
+            const float inv = lim > 0 ? 1.0f / l : 0.f;
+            T* out = static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
+                     static_cast<long long>(g * a.group + r % a.group) * a.o_head;
+            const bool bad = *poison;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                if (end[t]) {
+                    tmem_ld32(to + 32 * c, o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    o[i] = lim > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
+                if (bad && mine) {
+                    for (int j = jclean * PR_KEYS; j < lim; ++j) {
+                        const uint4* vp = reinterpret_cast<const uint4*>(
+                            static_cast<const T*>(a.v) + static_cast<long long>(tile.k0 + j) * a.v_row +
+                            static_cast<long long>(g) * a.v_head + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 w = vp[i];
+                            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t n = non_finite2<T>(u[e]);
+                                float& lo = reinterpret_cast<float&>(o[8 * i + 2 * e]);
+                                float& hi = reinterpret_cast<float&>(o[8 * i + 2 * e + 1]);
+                                if (n & 0x8000u)
+                                    lo += one16<T>(u[e] & 0xffffu);
+                                if (n & 0x80000000u)
+                                    hi += one16<T>(u[e] >> 16);
+                            }
+                        }
+                    }
+                }
+                if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint4 w;
+                        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = pack2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]),
+                                         static_cast<const T*>(nullptr));
+                        *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = w;
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == PR_MMA_WARP)
+        tmem_dealloc(tbase, PR_TCOLS);
 }
 
 }  // namespace dq
+
+namespace dqhost {
+
+// A 16-bit tensor [outer][middle][128] with the given strides (elements), copied in
+// boxes of 64 dims with the 128-byte swizzle.
+static bool prompt_map(EncodeTiled enc, CUtensorMap* m, int type, const void* p, int middle, long long middle_stride,
+                       int outer, long long outer_stride, int box_middle, int box_outer)
+{
+    const cuuint64_t dims[3] = {dq::PR_HD, static_cast<cuuint64_t>(middle), static_cast<cuuint64_t>(outer)};
+    // a stride of a dimension of one is never used, but has to be one that the encoder takes
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(middle > 1 ? middle_stride : dq::PR_HD) * 2,
+                                   static_cast<cuuint64_t>(outer > 1 ? outer_stride : dq::PR_HD) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_middle), static_cast<cuuint32_t>(box_outer)};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return enc(m, type == DQ_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+               const_cast<void*>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The kernel's shared memory, asked for once per device.
+template <typename T>
+static cudaError_t prompt_prepare()
+{
+    static std::mutex mu;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(dq::prompt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq::PR_SMEM);
+        if (e == cudaSuccess && dev >= 0 && dev < 64)
+            done[dev] = true;
+    }
+    return e;
+}
+
+}  // namespace dqhost
 
 extern "C" {
 
@@ -87,29 +558,59 @@ DQ_API int dq_attention_prompt(const dq_prompt* p, void* stream)
     const long long heads[4] = {p->q_head_stride, p->k_head_stride, p->v_head_stride, p->out_head_stride};
     for (int i = 0; i < 4; ++i) {
         const bool kv = i == 1 || i == 2;
-        if (((kv ? p->total_k : p->total_q) > 1 && rows[i] < dq::ATT_HD) ||
-            ((kv ? p->n_kv : p->n_q) > 1 && heads[i] < dq::ATT_HD))
+        if (((kv ? p->total_k : p->total_q) > 1 && rows[i] < dq::PR_HD) ||
+            ((kv ? p->n_kv : p->n_q) > 1 && heads[i] < dq::PR_HD))
             return DQ_ERR_SHAPE;
     }
-    if (p->head_dim != dq::ATT_HD || p->n_q / p->n_kv > 128 || p->total_q > (1 << 30) || p->total_k > (1 << 30))
+    if (p->head_dim != dq::PR_HD || p->n_q / p->n_kv > 128 || p->total_q > (1 << 30) || p->total_k > (1 << 30))
         return DQ_ERR_UNSUPPORTED;
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {
         if (rows[i] % 8 || heads[i] % 8)
             return DQ_ERR_ALIGN;
+        if (rows[i] >= (1ll << 38) || heads[i] >= (1ll << 38))  // the tensor maps' strides are below 2^40 bytes
+            return DQ_ERR_UNSUPPORTED;
+    }
     if (!dqhost::aligned16(p->q) || !dqhost::aligned16(p->k) || !dqhost::aligned16(p->v) || !dqhost::aligned16(p->out))
         return DQ_ERR_ALIGN;
-    dq::PromptArgs a{p->q, p->k, p->v, p->out, rows[0], heads[0], rows[1], heads[1], rows[2], heads[2], rows[3], heads[3],
-                     p->cu_q, p->cu_k ? p->cu_k : p->cu_q, p->n_seq, p->total_q, p->total_k, p->n_q, p->n_q / p->n_kv,
-                     dqhost::device_error_flag()};
-    const long long blocks = (static_cast<long long>(p->total_q) * p->n_q + dq::PROMPT_WARPS - 1) / dq::PROMPT_WARPS;
+    const int group = p->n_q / p->n_kv, tokens = 128 / group;
+    const long long blocks = (static_cast<long long>(p->total_q) / (2 * tokens) + p->n_seq) * p->n_kv;
     if (blocks > 0x7fffffffll)
         return DQ_ERR_UNSUPPORTED;
+    dqhost::EncodeTiled enc = dqhost::encode_tiled();
+    if (!enc)
+        return DQ_ERR_UNSUPPORTED;
+    dq::PromptArgs a{};
+    if (!dqhost::prompt_map(enc, &a.tq, p->type, p->q, p->n_q, heads[0], p->total_q, rows[0], group, tokens) ||
+        !dqhost::prompt_map(enc, &a.tk, p->type, p->k, p->total_k, rows[1], p->n_kv, heads[1], dq::PR_KEYS, 1) ||
+        !dqhost::prompt_map(enc, &a.tv, p->type, p->v, p->total_k, rows[2], p->n_kv, heads[2], dq::PR_KEYS, 1))
+        return DQ_ERR_UNSUPPORTED;
+    a.v = p->v;
+    a.out = p->out;
+    a.v_row = rows[2];
+    a.v_head = heads[2];
+    a.o_row = rows[3];
+    a.o_head = heads[3];
+    a.cu_q = p->cu_q;
+    a.cu_k = p->cu_k ? p->cu_k : p->cu_q;
+    a.n_seq = p->n_seq;
+    a.total_q = p->total_q;
+    a.total_k = p->total_k;
+    a.n_kv = p->n_kv;
+    a.group = group;
+    a.tq_tokens = tokens;
+    a.err = dqhost::device_error_flag();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (p->type == DQ_TYPE_F16)
-        dq::prompt_kernel<__half><<<static_cast<unsigned>(blocks), 32 * dq::PROMPT_WARPS, 0, s>>>(a);
-    else
-        dq::prompt_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), 32 * dq::PROMPT_WARPS, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const unsigned grid = static_cast<unsigned>(blocks);
+    cudaError_t e;
+    if (p->type == DQ_TYPE_F16) {
+        if ((e = dqhost::prompt_prepare<__half>()) == cudaSuccess)
+            dq::prompt_kernel<__half><<<grid, dq::PR_THREADS, dq::PR_SMEM, s>>>(a);
+    } else {
+        if ((e = dqhost::prompt_prepare<__nv_bfloat16>()) == cudaSuccess)
+            dq::prompt_kernel<__nv_bfloat16><<<grid, dq::PR_THREADS, dq::PR_SMEM, s>>>(a);
+    }
+    if (e == cudaSuccess)
+        e = cudaGetLastError();
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }
 

@@ -54,6 +54,25 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16_f32(int M, int N)
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same fields for fp16 (bf16 = false) or bf16 operands, B K-major or, with
+// `b_mn`, N-major (bit 16).
+__host__ __device__ constexpr uint32_t umma_idesc_16bit(int M, int N, bool bf16, bool b_mn)
+{
+    return umma_idesc_f16_f32(M, N) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
+// Shared-memory matrix descriptor with the 128-byte swizzle (layout type 2 at bits
+// 61-63), base 1024-byte aligned up to a K advance: rows of 128 bytes, eight-row
+// groups of 1024 bytes.  K-major (a row is one M or N index, 64 K values): `sbo`
+// is the distance of eight-row groups along M or N, `lbo` is not used.  N-major (a
+// row is one K index, 64 N values): `sbo` is the distance of eight-row groups along
+// K, `lbo` that of the 64-wide panels along N.
+__device__ __forceinline__ uint64_t umma_desc_sw128(uint32_t smem, uint32_t lbo, uint32_t sbo)
+{
+    return static_cast<uint64_t>((smem >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
 // D (tensor memory) [+]= A (shared, M x 16) * B (shared, 16 x N): one MMA of
 // K = 16, issued by one thread.  `accum` = 0 overwrites D.
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -97,6 +116,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// 32 consecutive 32-bit columns, as tmem_ld16.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr)
         : "memory");
 }
