@@ -427,8 +427,9 @@ DQ_API int dq_kv4_read(const void* pool, const int* slots, int type, void* k_out
  * sets the bad-argument bit of the device's error flag (the sequence's output is
  * then zero, a bad page's keys take no part).  max_keys: a bound on every n_keys,
  * known to the host (it sets the split), at most max_pages * page_size.  Scores,
- * softmax and sums are fp32; queries and probabilities enter the matrix
- * instructions as two fp16 parts each (relative error about 2^-22).
+ * softmax and sums are fp32.  For fp32 queries and outputs the queries and
+ * probabilities enter the matrix instructions as two fp16 parts each (relative
+ * error about 2^-22); for 16-bit ones a probability is one fp16 number.
  * workspace: dq_attention_decode_kv4_workspace_bytes(...) bytes of device scratch
  * (NULL where that is 0), 16-byte aligned, its content before and after the call
  * of no meaning; calls that share one must not overlap in time.

@@ -8,8 +8,8 @@
 // the block's warps meet once at the end, the blocks of one sequence in a second
 // kernel.  The cache bytes bound it, so the arithmetic goes to the (warp-level)
 // matrix instructions m16n8k16, whose 16 rows hold the group's up to 8 query heads
-// twice: the fp16 part of a query in row h and the rest of it in row 8 + h, which
-// gives 22 bits for the price of 11 with so few rows.  The codes c - 8 are exact in
+// twice: the fp16 part of a query in row h and, for fp32 results, the rest of it in row
+// 8 + h, which gives 22 bits for the price of 11 with so few rows.  The codes c - 8 are exact in
 // fp16 and need no scale before the product:
 //   s_j   = sum_g d_jg (sum_{n in g} q_n (c_jn - 8)) + z_jg (sum_{n in g} q_n)
 //   out_n = sum_j (p_j d_jg) (c_jn - 8) + sum_j p_j z_jg
@@ -25,7 +25,9 @@
 namespace dq {
 
 constexpr int KA_WARPS = 4;
-constexpr int KA_NS = 4;       // ring stages a warp
+constexpr int KA_STEP = 2;     // cache blocks a ring stage
+constexpr int KA_NS = 2;       // ring stages a warp
+constexpr int KA_RESIDENT = 3; // blocks an SM (4, at 128 registers: 96.5 against 94.0 us, 48 sequences)
 constexpr int KA_PART = 132;   // floats of a partial result: r, l, two unused, 128 sums
 constexpr float KA_CAP = 12.f;   // p_j <= 2^cap where every d <= 8
 constexpr float KA_HEAD = 3.f;   // log2 that the maximum may grow before r follows it
@@ -86,13 +88,27 @@ __device__ __forceinline__ float ka_ex2(float x)
     return y;
 }
 
+// (w & m) | o as one instruction: with both constants immediate it would be two.
+__device__ __forceinline__ uint32_t ka_and_or(uint32_t w, uint32_t m, uint32_t o)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(m), "r"(o));
+    return r;
+}
+__device__ __forceinline__ uint32_t ka_opaque(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // Four fp16 pairs c - 8 from a word: pair i has the codes at bits 4 i and 16 + 4 i.
 // A code in mantissa bits 0-3 of 1024 is 1024 + c, in bits 4-7 of 64 it is 64 + c.
-__device__ __forceinline__ void ka_codes(uint32_t w, uint32_t (&p)[4])
+__device__ __forceinline__ void ka_codes(uint32_t w, uint32_t k1024, uint32_t k64, uint32_t (&p)[4])
 {
     const uint32_t w8 = w >> 8;
-    const uint32_t a = (w & 0x000F000Fu) | 0x64006400u, b = (w & 0x00F000F0u) | 0x54005400u;
-    const uint32_t c = (w8 & 0x000F000Fu) | 0x64006400u, d = (w8 & 0x00F000F0u) | 0x54005400u;
+    const uint32_t a = ka_and_or(w, 0x000F000Fu, k1024), b = ka_and_or(w, 0x00F000F0u, k64);
+    const uint32_t c = ka_and_or(w8, 0x000F000Fu, k1024), d = ka_and_or(w8, 0x00F000F0u, k64);
     // -1032 = 0xE408, -72 = 0xD480
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(p[0]) : "r"(a), "r"(0xE408E408u));
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(p[1]) : "r"(b), "r"(0xD480D480u));
@@ -100,29 +116,53 @@ __device__ __forceinline__ void ka_codes(uint32_t w, uint32_t (&p)[4])
     asm("add.rn.f16x2 %0, %1, %2;" : "=r"(p[3]) : "r"(d), "r"(0xD480D480u));
 }
 
-__device__ __forceinline__ void ka_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1)
+// The same pairs without the 8, as fp16 numbers below the normal range: 2^-24 c for
+// even pairs, 2^-20 c for odd ones.
+__device__ __forceinline__ void ka_small_codes(uint32_t w, uint32_t (&p)[4])
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    const uint32_t w8 = w >> 8;
+    p[0] = w & 0x000F000Fu;
+    p[1] = w & 0x00F000F0u;
+    p[2] = w8 & 0x000F000Fu;
+    p[3] = w8 & 0x00F000F0u;
 }
 
-// x, y as an fp16 pair and what is left of them as another.
+__device__ __forceinline__ void ka_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1, float c0, float c1, float c2, float c3)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// A row's result: the product of its first part and, with two, of its second.
+template <bool TWO>
+__device__ __forceinline__ uint64_t ka_both(const float (&d)[4])
+{
+    return TWO ? add2(f2(d[0], d[1]), f2(d[2], d[3])) : f2(d[0], d[1]);
+}
+
+// x, y as an fp16 pair and, with two parts, what is left of them as another.
+template <bool TWO>
 __device__ __forceinline__ void ka_split(uint64_t v, uint32_t& hi, uint32_t& lo)
 {
     const float2 x = un2(v);
     hi = pack2(x.x, x.y, static_cast<const __half*>(nullptr));
+    lo = 0u;
+    if (!TWO)
+        return;
     const float2 rest = un2(fma2(half2_f2(hi), f2(-1.f, -1.f), v));
     lo = pack2(rest.x, rest.y, static_cast<const __half*>(nullptr));
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4AttnArgs a)
+__global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(const Kv4AttnArgs a)
 {
-    __shared__ __align__(128) unsigned char ring[KA_WARPS][KA_NS][KV4_BYTES];
+    // two fp16 parts a query and probability, and centred key codes, where the result is
+    // fp32; one part, as wide as the result's own mantissa or wider, where it has 16 bits
+    constexpr bool TWO = std::is_same<T, float>::value;
+    __shared__ __align__(128) unsigned char ring[KA_WARPS][KA_NS][KA_STEP][KV4_BYTES];
     __shared__ uint64_t full[KA_WARPS][KA_NS];
-    __shared__ int skip[KA_WARPS][KA_NS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = lane >> 2, tq = lane & 3;  // this lane's head of the group, and quarter
     int x = blockIdx.x;
@@ -139,7 +179,10 @@ __global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4Att
     const int blk0 = c * a.chunk, blk1 = min(blk0 + a.chunk, (n + KV4_ROWS - 1) / KV4_ROWS);
     if (a.part && blk0 >= blk1)
         return;  // the join does not look at it
-    const int cnt = blk0 + warp < blk1 ? (blk1 - blk0 - warp + KA_WARPS - 1) / KA_WARPS : 0;
+    // the warp's i-th cache block is blk0 + KA_STEP (warp + KA_WARPS (i / KA_STEP)) + i % KA_STEP
+    const int first = blk0 + KA_STEP * warp;
+    auto block_at = [&](int i) { return first + KA_STEP * KA_WARPS * (i / KA_STEP) + i % KA_STEP; };
+    const int cnt = first < blk1 ? (blk1 - first + KA_STEP * KA_WARPS - 1) / (KA_STEP * KA_WARPS) : 0;  // stages
 
     if (lane == 0) {
         for (int i = 0; i < KA_NS; ++i)
@@ -148,44 +191,50 @@ __global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4Att
     }
     __syncwarp();
 
-    // ---- this warp's cache blocks: lane i has the page of the i-th of the next 32
+    // ---- lane i has the pool offset of the i-th of the next 32 cache blocks; a bad
+    // page's bit is set in `bad` and its copy is page 0's, whose keys are then skipped
     const int bpp = a.s.page_rows / KV4_ROWS;
     const int* pages = a.pages + static_cast<size_t>(b) * a.max_pages;
-    auto block_at = [&](int i) { return blk0 + warp + KA_WARPS * i; };
-    auto page_of = [&](int i) { return i < cnt ? __ldg(pages + block_at(i) / bpp) : 0; };
+    auto page_of = [&](int i) {
+        const int blk = block_at(i);
+        return blk < blk1 ? __ldg(pages + blk / bpp) : 0;
+    };
     int next_page = page_of(lane);
     long long off = 0;
-    auto issue = [&](int i) {
-        if ((i & 31) == 0) {
-            off = next_page < 0 || next_page >= a.s.n_pages
-                      ? -1
-                      : ((static_cast<long long>(next_page) * a.s.n_kv + g) * bpp + block_at(i + lane) % bpp) * KV4_BYTES;
-            next_page = page_of(i + 32 + lane);
-        }
-        const long long at = __shfl_sync(0xffffffffu, off, i & 31);
-        if (lane == 0) {
-            uint64_t* bar = &full[warp][i % KA_NS];
-            skip[warp][i % KA_NS] = at < 0;
-            if (at < 0) {
+    unsigned bad = 0, bad_next = 0;
+    auto issue = [&](int i) {  // stage i
+        const int at = KA_STEP * i;
+        if ((at & 31) == 0) {
+            const bool wrong = next_page < 0 || next_page >= a.s.n_pages;
+            bad_next = __ballot_sync(0xffffffffu, wrong);
+            off = ((static_cast<long long>(wrong ? 0 : next_page) * a.s.n_kv + g) * bpp + block_at(at + lane) % bpp) *
+                  KV4_BYTES;
+            next_page = page_of(at + 32 + lane);
+            if (bad_next && lane == 0)
                 set_error(a.err, DEVERR_BAD_ARG);
-                mbar_arrive(bar);
-            } else {
-                mbar_arrive_expect_tx(bar, KV4_BYTES);
-                asm volatile(
-                    "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                        smem_addr(ring[warp][i % KA_NS])),
-                    "l"(a.pool + at), "r"(KV4_BYTES), "r"(smem_addr(bar))
-                    : "memory");
-            }
         }
+        const bool two = block_at(at) + 1 < blk1;
+        if (lane == 0)
+            mbar_arrive_expect_tx(&full[warp][i % KA_NS], two ? 2 * KV4_BYTES : KV4_BYTES);
         __syncwarp();
+        const int k = lane - (at & 31);  // the lanes that have the stage's blocks copy them
+        if (k == 0 || (k == 1 && two))
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                    smem_addr(ring[warp][i % KA_NS][k])),
+                "l"(a.pool + off), "r"(KV4_BYTES), "r"(smem_addr(&full[warp][i % KA_NS]))
+                : "memory");
     };
     for (int i = 0; i < min(cnt, KA_NS); ++i)
         issue(i);
 
-    // ---- queries: scaled by a power of two a head into fp16's range, in two parts
+    // ---- queries: scaled by a power of two a head into fp16's range, in two parts;
+    // the sums of a group's queries, for the codes' 8 and for z
     uint32_t qa[8][4];
-    float qsum[4], unscale;
+    float unscale;
+    // the two parts of the groups' sums of q as the operand of the z product, and -8 times
+    // them for the d product that centres small codes: see below
+    uint32_t qz, qd;
     {
         float4 v[4][2];
         const T* q = static_cast<const T*>(a.q) + (static_cast<size_t>(b) * a.n_q + g * a.group + h) * ATT_HD + 8 * tq;
@@ -199,11 +248,15 @@ __global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4Att
             }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // largest |q| into [2^13, 2^14): the exponent field moves, nothing is rounded
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 13;
-        e = max(-100, min(114, e));
+        // largest |q| into [2^6, 2^7), so that 8 * 32 of them stay below fp16's 2^16: the
+        // exponent field moves, nothing is rounded
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 6;
+        e = max(-100, min(121, e));
         const float scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        unscale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (0.08838834764831845f * 1.4426950408889634f);
+        // to scores in powers of two; from small codes they come in units of 2^-24
+        unscale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) *
+                  ((TWO ? 1.f : 16777216.f) * 0.08838834764831845f * 1.4426950408889634f);
+        float qsum[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             float sum = 0.f;
@@ -211,8 +264,9 @@ __global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4Att
             for (int m = 0; m < 2; ++m) {
                 const float4 w = v[k][m];
                 const uint64_t p0 = f2(w.x * scale, w.y * scale), p1 = f2(w.z * scale, w.w * scale);
-                ka_split(p0, qa[2 * k + m][0], qa[2 * k + m][1]);
-                ka_split(p1, qa[2 * k + m][2], qa[2 * k + m][3]);
+                ka_split<TWO>(p0, qa[2 * k + m][0], qa[2 * k + m][1]);
+                // odd pairs of small codes are 2^-20 c
+                ka_split<TWO>(TWO ? p1 : mul2(p1, f2(0.0625f, 0.0625f)), qa[2 * k + m][2], qa[2 * k + m][3]);
                 const float2 s0 = un2(p0), s1 = un2(p1);
                 sum += (s0.x + s0.y) + (s1.x + s1.y);
             }
@@ -220,134 +274,188 @@ __global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4Att
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             qsum[k] = sum;
         }
+        uint32_t h01, l01, h23, l23;
+        ka_split<true>(f2(qsum[0], qsum[1]), h01, l01);
+        ka_split<true>(f2(qsum[2], qsum[3]), h23, l23);
+        qz = tq == 0 ? h01 : tq == 1 ? h23 : tq == 2 ? l01 : l23;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(qd) : "r"(qz), "r"(0xC800C800u));  // -8
+        if (TWO)
+            qd = 0u;
     }
+    const uint32_t k1024 = ka_opaque(0x64006400u), k64 = ka_opaque(0x54005400u);
+    const uint32_t odd = (h & 1) ? 0x7632u : 0x5410u;  // the halves of key h of a pair
 
-    uint64_t o[4][4];  // group g, i: head h, dims 32 g + 8 tq + i and + 4 + i
-    uint64_t zacc[4], lacc = 0ull;
+    uint64_t o[4][4];  // group k, i: dim 32 k + 4 h + i of the group's heads 2 tq and 2 tq + 1
+    uint64_t zacc = 0ull, lacc = 0ull;  // z: group h & 3 of heads 2 tq and 2 tq + 1; l: head h
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        zacc[k] = 0ull;
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             o[k][i] = 0ull;
-    }
     float r = -INFINITY, cap = KA_CAP;
+
+    // the zero accumulator operand, kept in registers: as a constant it would be written
+    // before every matrix instruction (64 moves a block)
+    const float zz[4] = {__uint_as_float(ka_opaque(0u)), __uint_as_float(ka_opaque(0u)), __uint_as_float(ka_opaque(0u)),
+                         __uint_as_float(ka_opaque(0u))};
+
+    // One cache block, `left` (1 or more) of its keys seen; all of them without TAIL.
+    auto block = [&](auto tail, unsigned char* kb, int left) {
+        constexpr bool TAIL = decltype(tail)::value;
+        if (TAIL && left < KV4_ROWS) {
+            // rows past the last key may hold anything: their value scales become zero (their
+            // scores are masked below); the warp's last block: nothing is copied over it
+            unsigned short* vs = reinterpret_cast<unsigned short*>(kb + KV4_VSCALES + 32 * h + 8 * tq);
+            if (2 * h >= left)
+                vs[0] = vs[2] = 0;
+            if (2 * h + 1 >= left)
+                vs[1] = vs[3] = 0;
+            __syncwarp();
+        }
+        // scores of keys 8 nt + 2 tq, + 1 for head h, before `unscale`
+        uint64_t s[2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const uint4 kw = lds128(kb + 64 * (8 * nt + h) + 16 * tq);
+            const uint4 sc0 = lds128(kb + KV4_KSCALES + 32 * (4 * nt + tq));
+            const uint4 sc1 = lds128(kb + KV4_KSCALES + 32 * (4 * nt + tq) + 16);
+            // z (and d) of key 8 nt + h, groups 2 (tq & 1) and the next: B's rows 0-3 are the
+            // groups' z against the sums' first parts, rows 4-7 against the second parts, rows
+            // 8-15 the same with d
+            const uint4 zs = lds128(kb + KV4_KSCALES + 32 * (4 * nt + (h >> 1)) + 16 * (tq & 1));
+            const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w}, dd[4] = {sc0.x, sc0.z, sc1.x, sc1.z};
+            float m[4];
+            ka_mma(m, qz, 0u, qd, 0u, __byte_perm(zs.y, zs.w, odd), TWO ? 0u : __byte_perm(zs.x, zs.z, odd), zz[0], zz[1],
+                   zz[2], zz[3]);
+            const float u24 = 1.f / 16777216.f;
+            uint64_t acc = TWO ? f2(m[0], m[1]) : mul2(f2(m[0], m[1]), f2(u24, u24));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                // small codes cost five instructions fewer a word, but their sum with -8 sum q
+                // cancels: a relative error of 1.4e-6 where centred ones give 2.9e-7
+                uint32_t p[4];
+                if (TWO)
+                    ka_codes(words[k], k1024, k64, p);
+                else
+                    ka_small_codes(words[k], p);
+                float t[4], t2[4];
+                ka_mma(t, qa[2 * k][0], qa[2 * k][1], qa[2 * k][2], qa[2 * k][3], p[0], p[1], zz[0], zz[1], zz[2], zz[3]);
+                ka_mma(t2, qa[2 * k + 1][0], qa[2 * k + 1][1], qa[2 * k + 1][2], qa[2 * k + 1][3], p[2], p[3], t[0], t[1],
+                       t[2], t[3]);
+                acc = fma2(ka_both<TWO>(t2), half2_f2(dd[k]), acc);
+            }
+            s[nt] = acc;
+        }
+        if (TAIL) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                float2 v = un2(s[nt]);
+                if (8 * nt + 2 * tq >= left)
+                    v.x = -INFINITY;
+                if (8 * nt + 2 * tq + 1 >= left)
+                    v.y = -INFINITY;
+                s[nt] = f2(v.x, v.y);
+            }
+        }
+        uint32_t vd[2][4];
+        __half2 dmax = __half2half2(__ushort_as_half(0));
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const uint4 sc0 = lds128(kb + KV4_VSCALES + 32 * (4 * nt + tq));
+            const uint4 sc1 = lds128(kb + KV4_VSCALES + 32 * (4 * nt + tq) + 16);
+            vd[nt][0] = sc0.x, vd[nt][1] = sc0.z, vd[nt][2] = sc1.x, vd[nt][3] = sc1.z;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                dmax = __hmax2(dmax, *reinterpret_cast<const __half2*>(&vd[nt][k]));
+        }
+        const float2 s0 = un2(s[0]), s1 = un2(s[1]);
+        const float top = fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)) * unscale;
+        // d <= 8 keeps p d below 2^15 under the cap; a larger one lowers the cap
+        const bool wide = !__hble2(dmax, __half2half2(__ushort_as_half(0x4800)));
+        if (__any_sync(0xffffffffu, top - r > cap || (wide && cap == KA_CAP))) {
+            float t = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+            if (__any_sync(0xffffffffu, wide))
+                cap = 15.f - 16.f;  // from now on for the largest scale there is
+            float f = 1.f;
+            if (t - r > cap) {
+                const float rn = t - (cap - KA_HEAD);
+                f = ka_ex2(r - rn);
+                r = rn;
+            }
+            __syncwarp();
+            lacc = mul2(lacc, f2(f, f));
+            const uint64_t ff = f2(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
+            zacc = mul2(zacc, ff);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[k][j] = mul2(o[k][j], ff);
+        }
+        const float2 e0 = un2(fma2(s[0], f2(unscale, unscale), f2(-r, -r)));
+        const float2 e1 = un2(fma2(s[1], f2(unscale, unscale), f2(-r, -r)));
+        const uint64_t p0 = f2(ka_ex2(e0.x), ka_ex2(e0.y)), p1 = f2(ka_ex2(e1.x), ka_ex2(e1.y));
+        lacc = add2(lacc, add2(p0, p1));
+        {
+            // p z: A's row n is group n & 3 (rows 4-15 are not used)
+            uint32_t h0, l0, h1, l1;
+            ka_split<TWO>(p0, h0, l0);
+            ka_split<TWO>(p1, h1, l1);
+            const unsigned char* zs = kb + KV4_VSCALES + 32 * tq + 8 * (h & 3) + 4;
+            const uint32_t z0 = lds32(zs), z1 = lds32(zs + 128);
+            float m[4], m2[4];
+            ka_mma(m, z0, z0, z1, z1, h0, h1, zz[0], zz[1], zz[2], zz[3]);
+            if (TWO)
+                ka_mma(m2, z0, z0, z1, z1, l0, l1, m[0], m[1], m[2], m[3]);
+            zacc = add2(zacc, TWO ? f2(m2[0], m2[1]) : f2(m[0], m[1]));
+        }
+        const uint4 va = lds128(kb + KV4_VCODES + 16 * lane), vb = lds128(kb + KV4_VCODES + 512 + 16 * lane);
+        const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h0, l0, h1, l1;
+            ka_split<TWO>(mul2(p0, half2_f2(vd[0][k])), h0, l0);
+            ka_split<TWO>(mul2(p1, half2_f2(vd[1][k])), h1, l1);
+            uint32_t b0[4], b1[4];
+            ka_codes(wa[k], k1024, k64, b0);
+            ka_codes(wb[k], k1024, k64, b1);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // 16 dims (i = 2 j in A's first 8 rows, 2 j + 1 in the others) by 16 keys, times
+                // 16 keys by 8 heads.  The sums over blocks are rounded adds: the matrix
+                // instruction's own accumulation cuts off (100001 keys: relative error 1.6e-6
+                // with it, 4.1e-7 so)
+                float m[4], m2[4];
+                ka_mma(m, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], h0, h1, zz[0], zz[1], zz[2], zz[3]);
+                if (TWO)
+                    ka_mma(m2, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], l0, l1, m[0], m[1], m[2], m[3]);
+                o[k][2 * j] = add2(o[k][2 * j], TWO ? f2(m2[0], m2[1]) : f2(m[0], m[1]));
+                o[k][2 * j + 1] = add2(o[k][2 * j + 1], TWO ? f2(m2[2], m2[3]) : f2(m[2], m[3]));
+            }
+        }
+    };
+
     bool ok = true;
     for (int i = 0; i < cnt; ++i) {
         const int st = i % KA_NS;
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][st], (i / KA_NS) & 1))) {
+        if ((KA_STEP * i & 31) == 0)
+            bad = bad_next;  // the copies are ahead, but by less than 32 blocks
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&full[warp][st], (i / KA_NS) & 1)) &&
+            !__all_sync(0xffffffffu, mbar_wait(&full[warp][st], (i / KA_NS) & 1))) {
             ok = false;
             break;
         }
-        if (!skip[warp][st]) {
-            unsigned char* kb = ring[warp][st];
-            const int left = n - KV4_ROWS * block_at(i);
-            if (left < KV4_ROWS) {
-                // rows past the last key may hold anything: their value scales become zero
-                // (their scores are masked below); the last block: nothing is copied over it
-                const int u = lane >> 2;
-                unsigned short* vs = reinterpret_cast<unsigned short*>(kb + KV4_VSCALES + 32 * u + 8 * (lane & 3));
-                if (2 * u >= left)
-                    vs[0] = vs[2] = 0;
-                if (2 * u + 1 >= left)
-                    vs[1] = vs[3] = 0;
-                __syncwarp();
-            }
-            // scores of keys 8 nt + 2 tq, + 1 for head h
-            uint64_t s[2];
+        const int blk = block_at(KA_STEP * i), left = n - KV4_ROWS * blk;
+        if (!bad && left >= KV4_ROWS * KA_STEP && blk + KA_STEP <= blk1) {
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const uint4 kw = lds128(kb + 64 * (8 * nt + h) + 16 * tq);
-                const uint4 sc0 = lds128(kb + KV4_KSCALES + 32 * (4 * nt + tq));
-                const uint4 sc1 = lds128(kb + KV4_KSCALES + 32 * (4 * nt + tq) + 16);
-                const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
-                const uint32_t dd[4] = {sc0.x, sc0.z, sc1.x, sc1.z}, zz[4] = {sc0.y, sc0.w, sc1.y, sc1.w};
-                uint64_t acc = 0ull;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t p[4];
-                    ka_codes(words[k], p);
-                    float m[4] = {0.f, 0.f, 0.f, 0.f};
-                    ka_mma(m, qa[2 * k][0], qa[2 * k][1], qa[2 * k][2], qa[2 * k][3], p[0], p[1]);
-                    ka_mma(m, qa[2 * k + 1][0], qa[2 * k + 1][1], qa[2 * k + 1][2], qa[2 * k + 1][3], p[2], p[3]);
-                    acc = fma2(add2(f2(m[0], m[1]), f2(m[2], m[3])), half2_f2(dd[k]), acc);
-                    acc = fma2(half2_f2(zz[k]), f2(qsum[k], qsum[k]), acc);
-                }
-                s[nt] = mul2(acc, f2(unscale, unscale));
-            }
-            if (left < KV4_ROWS) {
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    float2 v = un2(s[nt]);
-                    if (8 * nt + 2 * tq >= left)
-                        v.x = -INFINITY;
-                    if (8 * nt + 2 * tq + 1 >= left)
-                        v.y = -INFINITY;
-                    s[nt] = f2(v.x, v.y);
-                }
-            }
-            uint32_t vd[2][4], vz[2][4];
-            __half2 dmax = __half2half2(__ushort_as_half(0));
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                const uint4 sc0 = lds128(kb + KV4_VSCALES + 32 * (4 * nt + tq));
-                const uint4 sc1 = lds128(kb + KV4_VSCALES + 32 * (4 * nt + tq) + 16);
-                vd[nt][0] = sc0.x, vz[nt][0] = sc0.y, vd[nt][1] = sc0.z, vz[nt][1] = sc0.w;
-                vd[nt][2] = sc1.x, vz[nt][2] = sc1.y, vd[nt][3] = sc1.z, vz[nt][3] = sc1.w;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    dmax = __hmax2(dmax, *reinterpret_cast<const __half2*>(&vd[nt][k]));
-            }
-            const float2 s0 = un2(s[0]), s1 = un2(s[1]);
-            const float top = fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y));
-            // d <= 8 keeps p d below 2^15 under the cap; a larger one lowers the cap
-            const bool wide = !__hble2(dmax, __half2half2(__ushort_as_half(0x4800)));
-            if (__any_sync(0xffffffffu, top - r > cap || (wide && cap == KA_CAP))) {
-                float d = fmaxf(__low2float(dmax), __high2float(dmax));
-                float t = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                d = warp_max(d);
-                if (d > 8.f)  // from now on for the largest scale there is
-                    cap = 15.f - 16.f;
-                if (t - r > cap) {
-                    const float rn = t - (cap - KA_HEAD);
-                    const float f = ka_ex2(r - rn);
-                    r = rn;
-                    lacc = mul2(lacc, f2(f, f));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        zacc[k] = mul2(zacc[k], f2(f, f));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[k][j] = mul2(o[k][j], f2(f, f));
-                    }
-                }
-                __syncwarp();
-            }
-            const float rr = r == -INFINITY ? 0.f : r;
-            const uint64_t p0 = f2(ka_ex2(s0.x - rr), ka_ex2(s0.y - rr)), p1 = f2(ka_ex2(s1.x - rr), ka_ex2(s1.y - rr));
-            lacc = add2(lacc, add2(p0, p1));
-            const uint4 va = lds128(kb + KV4_VCODES + 16 * lane), vb = lds128(kb + KV4_VCODES + 512 + 16 * lane);
-            const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t h0, l0, h1, l1;
-                ka_split(mul2(p0, half2_f2(vd[0][k])), h0, l0);
-                ka_split(mul2(p1, half2_f2(vd[1][k])), h1, l1);
-                zacc[k] = fma2(p0, half2_f2(vz[0][k]), zacc[k]);
-                zacc[k] = fma2(p1, half2_f2(vz[1][k]), zacc[k]);
-                uint32_t b0[4], b1[4];
-                ka_codes(wa[k], b0);
-                ka_codes(wb[k], b1);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // the sums over blocks are rounded adds: the matrix instruction's own
-                    // accumulation cuts off (100001 keys: relative error 1.6e-6 with it)
-                    float m[4] = {0.f, 0.f, 0.f, 0.f};
-                    ka_mma(m, h0, l0, h1, l1, b0[j], b1[j]);
-                    o[k][j] = add2(o[k][j], add2(f2(m[0], m[1]), f2(m[2], m[3])));
-                }
-            }
+            for (int k = 0; k < KA_STEP; ++k)
+                block(std::false_type{}, ring[warp][st][k], KV4_ROWS);
+        } else {
+#pragma unroll 1
+            for (int k = 0; k < KA_STEP; ++k)
+                if (blk + k < blk1 && !(bad >> (KA_STEP * i + k & 31) & 1))
+                    block(std::true_type{}, ring[warp][st][k], left - KV4_ROWS * k);
         }
         __syncwarp();  // every lane has read the stage
         if (i + KA_NS < cnt)
@@ -367,26 +475,22 @@ __global__ void __launch_bounds__(32 * KA_WARPS, 3) kv4_attn_kernel(const Kv4Att
     float* meet = reinterpret_cast<float*>(ring);
     static_assert(sizeof(ring) >= KA_WARPS * 8 * KA_PART * 4, "the ring holds the warps' results");
     {
-        const float2 l2 = un2(lacc);
+        const float2 l2 = un2(lacc), z2 = un2(zacc);
         float l = l2.x + l2.y;
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        float* mp = meet + (warp * 8 + h) * KA_PART;
+        float* mp = meet + warp * 8 * KA_PART;
         if (tq == 0) {
-            mp[0] = r;
-            mp[1] = l;
+            mp[h * KA_PART] = r;
+            mp[h * KA_PART + 1] = l;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float2 z2 = un2(zacc[k]);
-            float z = z2.x + z2.y;
-            z += __shfl_xor_sync(0xffffffffu, z, 1);
-            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            const float za = __shfl_sync(0xffffffffu, z2.x, 4 * k + tq), zb = __shfl_sync(0xffffffffu, z2.y, 4 * k + tq);
             const float2 y0 = un2(o[k][0]), y1 = un2(o[k][1]), y2 = un2(o[k][2]), y3 = un2(o[k][3]);
-            const float4 lo = make_float4(y0.x + z, y1.x + z, y2.x + z, y3.x + z);
-            const float4 hi = make_float4(y0.y + z, y1.y + z, y2.y + z, y3.y + z);
-            *reinterpret_cast<float4*>(mp + 4 + 32 * k + 8 * tq) = lo;
-            *reinterpret_cast<float4*>(mp + 4 + 32 * k + 8 * tq + 4) = hi;
+            float* at = mp + 2 * tq * KA_PART + 4 + 32 * k + 4 * h;
+            *reinterpret_cast<float4*>(at) = make_float4(y0.x + za, y1.x + za, y2.x + za, y3.x + za);
+            *reinterpret_cast<float4*>(at + KA_PART) = make_float4(y0.y + zb, y1.y + zb, y2.y + zb, y3.y + zb);
         }
     }
     __syncthreads();
@@ -472,11 +576,11 @@ struct Kv4Split {
 static Kv4Split kv4_split(int n_seq, int n_kv, int max_keys)
 {
     const long long blocks = (static_cast<long long>(max_keys) + dq::KV4_ROWS - 1) / dq::KV4_ROWS;
-    const long long all = blocks * n_seq * n_kv, room = 3ll * sm_count();
+    const long long all = blocks * n_seq * n_kv, room = static_cast<long long>(dq::KA_RESIDENT) * sm_count();
     long long chunk = (all + room - 1) / room;
     if (n_seq > 1)
         chunk = std::min(chunk, 64ll);
-    chunk = std::max<long long>(chunk, dq::KA_WARPS);
+    chunk = std::max<long long>(chunk, dq::KA_WARPS * dq::KA_STEP);
     return {static_cast<int>(chunk), static_cast<int>((blocks + chunk - 1) / chunk)};
 }
 

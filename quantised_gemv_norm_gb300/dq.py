@@ -347,6 +347,12 @@ _TYPES = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE
 KV4_BLOCK_ROWS, KV4_BLOCK_BYTES = 16, 2560
 
 
+# These calls are short beside a Python statement's cost, so the checks below are few and
+# flat, and the current stream's handle is asked for without a Stream object around it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _type(dtype) -> int:
     t = _TYPES.get(dtype)
     if t is None:
@@ -354,63 +360,87 @@ def _type(dtype) -> int:
     return t
 
 
-def _on_device(*tensors):
-    """The tensors' addresses; all on the current CUDA device, which the library launches on."""
+def _device(*tensors) -> int:
+    """The current CUDA device, which the library launches on; every tensor has to be there."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if not t.is_cuda or t.device.index != dev:
+        if t.get_device() != dev:
             raise ValueError("tensors must be on the current CUDA device")
-    return [t.data_ptr() for t in tensors]
+    return dev
 
 
 def _int32(name, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 tensor of shape %s" % (name, tuple(shape)))
 
 
-def _rows(name, t, dtype=None):
+def _rows(name, t, dtype):
     """Row and head stride (elements) of a [rows, heads, 128] tensor with contiguous heads of 128."""
-    if t.dim() != 3 or t.shape[2] != 128 or (t.stride(2) != 1) or (dtype is not None and t.dtype != dtype):
-        raise ValueError("%s must be [rows, heads, 128]%s with contiguous 128" % (name, " %s" % dtype if dtype else ""))
-    heads = t.shape[1]
-    head = t.stride(1) if heads > 1 else 128
-    return (t.stride(0) if t.shape[0] > 1 else max(head * heads, 128)), head
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or t.dtype is not dtype:
+        raise ValueError("%s must be a %s tensor [rows, heads, 128]" % (name, dtype))
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError("%s must have contiguous heads of 128" % name)
+    if shape[1] == 1:
+        head = 128
+    return (row if shape[0] > 1 else max(head * shape[1], 128)), head
 
 
-def _out(name, t, like_shape, dtype, device):
-    if t is None:
-        return torch.empty(like_shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(like_shape) or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(like_shape)))
+def _checked_out(name, t, shape, dtype):
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
     return t
+
+
+def _scratch(workspace, nbytes, device):
+    """Address and size of a workspace, made here where none is given; the tensor keeps it alive until the call is in."""
+    if workspace is None:
+        if not nbytes:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("a workspace must be contiguous and on the tensors' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def qkv_rope(qkv: torch.Tensor, positions: torch.Tensor, rope: torch.Tensor, n_q: int, n_kv: int, q_norm=None,
              k_norm=None, eps: float = 1e-6, dtype=torch.float16, out=None):
     """qkv: fp32 [rows, >= (n_q + 2 n_kv) 128] (a row stride is fine), positions int32 [rows] (negative: a padding
     row, left as it was), rope from rope_table -> (q [rows, n_q, 128], k, v [rows, n_kv, 128]) of ``dtype``."""
-    lib = load()
-    if qkv.dim() != 2 or qkv.dtype != torch.float32 or (qkv.stride(1) != 1 and qkv.shape[1] > 1):
-        raise ValueError("qkv must be a 2-D fp32 tensor with contiguous rows")
+    lib = _lib or load()
+    if qkv.dim() != 2 or qkv.dtype is not torch.float32:
+        raise ValueError("qkv must be a 2-D fp32 tensor")
     rows, width = qkv.shape
-    if width < (n_q + 2 * n_kv) * 128:
-        raise ValueError("qkv has %d columns, %d heads of 128 are wanted" % (width, n_q + 2 * n_kv))
-    if rope.dtype != torch.float32 or tuple(rope.shape[1:]) != (64, 2) or not rope.is_contiguous():
+    stride, one = qkv.stride()
+    if width < (n_q + 2 * n_kv) * 128 or one != 1:
+        raise ValueError("qkv must have contiguous rows of %d heads of 128" % (n_q + 2 * n_kv))
+    if rope.dtype is not torch.float32 or rope.shape[1:] != (64, 2) or not rope.is_contiguous():
         raise ValueError("rope must be a contiguous fp32 [max_ctx, 64, 2] table")
     _int32("positions", positions, (rows,))
-    for w in (q_norm, k_norm):
-        if w is not None and (w.dtype != torch.float32 or w.numel() != 128 or not w.is_contiguous()):
-            raise ValueError("a head norm's weight must be fp32 [128]")
+    wq = wk = None
+    if q_norm is not None or k_norm is not None:
+        for w in (q_norm, k_norm):
+            if w is None or w.dtype is not torch.float32 or w.numel() != 128 or not w.is_contiguous():
+                raise ValueError("both head norms' weights must be fp32 [128], or both None")
+        wq, wk = q_norm.data_ptr(), k_norm.data_ptr()
     t = _type(dtype)
-    q, k, v = out if out is not None else (None, None, None)
-    dev = qkv.device
-    q = _out("q", q, (rows, n_q, 128), dtype, dev)
-    k, v = _out("k", k, (rows, n_kv, 128), dtype, dev), _out("v", v, (rows, n_kv, 128), dtype, dev)
-    px, pp, pr, pq, pk, pv = _on_device(qkv, positions, rope, q, k, v)
-    wq, wk = (None if w is None else _on_device(w)[0] for w in (q_norm, k_norm))
-    stride = qkv.stride(0) if rows > 1 else -(-width // 4) * 4
-    _check("dq_qkv_rope", lib.dq_qkv_rope(px, stride, pp, wq, wk, pr, eps, rows, n_q, n_kv, 128, rope.shape[0], t,
-                                          pq, pk, pv, _stream()))
+    q_shape, kv_shape = (rows, n_q, 128), (rows, n_kv, 128)
+    if out is None:
+        dev = qkv.device
+        q = torch.empty(q_shape, dtype=dtype, device=dev)
+        k = torch.empty(kv_shape, dtype=dtype, device=dev)
+        v = torch.empty(kv_shape, dtype=dtype, device=dev)
+    else:
+        q, k, v = out
+        for name, x, shape in (("q", q, q_shape), ("k", k, kv_shape), ("v", v, kv_shape)):
+            _checked_out(name, x, shape, dtype)
+    dev = _device(qkv, positions, rope, q, k, v) if wq is None else _device(qkv, positions, rope, q, k, v, q_norm, k_norm)
+    st = lib.dq_qkv_rope(qkv.data_ptr(), stride if rows > 1 else -(-width // 4) * 4, positions.data_ptr(), wq, wk,
+                         rope.data_ptr(), eps, rows, n_q, n_kv, 128, rope.shape[0], t, q.data_ptr(), k.data_ptr(),
+                         v.data_ptr(), _raw_stream(dev))
+    if st:
+        raise DQError("dq_qkv_rope", st)
     return q, k, v
 
 
@@ -435,10 +465,11 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     row and head strides (slices of one projection, a cache plane transposed); cu_q, cu_k int32 [n_seq + 1].
     Query i of a sequence sees keys j <= i + Lk - Lq.  Rows of no sequence are left as they were (uninitialised
     where ``out`` is not given)."""
-    lib = load()
-    q_row, q_head = _rows("q", q)
-    k_row, k_head = _rows("k", k, q.dtype)
-    v_row, v_head = _rows("v", v, q.dtype)
+    lib = _lib or load()
+    dtype = q.dtype
+    q_row, q_head = _rows("q", q, dtype)
+    k_row, k_head = _rows("k", k, dtype)
+    v_row, v_head = _rows("v", v, dtype)
     total_q, n_q, _ = q.shape
     total_k, n_kv, _ = k.shape
     if v.shape != k.shape:
@@ -447,21 +478,23 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     _int32("cu_q", cu_q, (n_seq + 1,))
     if cu_k is not None:
         _int32("cu_k", cu_k, (n_seq + 1,))
+    t = _type(dtype)
     if out is None:
-        out = torch.empty((total_q, n_q, 128), dtype=q.dtype, device=q.device)
+        out = torch.empty((total_q, n_q, 128), dtype=dtype, device=q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    o_row, o_head = _rows("out", out, q.dtype)
-    if workspace is None:
-        n = lib.dq_attention_prompt_workspace_bytes(n_seq, total_q, total_k, n_q, n_kv)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    pq, pk, pv, po, pc = _on_device(q, k, v, out, cu_q)
-    pck = None if cu_k is None else _on_device(cu_k)[0]
-    pw, nw = (None, 0) if workspace is None else (_on_device(workspace)[0], workspace.numel() * workspace.element_size())
-    d = _Prompt(pq, pk, pv, po, q_row, q_head, k_row, k_head, v_row, v_head, o_row, o_head, pc, pck, _type(q.dtype),
-                n_seq, total_q, total_k, n_q, n_kv, 128, pw, nw)
-    _check("dq_attention_prompt", lib.dq_attention_prompt(ctypes.byref(d), _stream()))
+    o_row, o_head = _rows("out", out, dtype)
+    dev = _device(q, k, v, cu_q, out)
+    if cu_k is not None:
+        _device(cu_k)
+    need = lib.dq_attention_prompt_workspace_bytes(n_seq, total_q, total_k, n_q, n_kv) if workspace is None else 0
+    pw, nw, workspace = _scratch(workspace, need, q.device)
+    d = _Prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), q_row, q_head, k_row, k_head, v_row, v_head,
+                o_row, o_head, cu_q.data_ptr(), None if cu_k is None else cu_k.data_ptr(), t, n_seq, total_q, total_k,
+                n_q, n_kv, 128, pw, nw)
+    st = lib.dq_attention_prompt(ctypes.addressof(d), _raw_stream(dev))
+    if st:
+        raise DQError("dq_attention_prompt", st)
     return out
 
 
@@ -474,39 +507,49 @@ def kv4_pool(n_pages: int, n_kv: int, page_size: int, device=None) -> torch.Tens
 
 
 def _pool(pool):
-    if pool.dim() != 4 or pool.dtype != torch.uint8 or pool.shape[3] != KV4_BLOCK_BYTES or not pool.is_contiguous():
+    shape = pool.shape
+    if len(shape) != 4 or pool.dtype is not torch.uint8 or shape[3] != KV4_BLOCK_BYTES or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous uint8 [n_pages, n_kv, page_size / 16, %d] tensor" % KV4_BLOCK_BYTES)
-    return pool.shape[0], pool.shape[1], pool.shape[2] * KV4_BLOCK_ROWS
+    return shape[0], shape[1], shape[2] * KV4_BLOCK_ROWS
 
 
 def kv4_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pool: torch.Tensor):
     """Store k and v [rows, n_kv, 128] (fp32, fp16 or bf16, any row and head strides) at slots (int32 [rows]: page *
     page_size + offset, negative to skip a row; all different) of the pool."""
-    lib = load()
+    lib = _lib or load()
     n_pages, n_kv, page = _pool(pool)
-    k_row, k_head = _rows("k", k)
+    k_row, k_head = _rows("k", k, k.dtype)
     v_row, v_head = _rows("v", v, k.dtype)
     rows = k.shape[0]
     if v.shape != k.shape or k.shape[1] != n_kv:
         raise ValueError("k and v must both be [rows, %d, 128]" % n_kv)
     _int32("slots", slots, (rows,))
     t = _type(k.dtype)
-    pk, pv, ps, pp = _on_device(k, v, slots, pool)
-    _check("dq_kv4_append", lib.dq_kv4_append(pk, pv, t, k_row, k_head, v_row, v_head, ps, pp, rows, n_kv,
-                                              128, n_pages, page, _stream()))
+    dev = _device(k, v, slots, pool)
+    st = lib.dq_kv4_append(k.data_ptr(), v.data_ptr(), t, k_row, k_head, v_row, v_head, slots.data_ptr(),
+                           pool.data_ptr(), rows, n_kv, 128, n_pages, page, _raw_stream(dev))
+    if st:
+        raise DQError("dq_kv4_append", st)
 
 
 def kv4_read(pool: torch.Tensor, slots: torch.Tensor, dtype=torch.float16, out=None):
     """The rows at ``slots`` (int32 [rows]) as values: (k, v), each [rows, n_kv, 128] of ``dtype``."""
-    lib = load()
+    lib = _lib or load()
     n_pages, n_kv, page = _pool(pool)
     rows = slots.numel()
     _int32("slots", slots, (rows,))
     t = _type(dtype)
-    k, v = out if out is not None else (None, None)
-    k, v = (_out("out", x, (rows, n_kv, 128), dtype, pool.device) for x in (k, v))
-    pp, ps, pk, pv = _on_device(pool, slots, k, v)
-    _check("dq_kv4_read", lib.dq_kv4_read(pp, ps, t, pk, pv, rows, n_kv, 128, n_pages, page, _stream()))
+    shape = (rows, n_kv, 128)
+    if out is None:
+        k = torch.empty(shape, dtype=dtype, device=pool.device)
+        v = torch.empty(shape, dtype=dtype, device=pool.device)
+    else:
+        k, v = (_checked_out("out", x, shape, dtype) for x in out)
+    dev = _device(pool, slots, k, v)
+    st = lib.dq_kv4_read(pool.data_ptr(), slots.data_ptr(), t, k.data_ptr(), v.data_ptr(), rows, n_kv, 128, n_pages, page,
+                         _raw_stream(dev))
+    if st:
+        raise DQError("dq_kv4_read", st)
     return k, v
 
 
@@ -521,28 +564,29 @@ def attention_decode_kv4(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tenso
     """One token a sequence over the 4-bit cache: q [n_seq, n_q, 128] (fp32, fp16 or bf16), pages int32 [n_seq,
     max_pages], n_keys int32 [n_seq] -> [n_seq, n_q, 128] of q's type.  ``max_keys``: a bound on n_keys known to the
     host (the work is split by it); all the table's pages where it is not given."""
-    lib = load()
+    lib = _lib or load()
     n_pages, n_kv, page = _pool(pool)
-    if q.dim() != 3 or q.shape[2] != 128 or not q.is_contiguous():
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != 128 or not q.is_contiguous():
         raise ValueError("q must be a contiguous [n_seq, n_q, 128] tensor")
-    n_seq, n_q, _ = q.shape
+    n_seq, n_q, _ = shape
     if pages.dim() != 2:
         raise ValueError("pages must be [n_seq, max_pages]")
     max_pages = pages.shape[1]
     _int32("pages", pages, (n_seq, max_pages))
     _int32("n_keys", n_keys, (n_seq,))
+    t = _type(dtype)
     if max_keys is None:
         max_keys = max_pages * page
-    out = _out("out", out, q.shape, q.dtype, q.device)
-    if workspace is None:
-        n = lib.dq_attention_decode_kv4_workspace_bytes(n_seq, n_q, n_kv, max_keys)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    pq, pp, pt, pn, po = _on_device(q, pool, pages, n_keys, out)
-    pw, nw = (None, 0) if workspace is None else (_on_device(workspace)[0], workspace.numel() * workspace.element_size())
-    _check("dq_attention_decode_kv4",
-           lib.dq_attention_decode_kv4(pq, _type(q.dtype), pp, pt, pn, po, n_seq, n_q, n_kv, 128, n_pages, page,
-                                       max_pages, max_keys, pw, nw, _stream()))
+    out = torch.empty(shape, dtype=dtype, device=q.device) if out is None else _checked_out("out", out, shape, dtype)
+    dev = _device(q, pool, pages, n_keys, out)
+    need = lib.dq_attention_decode_kv4_workspace_bytes(n_seq, n_q, n_kv, max_keys) if workspace is None else 0
+    pw, nw, workspace = _scratch(workspace, need, q.device)
+    st = lib.dq_attention_decode_kv4(q.data_ptr(), t, pool.data_ptr(), pages.data_ptr(), n_keys.data_ptr(),
+                                     out.data_ptr(), n_seq, n_q, n_kv, 128, n_pages, page, max_pages, max_keys, pw, nw,
+                                     _raw_stream(dev))
+    if st:
+        raise DQError("dq_attention_decode_kv4", st)
     return out
 
 

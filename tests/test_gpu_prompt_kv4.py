@@ -6,7 +6,10 @@ Bounds (per element, u = half a step of the output type: 2^-25 in fp32 terms of 
   prompt     probabilities are rounded to the type (u), scores are off by at most about 128 roundings of
              sum |q k| / sqrt(128) (4e-5 of a probability at these inputs):  (u + 4e-5) A + u |r|, A = sum p |v|
   read       one rounding of the exact d (c - 8) + z: u |r|
-  decode     two-part operands (2^-22 of sum |q k|) and fp32 sums: 2e-5 A + u |r|
+  decode     fp32: two-part operands (2^-22 of sum |q k|) and fp32 sums: 2e-5 A + u |r|.  16-bit: the probabilities are
+             one fp16 number each in the products p d (c - 8) and p z, half a step 2^-11 either: 2^-11 B more, with
+             B = sum p (|v - z| + |z|); scores from uncentred codes, fp32 sums of up to 15 d sum |q| / sqrt(128) per group
+             (d about 0.3: 41 at these inputs), four roundings of 2^-23 each: 2e-5, twice that of a probability: 6e-5 A
 fp16 results below the normal range are off by half of 2^-24 instead of u |r|: 2^-25 is added for them.
 """
 import math
@@ -429,13 +432,13 @@ def build_cache(dq, seed, lengths, n_kv, page, spare=2):
     pool = torch.full((pages, n_kv, page // 16, 2560), 0xFF, dtype=torch.uint8, device="cuda")
     order = torch.randperm(pages, device="cuda", generator=g).int()
     table = torch.full((len(lengths), max(need) + 1), -12345, dtype=torch.int32, device="cuda")
-    ks, vs, at = [], [], 0
+    ks, vs, zs, at = [], [], [], 0
     for b, n in enumerate(lengths):
         mine = order[at:at + need[b]]
         at += need[b]
         table[b, :need[b]] = mine
         if n == 0:
-            ks.append(None), vs.append(None)
+            ks.append(None), vs.append(None), zs.append(None)
             continue
         k, v = randn(g, n, n_kv, HD), randn(g, n, n_kv, HD)
         j = torch.arange(n, device="cuda")
@@ -443,7 +446,16 @@ def build_cache(dq, seed, lengths, n_kv, page, spare=2):
         dq.kv4_append(k, v, slots, pool)
         kk, vv = dq.kv4_read(pool, slots, dtype=torch.float32)  # exact: checked above
         ks.append(kk.double()), vs.append(vv.double())
-    return pool, table, ks, vs
+        z = torch.from_numpy(quantise_ref(v.cpu().numpy())[1].astype(np.float64)).cuda()
+        zs.append(z.repeat_interleave(32, -1))
+    return pool, table, ks, vs, zs
+
+
+def decode_slack(q, ks, vs, zs, lengths, size):
+    if q.dtype == torch.float32:
+        return 2e-5 * size
+    parts = [None if v is None else (v - z).abs() + z.abs() for v, z in zip(vs, zs)]
+    return 6e-5 * size + 2.0 ** -11 * decode_ref(q, ks, parts, lengths)[0]
 
 
 @pytest.mark.parametrize("n_q,n_kv,lengths,page,dtype", [
@@ -454,13 +466,13 @@ def build_cache(dq, seed, lengths, n_kv, page, spare=2):
     (12, 2, [2047, 2048, 2049, 511, 512], 64, torch.bfloat16), (64, 64, [200], 64, torch.float32),
 ])
 def test_decode(dq, n_q, n_kv, lengths, page, dtype):
-    pool, table, ks, vs = build_cache(dq, sum(lengths), lengths, n_kv, page)
+    pool, table, ks, vs, zs = build_cache(dq, sum(lengths), lengths, n_kv, page)
     q = randn(gen(31), len(lengths), n_q, HD, dtype=dtype)
     r, size = decode_ref(q, ks, vs, lengths)
     for most in (max(1, max(lengths)), table.shape[1] * page):  # the split goes by the bound, the result does not
         y = dq.attention_decode_kv4(q, pool, table, i32(lengths), most)
         assert dq.device_error() == 0
-        within(y, r, 2e-5 * size)
+        within(y, r, decode_slack(q, ks, vs, zs, lengths, size))
     for b, n in enumerate(lengths):
         assert n > 0 or bool((y[b] == 0).all())
     assert torch.equal(dq.attention_decode_kv4(q, pool, table, i32(lengths)), y)  # the same call, the same bits
@@ -468,7 +480,7 @@ def test_decode(dq, n_q, n_kv, lengths, page, dtype):
 
 def test_decode_peaked_and_shared_pages(dq):
     # two sequences over the same pages (a fork), queries large enough that one key takes most of the weight
-    pool, table, ks, vs = build_cache(dq, 41, [700], 2, 64)
+    pool, table, ks, vs, zs = build_cache(dq, 41, [700], 2, 64)
     q = randn(gen(42), 2, 8, HD) * 12
     both = table.repeat(2, 1)
     y = dq.attention_decode_kv4(q, pool, both, i32([700, 350]), 700)
@@ -478,7 +490,7 @@ def test_decode_peaked_and_shared_pages(dq):
 
 
 def test_decode_masked_rows_may_hold_anything(dq):
-    pool, table, ks, vs = build_cache(dq, 43, [70, 0, 5], 2, 64)  # unused rows: NaN scales, all codes 15
+    pool, table, ks, vs, zs = build_cache(dq, 43, [70, 0, 5], 2, 64)  # unused rows: NaN scales, all codes 15
     q = randn(gen(44), 3, 4, HD)
     r, size = decode_ref(q, ks, vs, [70, 0, 5])
     within(dq.attention_decode_kv4(q, pool, table, i32([70, 0, 5]), 128), r, 2e-5 * size)
@@ -492,7 +504,7 @@ def test_decode_masked_rows_may_hold_anything(dq):
 
 
 def test_decode_reports_bad_counts_and_pages(dq):
-    pool, table, ks, vs = build_cache(dq, 45, [70, 40, 9], 2, 32)
+    pool, table, ks, vs, zs = build_cache(dq, 45, [70, 40, 9], 2, 32)
     q = randn(gen(46), 3, 4, HD)
     r, size = decode_ref(q, ks, vs, [70, 40, 9])
     for bad in (-1, 97, 2147483647):
@@ -511,7 +523,7 @@ def test_decode_reports_bad_counts_and_pages(dq):
 
 
 def test_decode_in_place(dq):
-    pool, table, ks, vs = build_cache(dq, 47, [300], 2, 32)
+    pool, table, ks, vs, zs = build_cache(dq, 47, [300], 2, 32)
     q = randn(gen(48), 1, 8, HD)
     want = dq.attention_decode_kv4(q, pool, table, i32([300]), 300)
     dq.attention_decode_kv4(q, pool, table, i32([300]), 300, out=q)
@@ -567,7 +579,7 @@ def test_prompt_then_tokens(dq):
 def test_captured_into_a_graph_and_replayed_on_another_stream(dq):
     g = gen(61)
     n_q, n_kv, page = 8, 2, 32
-    pool, table, _, _ = build_cache(dq, 62, [300, 45], n_kv, page, spare=4)
+    pool, table, _, _, _ = build_cache(dq, 62, [300, 45], n_kv, page, spare=4)
     n_keys = i32([300, 45])
     x = randn(g, 2, (n_q + 2 * n_kv) * HD)
     rope = dq.rope_table(512)
