@@ -22,6 +22,7 @@
 // have their infinities and NaNs in V replaced by zero before the product, since a
 // probability of 0 would not stop them; where such a key is seen by some row, the
 // epilogue adds the values themselves to the rows that see them.
+#include <algorithm>
 #include <mutex>
 
 #include "dq_tc.cuh"
@@ -53,6 +54,11 @@ struct PromptArgs {
     const int* cu_q;
     const int* cu_k;
     int n_seq, total_q, total_k, n_kv, group, tq_tokens;  // tokens a query tile
+    // the keys of a block tile shared by `splits` blocks: their unscaled outputs, by block
+    // tile, KV head, split and query tile [32][128 rows][4], and maxima and sums [2][128]
+    float* part;
+    float* part_ml;
+    int splits;
     int* err;
 };
 
@@ -119,6 +125,36 @@ __device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, 
     return t;
 }
 
+// Key tiles of each of a block's two query tiles, its tokens, and the keys that all of
+// the block's rows see.
+struct PromptSpan {
+    int ntok[2], end[2], open;
+};
+
+__device__ __forceinline__ PromptSpan prompt_span(const PromptTile& tile, int tokens)
+{
+    PromptSpan p;
+    p.open = 0x7fffffff;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int ts = tile.t0 + t * tokens;
+        p.ntok[t] = max(0, min(tokens, tile.lq - ts));
+        const int hi = min(tile.lk, max(0, ts + p.ntok[t] + tile.lk - tile.lq));
+        p.end[t] = p.ntok[t] ? (hi + PR_KEYS - 1) / PR_KEYS : 0;
+        if (p.ntok[t])
+            p.open = min(p.open, min(tile.lk, max(0, ts + 1 + tile.lk - tile.lq)));
+    }
+    return p;
+}
+
+// Key tiles [j0, j1) of split c.
+__device__ __forceinline__ void prompt_split(const PromptSpan& p, int splits, int c, int& j0, int& j1)
+{
+    const int all = max(p.end[0], p.end[1]), per = (all + splits - 1) / splits;
+    j0 = min(all, c * per);
+    j1 = min(all, j0 + per);
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {
     asm volatile(
@@ -176,10 +212,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     volatile int* poison = fail + 1;  // a seen value is an infinity or NaN
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = blockIdx.x % a.n_kv;
+    const int c = blockIdx.x % a.splits, g = blockIdx.x / a.splits % a.n_kv, idx = blockIdx.x / (a.splits * a.n_kv);
     const int rows = a.tq_tokens * a.group;
+    pdl_trigger();
     if (warp == 0) {
-        const PromptTile t = prompt_find(a, blockIdx.x / a.n_kv, 2 * a.tq_tokens, lane);
+        const PromptTile t = prompt_find(a, idx, 2 * a.tq_tokens, lane);
         if (lane == 0)
             *shared_tile = t;
     } else if (warp == PR_MMA_WARP) {
@@ -213,19 +250,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     const PromptTile tile = *shared_tile;
     const uint32_t tbase = *tslot;
 
-    // tokens, key tiles and the keys that every row of the tile sees, per query tile
-    int ntok[2], end[2], open = 0x7fffffff;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int ts = tile.t0 + t * a.tq_tokens;
-        ntok[t] = max(0, min(a.tq_tokens, tile.lq - ts));
-        const int hi = min(tile.lk, max(0, ts + ntok[t] + tile.lk - tile.lq));
-        end[t] = ntok[t] ? (hi + PR_KEYS - 1) / PR_KEYS : 0;
-        if (ntok[t])
-            open = min(open, min(tile.lk, max(0, ts + 1 + tile.lk - tile.lq)));
-    }
-    const int jmax = max(end[0], end[1]);
-    const int jclean = open / PR_KEYS;  // the first key tile with a masked key for some row
+    const PromptSpan sp = prompt_span(tile, a.tq_tokens);
+    // this block's key tiles j0 + i, i < n, and i < end[t] for query tile t
+    int j0, j1;
+    prompt_split(sp, a.splits, c, j0, j1);
+    const int n = j1 - j0, end[2] = {max(0, min(sp.end[0], j1) - j0), max(0, min(sp.end[1], j1) - j0)};
+    const int jclean = sp.open / PR_KEYS - j0;  // the first of them with a masked key for some row, may be below 0
 
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
         if (mbar_try_wait(bar, parity))
@@ -244,7 +274,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     };
 
     if (tile.live && warp == PR_TMA_WARP) {
-        if (lane == 0 && jmax > 0) {
+        if (lane == 0 && n > 0) {
             for (int t = 0; t < 2; ++t) {
                 if (!end[t])
                     continue;
@@ -254,7 +284,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                                 tile.q0 + tile.t0 + t * a.tq_tokens, &q_full[t]);
             }
             int issued = 0, cleans = 0;
-            for (; issued < 2 * jmax; ++issued) {  // key tile 0, value tile 0, key tile 1, ...
+            for (; issued < 2 * n; ++issued) {  // key tile 0, value tile 0, key tile 1, ...
                 const int s = issued % PR_STAGES;
                 if (issued >= PR_STAGES && !wait(&freed[s], ((issued / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
                     break;
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 mbar_arrive_expect_tx(bar, PR_TILE);
                 for (int p = 0; p < 2; ++p)
                     tma_load_3d(ring + s * PR_TILE + p * PR_PANEL, (issued & 1) ? &a.tv : &a.tk, 64 * p,
-                                tile.k0 + j * PR_KEYS, g, bar);
+                                tile.k0 + (j0 + j) * PR_KEYS, g, bar);
                 if (clean) {
                     mbar_arrive(&full[s]);  // the slot's phase goes on
                     ++cleans;
@@ -283,7 +313,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         }
         __syncwarp();
     } else if (tile.live && warp == PR_MMA_WARP) {
-        if (lane == 0 && jmax > 0) {
+        if (lane == 0 && n > 0) {
             constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
             constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
             constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
@@ -312,11 +342,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 if (end[t] && (ok = wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
                     qk(t, 0);
             umma_commit(&freed[0]);
-            for (int j = 0; ok && j < jmax; ++j) {
+            for (int j = 0; ok && j < n; ++j) {
                 const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
                 ok = j >= jclean ? wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
                                  : wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                if (ok && j + 1 < jmax)
+                if (ok && j + 1 < n)
                     ok = wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
                 for (int t = 0; ok && t < 2; ++t) {
                     if (j >= end[t])
@@ -329,7 +359,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                         qk(t, j + 1);
                 }
                 umma_commit(&freed[sv]);
-                if (j + 1 < jmax)
+                if (j + 1 < n)
                     umma_commit(&freed[sk]);
             }
             umma_commit(drain);  // every product is done before the block ends
@@ -340,7 +370,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     } else if (tile.live && warp >= PR_CLEAN_WARP) {
         // infinities and NaNs of the value tiles with masked keys become zero
         const int ct = tid - 32 * PR_CLEAN_WARP;
-        for (int j = jclean; j < jmax; ++j) {
+        for (int j = max(0, jclean); j < n; ++j) {
             if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
                 break;
             uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
@@ -356,7 +386,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     w.z &= ~((nz >> 15) * 0xffffu);
                     w.w &= ~((nw >> 15) * 0xffffu);
                     *reinterpret_cast<uint4*>(vt + 16 * i) = w;
-                    seen |= j * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
+                    seen |= (j0 + j) * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
                 }
             }
             if (seen)
@@ -372,7 +402,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + PR_S0 + 128 * t, to = tbase + lanes + PR_O0 + 128 * t;
         const int tok = tile.t0 + t * a.tq_tokens + r / a.group;  // within the sequence
-        const bool mine = r / a.group < ntok[t];
+        const bool mine = r / a.group < sp.ntok[t];
         const int lim = min(tile.lk, max(0, tok + 1 + tile.lk - tile.lq));  // keys this row sees
         float m = -INFINITY, l = 0.f;
         bool ok = true;
@@ -386,7 +416,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 tmem_ld32(ts + 32 * c, s + 32 * c);
             tmem_ld_wait();
             if (j >= jclean) {
-                const int left = lim - j * PR_KEYS;
+                const int left = lim - (j0 + j) * PR_KEYS;
 #pragma unroll
                 for (int c = 0; c < 128; ++c)
                     if (c >= left)
@@ -442,12 +472,56 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         if (ok && end[t])
             ok = warp_wait(&o_full[t], (end[t] - 1) & 1, DEVERR_TIMEOUT_FULL);
         tc_fence_after_sync();
-        if (ok && ntok[t]) {
+        const bool bad = *poison;
+        // a seen infinity or NaN of V, which the products left out, added to a row's 32 dims
+        auto add_poison = [&](uint32_t* o, int c32) {
+            const int last = min(lim, j1 * PR_KEYS);
+            for (int j = max(j0, j0 + jclean) * PR_KEYS; j < last; ++j) {
+                const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) +
+                                                                 static_cast<long long>(tile.k0 + j) * a.v_row +
+                                                                 static_cast<long long>(g) * a.v_head + 32 * c32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w = vp[i];
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t nf = non_finite2<T>(u[e]);
+                        float& lo = reinterpret_cast<float&>(o[8 * i + 2 * e]);
+                        float& hi = reinterpret_cast<float&>(o[8 * i + 2 * e + 1]);
+                        if (nf & 0x8000u)
+                            lo += one16<T>(u[e] & 0xffffu);
+                        if (nf & 0x80000000u)
+                            hi += one16<T>(u[e] >> 16);
+                    }
+                }
+            }
+        };
+        if (ok && a.splits > 1) {
+            if (end[t]) {
+                const size_t at = ((static_cast<size_t>(idx) * a.n_kv + g) * a.splits + c) * 2 + t;
+                a.part_ml[at * 256 + r] = m;
+                a.part_ml[at * 256 + 128 + r] = l;
+                float4* po = reinterpret_cast<float4*>(a.part) + at * 32 * 128 + r;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * q, o);
+                    tmem_ld_wait();
+                    if (bad && mine)
+                        add_poison(o, q);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        po[(8 * q + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                            __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                }
+            }
+        } else if (ok && sp.ntok[t]) {
             // a row that sees no key is zero, one whose scores are all -infinity NaN (0 / 0)
             const float inv = lim > 0 ? 1.0f / l : 0.f;
             T* out = static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
                      static_cast<long long>(g * a.group + r % a.group) * a.o_head;
-            const bool bad = *poison;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
@@ -458,28 +532,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     o[i] = lim > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
-                if (bad && mine) {
-                    for (int j = jclean * PR_KEYS; j < lim; ++j) {
-                        const uint4* vp = reinterpret_cast<const uint4*>(
-                            static_cast<const T*>(a.v) + static_cast<long long>(tile.k0 + j) * a.v_row +
-                            static_cast<long long>(g) * a.v_head + 32 * c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 w = vp[i];
-                            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t n = non_finite2<T>(u[e]);
-                                float& lo = reinterpret_cast<float&>(o[8 * i + 2 * e]);
-                                float& hi = reinterpret_cast<float&>(o[8 * i + 2 * e + 1]);
-                                if (n & 0x8000u)
-                                    lo += one16<T>(u[e] & 0xffffu);
-                                if (n & 0x80000000u)
-                                    hi += one16<T>(u[e] >> 16);
-                            }
-                        }
-                    }
-                }
+                if (bad && mine)
+                    add_poison(o, c);
                 if (mine) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -502,9 +556,86 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         tmem_dealloc(tbase, PR_TCOLS);
 }
 
+// The splits of one block tile, KV head and query tile: a thread takes one row and 16
+// of its dims.
+template <typename T>
+__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a)
+{
+    __shared__ PromptTile shared_tile;
+    const int r = threadIdx.x, q = blockIdx.y & 7, t = blockIdx.y >> 3;
+    const int g = blockIdx.x % a.n_kv, idx = blockIdx.x / a.n_kv;
+    if (threadIdx.x < 32) {
+        const PromptTile x = prompt_find(a, idx, 2 * a.tq_tokens, threadIdx.x);
+        if (threadIdx.x == 0)
+            shared_tile = x;
+    }
+    __syncthreads();
+    const PromptTile tile = shared_tile;
+    pdl_wait();
+    const PromptSpan sp = prompt_span(tile, a.tq_tokens);
+    if (!tile.live || r / a.group >= sp.ntok[t])
+        return;
+    const int tok = tile.t0 + t * a.tq_tokens + r / a.group;
+    const size_t first = (static_cast<size_t>(idx) * a.n_kv + g) * a.splits;
+    auto has = [&](int c) {
+        int j0, j1;
+        prompt_split(sp, a.splits, c, j0, j1);
+        return min(sp.end[t], j1) > j0;
+    };
+    float m = -INFINITY;
+    for (int c = 0; c < a.splits && has(c); ++c)
+        m = fmaxf(m, __ldcg(a.part_ml + ((first + c) * 2 + t) * 256 + r));
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o[4] = {};
+    for (int c = 0; c < a.splits && has(c); ++c) {
+        const size_t at = (first + c) * 2 + t;
+        const float f = ex2((__ldcg(a.part_ml + at * 256 + r) - base) * PR_C);
+        l += f * __ldcg(a.part_ml + at * 256 + 128 + r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part) + at * 32 * 128 + (4 * q + i) * 128 + r);
+            o[i].x = fmaf(f, x.x, o[i].x);
+            o[i].y = fmaf(f, x.y, o[i].y);
+            o[i].z = fmaf(f, x.z, o[i].z);
+            o[i].w = fmaf(f, x.w, o[i].w);
+        }
+    }
+    const bool sees = tok + 1 + tile.lk - tile.lq > 0 && tile.lk > 0;
+    const float inv = sees ? 1.0f / l : 0.f;
+    T* out = static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
+             static_cast<long long>(g * a.group + r % a.group) * a.o_head + 16 * q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        store4(out + 4 * i, sees ? make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f));
+}
+
 }  // namespace dq
 
 namespace dqhost {
+
+// How a call is cut into blocks: block tiles (at most, over all sequences) and the
+// splits of each one's keys.
+struct PromptCut {
+    long long tiles;
+    int splits;
+};
+
+static PromptCut prompt_cut(int n_seq, int total_q, int total_k, int n_q, int n_kv)
+{
+    const long long span = 2 * (128 / (n_q / n_kv)), seqs = std::min(n_seq, total_q);
+    const long long tiles = (total_q - seqs) / span + seqs;
+    const long long keys = (static_cast<long long>(total_k) + seqs * dq::PR_KEYS - 1) / (seqs * dq::PR_KEYS);
+    // too few blocks for the card: the keys are split, into two key tiles at least
+    const long long splits = std::min(sm_count() / (tiles * n_kv), keys / 2);
+    return {tiles, static_cast<int>(std::max(1ll, splits))};
+}
+
+static size_t prompt_part_floats(const PromptCut& cut, int n_kv)
+{
+    return static_cast<size_t>(cut.tiles) * n_kv * cut.splits * 2 * 128;
+}
 
 // A 16-bit tensor [outer][middle][128] with the given strides (elements), copied in
 // boxes of 64 dims with the 128-byte swizzle.
@@ -541,11 +672,39 @@ static cudaError_t prompt_prepare()
     return e;
 }
 
+template <typename T>
+static cudaError_t prompt_launch(const dq::PromptArgs& a, unsigned grid, const PromptCut& cut, cudaStream_t s)
+{
+    cudaError_t e = prompt_prepare<T>();
+    if (e != cudaSuccess)
+        return e;
+    dq::prompt_kernel<T><<<grid, dq::PR_THREADS, dq::PR_SMEM, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess || cut.splits == 1)
+        return e;
+    // a dependent launch: it finds its tiles while the last blocks run
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.tiles * a.n_kv), 16);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dq::prompt_join_kernel<T>, a);
+}
+
 }  // namespace dqhost
 
 extern "C" {
 
-DQ_API size_t dq_attention_prompt_workspace_bytes(int n_seq, int total_q, int total_k, int n_q, int n_kv) { return 0; }
+DQ_API size_t dq_attention_prompt_workspace_bytes(int n_seq, int total_q, int total_k, int n_q, int n_kv)
+{
+    if (n_seq < 1 || total_q < 1 || total_k < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv || n_q / n_kv > 128)
+        return 0;
+    const dqhost::PromptCut cut = dqhost::prompt_cut(n_seq, total_q, total_k, n_q, n_kv);
+    return cut.splits > 1 ? dqhost::prompt_part_floats(cut, n_kv) * (dq::PR_HD + 2) * sizeof(float) : 0;
+}
 
 DQ_API int dq_attention_prompt(const dq_prompt* p, void* stream)
 {
@@ -573,9 +732,18 @@ DQ_API int dq_attention_prompt(const dq_prompt* p, void* stream)
     if (!dqhost::aligned16(p->q) || !dqhost::aligned16(p->k) || !dqhost::aligned16(p->v) || !dqhost::aligned16(p->out))
         return DQ_ERR_ALIGN;
     const int group = p->n_q / p->n_kv, tokens = 128 / group;
-    const long long blocks = (static_cast<long long>(p->total_q) / (2 * tokens) + p->n_seq) * p->n_kv;
+    const dqhost::PromptCut cut = dqhost::prompt_cut(p->n_seq, p->total_q, p->total_k, p->n_q, p->n_kv);
+    const long long blocks = cut.tiles * p->n_kv * cut.splits;
     if (blocks > 0x7fffffffll)
         return DQ_ERR_UNSUPPORTED;
+    if (cut.splits > 1) {
+        if (!p->workspace)
+            return DQ_ERR_NULL;
+        if (p->workspace_bytes < dqhost::prompt_part_floats(cut, p->n_kv) * (dq::PR_HD + 2) * sizeof(float))
+            return DQ_ERR_SHAPE;
+        if (!dqhost::aligned16(p->workspace))
+            return DQ_ERR_ALIGN;
+    }
     dqhost::EncodeTiled enc = dqhost::encode_tiled();
     if (!enc)
         return DQ_ERR_UNSUPPORTED;
@@ -598,19 +766,16 @@ DQ_API int dq_attention_prompt(const dq_prompt* p, void* stream)
     a.n_kv = p->n_kv;
     a.group = group;
     a.tq_tokens = tokens;
+    a.splits = cut.splits;
+    if (cut.splits > 1) {
+        a.part = static_cast<float*>(p->workspace);
+        a.part_ml = a.part + dqhost::prompt_part_floats(cut, p->n_kv) * dq::PR_HD;
+    }
     a.err = dqhost::device_error_flag();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned grid = static_cast<unsigned>(blocks);
-    cudaError_t e;
-    if (p->type == DQ_TYPE_F16) {
-        if ((e = dqhost::prompt_prepare<__half>()) == cudaSuccess)
-            dq::prompt_kernel<__half><<<grid, dq::PR_THREADS, dq::PR_SMEM, s>>>(a);
-    } else {
-        if ((e = dqhost::prompt_prepare<__nv_bfloat16>()) == cudaSuccess)
-            dq::prompt_kernel<__nv_bfloat16><<<grid, dq::PR_THREADS, dq::PR_SMEM, s>>>(a);
-    }
-    if (e == cudaSuccess)
-        e = cudaGetLastError();
+    cudaError_t e = p->type == DQ_TYPE_F16 ? dqhost::prompt_launch<__half>(a, grid, cut, s)
+                                           : dqhost::prompt_launch<__nv_bfloat16>(a, grid, cut, s);
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }
 

@@ -252,6 +252,27 @@ def test_prompt_masked_infinities_and_nans_take_no_part(dq):
     assert torch.equal(y[260:300, 4:], want[260:300, 4:])
 
 
+def test_prompt_split_keys_with_infinities_and_nans(dq):
+    # few queries over many keys: several blocks share the keys of one query tile
+    g = gen(14)
+    lk, n = 3000, 10
+    q, k, v = randn(g, n, 8, HD, dtype=torch.bfloat16), *(randn(g, lk, 2, HD, dtype=torch.bfloat16) for _ in range(2))
+    cu, ck = i32([0, n]), i32([0, lk])
+    clean = dq.attention_prompt(q, k, v, cu, ck)
+    r, size = prompt_ref(q, k, v, [0, n], [0, lk])
+    within(clean, r, (U[q.dtype] + 4e-5) * size)
+    v2 = v.clone()
+    v2[lk - 3, 0, 9] = float("inf")  # seen by the last three queries
+    v2[lk - 1, 1, 100] = float("nan")  # by the last one
+    v2[100, 1, 7] = float("-inf")  # by all
+    y = dq.attention_prompt(q, k, v2, cu, ck)
+    want = clean.clone()
+    want[n - 3:, :4, 9] = float("inf")
+    want[n - 1, 4:, 100] = float("nan")
+    want[:, 4:, 7] = float("-inf")
+    assert torch.equal(torch.nan_to_num(y, nan=12345.0), torch.nan_to_num(want, nan=12345.0))
+
+
 def test_prompt_leaves_other_rows_and_reports_bad_offsets(dq):
     g = gen(12)
     q, k, v = (randn(g, 60, n, HD, dtype=torch.bfloat16) for n in (4, 2, 2))
