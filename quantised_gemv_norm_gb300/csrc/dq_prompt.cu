@@ -41,6 +41,9 @@ constexpr int PR_THREADS = 384;
 // A block's rows end within 256 keys of one another: at most this many key tiles
 // are seen by some rows in part.
 constexpr int PR_CLEAN = 3;
+// registers a thread: 384 x 168 at the launch, moved to the softmax warps
+constexpr int PR_SOFTMAX_REGS = 208, PR_OTHER_REGS = 88;
+static_assert(256 * PR_SOFTMAX_REGS + 128 * PR_OTHER_REGS <= PR_THREADS * 168, "no more than the launch has");
 constexpr int PR_SMEM = (2 + PR_STAGES) * PR_TILE + 1024 /* alignment */ + 512;
 constexpr uint32_t PR_S0 = 0, PR_O0 = 256, PR_TCOLS = 512;  // tensor memory columns: S0 S1 O0 O1
 constexpr float PR_C = 0.08838834764831845f * 1.4426950408889634f;
@@ -273,130 +276,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         return __all_sync(0xffffffffu, wait(bar, parity, code)) != 0;
     };
 
-    if (tile.live && warp == PR_TMA_WARP) {
-        if (lane == 0 && n > 0) {
-            for (int t = 0; t < 2; ++t) {
-                if (!end[t])
-                    continue;
-                mbar_arrive_expect_tx(&q_full[t], static_cast<uint32_t>(2 * rows * 128));
-                for (int p = 0; p < 2; ++p)
-                    tma_load_3d(qs + t * PR_TILE + p * PR_PANEL, &a.tq, 64 * p, g * a.group,
-                                tile.q0 + tile.t0 + t * a.tq_tokens, &q_full[t]);
-            }
-            int issued = 0, cleans = 0;
-            for (; issued < 2 * n; ++issued) {  // key tile 0, value tile 0, key tile 1, ...
-                const int s = issued % PR_STAGES;
-                if (issued >= PR_STAGES && !wait(&freed[s], ((issued / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
-                    break;
-                const int j = issued >> 1;
-                const bool clean = (issued & 1) && j >= jclean;
-                uint64_t* bar = clean ? &v_full[j - jclean] : &full[s];
-                mbar_arrive_expect_tx(bar, PR_TILE);
-                for (int p = 0; p < 2; ++p)
-                    tma_load_3d(ring + s * PR_TILE + p * PR_PANEL, (issued & 1) ? &a.tv : &a.tk, 64 * p,
-                                tile.k0 + (j0 + j) * PR_KEYS, g, bar);
-                if (clean) {
-                    mbar_arrive(&full[s]);  // the slot's phase goes on
-                    ++cleans;
-                }
-            }
-            // every copy has landed before the block ends
-            for (int i = max(0, issued - PR_STAGES); i < issued; ++i)
-                if (!mbar_wait(&full[i % PR_STAGES], (i / PR_STAGES) & 1))
-                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-            for (int i = 0; i < cleans; ++i)
-                if (!mbar_wait(&v_full[i], 0))
-                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-            for (int t = 0; t < 2; ++t)
-                if (end[t] && !mbar_wait(&q_full[t], 0))
-                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-        }
-        __syncwarp();
-    } else if (tile.live && warp == PR_MMA_WARP) {
-        if (lane == 0 && n > 0) {
-            constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-            constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
-            constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
-            bool ok = true;
-            auto qk = [&](int t, int j) {  // S_t = Q_t K_j^T: eight steps of 16 dims, four a panel
-                const uint32_t kb = smem_addr(ring + (2 * j % PR_STAGES) * PR_TILE);
-                const uint64_t ad = umma_desc_sw128(smem_addr(qs + t * PR_TILE), 16, 1024);
-                const uint64_t bd = umma_desc_sw128(kb, 16, 1024);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint64_t step = ((s >> 2) * PR_PANEL + (s & 3) * 32) >> 4;
-                    umma_f16(tbase + PR_S0 + 128 * t, ad + step, bd + step, id_qk, s > 0);
-                }
-                umma_commit(&s_full[t]);
-            };
-            auto pv = [&](int t, int j) {  // O_t += P_t V_j: eight steps of 16 keys
-                const uint64_t bd = umma_desc_sw128(smem_addr(ring + ((2 * j + 1) % PR_STAGES) * PR_TILE), PR_PANEL, 1024);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    umma_f16_ta(tbase + PR_O0 + 128 * t, tbase + PR_S0 + 128 * t + 8 * s,
-                                bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, j > 0 || s > 0);
-                umma_commit(&o_full[t]);
-            };
-            ok = wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
-            for (int t = 0; ok && t < 2; ++t)
-                if (end[t] && (ok = wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
-                    qk(t, 0);
-            umma_commit(&freed[0]);
-            for (int j = 0; ok && j < n; ++j) {
-                const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
-                ok = j >= jclean ? wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
-                                 : wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                if (ok && j + 1 < n)
-                    ok = wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (j >= end[t])
-                        continue;
-                    if (!(ok = wait(&p_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
-                        break;
-                    tc_fence_after_sync();
-                    pv(t, j);
-                    if (j + 1 < end[t])
-                        qk(t, j + 1);
-                }
-                umma_commit(&freed[sv]);
-                if (j + 1 < n)
-                    umma_commit(&freed[sk]);
-            }
-            umma_commit(drain);  // every product is done before the block ends
-            if (!mbar_wait(drain, 0))
-                set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-        }
-        __syncwarp();
-    } else if (tile.live && warp >= PR_CLEAN_WARP) {
-        // infinities and NaNs of the value tiles with masked keys become zero
-        const int ct = tid - 32 * PR_CLEAN_WARP;
-        for (int j = max(0, jclean); j < n; ++j) {
-            if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
-                break;
-            uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
-            bool seen = false;
-            for (int i = ct; i < PR_TILE / 16; i += 64) {
-                uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
-                const uint32_t nx = non_finite2<T>(w.x), ny = non_finite2<T>(w.y), nz = non_finite2<T>(w.z),
-                               nw = non_finite2<T>(w.w);
-                if (nx | ny | nz | nw) {
-                    // 0x8000 -> 0xffff per half: the halves to clear
-                    w.x &= ~((nx >> 15) * 0xffffu);
-                    w.y &= ~((ny >> 15) * 0xffffu);
-                    w.z &= ~((nz >> 15) * 0xffffu);
-                    w.w &= ~((nw >> 15) * 0xffffu);
-                    *reinterpret_cast<uint4*>(vt + 16 * i) = w;
-                    seen |= (j0 + j) * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
-                }
-            }
-            if (seen)
-                *poison = 1;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&cleaned[j - jclean]);
-        }
-    } else if (tile.live) {
+    if (tile.live && warp < PR_MMA_WARP) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PR_SOFTMAX_REGS));
         // ---- softmax and epilogue: warps 4 t .. 4 t + 3, thread r of them owns row r
         const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -549,6 +430,132 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 __syncwarp();
             }
         }
+    } else if (tile.live) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PR_OTHER_REGS));
+        if (warp == PR_TMA_WARP) {
+        if (lane == 0 && n > 0) {
+            for (int t = 0; t < 2; ++t) {
+                if (!end[t])
+                    continue;
+                mbar_arrive_expect_tx(&q_full[t], static_cast<uint32_t>(2 * rows * 128));
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(qs + t * PR_TILE + p * PR_PANEL, &a.tq, 64 * p, g * a.group,
+                                tile.q0 + tile.t0 + t * a.tq_tokens, &q_full[t]);
+            }
+            int issued = 0, cleans = 0;
+            for (; issued < 2 * n; ++issued) {  // key tile 0, value tile 0, key tile 1, ...
+                const int s = issued % PR_STAGES;
+                if (issued >= PR_STAGES && !wait(&freed[s], ((issued / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
+                    break;
+                const int j = issued >> 1;
+                const bool clean = (issued & 1) && j >= jclean;
+                uint64_t* bar = clean ? &v_full[j - jclean] : &full[s];
+                mbar_arrive_expect_tx(bar, PR_TILE);
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(ring + s * PR_TILE + p * PR_PANEL, (issued & 1) ? &a.tv : &a.tk, 64 * p,
+                                tile.k0 + (j0 + j) * PR_KEYS, g, bar);
+                if (clean) {
+                    mbar_arrive(&full[s]);  // the slot's phase goes on
+                    ++cleans;
+                }
+            }
+            // every copy has landed before the block ends
+            for (int i = max(0, issued - PR_STAGES); i < issued; ++i)
+                if (!mbar_wait(&full[i % PR_STAGES], (i / PR_STAGES) & 1))
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+            for (int i = 0; i < cleans; ++i)
+                if (!mbar_wait(&v_full[i], 0))
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+            for (int t = 0; t < 2; ++t)
+                if (end[t] && !mbar_wait(&q_full[t], 0))
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp == PR_MMA_WARP) {
+        if (n > 0) {
+            constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+            constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
+            constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
+            bool ok = true;
+            auto qk = [&](int t, int j) {  // S_t = Q_t K_j^T: eight steps of 16 dims, four a panel
+                const uint32_t kb = smem_addr(ring + (2 * j % PR_STAGES) * PR_TILE);
+                const uint64_t ad = umma_desc_sw128(smem_addr(qs + t * PR_TILE), 16, 1024);
+                const uint64_t bd = umma_desc_sw128(kb, 16, 1024);
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint64_t step = ((s >> 2) * PR_PANEL + (s & 3) * 32) >> 4;
+                    umma_f16_warp(tbase + PR_S0 + 128 * t, ad + step, bd + step, id_qk, s > 0);
+                }
+                umma_commit_warp(&s_full[t]);
+            };
+            auto pv = [&](int t, int j) {  // O_t += P_t V_j: eight steps of 16 keys
+                const uint64_t bd = umma_desc_sw128(smem_addr(ring + ((2 * j + 1) % PR_STAGES) * PR_TILE), PR_PANEL, 1024);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    umma_f16_ta_warp(tbase + PR_O0 + 128 * t, tbase + PR_S0 + 128 * t + 8 * s,
+                                bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, j > 0 || s > 0);
+                umma_commit_warp(&o_full[t]);
+            };
+            ok = warp_wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
+            for (int t = 0; ok && t < 2; ++t)
+                if (end[t] && (ok = warp_wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
+                    qk(t, 0);
+            umma_commit_warp(&freed[0]);
+            for (int j = 0; ok && j < n; ++j) {
+                const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
+                ok = j >= jclean ? warp_wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
+                                 : warp_wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
+                if (ok && j + 1 < n)
+                    ok = warp_wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
+                for (int t = 0; ok && t < 2; ++t) {
+                    if (j >= end[t])
+                        continue;
+                    if (!(ok = warp_wait(&p_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
+                        break;
+                    tc_fence_after_sync();
+                    pv(t, j);
+                    if (j + 1 < end[t])
+                        qk(t, j + 1);
+                }
+                umma_commit_warp(&freed[sv]);
+                if (j + 1 < n)
+                    umma_commit_warp(&freed[sk]);
+            }
+            umma_commit_warp(drain);  // every product is done before the block ends
+            if (!mbar_wait(drain, 0) && lane == 0)
+                set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+        }
+        __syncwarp();
+    } else {
+        // infinities and NaNs of the value tiles with masked keys become zero
+        const int ct = tid - 32 * PR_CLEAN_WARP;
+        for (int j = max(0, jclean); j < n; ++j) {
+            if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
+                break;
+            uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
+            bool seen = false;
+            for (int i = ct; i < PR_TILE / 16; i += 64) {
+                uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
+                const uint32_t nx = non_finite2<T>(w.x), ny = non_finite2<T>(w.y), nz = non_finite2<T>(w.z),
+                               nw = non_finite2<T>(w.w);
+                if (nx | ny | nz | nw) {
+                    // 0x8000 -> 0xffff per half: the halves to clear
+                    w.x &= ~((nx >> 15) * 0xffffu);
+                    w.y &= ~((ny >> 15) * 0xffffu);
+                    w.z &= ~((nz >> 15) * 0xffffu);
+                    w.w &= ~((nw >> 15) * 0xffffu);
+                    *reinterpret_cast<uint4*>(vt + 16 * i) = w;
+                    seen |= (j0 + j) * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
+                }
+            }
+            if (seen)
+                *poison = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&cleaned[j - jclean]);
+        }
+    }
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -577,24 +584,26 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
         return;
     const int tok = tile.t0 + t * a.tq_tokens + r / a.group;
     const size_t first = (static_cast<size_t>(idx) * a.n_kv + g) * a.splits;
-    auto has = [&](int c) {
-        int j0, j1;
-        prompt_split(sp, a.splits, c, j0, j1);
-        return min(sp.end[t], j1) > j0;
-    };
+    // the splits that have keys for this query tile are the first ones
+    int j0, per;
+    prompt_split(sp, a.splits, 0, j0, per);
+    const int n = per > 0 ? min(a.splits, (sp.end[t] + per - 1) / per) : 0;
+    const float* ml = a.part_ml + (first * 2 + t) * 256 + r;
+    const float4* po = reinterpret_cast<const float4*>(a.part) + (first * 2 + t) * 32 * 128 + 4 * q * 128 + r;
     float m = -INFINITY;
-    for (int c = 0; c < a.splits && has(c); ++c)
-        m = fmaxf(m, __ldcg(a.part_ml + ((first + c) * 2 + t) * 256 + r));
+#pragma unroll 4
+    for (int c = 0; c < n; ++c)
+        m = fmaxf(m, __ldcg(ml + c * 512));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     float4 o[4] = {};
-    for (int c = 0; c < a.splits && has(c); ++c) {
-        const size_t at = (first + c) * 2 + t;
-        const float f = ex2((__ldcg(a.part_ml + at * 256 + r) - base) * PR_C);
-        l += f * __ldcg(a.part_ml + at * 256 + 128 + r);
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+        const float f = ex2((__ldcg(ml + c * 512) - base) * PR_C);
+        l += f * __ldcg(ml + c * 512 + 128);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part) + at * 32 * 128 + (4 * q + i) * 128 + r);
+            const float4 x = __ldcg(po + static_cast<size_t>(c) * 2 * 32 * 128 + i * 128);
             o[i].x = fmaf(f, x.x, o[i].x);
             o[i].y = fmaf(f, x.y, o[i].y);
             o[i].z = fmaf(f, x.z, o[i].z);
