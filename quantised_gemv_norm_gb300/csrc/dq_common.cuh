@@ -216,6 +216,12 @@ __device__ __forceinline__ void named_bar_sync(int id, int nthreads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Arrive without waiting (a whole warp); the others wait with named_bar_sync.
+__device__ __forceinline__ void named_bar_arrive(int id, int nthreads)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
 // A named barrier that also returns, to every participating thread, whether any
 // of them passed `pred` true.
 __device__ __forceinline__ bool named_bar_red_or(int id, int nthreads, bool pred)

@@ -45,49 +45,6 @@ struct Kv4AttnArgs {
     int* err;
 };
 
-__device__ __forceinline__ uint64_t f2(float x, float y)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 un2(uint64_t v)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t half2_f2(uint32_t h)
-{
-    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return f2(v.x, v.y);
-}
-
-__device__ __forceinline__ float ka_ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // (w & m) | o as one instruction: with both constants immediate it would be two.
 __device__ __forceinline__ uint32_t ka_and_or(uint32_t w, uint32_t m, uint32_t o)
 {
@@ -380,7 +337,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             float f = 1.f;
             if (t - r > cap) {
                 const float rn = t - (cap - KA_HEAD);
-                f = ka_ex2(r - rn);
+                f = ex2(r - rn);
                 r = rn;
             }
             __syncwarp();
@@ -395,7 +352,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
         }
         const float2 e0 = un2(fma2(s[0], f2(unscale, unscale), f2(-r, -r)));
         const float2 e1 = un2(fma2(s[1], f2(unscale, unscale), f2(-r, -r)));
-        const uint64_t p0 = f2(ka_ex2(e0.x), ka_ex2(e0.y)), p1 = f2(ka_ex2(e1.x), ka_ex2(e1.y));
+        const uint64_t p0 = f2(ex2(e0.x), ex2(e0.y)), p1 = f2(ex2(e1.x), ex2(e1.y));
         lacc = add2(lacc, add2(p0, p1));
         {
             // p z: A's row n is group n & 3 (rows 4-15 are not used)
@@ -505,7 +462,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
         for (int w = 0; w < KA_WARPS; ++w) {
             const float* mp = meet + (w * 8 + hd) * KA_PART;
             // a warp without keys has r = -infinity and sums of 0
-            const float f = mp[0] == m ? 1.f : ka_ex2(mp[0] - m);
+            const float f = mp[0] == m ? 1.f : ex2(mp[0] - m);
             const float4 y = *reinterpret_cast<const float4*>(mp + 4 + 4 * lane);
             l += f * mp[1];
             v.x += f * y.x;
@@ -551,7 +508,7 @@ __global__ void __launch_bounds__(32) kv4_join_kernel(const Kv4AttnArgs a)
         const float* pp = base + c * step;
         const float2 rl = __ldcg(reinterpret_cast<const float2*>(pp));
         const float4 y = __ldcg(reinterpret_cast<const float4*>(pp + 4) + lane);
-        const float f = rl.x == m ? 1.f : ka_ex2(rl.x - m);
+        const float f = rl.x == m ? 1.f : ex2(rl.x - m);
         l += f * rl.y;
         v.x += f * y.x;
         v.y += f * y.y;

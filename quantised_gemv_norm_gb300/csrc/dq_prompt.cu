@@ -37,7 +37,9 @@ constexpr int PR_STAGES = 5;                  // ring of key and value tiles, in
 constexpr int PR_TILE = PR_KEYS * PR_HD * 2;  // bytes of a key, value or query tile
 constexpr int PR_PANEL = PR_TILE / 2;         // 64 dims of it
 constexpr int PR_MMA_WARP = 8, PR_TMA_WARP = 9, PR_CLEAN_WARP = 10;
+constexpr int PR_CLEAN_BAR = 1;  // named barrier of the copying and the cleaning warps
 constexpr int PR_THREADS = 384;
+constexpr int PR_MAX_SPLITS = 64;
 // A block's rows end within 256 keys of one another: at most this many key tiles
 // are seen by some rows in part.
 constexpr int PR_CLEAN = 3;
@@ -88,10 +90,14 @@ __device__ __forceinline__ bool prompt_seq(const PromptArgs& a, int s, int& q0, 
 __device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, int span, int lane)
 {
     PromptTile t{0, 0, 0, 0, 0, 0};
+    int q0 = 0, lq = 0, k0 = 0, lk = 0;
+    auto load = [&](int s0) {
+        lq = lk = 0;
+        return s0 + lane >= a.n_seq || prompt_seq(a, s0 + lane, q0, lq, k0, lk);
+    };
     int total = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
-        int q0, lq = 0, k0, lk;
-        if (s0 + lane < a.n_seq && !prompt_seq(a, s0 + lane, q0, lq, k0, lk) && idx == 0)
+        if (!load(s0) && idx == 0)
             set_error(a.err, DEVERR_BAD_ARG);
         total += __reduce_add_sync(0xffffffffu, (lq + span - 1) / span);
     }
@@ -100,9 +106,8 @@ __device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, 
         return t;
     int before = 0;
     for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
-        int q0 = 0, lq = 0, k0 = 0, lk = 0;
-        if (s0 + lane < a.n_seq)
-            prompt_seq(a, s0 + lane, q0, lq, k0, lk);
+        if (a.n_seq > 32)  // else they are in the registers
+            load(s0);
         const int n = (lq + span - 1) / span;
         int incl = n;
 #pragma unroll
@@ -167,13 +172,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Bits 15 and 31 set where the low and the high 16-bit value is an infinity or NaN.
 template <typename T>
 __device__ __forceinline__ uint32_t non_finite2(uint32_t w)
@@ -216,49 +214,82 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c = blockIdx.x % a.splits, g = blockIdx.x / a.splits % a.n_kv, idx = blockIdx.x / (a.splits * a.n_kv);
-    const int rows = a.tq_tokens * a.group;
+    PromptTile tile{0, 0, 0, 0, 0, 0};
+    PromptSpan sp;
+    // this block's key tiles j0 + j, j < n, and j < end0 or end1 for query tile 0 or 1
+    int j0 = 0, j1 = 0, n = 0, end0 = 0, end1 = 0;
+    int jclean = 0;  // the first of them with a masked key for some row, may be below 0
+    auto set_span = [&] {
+        sp = prompt_span(tile, a.tq_tokens);
+        prompt_split(sp, a.splits, c, j0, j1);
+        n = j1 - j0;
+        end0 = max(0, min(sp.end[0], j1) - j0);
+        end1 = max(0, min(sp.end[1], j1) - j0);
+        jclean = sp.open / PR_KEYS - j0;
+    };
+    // one copy of the ring: key tile 0, value tile 0, key tile 1, ...
+    auto load_tile = [&](int i) {
+        const int s = i % PR_STAGES, j = i >> 1;
+        const bool clean = (i & 1) && j >= jclean;
+        uint64_t* bar = clean ? &v_full[j - jclean] : &full[s];
+        mbar_arrive_expect_tx(bar, PR_TILE);
+        for (int p = 0; p < 2; ++p)
+            tma_load_3d(ring + s * PR_TILE + p * PR_PANEL, (i & 1) ? &a.tv : &a.tk, 64 * p, tile.k0 + (j0 + j) * PR_KEYS,
+                        g, bar);
+        if (clean)
+            mbar_arrive(&full[s]);  // the slot's phase goes on
+    };
     pdl_trigger();
-    if (warp == 0) {
-        const PromptTile t = prompt_find(a, idx, 2 * a.tq_tokens, lane);
-        if (lane == 0)
-            *shared_tile = t;
+    if (warp == PR_TMA_WARP) {
+        // the copying warp finds the block's tile and starts its copies while the others
+        // are set up
+        tile = prompt_find(a, idx, 2 * a.tq_tokens, lane);
+        set_span();
+        if (lane == 0) {
+            *shared_tile = tile;
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&q_full[i], 1);
+                mbar_init(&s_full[i], 1);
+                mbar_init(&p_full[i], 4);
+                mbar_init(&o_full[i], 1);
+            }
+            for (int i = 0; i < PR_STAGES; ++i) {
+                mbar_init(&full[i], 1);
+                mbar_init(&freed[i], 1);
+            }
+            for (int i = 0; i < PR_CLEAN; ++i) {
+                mbar_init(&v_full[i], 1);
+                mbar_init(&cleaned[i], 2);
+            }
+            mbar_init(drain, 1);
+            fence_mbar_init();
+            *fail = 0;
+            *poison = 0;
+            for (int t = 0; t < 2; ++t) {
+                if (!(t ? end1 : end0))
+                    continue;
+                mbar_arrive_expect_tx(&q_full[t], static_cast<uint32_t>(2 * a.tq_tokens * a.group * 128));
+                for (int p = 0; p < 2; ++p)
+                    tma_load_3d(qs + t * PR_TILE + p * PR_PANEL, &a.tq, 64 * p, g * a.group,
+                                tile.q0 + tile.t0 + t * a.tq_tokens, &q_full[t]);
+                if (t == 0 && n > 0)
+                    load_tile(0);
+            }
+            for (int i = end0 ? 1 : 0; i < min(2 * n, PR_STAGES); ++i)
+                load_tile(i);
+        }
+        __syncwarp();
     } else if (warp == PR_MMA_WARP) {
         tmem_alloc(tslot, PR_TCOLS);
-    } else if (warp == PR_TMA_WARP && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tq)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tk)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a.tv)) : "memory");
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
-        }
-        for (int i = 0; i < PR_STAGES; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&freed[i], 1);
-        }
-        for (int i = 0; i < PR_CLEAN; ++i) {
-            mbar_init(&v_full[i], 1);
-            mbar_init(&cleaned[i], 2);
-        }
-        mbar_init(drain, 1);
-        fence_mbar_init();
-        *fail = 0;
-        *poison = 0;
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const PromptTile tile = *shared_tile;
+    if (warp != PR_TMA_WARP) {
+        tile = *shared_tile;
+        set_span();
+    }
     const uint32_t tbase = *tslot;
-
-    const PromptSpan sp = prompt_span(tile, a.tq_tokens);
-    // this block's key tiles j0 + i, i < n, and i < end[t] for query tile t
-    int j0, j1;
-    prompt_split(sp, a.splits, c, j0, j1);
-    const int n = j1 - j0, end[2] = {max(0, min(sp.end[0], j1) - j0), max(0, min(sp.end[1], j1) - j0)};
-    const int jclean = sp.open / PR_KEYS - j0;  // the first of them with a masked key for some row, may be below 0
 
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
         if (mbar_try_wait(bar, parity))
@@ -279,7 +310,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     if (tile.live && warp < PR_MMA_WARP) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PR_SOFTMAX_REGS));
         // ---- softmax and epilogue: warps 4 t .. 4 t + 3, thread r of them owns row r
-        const int t = warp >> 2, r = tid & 127;
+        const int t = warp >> 2, r = tid & 127, end = t ? end1 : end0;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + PR_S0 + 128 * t, to = tbase + lanes + PR_O0 + 128 * t;
         const int tok = tile.t0 + t * a.tq_tokens + r / a.group;  // within the sequence
@@ -287,26 +318,36 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         const int lim = min(tile.lk, max(0, tok + 1 + tile.lk - tile.lq));  // keys this row sees
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < end[t]; ++j) {
+        for (int j = 0; j < end; ++j) {
             if (!(ok = warp_wait(&s_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
                 break;
             tc_fence_after_sync();
             uint32_t s[128];
+            // the maximum of the first half while the second is on its way
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            const int left = lim - (j0 + j) * PR_KEYS;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tmem_ld32(ts + 32 * c, s + 32 * c);
-            tmem_ld_wait();
-            if (j >= jclean) {
-                const int left = lim - (j0 + j) * PR_KEYS;
+            for (int q = 0; q < 2; ++q) {
+                if (q == 0) {
+                    tmem_ld32(ts, s);
+                    tmem_ld32(ts + 32, s + 32);
+                }
+                tmem_ld_wait();
+                if (q == 0) {
+                    tmem_ld32(ts + 64, s + 64);
+                    tmem_ld32(ts + 96, s + 96);
+                }
+                if (j >= jclean) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (c >= left)
-                        s[c] = 0xff800000u;  // -infinity
+                    for (int i = 64 * q; i < 64 * q + 64; ++i)
+                        if (i >= left)
+                            s[i] = 0xff800000u;  // -infinity
+                }
+#pragma unroll
+                for (int i = 64 * q; i < 64 * q + 64; ++i)
+                    top4[i & 3] = fmaxf(top4[i & 3], __uint_as_float(s[i]));
             }
-            float top = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-                top = fmaxf(top, __uint_as_float(s[c]));
+            const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             const bool grow = (top - m) * PR_C > PR_GROW;
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = grow ? top : m;
@@ -317,41 +358,47 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     if (!(ok = warp_wait(&o_full[t], (j - 1) & 1, DEVERR_TIMEOUT_FULL)))
                         break;
                     tc_fence_after_sync();
-                    for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
                         uint32_t o[32];
-                        tmem_ld32(to + 32 * c, o);
+                        tmem_ld32(to + 32 * q, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(to + 32 * c, o);
+                        tmem_st32(to + 32 * q, o);
                     }
                 }
             }
-            const float base = m == -INFINITY ? 0.f : m * PR_C;
-            float sum0 = 0.f, sum1 = 0.f;
+            const float base = m == -INFINITY ? 0.f : -m * PR_C;
+            const uint64_t c2 = f2(PR_C, PR_C), b2 = f2(base, base);
+            uint64_t sum0 = 0ull, sum1 = 0ull;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int q = 0; q < 2; ++q) {
                 uint32_t p[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
-                    const float x = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i]), PR_C, -base));
-                    const float y = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]), PR_C, -base));
-                    sum0 += x;
-                    sum1 += y;
-                    p[i] = pack2(x, y, static_cast<const T*>(nullptr));
+                    const float2 x = un2(fma2(f2(__uint_as_float(s[64 * q + 2 * i]), __uint_as_float(s[64 * q + 2 * i + 1])),
+                                              c2, b2));
+                    const float y0 = ex2(x.x), y1 = ex2(x.y);
+                    if (i & 1)
+                        sum1 = add2(sum1, f2(y0, y1));
+                    else
+                        sum0 = add2(sum0, f2(y0, y1));
+                    p[i] = pack2(y0, y1, static_cast<const T*>(nullptr));
                 }
-                tmem_st32(ts + 32 * c, p);
+                tmem_st32(ts + 32 * q, p);
             }
-            l += sum0 + sum1;
+            const float2 sum = un2(add2(sum0, sum1));
+            l += sum.x + sum.y;
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&p_full[t]);
         }
-        if (ok && end[t])
-            ok = warp_wait(&o_full[t], (end[t] - 1) & 1, DEVERR_TIMEOUT_FULL);
+        if (ok && end)
+            ok = warp_wait(&o_full[t], (end - 1) & 1, DEVERR_TIMEOUT_FULL);
         tc_fence_after_sync();
         const bool bad = *poison;
         // a seen infinity or NaN of V, which the products left out, added to a row's 32 dims
@@ -379,7 +426,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
             }
         };
         if (ok && a.splits > 1) {
-            if (end[t]) {
+            if (end) {
                 const size_t at = ((static_cast<size_t>(idx) * a.n_kv + g) * a.splits + c) * 2 + t;
                 a.part_ml[at * 256 + r] = m;
                 a.part_ml[at * 256 + 128 + r] = l;
@@ -406,7 +453,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t o[32];
-                if (end[t]) {
+                if (end) {
                     tmem_ld32(to + 32 * c, o);
                     tmem_ld_wait();
                 }
@@ -432,130 +479,121 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         }
     } else if (tile.live) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PR_OTHER_REGS));
+        const int first_clean = 2 * max(0, jclean) + 1;  // the copy of the first value tile to be cleaned
         if (warp == PR_TMA_WARP) {
-        if (lane == 0 && n > 0) {
-            for (int t = 0; t < 2; ++t) {
-                if (!end[t])
-                    continue;
-                mbar_arrive_expect_tx(&q_full[t], static_cast<uint32_t>(2 * rows * 128));
-                for (int p = 0; p < 2; ++p)
-                    tma_load_3d(qs + t * PR_TILE + p * PR_PANEL, &a.tq, 64 * p, g * a.group,
-                                tile.q0 + tile.t0 + t * a.tq_tokens, &q_full[t]);
-            }
-            int issued = 0, cleans = 0;
-            for (; issued < 2 * n; ++issued) {  // key tile 0, value tile 0, key tile 1, ...
-                const int s = issued % PR_STAGES;
-                if (issued >= PR_STAGES && !wait(&freed[s], ((issued / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
+            int i = min(2 * n, PR_STAGES);
+            bool called = first_clean >= 2 * n;  // the cleaning warps sleep until their first tile is on its way
+            for (; i < 2 * n; ++i) {
+                if (!called && first_clean < i) {
+                    called = true;
+                    named_bar_arrive(PR_CLEAN_BAR, 96);
+                }
+                if (!warp_wait(&freed[i % PR_STAGES], ((i / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
                     break;
-                const int j = issued >> 1;
-                const bool clean = (issued & 1) && j >= jclean;
-                uint64_t* bar = clean ? &v_full[j - jclean] : &full[s];
-                mbar_arrive_expect_tx(bar, PR_TILE);
-                for (int p = 0; p < 2; ++p)
-                    tma_load_3d(ring + s * PR_TILE + p * PR_PANEL, (issued & 1) ? &a.tv : &a.tk, 64 * p,
-                                tile.k0 + (j0 + j) * PR_KEYS, g, bar);
-                if (clean) {
-                    mbar_arrive(&full[s]);  // the slot's phase goes on
-                    ++cleans;
-                }
+                if (lane == 0)
+                    load_tile(i);
             }
+            if (!called)
+                named_bar_arrive(PR_CLEAN_BAR, 96);
             // every copy has landed before the block ends
-            for (int i = max(0, issued - PR_STAGES); i < issued; ++i)
-                if (!mbar_wait(&full[i % PR_STAGES], (i / PR_STAGES) & 1))
+            if (lane == 0) {
+                bool landed = true;
+                for (int k = max(0, i - PR_STAGES); k < i; ++k)
+                    landed = mbar_wait(&full[k % PR_STAGES], (k / PR_STAGES) & 1) && landed;
+                for (int k = 0; k < PR_CLEAN && first_clean + 2 * k < i; ++k)
+                    landed = mbar_wait(&v_full[max(0, -jclean) + k], 0) && landed;
+                for (int t = 0; t < 2; ++t)
+                    landed = (!(t ? end1 : end0) || mbar_wait(&q_full[t], 0)) && landed;
+                if (!landed)
                     set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-            for (int i = 0; i < cleans; ++i)
-                if (!mbar_wait(&v_full[i], 0))
-                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-            for (int t = 0; t < 2; ++t)
-                if (end[t] && !mbar_wait(&q_full[t], 0))
-                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-        }
-        __syncwarp();
-    } else if (warp == PR_MMA_WARP) {
-        if (n > 0) {
-            constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-            constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
-            constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
-            bool ok = true;
-            auto qk = [&](int t, int j) {  // S_t = Q_t K_j^T: eight steps of 16 dims, four a panel
-                const uint32_t kb = smem_addr(ring + (2 * j % PR_STAGES) * PR_TILE);
-                const uint64_t ad = umma_desc_sw128(smem_addr(qs + t * PR_TILE), 16, 1024);
-                const uint64_t bd = umma_desc_sw128(kb, 16, 1024);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint64_t step = ((s >> 2) * PR_PANEL + (s & 3) * 32) >> 4;
-                    umma_f16_warp(tbase + PR_S0 + 128 * t, ad + step, bd + step, id_qk, s > 0);
-                }
-                umma_commit_warp(&s_full[t]);
-            };
-            auto pv = [&](int t, int j) {  // O_t += P_t V_j: eight steps of 16 keys
-                const uint64_t bd = umma_desc_sw128(smem_addr(ring + ((2 * j + 1) % PR_STAGES) * PR_TILE), PR_PANEL, 1024);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    umma_f16_ta_warp(tbase + PR_O0 + 128 * t, tbase + PR_S0 + 128 * t + 8 * s,
-                                bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, j > 0 || s > 0);
-                umma_commit_warp(&o_full[t]);
-            };
-            ok = warp_wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
-            for (int t = 0; ok && t < 2; ++t)
-                if (end[t] && (ok = warp_wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
-                    qk(t, 0);
-            umma_commit_warp(&freed[0]);
-            for (int j = 0; ok && j < n; ++j) {
-                const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
-                ok = j >= jclean ? warp_wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
-                                 : warp_wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                if (ok && j + 1 < n)
-                    ok = warp_wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                for (int t = 0; ok && t < 2; ++t) {
-                    if (j >= end[t])
-                        continue;
-                    if (!(ok = warp_wait(&p_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
-                        break;
-                    tc_fence_after_sync();
-                    pv(t, j);
-                    if (j + 1 < end[t])
-                        qk(t, j + 1);
-                }
-                umma_commit_warp(&freed[sv]);
-                if (j + 1 < n)
-                    umma_commit_warp(&freed[sk]);
             }
-            umma_commit_warp(drain);  // every product is done before the block ends
-            if (!mbar_wait(drain, 0) && lane == 0)
-                set_error(a.err, DEVERR_TIMEOUT_DRAIN);
-        }
-        __syncwarp();
-    } else {
-        // infinities and NaNs of the value tiles with masked keys become zero
-        const int ct = tid - 32 * PR_CLEAN_WARP;
-        for (int j = max(0, jclean); j < n; ++j) {
-            if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
-                break;
-            uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
-            bool seen = false;
-            for (int i = ct; i < PR_TILE / 16; i += 64) {
-                uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
-                const uint32_t nx = non_finite2<T>(w.x), ny = non_finite2<T>(w.y), nz = non_finite2<T>(w.z),
-                               nw = non_finite2<T>(w.w);
-                if (nx | ny | nz | nw) {
-                    // 0x8000 -> 0xffff per half: the halves to clear
-                    w.x &= ~((nx >> 15) * 0xffffu);
-                    w.y &= ~((ny >> 15) * 0xffffu);
-                    w.z &= ~((nz >> 15) * 0xffffu);
-                    w.w &= ~((nw >> 15) * 0xffffu);
-                    *reinterpret_cast<uint4*>(vt + 16 * i) = w;
-                    seen |= (j0 + j) * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
-                }
-            }
-            if (seen)
-                *poison = 1;
-            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&cleaned[j - jclean]);
+        } else if (warp == PR_MMA_WARP) {
+            if (n > 0) {
+                constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+                constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
+                constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
+                bool ok = true;
+                auto qk = [&](int t, int j) {  // S_t = Q_t K_j^T: eight steps of 16 dims, four a panel
+                    const uint32_t kb = smem_addr(ring + (2 * j % PR_STAGES) * PR_TILE);
+                    const uint64_t ad = umma_desc_sw128(smem_addr(qs + t * PR_TILE), 16, 1024);
+                    const uint64_t bd = umma_desc_sw128(kb, 16, 1024);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const uint64_t step = ((s >> 2) * PR_PANEL + (s & 3) * 32) >> 4;
+                        umma_f16_warp(tbase + PR_S0 + 128 * t, ad + step, bd + step, id_qk, s > 0);
+                    }
+                    umma_commit_warp(&s_full[t]);
+                };
+                auto pv = [&](int t, int j) {  // O_t += P_t V_j: eight steps of 16 keys
+                    const uint64_t bd = umma_desc_sw128(smem_addr(ring + ((2 * j + 1) % PR_STAGES) * PR_TILE), PR_PANEL, 1024);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        umma_f16_ta_warp(tbase + PR_O0 + 128 * t, tbase + PR_S0 + 128 * t + 8 * s,
+                                    bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, j > 0 || s > 0);
+                    umma_commit_warp(&o_full[t]);
+                };
+                ok = warp_wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
+                for (int t = 0; ok && t < 2; ++t)
+                    if ((t ? end1 : end0) && (ok = warp_wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
+                        qk(t, 0);
+                umma_commit_warp(&freed[0]);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
+                    ok = j >= jclean ? warp_wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
+                                     : warp_wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
+                    if (ok && j + 1 < n)
+                        ok = warp_wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
+                    for (int t = 0; ok && t < 2; ++t) {
+                        if (j >= (t ? end1 : end0))
+                            continue;
+                        if (!(ok = warp_wait(&p_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
+                            break;
+                        tc_fence_after_sync();
+                        pv(t, j);
+                        if (j + 1 < (t ? end1 : end0))
+                            qk(t, j + 1);
+                    }
+                    umma_commit_warp(&freed[sv]);
+                    if (j + 1 < n)
+                        umma_commit_warp(&freed[sk]);
+                }
+                umma_commit_warp(drain);  // every product is done before the block ends
+                if (!mbar_wait(drain, 0) && lane == 0)
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+            }
+            __syncwarp();
+        } else if (first_clean < 2 * n) {
+            named_bar_sync(PR_CLEAN_BAR, 96);
+            // infinities and NaNs of the value tiles with masked keys become zero
+            const int ct = tid - 32 * PR_CLEAN_WARP;
+            for (int j = max(0, jclean); j < n; ++j) {
+                if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
+                    break;
+                uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
+                bool seen = false;
+                for (int i = ct; i < PR_TILE / 16; i += 64) {
+                    uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
+                    const uint32_t nx = non_finite2<T>(w.x), ny = non_finite2<T>(w.y), nz = non_finite2<T>(w.z),
+                                   nw = non_finite2<T>(w.w);
+                    if (nx | ny | nz | nw) {
+                        // 0x8000 -> 0xffff per half: the halves to clear
+                        w.x &= ~((nx >> 15) * 0xffffu);
+                        w.y &= ~((ny >> 15) * 0xffffu);
+                        w.z &= ~((nz >> 15) * 0xffffu);
+                        w.w &= ~((nw >> 15) * 0xffffu);
+                        *reinterpret_cast<uint4*>(vt + 16 * i) = w;
+                        seen |= (j0 + j) * PR_KEYS + (i & 1023) / 8 < tile.lk;  // a panel's rows are 8 of these
+                    }
+                }
+                if (seen)
+                    *poison = 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&cleaned[j - jclean]);
+            }
         }
-    }
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -563,13 +601,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         tmem_dealloc(tbase, PR_TCOLS);
 }
 
-// The splits of one block tile, KV head and query tile: a thread takes one row and 16
-// of its dims.
+// The splits of one block tile, KV head and query tile: a thread takes one row and 8 of
+// its dims.  The splits' weights of the row come first, then all their loads are free of
+// one another.
 template <typename T>
 __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a)
 {
     __shared__ PromptTile shared_tile;
-    const int r = threadIdx.x, q = blockIdx.y & 7, t = blockIdx.y >> 3;
+    __shared__ float weight[PR_MAX_SPLITS][128];
+    const int r = threadIdx.x, q = blockIdx.y & 15, t = blockIdx.y >> 4;
     const int g = blockIdx.x % a.n_kv, idx = blockIdx.x / a.n_kv;
     if (threadIdx.x < 32) {
         const PromptTile x = prompt_find(a, idx, 2 * a.tq_tokens, threadIdx.x);
@@ -578,8 +618,8 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     }
     __syncthreads();
     const PromptTile tile = shared_tile;
-    pdl_wait();
     const PromptSpan sp = prompt_span(tile, a.tq_tokens);
+    pdl_wait();
     if (!tile.live || r / a.group >= sp.ntok[t])
         return;
     const int tok = tile.t0 + t * a.tq_tokens + r / a.group;
@@ -589,20 +629,28 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     prompt_split(sp, a.splits, 0, j0, per);
     const int n = per > 0 ? min(a.splits, (sp.end[t] + per - 1) / per) : 0;
     const float* ml = a.part_ml + (first * 2 + t) * 256 + r;
-    const float4* po = reinterpret_cast<const float4*>(a.part) + (first * 2 + t) * 32 * 128 + 4 * q * 128 + r;
+    const float4* po = reinterpret_cast<const float4*>(a.part) + (first * 2 + t) * 32 * 128 + 2 * q * 128 + r;
     float m = -INFINITY;
-#pragma unroll 4
-    for (int c = 0; c < n; ++c)
-        m = fmaxf(m, __ldcg(ml + c * 512));
+#pragma unroll 8
+    for (int c = 0; c < n; ++c) {
+        const float x = __ldcg(ml + c * 512);
+        weight[c][r] = x;  // this thread's alone
+        m = fmaxf(m, x);
+    }
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    float4 o[4] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int c = 0; c < n; ++c) {
-        const float f = ex2((__ldcg(ml + c * 512) - base) * PR_C);
-        l += f * __ldcg(ml + c * 512 + 128);
+        const float f = ex2((weight[c][r] - base) * PR_C);
+        weight[c][r] = f;
+        l = fmaf(f, __ldcg(ml + c * 512 + 128), l);
+    }
+    float4 o[2] = {};
+#pragma unroll 8
+    for (int c = 0; c < n; ++c) {
+        const float f = weight[c][r];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const float4 x = __ldcg(po + static_cast<size_t>(c) * 2 * 32 * 128 + i * 128);
             o[i].x = fmaf(f, x.x, o[i].x);
             o[i].y = fmaf(f, x.y, o[i].y);
@@ -613,9 +661,9 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     const bool sees = tok + 1 + tile.lk - tile.lq > 0 && tile.lk > 0;
     const float inv = sees ? 1.0f / l : 0.f;
     T* out = static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
-             static_cast<long long>(g * a.group + r % a.group) * a.o_head + 16 * q;
+             static_cast<long long>(g * a.group + r % a.group) * a.o_head + 8 * q;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
         store4(out + 4 * i, sees ? make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv)
                                  : make_float4(0.f, 0.f, 0.f, 0.f));
 }
@@ -637,7 +685,7 @@ static PromptCut prompt_cut(int n_seq, int total_q, int total_k, int n_q, int n_
     const long long tiles = (total_q - seqs) / span + seqs;
     const long long keys = (static_cast<long long>(total_k) + seqs * dq::PR_KEYS - 1) / (seqs * dq::PR_KEYS);
     // too few blocks for the card: the keys are split, into two key tiles at least
-    const long long splits = std::min(sm_count() / (tiles * n_kv), keys / 2);
+    const long long splits = std::min({sm_count() / (tiles * n_kv), keys / 2, static_cast<long long>(dq::PR_MAX_SPLITS)});
     return {tiles, static_cast<int>(std::max(1ll, splits))};
 }
 
@@ -692,7 +740,7 @@ static cudaError_t prompt_launch(const dq::PromptArgs& a, unsigned grid, const P
         return e;
     // a dependent launch: it finds its tiles while the last blocks run
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cut.tiles * a.n_kv), 16);
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.tiles * a.n_kv), 32);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
