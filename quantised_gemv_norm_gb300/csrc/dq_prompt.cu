@@ -33,9 +33,12 @@ namespace dq {
 
 constexpr int PR_HD = 128;
 constexpr int PR_KEYS = 128;                  // keys a tile
-constexpr int PR_STAGES = 5;                  // ring of key and value tiles, in turn
+constexpr int PR_STAGES = 5;                  // ring of key and value tiles, in turn (odd: see the products' loop)
 constexpr int PR_TILE = PR_KEYS * PR_HD * 2;  // bytes of a key, value or query tile
 constexpr int PR_PANEL = PR_TILE / 2;         // 64 dims of it
+// warps 0-7 softmax, then one that issues the products (of both query tiles: two warps
+// let the tiles fall into step, products and exponentials in turn: 397 -> 505 us), one
+// that copies and two that clean value tiles
 constexpr int PR_MMA_WARP = 8, PR_TMA_WARP = 9, PR_CLEAN_WARP = 10;
 constexpr int PR_CLEAN_BAR = 1;  // named barrier of the copying and the cleaning warps
 constexpr int PR_THREADS = 384;
@@ -189,6 +192,21 @@ __device__ __forceinline__ float one16(uint32_t bits)
     return half_bits_to_float(bits);
 }
 
+// The rest of a wait whose first poll found nothing.
+__device__ __forceinline__ void prompt_wait_on(uint64_t* bar, uint32_t parity, volatile int* fail, int* err, int code)
+{
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+        if (*fail)
+            return;
+        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            *fail = 1;
+            set_error(err, code);
+            return;
+        }
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_constant__ PromptArgs a)
 {
@@ -204,8 +222,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     uint64_t* v_full = freed + PR_STAGES;    // [PR_CLEAN] landed
     uint64_t* cleaned = v_full + PR_CLEAN;   // [PR_CLEAN] infinities and NaNs are out
     uint64_t* s_full = cleaned + PR_CLEAN;   // [2] S of a query tile written
-    uint64_t* p_full = s_full + 2;           // [2] P written
-    uint64_t* o_full = p_full + 2;           // [2] a product P V done
+    uint64_t* p_full = s_full + 2;           // [2][2] a half of P's keys written
+    uint64_t* o_full = p_full + 4;           // [2] a product P V done
     uint64_t* drain = o_full + 2;
     PromptTile* shared_tile = reinterpret_cast<PromptTile*>(drain + 1);
     uint32_t* tslot = reinterpret_cast<uint32_t*>(shared_tile + 1);
@@ -250,7 +268,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&q_full[i], 1);
                 mbar_init(&s_full[i], 1);
-                mbar_init(&p_full[i], 4);
+                mbar_init(&p_full[2 * i], 4);
+                mbar_init(&p_full[2 * i + 1], 4);
                 mbar_init(&o_full[i], 1);
             }
             for (int i = 0; i < PR_STAGES; ++i) {
@@ -291,20 +310,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     }
     const uint32_t tbase = *tslot;
 
-    auto wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if (*fail)
-            return false;
-        if (!mbar_wait(bar, parity)) {
-            *fail = 1;
-            set_error(a.err, code);
-            return false;
-        }
-        return true;
-    };
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity, int code) -> bool {
-        return __all_sync(0xffffffffu, wait(bar, parity, code)) != 0;
+    // Bounded waits.  Once one has run out the block has given up: the others return at
+    // once, every role runs to its end over whatever is there, and nothing is written.
+    auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+        if (!mbar_try_wait(bar, parity))
+            prompt_wait_on(bar, parity, fail, a.err, code);
     };
 
     if (tile.live && warp < PR_MMA_WARP) {
@@ -317,10 +327,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         const bool mine = r / a.group < sp.ntok[t];
         const int lim = min(tile.lk, max(0, tok + 1 + tile.lk - tile.lq));  // keys this row sees
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
         for (int j = 0; j < end; ++j) {
-            if (!(ok = warp_wait(&s_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
-                break;
+            wait(&s_full[t], j & 1, DEVERR_TIMEOUT_FULL);
+            __syncwarp();
             tc_fence_after_sync();
             uint32_t s[128];
             // the maximum of the first half while the second is on its way
@@ -355,8 +364,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 m = mn;
                 l *= alpha;
                 if (j > 0) {
-                    if (!(ok = warp_wait(&o_full[t], (j - 1) & 1, DEVERR_TIMEOUT_FULL)))
-                        break;
+                    wait(&o_full[t], (j - 1) & 1, DEVERR_TIMEOUT_FULL);
+                    __syncwarp();
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
@@ -387,18 +396,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                         sum0 = add2(sum0, f2(y0, y1));
                     p[i] = pack2(y0, y1, static_cast<const T*>(nullptr));
                 }
+                // each half of the keys is multiplied while the next exponentials run
                 tmem_st32(ts + 32 * q, p);
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[2 * t + q]);
             }
             const float2 sum = un2(add2(sum0, sum1));
             l += sum.x + sum.y;
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&p_full[t]);
         }
-        if (ok && end)
-            ok = warp_wait(&o_full[t], (end - 1) & 1, DEVERR_TIMEOUT_FULL);
+        if (end)
+            wait(&o_full[t], (end - 1) & 1, DEVERR_TIMEOUT_FULL);
+        const bool ok = __all_sync(0xffffffffu, !*fail);
         tc_fence_after_sync();
         const bool bad = *poison;
         // a seen infinity or NaN of V, which the products left out, added to a row's 32 dims
@@ -488,7 +499,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     called = true;
                     named_bar_arrive(PR_CLEAN_BAR, 96);
                 }
-                if (!warp_wait(&freed[i % PR_STAGES], ((i / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY))
+                wait(&freed[i % PR_STAGES], ((i / PR_STAGES) & 1) ^ 1, DEVERR_TIMEOUT_EMPTY);
+                __syncwarp();
+                if (__any_sync(0xffffffffu, *fail))
                     break;
                 if (lane == 0)
                     load_tile(i);
@@ -513,11 +526,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
                 constexpr uint32_t id_qk = umma_idesc_16bit(128, PR_KEYS, bf, false);
                 constexpr uint32_t id_pv = umma_idesc_16bit(128, PR_HD, bf, true);
-                bool ok = true;
-                auto qk = [&](int t, int j) {  // S_t = Q_t K_j^T: eight steps of 16 dims, four a panel
-                    const uint32_t kb = smem_addr(ring + (2 * j % PR_STAGES) * PR_TILE);
-                    const uint64_t ad = umma_desc_sw128(smem_addr(qs + t * PR_TILE), 16, 1024);
-                    const uint64_t bd = umma_desc_sw128(kb, 16, 1024);
+                const uint64_t qd0 = umma_desc_sw128(smem_addr(qs), 16, 1024);
+                const uint64_t kd0 = umma_desc_sw128(smem_addr(ring), 16, 1024);
+                const uint64_t vd0 = umma_desc_sw128(smem_addr(ring), PR_PANEL, 1024);
+                // S_t = Q_t K^T: eight steps of 16 dims, four a panel
+                auto qk = [&](int t, int slot) {
+                    const uint64_t ad = qd0 + static_cast<uint64_t>(t * (PR_TILE >> 4));
+                    const uint64_t bd = kd0 + static_cast<uint64_t>(slot * (PR_TILE >> 4));
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
                         const uint64_t step = ((s >> 2) * PR_PANEL + (s & 3) * 32) >> 4;
@@ -525,38 +540,58 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     }
                     umma_commit_warp(&s_full[t]);
                 };
-                auto pv = [&](int t, int j) {  // O_t += P_t V_j: eight steps of 16 keys
-                    const uint64_t bd = umma_desc_sw128(smem_addr(ring + ((2 * j + 1) % PR_STAGES) * PR_TILE), PR_PANEL, 1024);
+                // O_t += P_t V: eight steps of 16 keys, four for each half of P
+                auto pv = [&](int t, int slot, int half, bool first) {
+                    const uint64_t bd = vd0 + static_cast<uint64_t>(slot * (PR_TILE >> 4));
 #pragma unroll
-                    for (int s = 0; s < 8; ++s)
+                    for (int s = 4 * half; s < 4 * half + 4; ++s)
                         umma_f16_ta_warp(tbase + PR_O0 + 128 * t, tbase + PR_S0 + 128 * t + 8 * s,
-                                    bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, j > 0 || s > 0);
-                    umma_commit_warp(&o_full[t]);
+                                         bd + static_cast<uint64_t>((s * 2048) >> 4), id_pv, !first || s > 0);
                 };
-                ok = warp_wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
-                for (int t = 0; ok && t < 2; ++t)
-                    if ((t ? end1 : end0) && (ok = warp_wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL)))
+                wait(&full[0], 0, DEVERR_TIMEOUT_FULL);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if ((t ? end1 : end0) > 0) {
+                        wait(&q_full[t], 0, DEVERR_TIMEOUT_FULL);
                         qk(t, 0);
+                    }
                 umma_commit_warp(&freed[0]);
-                for (int j = 0; ok && j < n; ++j) {
-                    const int iv = 2 * j + 1, sv = iv % PR_STAGES, ik = 2 * j + 2, sk = ik % PR_STAGES;
-                    ok = j >= jclean ? warp_wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL)
-                                     : warp_wait(&full[sv], (iv / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                    if (ok && j + 1 < n)
-                        ok = warp_wait(&full[sk], (ik / PR_STAGES) & 1, DEVERR_TIMEOUT_FULL);
-                    for (int t = 0; ok && t < 2; ++t) {
+                // ring slots of value tile j and key tile j + 1, and their phases
+                int sv = 1, sk = 2;
+                uint32_t vphase = 0, kphase = 0;
+                for (int j = 0; j < n; ++j) {
+                    if (j >= jclean)
+                        wait(&cleaned[j - jclean], 0, DEVERR_TIMEOUT_FULL);
+                    else
+                        wait(&full[sv], vphase, DEVERR_TIMEOUT_FULL);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
                         if (j >= (t ? end1 : end0))
                             continue;
-                        if (!(ok = warp_wait(&p_full[t], j & 1, DEVERR_TIMEOUT_FULL)))
-                            break;
-                        tc_fence_after_sync();
-                        pv(t, j);
-                        if (j + 1 < (t ? end1 : end0))
-                            qk(t, j + 1);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            wait(&p_full[2 * t + half], j & 1, DEVERR_TIMEOUT_FULL);
+                            tc_fence_after_sync();
+                            pv(t, sv, half, j == 0);
+                        }
+                        umma_commit_warp(&o_full[t]);
+                        if (j + 1 < (t ? end1 : end0)) {
+                            if (t == 0 || end0 <= j + 1)
+                                wait(&full[sk], kphase, DEVERR_TIMEOUT_FULL);
+                            qk(t, sk);
+                        }
                     }
                     umma_commit_warp(&freed[sv]);
                     if (j + 1 < n)
                         umma_commit_warp(&freed[sk]);
+                    if ((sv += 2) >= PR_STAGES) {
+                        sv -= PR_STAGES;
+                        vphase ^= 1;
+                    }
+                    if ((sk += 2) >= PR_STAGES) {
+                        sk -= PR_STAGES;
+                        kphase ^= 1;
+                    }
                 }
                 umma_commit_warp(drain);  // every product is done before the block ends
                 if (!mbar_wait(drain, 0) && lane == 0)
@@ -566,13 +601,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         } else if (first_clean < 2 * n) {
             named_bar_sync(PR_CLEAN_BAR, 96);
             // infinities and NaNs of the value tiles with masked keys become zero
-            const int ct = tid - 32 * PR_CLEAN_WARP;
-            for (int j = max(0, jclean); j < n; ++j) {
-                if (!warp_wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL))
-                    break;
+                        for (int j = max(0, jclean); j < n; ++j) {
+                wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL);
                 uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
                 bool seen = false;
-                for (int i = ct; i < PR_TILE / 16; i += 64) {
+#pragma unroll 8
+                for (int i = tid - 32 * PR_CLEAN_WARP; i < PR_TILE / 16; i += 64) {
                     uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
                     const uint32_t nx = non_finite2<T>(w.x), ny = non_finite2<T>(w.y), nz = non_finite2<T>(w.z),
                                    nw = non_finite2<T>(w.w);
