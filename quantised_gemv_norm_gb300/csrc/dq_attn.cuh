@@ -198,22 +198,6 @@ __device__ __forceinline__ float4 head_norm_rope(float4 v, const NormRope& nr, f
                        fmaf(v.z, c23.x, sg * o.z * c23.y), fmaf(v.w, c23.z, sg * o.w * c23.w));
 }
 
-// The rotation of head_norm_rope alone.
-__device__ __forceinline__ float4 head_rope(float4 v, const float2* __restrict__ cs, int lane)
-{
-    const int i0 = (4 * lane) & (ATT_HD / 2 - 1);
-    const float4 c01 = __ldg(reinterpret_cast<const float4*>(cs + i0));
-    const float4 c23 = __ldg(reinterpret_cast<const float4*>(cs + i0 + 2));
-    float4 o;
-    o.x = __shfl_xor_sync(0xffffffffu, v.x, 16);
-    o.y = __shfl_xor_sync(0xffffffffu, v.y, 16);
-    o.z = __shfl_xor_sync(0xffffffffu, v.z, 16);
-    o.w = __shfl_xor_sync(0xffffffffu, v.w, 16);
-    const float sg = lane < 16 ? -1.0f : 1.0f;
-    return make_float4(fmaf(v.x, c01.x, sg * o.x * c01.y), fmaf(v.y, c01.z, sg * o.y * c01.w),
-                       fmaf(v.z, c23.x, sg * o.z * c23.y), fmaf(v.w, c23.z, sg * o.w * c23.w));
-}
-
 // Block (c, g) of the decode attention, run by `group` warps of the calling
 // block (threads tbase .. tbase + 32 group - 1, synchronised by named barrier
 // bar), with `sm` (AttnSmem) as shared staging.  Used by the standalone kernel

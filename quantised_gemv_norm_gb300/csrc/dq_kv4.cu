@@ -1,8 +1,12 @@
 // dq_kv4.cu -- rows into a paged 4-bit cache and back (dq_kv4_append,
 // dq_kv4_read).
 //
-// One warp takes one head's key or value row, four dims a lane, so a group of 32
-// dims with one scale is eight lanes: its extremes are three shuffles.
+// Half a warp takes one head's key and value row, eight dims a lane: 16 bytes of a
+// 16-bit row, one 32-bit word of key codes, two halves of value words.  A group of 32
+// dims with one scale is four lanes: its extremes are two shuffles.  Memory bounds
+// both (160 bytes a row and head in the cache, 256 or 512 outside); with a warp a
+// row and a division for each code the instructions did (8000 rows of 8 heads, store
+// and read back: 55 us).
 #include "dq_kv4.cuh"
 
 namespace dq {
@@ -17,129 +21,151 @@ struct Kv4AppendArgs {
     unsigned char* pool;
     int rows;
     Kv4Shape s;
+    FastDiv by_kv, by_page;
     int* err;
 };
 
-// d, z and the four codes (nibbles 0..3, unsigned) of a lane's dims; the group is
-// the lane's eight neighbours.  Every step is one IEEE operation, as the format
-// defines it.
-__device__ __forceinline__ uint32_t kv4_quantise(float4 x, float& d, float& z)
+// The cache block of a slot (a page's rows are consecutive) and head; null, and the
+// error bit, where the slot is past the pool.  Sets j, the row in the block.
+__device__ __forceinline__ unsigned char* kv4_find(unsigned char* pool, const Kv4Shape& s, const FastDiv& by_page, int slot,
+                                                   int g, int* err, int& j)
 {
-    float lo = fminf(fminf(x.x, x.y), fminf(x.z, x.w)), hi = fmaxf(fmaxf(x.x, x.y), fmaxf(x.z, x.w));
-    // 0 * x is NaN for an infinity or NaN, which fminf and fmaxf would pass over
-    bool bad = !(0.f * x.x + 0.f * x.y + 0.f * x.z + 0.f * x.w == 0.f);
+    const int page = static_cast<int>(fast_div(static_cast<uint32_t>(slot), by_page));
+    const int off = slot - page * s.page_rows;
+    j = off % KV4_ROWS;
+    if (page >= s.n_pages) {
+        if ((threadIdx.x & 15) == 0)
+            set_error(err, DEVERR_BAD_ARG);
+        return nullptr;
+    }
+    return pool + ((static_cast<size_t>(page) * s.n_kv + g) * (s.page_rows / KV4_ROWS) + off / KV4_ROWS) * KV4_BYTES;
+}
+
+// d, z and eight codes (0..15) of a lane's dims; the group is the lane and its three
+// neighbours.  Extremes, d, z and x - z are the format's IEEE operations.  The quotient
+// is a product with 1 / d, off by less than 1e-5 where it is below 16: only within
+// that of a half can the rounding differ from the quotient's own, and there the
+// division is done.
+__device__ __forceinline__ void kv4_quantise(const float (&x)[8], float& d, float& z, uint32_t (&code)[8])
+{
+    float lo = x[0], hi = x[0], sum = 0.f;
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
+    for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        sum = fmaf(x[i], 0.f, sum);  // 0, or NaN from an infinity or NaN, which fminf and fmaxf may pass over
+    }
+#pragma unroll
+    for (int o = 2; o > 0; o >>= 1) {
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    const uint32_t group = 0xffu << (threadIdx.x & 24);
-    bad = (__ballot_sync(0xffffffffu, bad) & group) != 0u;
     d = __half2float(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)));
     z = __half2float(__float2half_rn(__fadd_rn(lo, 8.0f * d)));
-    if (bad || !(fabsf(d) <= 65504.f) || !(fabsf(z) <= 65504.f)) {
+    if (!(sum == 0.f) || !(d <= 65504.f) || !(fabsf(z) <= 65504.f))
         d = z = __int_as_float(0x7fc00000);
-        return 0x8888u;
-    }
-    if (d == 0.f)
-        return 0x8888u;
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    uint32_t c = 0;
+    const float inv = d > 0.f ? __frcp_rn(d) : 0.f;  // 0 or NaN: every code is 8
+    constexpr float M = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, halves to even
+    float off = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float t = rintf(__fdiv_rn(__fsub_rn(v[i], z), d)) + 8.0f;
-        c |= static_cast<uint32_t>(fminf(fmaxf(t, 0.f), 15.f)) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+        float t = fmaf(__fsub_rn(x[i], z), inv, 8.f);
+        t = d > 0.f ? fminf(fmaxf(t, 0.f), 15.f) : 8.f;
+        const float u = __fadd_rn(t, M);
+        off = fmaxf(off, fabsf(t - __fsub_rn(u, M)));
+        code[i] = __float_as_uint(u) & 15u;
     }
-    return c;
+    if (off > 0.49998f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float t = rintf(__fdiv_rn(__fsub_rn(x[i], z), d)) + 8.f;
+            code[i] = static_cast<uint32_t>(fminf(fmaxf(t, 0.f), 15.f));
+        }
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * KV4_WARPS) kv4_append_kernel(Kv4AppendArgs a)
+__global__ void __launch_bounds__(32 * KV4_WARPS) kv4_append_kernel(const Kv4AppendArgs a)
 {
-    const int lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * KV4_WARPS + (threadIdx.x >> 5);
-    const int per = 2 * a.s.n_kv;
-    if (item >= static_cast<long long>(a.rows) * per)
+    // a warp takes rows 2 i and 2 i + 1 of one head
+    const uint32_t item = blockIdx.x * KV4_WARPS + (threadIdx.x >> 5);
+    const uint32_t pair = fast_div(item, a.by_kv), g = item - pair * a.by_kv.d;
+    const int row = static_cast<int>(2 * pair + ((threadIdx.x >> 4) & 1));
+    const int slot = row < a.rows ? __ldg(a.slots + row) : -1;
+    int j = 0;
+    unsigned char* b = slot < 0 ? nullptr : kv4_find(a.pool, a.s, a.by_page, slot, g, a.err, j);
+    if (!__any_sync(0xffffffffu, b != nullptr))
         return;
-    const int row = static_cast<int>(item / per), hh = static_cast<int>(item % per);
-    const int g = hh >> 1, value = hh & 1;
-    const int slot = __ldg(a.slots + row);
-    if (slot < 0)
-        return;
-    const int page = slot / a.s.page_rows, off = slot % a.s.page_rows, j = off % KV4_ROWS;
-    if (page >= a.s.n_pages) {
-        if (lane == 0)
-            set_error(a.err, DEVERR_BAD_ARG);
-        return;
+    const int dim = threadIdx.x & 15, grp = dim >> 2, t = dim & 3;
+    float x[2][8] = {};
+    if (b) {
+        load8(static_cast<const T*>(a.k) + row * a.k_row + g * a.k_head + 8 * dim, x[0]);
+        load8(static_cast<const T*>(a.v) + row * a.v_row + g * a.v_head + 8 * dim, x[1]);
     }
-    const T* src = value ? static_cast<const T*>(a.v) + row * a.v_row + g * a.v_head
-                         : static_cast<const T*>(a.k) + row * a.k_row + g * a.k_head;
-    float d, z;
-    uint32_t c = kv4_quantise(load4(src + 4 * lane), d, z);
-    unsigned char* b = a.pool + kv4_block(a.s, page, off, g);
-    const int grp = lane >> 3, w = lane & 7;
-    if (value) {
-        *reinterpret_cast<unsigned short*>(b + kv4_value_half(j, w, grp)) = static_cast<unsigned short>(c);
-    } else {
-        // dims e = 0..3 (even lane) or 4..7: e = 2 i + s at bits 4 i + 16 s
-        c = (c & 0xfu) | ((c >> 4) & 0xfu) << 16 | ((c >> 8) & 0xfu) << 4 | ((c >> 12) & 0xfu) << 20;
-        c <<= 8 * (lane & 1);
-        c |= __shfl_xor_sync(0xffffffffu, c, 1);
-        if (!(lane & 1))
-            *reinterpret_cast<uint32_t*>(b + kv4_key_word(j, w >> 1, grp)) = c;
-    }
-    if (w == 0) {
-        __half* p = reinterpret_cast<__half*>(b + kv4_scale(value ? KV4_VSCALES : KV4_KSCALES, j, grp));
-        p[0] = __float2half_rn(d);
-        p[2] = __float2half_rn(z);
+#pragma unroll
+    for (int value = 0; value < 2; ++value) {
+        float d, z;
+        uint32_t c[8];
+        kv4_quantise(x[value], d, z, c);
+        if (!b)
+            continue;
+        if (value) {
+            unsigned short* p = reinterpret_cast<unsigned short*>(b + kv4_value_half(j, t, grp));
+            p[0] = static_cast<unsigned short>(c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12);
+            p[32] = static_cast<unsigned short>(c[4] | c[5] << 4 | c[6] << 8 | c[7] << 12);
+        } else {
+            *reinterpret_cast<uint32_t*>(b + kv4_key_word(j, t, grp)) = (c[0] | c[2] << 4 | c[4] << 8 | c[6] << 12) |
+                                                                        (c[1] | c[3] << 4 | c[5] << 8 | c[7] << 12) << 16;
+        }
+        if (t == 0) {
+            __half* p = reinterpret_cast<__half*>(b + kv4_scale(value ? KV4_VSCALES : KV4_KSCALES, j, grp));
+            p[0] = __float2half_rn(d);
+            p[2] = __float2half_rn(z);
+        }
     }
 }
 
 struct Kv4ReadArgs {
-    const unsigned char* pool;
+    unsigned char* pool;  // read
     const int* slots;
     int rows;
     Kv4Shape s;
+    FastDiv by_kv, by_page;
     int* err;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(32 * KV4_WARPS) kv4_read_kernel(Kv4ReadArgs a, T* __restrict__ k, T* __restrict__ v)
+__global__ void __launch_bounds__(32 * KV4_WARPS) kv4_read_kernel(const Kv4ReadArgs a, T* __restrict__ k, T* __restrict__ v)
 {
-    const int lane = threadIdx.x & 31;
-    const long long item = static_cast<long long>(blockIdx.x) * KV4_WARPS + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(a.rows) * a.s.n_kv)
+    const uint32_t item = 2 * (blockIdx.x * KV4_WARPS + (threadIdx.x >> 5)) + ((threadIdx.x >> 4) & 1);
+    const uint32_t row = fast_div(item, a.by_kv), g = item - row * a.by_kv.d;
+    const int slot = row < static_cast<uint32_t>(a.rows) ? __ldg(a.slots + row) : -1;
+    int j = 0;
+    const unsigned char* b = slot < 0 ? nullptr : kv4_find(a.pool, a.s, a.by_page, slot, g, a.err, j);
+    if (!b)
         return;
-    const int row = static_cast<int>(item / a.s.n_kv), g = static_cast<int>(item % a.s.n_kv);
-    const int slot = __ldg(a.slots + row);
-    if (slot < 0)
-        return;
-    const int page = slot / a.s.page_rows, off = slot % a.s.page_rows, j = off % KV4_ROWS;
-    if (page >= a.s.n_pages) {
-        if (lane == 0)
-            set_error(a.err, DEVERR_BAD_ARG);
-        return;
-    }
-    const unsigned char* b = a.pool + kv4_block(a.s, page, off, g);
-    const int grp = lane >> 3, w = lane & 7;
+    const int dim = threadIdx.x & 15, grp = dim >> 2, t = dim & 3;
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(b + kv4_key_word(j, t, grp));
+    const unsigned short* vp = reinterpret_cast<const unsigned short*>(b + kv4_value_half(j, t, grp));
+    const uint32_t vw = vp[0] | static_cast<uint32_t>(vp[32]) << 16;
+    const __half* ks = reinterpret_cast<const __half*>(b + kv4_scale(KV4_KSCALES, j, grp));
+    const __half* vs = reinterpret_cast<const __half*>(b + kv4_scale(KV4_VSCALES, j, grp));
+    const float kd = __half2float(ks[0]), kz = __half2float(ks[2]), vd = __half2float(vs[0]), vz = __half2float(vs[2]);
+    // c under 2^23's mantissa is 2^23 + c exactly
+    auto value = [](uint32_t w, int bit, float d, float z) {
+        return fmaf(d, __uint_as_float(((w >> bit) & 15u) | 0x4B000000u) - 8388616.f, z);
+    };
+    const size_t at = static_cast<size_t>(item) * ATT_HD + 8 * dim;
+    float x[8];
 #pragma unroll
-    for (int value = 0; value < 2; ++value) {
-        uint32_t c;
-        if (value) {
-            c = *reinterpret_cast<const unsigned short*>(b + kv4_value_half(j, w, grp));
-        } else {
-            c = *reinterpret_cast<const uint32_t*>(b + kv4_key_word(j, w >> 1, grp)) >> (8 * (lane & 1));
-            c = (c & 0xfu) | ((c >> 16) & 0xfu) << 4 | ((c >> 4) & 0xfu) << 8 | ((c >> 20) & 0xfu) << 12;
-        }
-        const __half* p = reinterpret_cast<const __half*>(b + kv4_scale(value ? KV4_VSCALES : KV4_KSCALES, j, grp));
-        const float d = __half2float(p[0]), z = __half2float(p[2]);
-        float4 x;
-        x.x = fmaf(d, static_cast<float>(static_cast<int>(c & 15u) - 8), z);
-        x.y = fmaf(d, static_cast<float>(static_cast<int>((c >> 4) & 15u) - 8), z);
-        x.z = fmaf(d, static_cast<float>(static_cast<int>((c >> 8) & 15u) - 8), z);
-        x.w = fmaf(d, static_cast<float>(static_cast<int>((c >> 12) & 15u) - 8), z);
-        store4((value ? v : k) + (static_cast<size_t>(row) * a.s.n_kv + g) * ATT_HD + 4 * lane, x);
-    }
+    for (int i = 0; i < 8; ++i)
+        x[i] = value(kw, 4 * (i >> 1) + 16 * (i & 1), kd, kz);
+    store8(k + at, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        x[i] = value(vw, 4 * i, vd, vz);
+    store8(v + at, x);
 }
 
 }  // namespace dq
@@ -166,9 +192,10 @@ DQ_API int dq_kv4_append(const void* k, const void* v, int type, long long k_row
         (n_kv > 1 && (k_head_stride % quad || v_head_stride % quad)))
         return DQ_ERR_ALIGN;
     dq::Kv4AppendArgs a{k, v, k_row_stride, k_head_stride, v_row_stride, v_head_stride, slots,
-                        static_cast<unsigned char*>(pool), rows, {n_kv, n_pages, page_size}, dqhost::device_error_flag()};
-    const long long blocks = (2ll * rows * n_kv + dq::KV4_WARPS - 1) / dq::KV4_WARPS;
-    if (blocks > 0x7fffffffll)
+                        static_cast<unsigned char*>(pool), rows, {n_kv, n_pages, page_size}, dqhost::fast_divisor(n_kv),
+                        dqhost::fast_divisor(page_size), dqhost::device_error_flag()};
+    const long long items = (static_cast<long long>(rows) + 1) / 2 * n_kv, blocks = (items + dq::KV4_WARPS - 1) / dq::KV4_WARPS;
+    if (items > 0x7fffff00ll)
         return DQ_ERR_UNSUPPORTED;
     cudaError_t e = dqhost::with_type(type, [&](auto* t) {
         dq::kv4_append_kernel<std::remove_pointer_t<decltype(t)>>
@@ -190,10 +217,11 @@ DQ_API int dq_kv4_read(const void* pool, const int* slots, int type, void* k_out
         return st;
     if (!dqhost::aligned16(pool) || !dqhost::aligned16(k_out) || !dqhost::aligned16(v_out))
         return DQ_ERR_ALIGN;
-    dq::Kv4ReadArgs a{static_cast<const unsigned char*>(pool), slots, rows, {n_kv, n_pages, page_size},
-                      dqhost::device_error_flag()};
-    const long long blocks = (static_cast<long long>(rows) * n_kv + dq::KV4_WARPS - 1) / dq::KV4_WARPS;
-    if (blocks > 0x7fffffffll)
+    dq::Kv4ReadArgs a{static_cast<unsigned char*>(const_cast<void*>(pool)), slots, rows, {n_kv, n_pages, page_size},
+                      dqhost::fast_divisor(n_kv), dqhost::fast_divisor(page_size), dqhost::device_error_flag()};
+    const long long items = static_cast<long long>(rows) * n_kv;
+    const long long blocks = (items + 2 * dq::KV4_WARPS - 1) / (2 * dq::KV4_WARPS);
+    if (items > 0x7fffff00ll)
         return DQ_ERR_UNSUPPORTED;
     cudaError_t e = dqhost::with_type(type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;

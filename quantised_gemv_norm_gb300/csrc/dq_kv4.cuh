@@ -13,10 +13,11 @@ constexpr int KV4_VCODES = 1024, KV4_KSCALES = 2048, KV4_VSCALES = 2304;
 
 // Byte offset of the 32-bit word with the 8 key codes of row j, dims 32 g + 8 t ...
 __device__ __forceinline__ int kv4_key_word(int j, int t, int g) { return 64 * j + 4 * (4 * t + g); }
-// Byte offset of the 16-bit half with the 4 value codes of row j, dims 32 g + 4 r ...
-__device__ __forceinline__ int kv4_value_half(int j, int r, int g)
+// Byte offset of the 16-bit half with the 4 value codes of row j, dims 32 g + 8 t ...
+// (r = 2 t); the half of the next 4 dims is 64 bytes further.
+__device__ __forceinline__ int kv4_value_half(int j, int t, int g)
 {
-    return KV4_VCODES + 512 * (j >> 3) + 16 * (4 * r + ((j >> 1) & 3)) + 4 * g + 2 * (j & 1);
+    return KV4_VCODES + 512 * (j >> 3) + 16 * (8 * t + ((j >> 1) & 3)) + 4 * g + 2 * (j & 1);
 }
 // Byte offset of row j's d for dims 32 g ...; z is 4 bytes further.
 __device__ __forceinline__ int kv4_scale(int base, int j, int g) { return base + 32 * (j >> 1) + 8 * g + 2 * (j & 1); }
@@ -24,12 +25,6 @@ __device__ __forceinline__ int kv4_scale(int base, int j, int g) { return base +
 struct Kv4Shape {
     int n_kv, n_pages, page_rows;  // page_rows: rows a page, a multiple of 16
 };
-
-// The block of row `slot` (page * page_rows + offset) of head g.
-__device__ __forceinline__ size_t kv4_block(const Kv4Shape& s, int page, int offset, int g)
-{
-    return ((static_cast<size_t>(page) * s.n_kv + g) * (s.page_rows / KV4_ROWS) + offset / KV4_ROWS) * KV4_BYTES;
-}
 
 }  // namespace dq
 

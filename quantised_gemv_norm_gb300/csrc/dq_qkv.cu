@@ -2,8 +2,12 @@
 // (dq_qkv_rope): the Qwen3 inputs of dq_attention_decode_rope for a prompt's or a
 // batch's rows, with the values converted beside them.
 //
-// One warp takes one head of one row, four dims a lane: the head's sum of squares
-// is one warp reduction, a dim's rotation partner sits 16 lanes away.
+// Half a warp takes one head, a warp eight heads of one row: lane i of 16 holds dims
+// 4 i .. 4 i + 3 and 64 + 4 i .., so a rotation's two dims are in one lane, the sum of
+// squares of two heads is four shuffles, and the row's angles are loaded once.  All
+// eight heads' loads are issued first.  Memory bounds it (8191 rows of 48 heads, 306
+// MB; one warp a head, with the partner dims 16 lanes away and divisions for the
+// index, was bound by its 150 instructions: 80 us).
 #include "dq_attn.cuh"
 #include "dq_types.cuh"
 
@@ -18,37 +22,75 @@ struct QkvArgs {
     const float2* rope;
     float eps;
     int rows, n_q, n_kv, max_ctx;
+    FastDiv by_chunks;  // warps a row
     int* err;
 };
 
 constexpr int QKV_WARPS = 8;
+constexpr int QKV_PAIRS = 4;  // pairs of heads a warp
 
 template <typename T>
-__global__ void __launch_bounds__(32 * QKV_WARPS) qkv_rope_kernel(QkvArgs a, T* __restrict__ q, T* __restrict__ k,
+__global__ void __launch_bounds__(32 * QKV_WARPS) qkv_rope_kernel(const QkvArgs a, T* __restrict__ q, T* __restrict__ k,
                                                                   T* __restrict__ v)
 {
-    const int lane = threadIdx.x & 31;
-    const int heads = a.n_q + 2 * a.n_kv;
-    const long long item = static_cast<long long>(blockIdx.x) * QKV_WARPS + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(a.rows) * heads)
+    const int lane = threadIdx.x & 31, half = lane >> 4, i = lane & 15;
+    const uint32_t item = blockIdx.x * QKV_WARPS + (threadIdx.x >> 5);
+    const uint32_t row = fast_div(item, a.by_chunks), chunk = item - row * a.by_chunks.d;
+    if (row >= static_cast<uint32_t>(a.rows))
         return;
-    const int row = static_cast<int>(item / heads), h = static_cast<int>(item % heads);
     const int pos = __ldg(a.pos + row);
     if (pos < 0 || pos >= a.max_ctx) {
         if (pos >= 0 && lane == 0)
             set_error(a.err, DEVERR_BAD_ARG);
         return;
     }
-    float4 x = load4(a.qkv + row * a.ld + static_cast<long long>(h) * ATT_HD + 4 * lane);
-    T* out = h < a.n_q ? q + (static_cast<size_t>(row) * a.n_q + h) * ATT_HD
-             : h < a.n_q + a.n_kv ? k + (static_cast<size_t>(row) * a.n_kv + (h - a.n_q)) * ATT_HD
-                                  : v + (static_cast<size_t>(row) * a.n_kv + (h - a.n_q - a.n_kv)) * ATT_HD;
-    if (h < a.n_q + a.n_kv) {
-        const float2* cs = a.rope + static_cast<size_t>(pos) * (ATT_HD / 2);
-        const float* w = h < a.n_q ? a.q_norm : a.k_norm;
-        x = w ? head_norm_rope(x, load_norm_rope(w, cs, lane), a.eps, lane) : head_rope(x, cs, lane);
+    const int heads = a.n_q + 2 * a.n_kv, turned = a.n_q + a.n_kv, h0 = 2 * QKV_PAIRS * chunk + half;
+    const float* src = a.qkv + row * a.ld + 4 * i;
+    float4 x[QKV_PAIRS], y[QKV_PAIRS];
+#pragma unroll
+    for (int p = 0; p < QKV_PAIRS; ++p) {
+        const int h = h0 + 2 * p;
+        if (h < heads) {
+            x[p] = __ldcs(reinterpret_cast<const float4*>(src + h * ATT_HD));
+            y[p] = __ldcs(reinterpret_cast<const float4*>(src + h * ATT_HD + 64));
+        }
     }
-    store4(out + 4 * lane, x);
+    const float4* cs = reinterpret_cast<const float4*>(a.rope + static_cast<size_t>(pos) * (ATT_HD / 2) + 4 * i);
+    const float4 c01 = __ldg(cs), c23 = __ldg(cs + 1);  // cos, sin, cos, sin
+#pragma unroll
+    for (int p = 0; p < QKV_PAIRS; ++p) {
+        const int h = h0 + 2 * p;
+        if (a.q_norm && h - half < turned) {  // not for a pair of value heads
+            float s = 0.f;
+            if (h < turned)
+                s = (x[p].x * x[p].x + x[p].y * x[p].y + x[p].z * x[p].z + x[p].w * x[p].w) +
+                    (y[p].x * y[p].x + y[p].y * y[p].y + y[p].z * y[p].z + y[p].w * y[p].w);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (h < turned) {
+                const float r = rsqrtf(s * (1.0f / ATT_HD) + a.eps);
+                const float4* w = reinterpret_cast<const float4*>(h < a.n_q ? a.q_norm : a.k_norm) + i;
+                const float4 u = __ldg(w), t = __ldg(w + 16);
+                x[p] = make_float4(x[p].x * r * u.x, x[p].y * r * u.y, x[p].z * r * u.z, x[p].w * r * u.w);
+                y[p] = make_float4(y[p].x * r * t.x, y[p].y * r * t.y, y[p].z * r * t.z, y[p].w * r * t.w);
+            }
+        }
+        if (h >= heads)
+            continue;
+        T* out = h < a.n_q   ? q + (static_cast<size_t>(row) * a.n_q + h) * ATT_HD
+                 : h < turned ? k + (static_cast<size_t>(row) * a.n_kv + (h - a.n_q)) * ATT_HD
+                              : v + (static_cast<size_t>(row) * a.n_kv + (h - turned)) * ATT_HD;
+        if (h < turned) {
+            const float4 b = x[p], c = y[p];
+            x[p] = make_float4(fmaf(b.x, c01.x, -(c.x * c01.y)), fmaf(b.y, c01.z, -(c.y * c01.w)),
+                               fmaf(b.z, c23.x, -(c.z * c23.y)), fmaf(b.w, c23.z, -(c.w * c23.w)));
+            y[p] = make_float4(fmaf(c.x, c01.x, b.x * c01.y), fmaf(c.y, c01.z, b.y * c01.w),
+                               fmaf(c.z, c23.x, b.z * c23.y), fmaf(c.w, c23.z, b.w * c23.w));
+        }
+        store4(out + 4 * i, x[p]);
+        store4(out + 64 + 4 * i, y[p]);
+    }
 }
 
 }  // namespace dq
@@ -73,10 +115,13 @@ DQ_API int dq_qkv_rope(const float* qkv, long long row_stride, const int* positi
         !dqhost::aligned16(k_norm))
         return DQ_ERR_ALIGN;
     dq::QkvArgs a{qkv,  row_stride, positions, q_norm,  k_norm, reinterpret_cast<const float2*>(rope_table), eps,
-                  rows, n_q,        n_kv,      max_ctx, dqhost::device_error_flag()};
-    const long long blocks = (rows * heads + dq::QKV_WARPS - 1) / dq::QKV_WARPS;
-    if (blocks > 0x7fffffffll)
+                  rows, n_q,        n_kv,      max_ctx};
+    const int chunks = static_cast<int>((heads + 2 * dq::QKV_PAIRS - 1) / (2 * dq::QKV_PAIRS));
+    const long long items = static_cast<long long>(rows) * chunks, blocks = (items + dq::QKV_WARPS - 1) / dq::QKV_WARPS;
+    if (items > 0x7fffff00ll)
         return DQ_ERR_UNSUPPORTED;
+    a.by_chunks = dqhost::fast_divisor(chunks);
+    a.err = dqhost::device_error_flag();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = dqhost::with_type(type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;

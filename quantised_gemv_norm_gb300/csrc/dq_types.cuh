@@ -4,6 +4,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "dq_common.cuh"
 
 namespace dq {
@@ -33,6 +35,45 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, const __nv_bfloat16*
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// Eight consecutive elements (16-byte aligned), one or two 16-byte accesses.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8])
+{
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8])
+{
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (std::is_same<T, __half>::value) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            x[2 * i] = v.x, x[2 * i + 1] = v.y;
+        } else {
+            x[2 * i] = bf16lo(w[i]), x[2 * i + 1] = bf16hi(w[i]);
+        }
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8])
+{
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8])
+{
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2(x[0], x[1], p), pack2(x[2], x[3], p), pack2(x[4], x[5], p), pack2(x[6], x[7], p));
+}
+
+// n / d for 0 <= n < 2^31 and a divisor known to the host: two instructions.
+struct FastDiv {
+    uint32_t mul, shift, d;
+};
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, const FastDiv& f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
 
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 template <typename T>
@@ -88,6 +129,14 @@ __device__ __forceinline__ float ex2(float x)
 }  // namespace dq
 
 namespace dqhost {
+
+inline dq::FastDiv fast_divisor(uint32_t d)  // 1 <= d < 2^31
+{
+    uint32_t shift = 0;
+    while ((1ull << shift) < d)
+        ++shift;
+    return {static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1), shift, d};
+}
 
 inline bool valid_type(int t) { return t == DQ_TYPE_F32 || t == DQ_TYPE_F16 || t == DQ_TYPE_BF16; }
 inline int type_bytes(int t) { return t == DQ_TYPE_F32 ? 4 : 2; }

@@ -111,7 +111,8 @@ def test_qkv_rope_leaves_padding_rows_and_reports_far_positions(dq):
 
 
 def test_qkv_rope_matches_the_single_token_attention_inputs(dq):
-    # attention_decode_rope writes the same key row: fp16 of the same fp32 steps
+    # attention_decode_rope writes the same key row; the squares are summed in another order, so a value
+    # next to a border between two fp16 numbers may round to either: one step apart
     g = gen(4)
     x = randn(g, 1, 48 * HD)
     wq, wk = 1 + 0.1 * randn(g, HD), 1 + 0.1 * randn(g, HD)
@@ -120,7 +121,8 @@ def test_qkv_rope_matches_the_single_token_attention_inputs(dq):
     planes = torch.zeros(2, 8, 64, HD, dtype=torch.float16, device="cuda")
     dq.attention_decode_rope(x[0, :32 * HD].reshape(32, HD), x[0, 32 * HD:40 * HD].reshape(8, HD), planes[0], planes[1],
                              wq, wk, table, 1)
-    assert torch.equal(planes[0, :, 0], k[0])
+    a, b = planes[0, :, 0].double(), k[0].double()
+    assert bool(((a - b).abs() <= 2 * U[torch.float16] * b.abs() + 2 * TINY).all())
 
 
 # ------------------------------------------------------------------ prompt
