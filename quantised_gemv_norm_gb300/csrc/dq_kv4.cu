@@ -41,48 +41,66 @@ __device__ __forceinline__ unsigned char* kv4_find(unsigned char* pool, const Kv
     return pool + ((static_cast<size_t>(page) * s.n_kv + g) * (s.page_rows / KV4_ROWS) + off / KV4_ROWS) * KV4_BYTES;
 }
 
-// d, z and eight codes (0..15) of a lane's dims; the group is the lane and its three
-// neighbours.  Extremes, d, z and x - z are the format's IEEE operations.  The quotient
-// is a product with 1 / d, off by less than 1e-5 where it is below 16: only within
-// that of a half can the rounding differ from the quotient's own, and there the
-// division is done.
-__device__ __forceinline__ void kv4_quantise(const float (&x)[8], float& d, float& z, uint32_t (&code)[8])
+__device__ __forceinline__ float min_nan(float a, float b)
 {
-    float lo = x[0], hi = x[0], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        sum = fmaf(x[i], 0.f, sum);  // 0, or NaN from an infinity or NaN, which fminf and fmaxf may pass over
-    }
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// d, z and eight codes of a lane's dims, code i at bits SHIFT(i) of the word; the group
+// is the lane and its three neighbours.  Extremes, d, z and x - z are the format's IEEE
+// operations.  The quotient is a product with 1 / d, off by less than 1e-5 where it is
+// below 16: only within that of a half can the rounding differ from the quotient's own,
+// and there the division is done.
+template <typename Shift>
+__device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], float& d, float& z, Shift shift)
+{
+    float lo = min_nan(min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), min_nan(min_nan(x[4], x[5]), min_nan(x[6], x[7])));
+    float hi = max_nan(max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])), max_nan(max_nan(x[4], x[5]), max_nan(x[6], x[7])));
 #pragma unroll
     for (int o = 2; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     d = __half2float(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)));
     z = __half2float(__float2half_rn(__fadd_rn(lo, 8.0f * d)));
-    if (!(sum == 0.f) || !(d <= 65504.f) || !(fabsf(z) <= 65504.f))
+    if (!(d <= 65504.f) || !(fabsf(z) <= 65504.f))  // also an infinity or NaN among them
         d = z = __int_as_float(0x7fc00000);
-    const float inv = d > 0.f ? __frcp_rn(d) : 0.f;  // 0 or NaN: every code is 8
+    const float inv = d > 0.f ? __frcp_rn(d) : 0.f;
     constexpr float M = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, halves to even
+    const uint64_t z2 = f2(-z, -z), inv2 = f2(inv, inv), eight = f2(8.f, 8.f), m2 = f2(M, M), nm2 = f2(-M, -M);
+    uint32_t word = 0, base = 0;
     float off = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float t = fmaf(__fsub_rn(x[i], z), inv, 8.f);
-        t = d > 0.f ? fminf(fmaxf(t, 0.f), 15.f) : 8.f;
-        const float u = __fadd_rn(t, M);
-        off = fmaxf(off, fabsf(t - __fsub_rn(u, M)));
-        code[i] = __float_as_uint(u) & 15u;
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = un2(fma2(add2(f2(x[2 * i], x[2 * i + 1]), z2), inv2, eight));
+        const uint64_t c = f2(fminf(fmaxf(t.x, 0.f), 15.f), fminf(fmaxf(t.y, 0.f), 15.f));
+        const uint64_t u = add2(c, m2);
+        const float2 e = un2(fma2(add2(u, nm2), f2(-1.f, -1.f), c)), bits = un2(u);
+        off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
+        // the integer in M's low mantissa bits, M's own bits taken off at the end
+        word += __float_as_uint(bits.x) << shift(2 * i);
+        word += __float_as_uint(bits.y) << shift(2 * i + 1);
+        base += 0x4B400000u << shift(2 * i);
+        base += 0x4B400000u << shift(2 * i + 1);
     }
+    word -= base;
     if (off > 0.49998f) {
+        word = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float t = rintf(__fdiv_rn(__fsub_rn(x[i], z), d)) + 8.f;
-            code[i] = static_cast<uint32_t>(fminf(fmaxf(t, 0.f), 15.f));
+            word |= static_cast<uint32_t>(fminf(fmaxf(t, 0.f), 15.f)) << shift(i);
         }
     }
+    return word;
 }
 
 template <typename T>
@@ -103,27 +121,18 @@ __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_append_kernel(const Kv4App
         load8(static_cast<const T*>(a.k) + row * a.k_row + g * a.k_head + 8 * dim, x[0]);
         load8(static_cast<const T*>(a.v) + row * a.v_row + g * a.v_head + 8 * dim, x[1]);
     }
-#pragma unroll
-    for (int value = 0; value < 2; ++value) {
-        float d, z;
-        uint32_t c[8];
-        kv4_quantise(x[value], d, z, c);
-        if (!b)
-            continue;
-        if (value) {
-            unsigned short* p = reinterpret_cast<unsigned short*>(b + kv4_value_half(j, t, grp));
-            p[0] = static_cast<unsigned short>(c[0] | c[1] << 4 | c[2] << 8 | c[3] << 12);
-            p[32] = static_cast<unsigned short>(c[4] | c[5] << 4 | c[6] << 8 | c[7] << 12);
-        } else {
-            *reinterpret_cast<uint32_t*>(b + kv4_key_word(j, t, grp)) = (c[0] | c[2] << 4 | c[4] << 8 | c[6] << 12) |
-                                                                        (c[1] | c[3] << 4 | c[5] << 8 | c[7] << 12) << 16;
-        }
-        if (t == 0) {
-            __half* p = reinterpret_cast<__half*>(b + kv4_scale(value ? KV4_VSCALES : KV4_KSCALES, j, grp));
-            p[0] = __float2half_rn(d);
-            p[2] = __float2half_rn(z);
-        }
-    }
+    float kd, kz, vd, vz;
+    const uint32_t kw = kv4_quantise(x[0], kd, kz, [](int i) { return 4 * (i >> 1) + 16 * (i & 1); });
+    const uint32_t vw = kv4_quantise(x[1], vd, vz, [](int i) { return 4 * i; });
+    if (!b)
+        return;
+    *reinterpret_cast<uint32_t*>(b + kv4_key_word(j, t, grp)) = kw;
+    unsigned short* p = reinterpret_cast<unsigned short*>(b + kv4_value_half(j, t, grp));
+    p[0] = static_cast<unsigned short>(vw);
+    p[32] = static_cast<unsigned short>(vw >> 16);
+    // the four scales of a group, one a lane: d and z of the key, d and z of the value
+    *reinterpret_cast<__half*>(b + kv4_scale(t & 2 ? KV4_VSCALES : KV4_KSCALES, j, grp) + 4 * (t & 1)) =
+        __float2half_rn(t & 2 ? (t & 1 ? vz : vd) : (t & 1 ? kz : kd));
 }
 
 struct Kv4ReadArgs {
@@ -152,19 +161,20 @@ __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_read_kernel(const Kv4ReadA
     const __half* ks = reinterpret_cast<const __half*>(b + kv4_scale(KV4_KSCALES, j, grp));
     const __half* vs = reinterpret_cast<const __half*>(b + kv4_scale(KV4_VSCALES, j, grp));
     const float kd = __half2float(ks[0]), kz = __half2float(ks[2]), vd = __half2float(vs[0]), vz = __half2float(vs[2]);
-    // c under 2^23's mantissa is 2^23 + c exactly
-    auto value = [](uint32_t w, int bit, float d, float z) {
-        return fmaf(d, __uint_as_float(((w >> bit) & 15u) | 0x4B000000u) - 8388616.f, z);
+    // a code at bits n .. n + 3 (n < 20) under 2^23 is 2^23 + 2^n c exactly, and d 2^-n exact
+    auto value = [](uint32_t w, int n, float d, float z) {
+        const float s = static_cast<float>(1 << n);
+        return fmaf(d * (1.f / s), __uint_as_float((w & (15u << n)) | 0x4B000000u) - (8388608.f + 8.f * s), z);
     };
     const size_t at = static_cast<size_t>(item) * ATT_HD + 8 * dim;
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        x[i] = value(kw, 4 * (i >> 1) + 16 * (i & 1), kd, kz);
+        x[i] = value(i & 1 ? kw >> 16 : kw, 4 * (i >> 1), kd, kz);
     store8(k + at, x);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        x[i] = value(vw, 4 * i, vd, vz);
+        x[i] = value(i & 4 ? vw >> 16 : vw, 4 * (i & 3), vd, vz);
     store8(v + at, x);
 }
 

@@ -25,6 +25,7 @@
 namespace dq {
 
 constexpr int KA_WARPS = 4;
+constexpr int KA_JOIN = 4;     // warps that join a head's splits
 constexpr int KA_STEP = 2;     // cache blocks a ring stage
 constexpr int KA_NS = 2;       // ring stages a warp
 constexpr int KA_RESIDENT = 3; // blocks an SM (4, at 128 registers: 96.5 against 94.0 us, 48 sequences)
@@ -92,6 +93,22 @@ __device__ __forceinline__ void ka_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
+// The same in place.
+__device__ __forceinline__ void ka_mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d += m, rounded.
+__device__ __forceinline__ void ka_add(float (&d)[4], const float (&m)[4])
+{
+    const float2 x = un2(add2(f2(d[0], d[1]), f2(m[0], m[1]))), y = un2(add2(f2(d[2], d[3]), f2(m[2], m[3])));
+    d[0] = x.x, d[1] = x.y, d[2] = y.x, d[3] = y.y;
+}
+
 // A row's result: the product of its first part and, with two, of its second.
 template <bool TWO>
 __device__ __forceinline__ uint64_t ka_both(const float (&d)[4])
@@ -122,6 +139,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
     __shared__ uint64_t full[KA_WARPS][KA_NS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = lane >> 2, tq = lane & 3;  // this lane's head of the group, and quarter
+    pdl_trigger();
     int x = blockIdx.x;
     const int c = x % a.splits;
     x /= a.splits;
@@ -242,13 +260,16 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
     const uint32_t k1024 = ka_opaque(0x64006400u), k64 = ka_opaque(0x54005400u);
     const uint32_t odd = (h & 1) ? 0x7632u : 0x5410u;  // the halves of key h of a pair
 
-    uint64_t o[4][4];  // group k, i: dim 32 k + 4 h + i of the group's heads 2 tq and 2 tq + 1
-    uint64_t zacc = 0ull, lacc = 0ull;  // z: group h & 3 of heads 2 tq and 2 tq + 1; l: head h
+    // group k, pair j: dims 32 k + 4 h + 2 j of the group's heads 2 tq and 2 tq + 1, then
+    // dims 32 k + 4 h + 2 j + 1 of the same
+    float o[4][2][4];
+    float zacc[4] = {0.f, 0.f, 0.f, 0.f};  // group h & 3 of heads 2 tq and 2 tq + 1, twice
+    uint64_t lacc = 0ull;                  // head h
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[k][i] = 0ull;
+        for (int i = 0; i < 8; ++i)
+            o[k][i >> 2][i & 3] = 0.f;
     float r = -INFINITY, cap = KA_CAP;
 
     // the zero accumulator operand, kept in registers: as a constant it would be written
@@ -342,13 +363,14 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             }
             __syncwarp();
             lacc = mul2(lacc, f2(f, f));
-            const uint64_t ff = f2(__shfl_sync(0xffffffffu, f, 8 * tq), __shfl_sync(0xffffffffu, f, 8 * tq + 4));
-            zacc = mul2(zacc, ff);
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * tq), f1 = __shfl_sync(0xffffffffu, f, 8 * tq + 4);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int e = 0; e < 4; ++e) {
+                zacc[e] *= e & 1 ? f1 : f0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    o[k][j] = mul2(o[k][j], ff);
+                for (int k = 0; k < 8; ++k)
+                    o[k >> 1][k & 1][e] *= e & 1 ? f1 : f0;
+            }
         }
         const float2 e0 = un2(fma2(s[0], f2(unscale, unscale), f2(-r, -r)));
         const float2 e1 = un2(fma2(s[1], f2(unscale, unscale), f2(-r, -r)));
@@ -361,11 +383,14 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             ka_split<TWO>(p1, h1, l1);
             const unsigned char* zs = kb + KV4_VSCALES + 32 * tq + 8 * (h & 3) + 4;
             const uint32_t z0 = lds32(zs), z1 = lds32(zs + 128);
-            float m[4], m2[4];
-            ka_mma(m, z0, z0, z1, z1, h0, h1, zz[0], zz[1], zz[2], zz[3]);
-            if (TWO)
+            if (TWO) {
+                float m[4], m2[4];
+                ka_mma(m, z0, z0, z1, z1, h0, h1, zz[0], zz[1], zz[2], zz[3]);
                 ka_mma(m2, z0, z0, z1, z1, l0, l1, m[0], m[1], m[2], m[3]);
-            zacc = add2(zacc, TWO ? f2(m2[0], m2[1]) : f2(m[0], m[1]));
+                ka_add(zacc, m2);
+            } else {
+                ka_mma_add(zacc, z0, z0, z1, z1, h0, h1);
+            }
         }
         const uint4 va = lds128(kb + KV4_VCODES + 16 * lane), vb = lds128(kb + KV4_VCODES + 512 + 16 * lane);
         const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
@@ -380,15 +405,17 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // 16 dims (i = 2 j in A's first 8 rows, 2 j + 1 in the others) by 16 keys, times
-                // 16 keys by 8 heads.  The sums over blocks are rounded adds: the matrix
-                // instruction's own accumulation cuts off (100001 keys: relative error 1.6e-6
-                // with it, 4.1e-7 so)
-                float m[4], m2[4];
-                ka_mma(m, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], h0, h1, zz[0], zz[1], zz[2], zz[3]);
-                if (TWO)
+                // 16 keys by 8 heads.  For fp32 results the sums over blocks are rounded adds:
+                // the matrix instruction's own accumulation cuts off (100001 keys: relative error
+                // 1.6e-6 with it, 4.1e-7 so)
+                if (TWO) {
+                    float m[4], m2[4];
+                    ka_mma(m, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], h0, h1, zz[0], zz[1], zz[2], zz[3]);
                     ka_mma(m2, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], l0, l1, m[0], m[1], m[2], m[3]);
-                o[k][2 * j] = add2(o[k][2 * j], TWO ? f2(m2[0], m2[1]) : f2(m[0], m[1]));
-                o[k][2 * j + 1] = add2(o[k][2 * j + 1], TWO ? f2(m2[2], m2[3]) : f2(m[2], m[3]));
+                    ka_add(o[k][j], m2);
+                } else {
+                    ka_mma_add(o[k][j], b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], h0, h1);
+                }
             }
         }
     };
@@ -432,7 +459,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
     float* meet = reinterpret_cast<float*>(ring);
     static_assert(sizeof(ring) >= KA_WARPS * 8 * KA_PART * 4, "the ring holds the warps' results");
     {
-        const float2 l2 = un2(lacc), z2 = un2(zacc);
+        const float2 l2 = un2(lacc);
         float l = l2.x + l2.y;
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -443,11 +470,11 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float za = __shfl_sync(0xffffffffu, z2.x, 4 * k + tq), zb = __shfl_sync(0xffffffffu, z2.y, 4 * k + tq);
-            const float2 y0 = un2(o[k][0]), y1 = un2(o[k][1]), y2 = un2(o[k][2]), y3 = un2(o[k][3]);
+            const float za = __shfl_sync(0xffffffffu, zacc[0], 4 * k + tq), zb = __shfl_sync(0xffffffffu, zacc[1], 4 * k + tq);
+            const float(&x)[4] = o[k][0], (&y)[4] = o[k][1];
             float* at = mp + 2 * tq * KA_PART + 4 + 32 * k + 4 * h;
-            *reinterpret_cast<float4*>(at) = make_float4(y0.x + za, y1.x + za, y2.x + za, y3.x + za);
-            *reinterpret_cast<float4*>(at + KA_PART) = make_float4(y0.y + zb, y1.y + zb, y2.y + zb, y3.y + zb);
+            *reinterpret_cast<float4*>(at) = make_float4(x[0] + za, x[2] + za, y[0] + za, y[2] + za);
+            *reinterpret_cast<float4*>(at + KA_PART) = make_float4(x[1] + zb, x[3] + zb, y[1] + zb, y[3] + zb);
         }
     }
     __syncthreads();
@@ -485,35 +512,79 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
     }
 }
 
-// The splits' results of one sequence and query head: one warp, four dims a lane.
+// The splits' results of one sequence and query head, four dims a lane: each warp adds
+// up every KA_JOIN-th split with a running maximum, four at a time so that their loads
+// are in flight together, then the warps' sums meet.
 template <typename T>
-__global__ void __launch_bounds__(32) kv4_join_kernel(const Kv4AttnArgs a)
+__global__ void __launch_bounds__(32 * KA_JOIN) kv4_join_kernel(const Kv4AttnArgs a)
 {
-    const int lane = threadIdx.x;
+    __shared__ float ml[KA_JOIN][2];
+    __shared__ float4 sums[KA_JOIN][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x / a.n_q, hq = blockIdx.x % a.n_q, g = hq / a.group, h = hq % a.group;
     int n = __ldg(a.n_keys + b);
     if (n < 0 || n > a.max_keys)
         n = 0;
     const int blocks = (n + KV4_ROWS - 1) / KV4_ROWS, splits = (blocks + a.chunk - 1) / a.chunk;
     const float* base = a.part + ((static_cast<size_t>(b) * a.s.n_kv + g) * a.splits * 8 + h) * KA_PART;
-    const size_t step = 8 * KA_PART;
+    constexpr size_t step = 8 * KA_PART;
     pdl_wait();
-    float m = -INFINITY;
-    for (int c = lane; c < splits; c += 32)
-        m = fmaxf(m, __ldcg(base + c * step));
-    m = warp_max(m);
-    float l = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < splits; ++c) {
-        const float* pp = base + c * step;
-        const float2 rl = __ldcg(reinterpret_cast<const float2*>(pp));
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(pp + 4) + lane);
-        const float f = rl.x == m ? 1.f : ex2(rl.x - m);
-        l += f * rl.y;
-        v.x += f * y.x;
-        v.y += f * y.y;
-        v.z += f * y.z;
-        v.w += f * y.w;
+    for (int c0 = warp; c0 < splits; c0 += 4 * KA_JOIN) {
+        float2 rl[4];
+        float4 y[4];
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + KA_JOIN * i;
+            rl[i] = make_float2(-INFINITY, 0.f);
+            y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < splits) {
+                const float* pp = base + c * step;
+                rl[i] = __ldcg(reinterpret_cast<const float2*>(pp));
+                y[i] = __ldcg(reinterpret_cast<const float4*>(pp + 4) + lane);
+            }
+            top = fmaxf(top, rl[i].x);
+        }
+        // equal references (also two of -infinity) have the weight 1
+        const float f = m == top ? 1.f : ex2(m - top);
+        m = top;
+        l *= f;
+        v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float w = rl[i].x == m ? 1.f : ex2(rl[i].x - m);
+            l = fmaf(w, rl[i].y, l);
+            v.x = fmaf(w, y[i].x, v.x);
+            v.y = fmaf(w, y[i].y, v.y);
+            v.z = fmaf(w, y[i].z, v.z);
+            v.w = fmaf(w, y[i].w, v.w);
+        }
+    }
+    if (lane == 0) {
+        ml[warp][0] = m;
+        ml[warp][1] = l;
+    }
+    sums[warp][lane] = v;
+    __syncthreads();
+    if (warp)
+        return;
+    float top = m;
+#pragma unroll
+    for (int w = 1; w < KA_JOIN; ++w)
+        top = fmaxf(top, ml[w][0]);
+    l = 0.f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < KA_JOIN; ++w) {
+        const float f = ml[w][0] == top ? 1.f : ex2(ml[w][0] - top);
+        const float4 y = sums[w][lane];
+        l = fmaf(f, ml[w][1], l);
+        v.x = fmaf(f, y.x, v.x);
+        v.y = fmaf(f, y.y, v.y);
+        v.z = fmaf(f, y.z, v.z);
+        v.w = fmaf(f, y.w, v.w);
     }
     const float inv = n > 0 && l != 0.f ? 1.0f / l : 0.f;
     store4(static_cast<T*>(a.out) + (static_cast<size_t>(b) * a.n_q + hq) * ATT_HD + 4 * lane,
@@ -530,14 +601,28 @@ struct Kv4Split {
     int chunk, splits;
 };
 
+// A thread block costs about two microseconds beside its keys, and a split's result
+// is written and read back.  So: 16 blocks (256 keys) or fewer are not split (1 x 256
+// keys: 5.5 us, 5.9 in two); where sequences and KV heads alone fill the card, splits
+// hold 512 keys or more (32 x 500: 10.4 us, 16 with 128 keys); else the work is spread
+// over two blocks an SM in splits of 128 to 512 keys (1 x 2000: 6.4 us, 9.8 with 512; 1
+// x 16000: 13.1 us with 512, 14.4 with 288), and more than that over the three that are
+// resident.  A batch's splits end at 1024 keys, so that sequences of different lengths
+// share the card evenly.
 static Kv4Split kv4_split(int n_seq, int n_kv, int max_keys)
 {
     const long long blocks = (static_cast<long long>(max_keys) + dq::KV4_ROWS - 1) / dq::KV4_ROWS;
-    const long long all = blocks * n_seq * n_kv, room = static_cast<long long>(dq::KA_RESIDENT) * sm_count();
-    long long chunk = (all + room - 1) / room;
+    const long long pairs = static_cast<long long>(n_seq) * n_kv, all = blocks * pairs, sms = sm_count();
+    if (blocks <= 16)
+        return {static_cast<int>(blocks), 1};
+    long long chunk = (all + 2 * sms - 1) / (2 * sms);
+    if (chunk > 32)
+        chunk = std::max((all + dq::KA_RESIDENT * sms - 1) / (dq::KA_RESIDENT * sms), 32ll);
+    chunk = std::max(chunk, pairs >= sms ? 32ll : 8ll);
     if (n_seq > 1)
         chunk = std::min(chunk, 64ll);
-    chunk = std::max<long long>(chunk, dq::KA_WARPS * dq::KA_STEP);
+    const long long round = dq::KA_WARPS * dq::KA_STEP;  // what the block's warps take at a time
+    chunk = (chunk + round - 1) / round * round;
     return {static_cast<int>(chunk), static_cast<int>((blocks + chunk - 1) / chunk)};
 }
 
@@ -589,9 +674,20 @@ DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, co
     cudaError_t e = dqhost::with_type(type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
         dq::kv4_attn_kernel<T><<<static_cast<unsigned>(blocks), 32 * dq::KA_WARPS, 0, s>>>(a);
-        if (sp.splits > 1)
-            dq::kv4_join_kernel<T><<<n_seq * n_q, 32, 0, s>>>(a);
-        return cudaGetLastError();
+        cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess || sp.splits == 1)
+            return err;
+        // a dependent launch: its blocks are there when the last of the first kernel's end
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(n_seq) * n_q);
+        cfg.blockDim = dim3(32 * dq::KA_JOIN);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, dq::kv4_join_kernel<T>, a);
     });
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }

@@ -57,10 +57,19 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8])
         }
     }
 }
+// store8 is called by both lanes of a pair (2 i, 2 i + 1) for 16 consecutive elements: in
+// fp32 they trade halves, so that each 16-byte access of the two fills a sector.
 __device__ __forceinline__ void store8(float* p, const float (&x)[8])
 {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    const bool odd = threadIdx.x & 1;
+    const unsigned pair = 3u << (threadIdx.x & 30);
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = __shfl_xor_sync(pair, odd ? x[i] : x[4 + i], 1);
+    float4* at = reinterpret_cast<float4*>(p) - (odd ? 1 : 0);
+    at[0] = odd ? make_float4(y[0], y[1], y[2], y[3]) : make_float4(x[0], x[1], x[2], x[3]);
+    at[2] = odd ? make_float4(x[4], x[5], x[6], x[7]) : make_float4(y[0], y[1], y[2], y[3]);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8])
