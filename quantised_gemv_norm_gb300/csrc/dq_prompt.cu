@@ -347,10 +347,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     tmem_ld32(ts + 96, s + 96);
                 }
                 if (j >= jclean) {
+                    // a warp's rows end within 32 keys of one another: most runs of 16 are seen by
+                    // all of them
 #pragma unroll
-                    for (int i = 64 * q; i < 64 * q + 64; ++i)
-                        if (i >= left)
-                            s[i] = 0xff800000u;  // -infinity
+                    for (int i0 = 64 * q; i0 < 64 * q + 64; i0 += 16)
+                        if (__any_sync(0xffffffffu, left < i0 + 16)) {
+#pragma unroll
+                            for (int i = i0; i < i0 + 16; ++i)
+                                if (i >= left)
+                                    s[i] = 0xff800000u;  // -infinity
+                        }
                 }
 #pragma unroll
                 for (int i = 64 * q; i < 64 * q + 64; ++i)
@@ -412,30 +418,40 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         const bool ok = __all_sync(0xffffffffu, !*fail);
         tc_fence_after_sync();
         const bool bad = *poison;
-        // a seen infinity or NaN of V, which the products left out, added to a row's 32 dims
-        auto add_poison = [&](uint32_t* o, int c32) {
-            const int last = min(lim, j1 * PR_KEYS);
-            for (int j = max(j0, j0 + jclean) * PR_KEYS; j < last; ++j) {
-                const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) +
-                                                                 static_cast<long long>(tile.k0 + j) * a.v_row +
-                                                                 static_cast<long long>(g) * a.v_head + 32 * c32);
+        if (ok && bad && end) {
+            // the seen infinities and NaNs of V, which the products left out, added to the rows'
+            // outputs (before these are scaled, which changes neither)
+#pragma unroll 1
+            for (int c32 = 0; c32 < 4; ++c32) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * c32, o);
+                tmem_ld_wait();
+                const int last = mine ? min(lim, j1 * PR_KEYS) : 0;
+                for (int j = max(j0, j0 + jclean) * PR_KEYS; j < last; ++j) {
+                    const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) +
+                                                                     static_cast<long long>(tile.k0 + j) * a.v_row +
+                                                                     static_cast<long long>(g) * a.v_head + 32 * c32);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 w = vp[i];
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w = vp[i];
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t nf = non_finite2<T>(u[e]);
-                        float& lo = reinterpret_cast<float&>(o[8 * i + 2 * e]);
-                        float& hi = reinterpret_cast<float&>(o[8 * i + 2 * e + 1]);
-                        if (nf & 0x8000u)
-                            lo += one16<T>(u[e] & 0xffffu);
-                        if (nf & 0x80000000u)
-                            hi += one16<T>(u[e] >> 16);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t nf = non_finite2<T>(u[e]);
+                            float& lo = reinterpret_cast<float&>(o[8 * i + 2 * e]);
+                            float& hi = reinterpret_cast<float&>(o[8 * i + 2 * e + 1]);
+                            if (nf & 0x8000u)
+                                lo += one16<T>(u[e] & 0xffffu);
+                            if (nf & 0x80000000u)
+                                hi += one16<T>(u[e] >> 16);
+                        }
                     }
                 }
+                __syncwarp();
+                tmem_st32(to + 32 * c32, o);
             }
-        };
+            tmem_st_wait();
+        }
         if (ok && a.splits > 1) {
             if (end) {
                 const size_t at = ((static_cast<size_t>(idx) * a.n_kv + g) * a.splits + c) * 2 + t;
@@ -447,9 +463,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     uint32_t o[32];
                     tmem_ld32(to + 32 * q, o);
                     tmem_ld_wait();
-                    if (bad && mine)
-                        add_poison(o, q);
-                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         po[(8 * q + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
@@ -459,33 +472,40 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         } else if (ok && sp.ntok[t]) {
             // a row that sees no key is zero, one whose scores are all -infinity NaN (0 / 0)
             const float inv = lim > 0 ? 1.0f / l : 0.f;
-            T* out = static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
-                     static_cast<long long>(g * a.group + r % a.group) * a.o_head;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                if (end) {
-                    tmem_ld32(to + 32 * c, o);
-                    tmem_ld_wait();
+            // The rows leave through the query tile's shared memory (its products are done), each
+            // warp its own 32, 16-byte pieces in an order that spreads them over the banks: a
+            // store then writes two whole rows and not 16 bytes of 32 (4-6 thousand clocks of a
+            // block's end).
+            uint8_t* stage = qs + t * PR_TILE + (r & ~31) * 256;
+            uint32_t o[128];
+            if (end) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32(to + 32 * c, o + 32 * c);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = __uint_as_float(o[8 * i + 2 * e]) * inv, y = __uint_as_float(o[8 * i + 2 * e + 1]) * inv;
+                    w[e] = lim > 0 ? pack2(x, y, static_cast<const T*>(nullptr)) : 0u;
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    o[i] = lim > 0 ? __float_as_uint(__uint_as_float(o[i]) * inv) : 0u;
-                if (bad && mine)
-                    add_poison(o, c);
-                if (mine) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint4 w;
-                        uint32_t* u = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            u[e] = pack2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]),
-                                         static_cast<const T*>(nullptr));
-                        *reinterpret_cast<uint4*>(out + 32 * c + 8 * i) = w;
-                    }
-                }
-                __syncwarp();
+                *reinterpret_cast<uint4*>(stage + lane * 256 + 16 * (i ^ (lane & 15))) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+            const uint64_t at = mine ? reinterpret_cast<uint64_t>(
+                                           static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
+                                           static_cast<long long>(g * a.group + r % a.group) * a.o_head)
+                                     : 0ull;
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const int row = 2 * i + (lane >> 4);
+                const uint64_t to_row = __shfl_sync(0xffffffffu, at, row);
+                const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 256 + 16 * ((lane & 15) ^ (row & 15)));
+                if (to_row)
+                    *reinterpret_cast<uint4*>(to_row + 16 * (lane & 15)) = w;
             }
         }
     } else if (tile.live) {
