@@ -67,6 +67,7 @@ struct PromptArgs {
     float* part;
     float* part_ml;
     int splits;
+    FastDiv by_splits, by_kv, by_group, by_span;  // span: tokens a block tile
     int* err;
 };
 
@@ -102,7 +103,7 @@ __device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, 
     for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
         if (!load(s0) && idx == 0)
             set_error(a.err, DEVERR_BAD_ARG);
-        total += __reduce_add_sync(0xffffffffu, (lq + span - 1) / span);
+        total += __reduce_add_sync(0xffffffffu, fast_div(lq + span - 1, a.by_span));
     }
     const int want = total - 1 - idx;
     if (want < 0)
@@ -111,7 +112,7 @@ __device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, 
     for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
         if (a.n_seq > 32)  // else they are in the registers
             load(s0);
-        const int n = (lq + span - 1) / span;
+        const int n = fast_div(lq + span - 1, a.by_span);
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -161,7 +162,7 @@ __device__ __forceinline__ PromptSpan prompt_span(const PromptTile& tile, int to
 // Key tiles [j0, j1) of split c.
 __device__ __forceinline__ void prompt_split(const PromptSpan& p, int splits, int c, int& j0, int& j1)
 {
-    const int all = max(p.end[0], p.end[1]), per = (all + splits - 1) / splits;
+    const int all = max(p.end[0], p.end[1]), per = splits == 1 ? all : (all + splits - 1) / splits;
     j0 = min(all, c * per);
     j1 = min(all, j0 + per);
 }
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
     volatile int* poison = fail + 1;  // a seen value is an infinity or NaN
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c = blockIdx.x % a.splits, g = blockIdx.x / a.splits % a.n_kv, idx = blockIdx.x / (a.splits * a.n_kv);
+    const int part = fast_div(blockIdx.x, a.by_splits), c = blockIdx.x - part * a.splits;
+    const int idx = fast_div(part, a.by_kv), g = part - idx * a.n_kv;
     PromptTile tile{0, 0, 0, 0, 0, 0};
     PromptSpan sp;
     // this block's key tiles j0 + j, j < n, and j < end0 or end1 for query tile 0 or 1
@@ -323,8 +325,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         const int t = warp >> 2, r = tid & 127, end = t ? end1 : end0;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + PR_S0 + 128 * t, to = tbase + lanes + PR_O0 + 128 * t;
-        const int tok = tile.t0 + t * a.tq_tokens + r / a.group;  // within the sequence
-        const bool mine = r / a.group < sp.ntok[t];
+        const int row_tok = fast_div(r, a.by_group);
+        const int tok = tile.t0 + t * a.tq_tokens + row_tok;  // within the sequence
+        const bool mine = row_tok < sp.ntok[t];
         const int lim = min(tile.lk, max(0, tok + 1 + tile.lk - tile.lq));  // keys this row sees
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < end; ++j) {
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
             __syncwarp();
             const uint64_t at = mine ? reinterpret_cast<uint64_t>(
                                            static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
-                                           static_cast<long long>(g * a.group + r % a.group) * a.o_head)
+                                           static_cast<long long>(g * a.group + r - row_tok * a.group) * a.o_head)
                                      : 0ull;
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
@@ -878,6 +881,10 @@ DQ_API int dq_attention_prompt(const dq_prompt* p, void* stream)
     a.group = group;
     a.tq_tokens = tokens;
     a.splits = cut.splits;
+    a.by_splits = dqhost::fast_divisor(cut.splits);
+    a.by_kv = dqhost::fast_divisor(p->n_kv);
+    a.by_group = dqhost::fast_divisor(group);
+    a.by_span = dqhost::fast_divisor(2 * tokens);
     if (cut.splits > 1) {
         a.part = static_cast<float*>(p->workspace);
         a.part_ml = a.part + dqhost::prompt_part_floats(cut, p->n_kv) * dq::PR_HD;
