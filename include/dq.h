@@ -350,13 +350,14 @@ DQ_API int dq_qkv_rope(const float* qkv, long long row_stride, const int* positi
  * flag and its sequence is left out.
  * Strides are multiples of 8, the base pointers 16-byte aligned; out must not
  * overlap the inputs.
- * workspace: device scratch of dq_attention_prompt_workspace_bytes(...) bytes (NULL
- * where that is 0), 16-byte aligned, its content before and after the call of no
- * meaning; calls that share one must not overlap in time.
- * Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, a stride < 128 or not matched to its neighbours
- * (a type other than fp16 or bf16, a workspace too small) -> DQ_ERR_SHAPE;
- * head_dim != 128, n_q / n_kv > 128, totals above 2^30 -> DQ_ERR_UNSUPPORTED;
- * DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
+ * workspace: device scratch of dq_attention_prompt_workspace_bytes(...) bytes for
+ * the same counts (NULL where that is 0; fewer queries can need more, since their
+ * keys are then split over more blocks), 16-byte aligned, its content before and
+ * after the call of no meaning; calls that share one must not overlap in time.
+ * Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, a stride < 128 where its
+ * count exceeds 1, a type other than fp16 or bf16, a workspace too small ->
+ * DQ_ERR_SHAPE; head_dim != 128, n_q / n_kv > 128, totals above 2^30, strides of
+ * 2^38 or more -> DQ_ERR_UNSUPPORTED; DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
 typedef struct {
     const void* q;
     const void* k;
@@ -431,11 +432,11 @@ DQ_API int dq_kv4_read(const void* pool, const int* slots, int type, void* k_out
  * probabilities enter the matrix instructions as two fp16 parts each (relative
  * error about 2^-22); for 16-bit ones a probability is one fp16 number.
  * workspace: dq_attention_decode_kv4_workspace_bytes(...) bytes of device scratch
- * (NULL where that is 0), 16-byte aligned, its content before and after the call
- * of no meaning; calls that share one must not overlap in time.
+ * for the same counts (NULL where that is 0), 16-byte aligned, its content before
+ * and after the call of no meaning; calls that share one must not overlap in time.
  * Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, page_size not a multiple of
  * 16, max_keys out of range, an unknown type, a workspace too small -> DQ_ERR_SHAPE;
- * head_dim != 128, n_q / n_kv > 8, n_pages * page_size >= 2^31 ->
+ * head_dim != 128, n_q / n_kv > 8, max_keys > 2^30, n_pages * page_size >= 2^31 ->
  * DQ_ERR_UNSUPPORTED; misaligned -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
 DQ_API size_t dq_attention_decode_kv4_workspace_bytes(int n_seq, int n_q, int n_kv, int max_keys);
 DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, const int* pages, const int* n_keys,

@@ -651,7 +651,7 @@ DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, co
         return st;
     if (max_keys > static_cast<long long>(max_pages) * page_size)
         return DQ_ERR_SHAPE;
-    if (n_q / n_kv > 8)
+    if (n_q / n_kv > 8 || max_keys > (1 << 30))
         return DQ_ERR_UNSUPPORTED;
     if (!dqhost::aligned16(q) || !dqhost::aligned16(pool) || !dqhost::aligned16(out))
         return DQ_ERR_ALIGN;

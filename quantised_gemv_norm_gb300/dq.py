@@ -454,7 +454,7 @@ class _Prompt(ctypes.Structure):
 
 
 def attention_prompt_workspace(n_seq: int, total_q: int, total_k: int, n_q: int, n_kv: int, device=None):
-    """Scratch for attention_prompt calls of at most these sizes (None where none is needed)."""
+    """Scratch for attention_prompt calls of exactly these sizes (None where none is needed)."""
     n = load().dq_attention_prompt_workspace_bytes(n_seq, total_q, total_k, n_q, n_kv)
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
 

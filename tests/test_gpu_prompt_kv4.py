@@ -201,7 +201,7 @@ def test_prompt_key_lengths(dq, lq, lk):
 def test_prompt_over_cache_planes_and_into_a_strided_output(dq):
     g = gen(9)
     planes = randn(g, 2, 4, 700, HD, dtype=torch.float16)  # [k or v][n_kv][max_ctx][128]
-    wide = torch.full((50, 24, HD), 3.0, dtype=torch.float16, device="cuda")
+    wide = torch.full((50, 26, HD), 3.0, dtype=torch.float16, device="cuda")
     q = randn(g, 50, 16, HD, dtype=torch.float16)
     k, v = planes[0].transpose(0, 1)[:600], planes[1].transpose(0, 1)[:600]
     y = check_prompt(dq, q, k, v, [50], [600], out=wide[:, 4:20])
@@ -551,6 +551,119 @@ def test_decode_in_place(dq):
     want = dq.attention_decode_kv4(q, pool, table, i32([300]), 300)
     dq.attention_decode_kv4(q, pool, table, i32([300]), 300, out=q)
     assert torch.equal(q, want)
+
+
+# ------------------------------------------------------- workspaces and devices
+
+
+def test_workspaces_are_checked(dq):
+    import ctypes
+
+    lib = dq.load()
+    g = gen(71)
+    # one query tile over many keys: split, so a workspace is needed
+    q, k, v = randn(g, 4, 8, HD, dtype=torch.float16), *(randn(g, 4000, 2, HD, dtype=torch.float16) for _ in range(2))
+    need = lib.dq_attention_prompt_workspace_bytes(1, 4, 4000, 8, 2)
+    assert need > 0
+    cu, ck, out = i32([0, 4]), i32([0, 4000]), torch.empty_like(q)
+    ws = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+
+    def call(w, n):
+        d = dq._Prompt(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), 1024, 128, 256, 128, 256, 128, 1024, 128,
+                       cu.data_ptr(), ck.data_ptr(), dq.TYPE_F16, 1, 4, 4000, 8, 2, 128, w, n)
+        return lib.dq_attention_prompt(ctypes.byref(d), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+
+    assert call(None, 0) == -1 and call(ws.data_ptr(), need - 1) == -2 and call(ws.data_ptr() + 8, need) == -3
+    ws.fill_(0xFF)  # its content is of no meaning
+    assert call(ws.data_ptr(), need) == 0
+    assert torch.equal(out, dq.attention_prompt(q, k, v, cu, ck))
+    with pytest.raises(dq.DQError):
+        dq.attention_prompt(q, k, v, cu, ck, workspace=ws[:64])
+
+    pool, table, _, _, _ = build_cache(dq, 72, [2000], 2, 64)
+    x, n = randn(g, 1, 8, HD), i32([2000])
+    ws = dq.attention_decode_kv4_workspace(1, 8, 2, 2000)
+    assert ws is not None
+    want = dq.attention_decode_kv4(x, pool, table, n, 2000)
+    ws.fill_(0xFF)
+    assert torch.equal(dq.attention_decode_kv4(x, pool, table, n, 2000, workspace=ws), want)
+    with pytest.raises(dq.DQError):
+        dq.attention_decode_kv4(x, pool, table, n, 2000, workspace=ws[:64])
+
+
+def test_tensors_off_the_current_device_are_refused(dq):
+    g = gen(73)
+    q, k = randn(g, 4, 8, HD, dtype=torch.float16), randn(g, 4, 2, HD, dtype=torch.float16)
+    cu, pool, slots = i32([0, 4]), dq.kv4_pool(1, 2, 16), i32([0, 1, 2, 3])
+    with pytest.raises(ValueError):
+        dq.attention_prompt(q, k.cpu(), k, cu)
+    with pytest.raises(ValueError):
+        dq.attention_prompt(q, k, k, cu.cpu())
+    with pytest.raises(ValueError):
+        dq.kv4_append(k, k, slots.cpu(), pool)
+    with pytest.raises(ValueError):
+        dq.kv4_read(pool.cpu(), slots)
+    with pytest.raises(ValueError):
+        dq.attention_decode_kv4(q, pool, torch.zeros(4, 1, dtype=torch.int32), slots, 16)
+    with pytest.raises(ValueError):
+        dq.qkv_rope(randn(g, 4, 4 * HD), slots, dq.rope_table(16), 2, 1, q_norm=torch.ones(HD), k_norm=torch.ones(HD))
+
+
+def test_two_streams_at_once(dq):
+    # calls without a shared workspace do not meet, whichever streams they run on
+    g = gen(74)
+    pool, table, _, _, _ = build_cache(dq, 75, [3000, 700], 2, 64)
+    n = i32([3000, 700])
+    x = [randn(g, 2, 8, HD) for _ in range(4)]
+    q = [randn(g, 700, 8, HD, dtype=torch.bfloat16) for _ in range(4)]
+    k = [randn(g, 700, 2, HD, dtype=torch.bfloat16) for _ in range(4)]
+    cu = i32([0, 33, 700])
+    want = [(dq.attention_decode_kv4(a, pool, table, n, 3000), dq.attention_prompt(b, c, c, cu)) for a, b, c in zip(x, q, k)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        got = []
+        for i in range(4):
+            with torch.cuda.stream(streams[i % 2]):
+                got.append((dq.attention_decode_kv4(x[i], pool, table, n, 3000), dq.attention_prompt(q[i], k[i], k[i], cu)))
+        torch.cuda.synchronize()
+        for (a, b), (c, d) in zip(got, want):
+            assert torch.equal(a, c) and torch.equal(b, d)
+
+
+def test_first_call_may_be_captured(tmp_path):
+    # a fresh process whose first use of the kernels is inside a capture
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys; sys.path.insert(0, %r)
+import torch
+from quantised_gemv_norm_gb300 import dq
+dq.load()
+q = torch.randn(70, 8, 128, device='cuda').half(); k = torch.randn(70, 2, 128, device='cuda').half()
+cu = torch.tensor([0, 70], dtype=torch.int32, device='cuda')
+x = torch.randn(70, 12 * 128, device='cuda'); pos = torch.arange(70, dtype=torch.int32, device='cuda')
+table = torch.ones(128, 64, 2, device='cuda'); pool = dq.kv4_pool(2, 2, 64); pages = pos[:2].reshape(1, 2)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = dq.attention_prompt(q, k, k, cu)
+    a, b, c = dq.qkv_rope(x, pos, table, 8, 2)
+    dq.kv4_append(b, c, pos, pool)
+    d, e = dq.kv4_read(pool, pos)
+    z = dq.attention_decode_kv4(a[:1].float(), pool, pages, pos[69:], 128)
+g.replay(); torch.cuda.synchronize()
+assert torch.equal(y, dq.attention_prompt(q, k, k, cu))
+assert torch.equal(z, dq.attention_decode_kv4(a[:1].float(), pool, pages, pos[69:], 128))
+assert dq.device_error() == 0
+print('captured')
+""" % root
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------- all together

@@ -102,7 +102,7 @@ DECODE = dict(q=A, type=0, pool=A, table=A, n=A, out=A, n_seq=1, n_q=32, n_kv=8,
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), NULL), (dict(pool=None), NULL), (dict(table=None), NULL), (dict(n=None), NULL), (dict(out=None), NULL),
     (dict(n_seq=0), SHAPE), (dict(n_q=30), SHAPE), (dict(max_pages=0), SHAPE), (dict(max_keys=0), SHAPE),
-    (dict(max_keys=257), SHAPE), (dict(page=40), SHAPE), (dict(type=4), SHAPE), (dict(n_q=72), UNSUPPORTED),
+    (dict(max_keys=257), SHAPE), (dict(max_keys=(1 << 30) + 1, max_pages=1 << 25), UNSUPPORTED), (dict(page=40), SHAPE), (dict(type=4), SHAPE), (dict(n_q=72), UNSUPPORTED),
     (dict(hd=64), UNSUPPORTED), (dict(q=P(4100)), ALIGN), (dict(out=P(4104)), ALIGN), (dict(pool=P(4104)), ALIGN),
 ])
 def test_attention_decode_kv4_refuses(lib, kw, status):
