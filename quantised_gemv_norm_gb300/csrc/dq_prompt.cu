@@ -658,16 +658,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         tmem_dealloc(tbase, PR_TCOLS);
 }
 
-// The splits of one block tile, KV head and query tile: a thread takes one row and 8 of
-// its dims.  The splits' weights of the row come first, then all their loads are free of
-// one another.
+// The splits of one block tile, KV head and query tile: a thread takes one row, 8 of its
+// dims and every PR_JOIN-th split, then the threads of a row meet in shared memory.  A
+// thread's maxima and sums are loaded together and then its outputs (two waits for
+// memory in all, up to PR_BATCH splits at a time).
+constexpr int PR_JOIN = 4, PR_BATCH = 8;
+
 template <typename T>
-__global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant__ PromptArgs a)
+__global__ void __launch_bounds__(128 * PR_JOIN) prompt_join_kernel(const __grid_constant__ PromptArgs a)
 {
     __shared__ PromptTile shared_tile;
-    __shared__ float weight[PR_MAX_SPLITS][128];
-    const int r = threadIdx.x, q = blockIdx.y & 15, t = blockIdx.y >> 4;
-    const int g = blockIdx.x % a.n_kv, idx = blockIdx.x / a.n_kv;
+    __shared__ float2 meet_ml[PR_JOIN - 1][128];
+    __shared__ float4 meet_o[PR_JOIN - 1][2][128];
+    const int r = threadIdx.x & 127, part = threadIdx.x >> 7, q = blockIdx.y & 15, t = blockIdx.y >> 4;
+    const int idx = fast_div(blockIdx.x, a.by_kv), g = blockIdx.x - idx * a.n_kv;
     if (threadIdx.x < 32) {
         const PromptTile x = prompt_find(a, idx, 2 * a.tq_tokens, threadIdx.x);
         if (threadIdx.x == 0)
@@ -676,52 +680,91 @@ __global__ void __launch_bounds__(128) prompt_join_kernel(const __grid_constant_
     __syncthreads();
     const PromptTile tile = shared_tile;
     const PromptSpan sp = prompt_span(tile, a.tq_tokens);
-    pdl_wait();
-    if (!tile.live || r / a.group >= sp.ntok[t])
-        return;
-    const int tok = tile.t0 + t * a.tq_tokens + r / a.group;
+    const int row_tok = fast_div(r, a.by_group), tok = tile.t0 + t * a.tq_tokens + row_tok;
+    const bool mine = tile.live && row_tok < sp.ntok[t];
     const size_t first = (static_cast<size_t>(idx) * a.n_kv + g) * a.splits;
     // the splits that have keys for this query tile are the first ones
     int j0, per;
     prompt_split(sp, a.splits, 0, j0, per);
-    const int n = per > 0 ? min(a.splits, (sp.end[t] + per - 1) / per) : 0;
+    const int n = mine && per > 0 ? min(a.splits, (sp.end[t] + per - 1) / per) : 0;
     const float* ml = a.part_ml + (first * 2 + t) * 256 + r;
     const float4* po = reinterpret_cast<const float4*>(a.part) + (first * 2 + t) * 32 * 128 + 2 * q * 128 + r;
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int c = 0; c < n; ++c) {
-        const float x = __ldcg(ml + c * 512);
-        weight[c][r] = x;  // this thread's alone
-        m = fmaxf(m, x);
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-#pragma unroll 8
-    for (int c = 0; c < n; ++c) {
-        const float f = ex2((weight[c][r] - base) * PR_C);
-        weight[c][r] = f;
-        l = fmaf(f, __ldcg(ml + c * 512 + 128), l);
-    }
+    pdl_wait();
+    float m = -INFINITY, l = 0.f;
     float4 o[2] = {};
-#pragma unroll 8
-    for (int c = 0; c < n; ++c) {
-        const float f = weight[c][r];
+    for (int c0 = part; c0 < n; c0 += PR_JOIN * PR_BATCH) {
+        float mc[PR_BATCH], lc[PR_BATCH], top = m;
+        float4 x[PR_BATCH][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 x = __ldcg(po + static_cast<size_t>(c) * 2 * 32 * 128 + i * 128);
-            o[i].x = fmaf(f, x.x, o[i].x);
-            o[i].y = fmaf(f, x.y, o[i].y);
-            o[i].z = fmaf(f, x.z, o[i].z);
-            o[i].w = fmaf(f, x.w, o[i].w);
+        for (int i = 0; i < PR_BATCH; ++i) {
+            const int c = c0 + PR_JOIN * i;
+            mc[i] = c < n ? __ldcg(ml + c * 512) : -INFINITY;
+            lc[i] = c < n ? __ldcg(ml + c * 512 + 128) : 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                x[i][h] = c < n ? __ldcg(po + static_cast<size_t>(c) * 2 * 32 * 128 + h * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < PR_BATCH; ++i)
+            top = fmaxf(top, mc[i]);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f = ex2((m - base) * PR_C);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            o[h] = make_float4(o[h].x * f, o[h].y * f, o[h].z * f, o[h].w * f);
+#pragma unroll
+        for (int i = 0; i < PR_BATCH; ++i) {
+            const float w = ex2((mc[i] - base) * PR_C);
+            l = fmaf(w, lc[i], l);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                o[h].x = fmaf(w, x[i][h].x, o[h].x);
+                o[h].y = fmaf(w, x[i][h].y, o[h].y);
+                o[h].z = fmaf(w, x[i][h].z, o[h].z);
+                o[h].w = fmaf(w, x[i][h].w, o[h].w);
+            }
+        }
+    }
+    if (part) {
+        meet_ml[part - 1][r] = make_float2(m, l);
+        meet_o[part - 1][0][r] = o[0];
+        meet_o[part - 1][1][r] = o[1];
+    }
+    __syncthreads();
+    if (part || !mine)
+        return;
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < PR_JOIN - 1; ++i)
+        top = fmaxf(top, meet_ml[i][r].x);
+    const float base = top == -INFINITY ? 0.f : top, f = ex2((m - base) * PR_C);
+    l *= f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        o[h] = make_float4(o[h].x * f, o[h].y * f, o[h].z * f, o[h].w * f);
+#pragma unroll
+    for (int i = 0; i < PR_JOIN - 1; ++i) {
+        const float2 y = meet_ml[i][r];
+        const float w = ex2((y.x - base) * PR_C);
+        l = fmaf(w, y.y, l);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 x = meet_o[i][h][r];
+            o[h].x = fmaf(w, x.x, o[h].x);
+            o[h].y = fmaf(w, x.y, o[h].y);
+            o[h].z = fmaf(w, x.z, o[h].z);
+            o[h].w = fmaf(w, x.w, o[h].w);
         }
     }
     const bool sees = tok + 1 + tile.lk - tile.lq > 0 && tile.lk > 0;
     const float inv = sees ? 1.0f / l : 0.f;
     T* out = static_cast<T*>(a.out) + static_cast<long long>(tile.q0 + tok) * a.o_row +
-             static_cast<long long>(g * a.group + r % a.group) * a.o_head + 8 * q;
+             static_cast<long long>(g * a.group + r - row_tok * a.group) * a.o_head + 8 * q;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        store4(out + 4 * i, sees ? make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv)
+    for (int h = 0; h < 2; ++h)
+        store4(out + 4 * h, sees ? make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv)
                                  : make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
@@ -798,7 +841,7 @@ static cudaError_t prompt_launch(const dq::PromptArgs& a, unsigned grid, const P
     // a dependent launch: it finds its tiles while the last blocks run
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cut.tiles * a.n_kv), 32);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(128 * dq::PR_JOIN);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
