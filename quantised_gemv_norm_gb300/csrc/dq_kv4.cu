@@ -69,11 +69,16 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], float& d, 
         lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    d = __half2float(__float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)));
+    // (hi - lo) / 15 as IEEE division rounds it: the product with 1 / 15, corrected once by
+    // its remainder (checked for every fp32 mantissa)
+    const float range = __fsub_rn(hi, lo), part = __fmul_rn(range, 1.f / 15.f);
+    d = __half2float(__float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, part, range), 1.f / 15.f, part)));
     z = __half2float(__float2half_rn(__fadd_rn(lo, 8.0f * d)));
     if (!(d <= 65504.f) || !(fabsf(z) <= 65504.f))  // also an infinity or NaN among them
         d = z = __int_as_float(0x7fc00000);
-    const float inv = d > 0.f ? __frcp_rn(d) : 0.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
+    inv = d > 0.f ? inv : 0.f;
     constexpr float M = 12582912.f;  // 1.5 2^23: adding it rounds to an integer, halves to even
     const uint64_t z2 = f2(-z, -z), inv2 = f2(inv, inv), eight = f2(8.f, 8.f), m2 = f2(M, M), nm2 = f2(-M, -M);
     uint32_t word = 0, base = 0;
@@ -162,9 +167,13 @@ __global__ void __launch_bounds__(32 * KV4_WARPS) kv4_read_kernel(const Kv4ReadA
     const __half* vs = reinterpret_cast<const __half*>(b + kv4_scale(KV4_VSCALES, j, grp));
     const float kd = __half2float(ks[0]), kz = __half2float(ks[2]), vd = __half2float(vs[0]), vz = __half2float(vs[2]);
     // a code at bits n .. n + 3 (n < 20) under 2^23 is 2^23 + 2^n c exactly, and d 2^-n exact
-    auto value = [](uint32_t w, int n, float d, float z) {
+    uint32_t e23;  // 2^23's bits in a register: as a constant beside the mask they cost an instruction more
+    asm volatile("mov.b32 %0, 0x4B000000;" : "=r"(e23));
+    auto value = [&](uint32_t w, int n, float d, float z) {
         const float s = static_cast<float>(1 << n);
-        return fmaf(d * (1.f / s), __uint_as_float((w & (15u << n)) | 0x4B000000u) - (8388608.f + 8.f * s), z);
+        uint32_t u;
+        asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w), "r"(15u << n), "r"(e23));
+        return fmaf(d * (1.f / s), __uint_as_float(u) - (8388608.f + 8.f * s), z);
     };
     const size_t at = static_cast<size_t>(item) * ATT_HD + 8 * dim;
     float x[8];
