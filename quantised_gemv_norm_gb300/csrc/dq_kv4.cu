@@ -3,10 +3,11 @@
 //
 // Half a warp takes one head's key and value row, eight dims a lane: 16 bytes of a
 // 16-bit row, one 32-bit word of key codes, two halves of value words.  A group of 32
-// dims with one scale is four lanes: its extremes are two shuffles.  Memory bounds
-// both (160 bytes a row and head in the cache, 256 or 512 outside); with a warp a
-// row and a division for each code the instructions did (8000 rows of 8 heads, store
-// and read back: 55 us).
+// dims with one scale is four lanes: its extremes are two shuffles.  A warp and a
+// division for each code took 55 us for 8000 rows of 8 heads stored and read back;
+// now the store takes 17 us (33 MB of fp16 in, 10 MB out; its 360 instructions for two
+// rows are issued at 0.7 of the rate) and the read to fp32 14 us (76 MB, 5.4 TB/s).
+// 16000 rows to bf16: 20.5 us, 86 MB, 4.2 TB/s.
 #include "dq_kv4.cuh"
 
 namespace dq {

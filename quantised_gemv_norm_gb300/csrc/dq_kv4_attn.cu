@@ -9,11 +9,18 @@
 // kernel.  The cache bytes bound it, so the arithmetic goes to the (warp-level)
 // matrix instructions m16n8k16, whose 16 rows hold the group's up to 8 query heads
 // twice: the fp16 part of a query in row h and, for fp32 results, the rest of it in row
-// 8 + h, which gives 22 bits for the price of 11 with so few rows.  The codes c - 8 are exact in
-// fp16 and need no scale before the product:
+// 8 + h, which gives 22 bits for the price of 11 with so few rows.  The codes c - 8 are
+// exact in fp16 and need no scale before the product:
 //   s_j   = sum_g d_jg (sum_{n in g} q_n (c_jn - 8)) + z_jg (sum_{n in g} q_n)
 //   out_n = sum_j (p_j d_jg) (c_jn - 8) + sum_j p_j z_jg
-// with g the groups of 32 dims; p_j d_jg is again two fp16 parts.
+// with g the groups of 32 dims; p_j d_jg is again two fp16 parts for fp32 results and
+// one for 16-bit ones.
+//
+// A cache block takes a warp 405 instructions with one part (half of them codes and
+// scales made into operands) and 450 with two; with 12 warps an SM these are issued at
+// 0.6 a clock and scheduler, and that, not the memory, bounds it: 48 sequences of 1 to
+// 12000 keys, 325 MB, 85 us (3.8 TB/s; 48 us at the memory's rate), one of 100001, 128
+// MB, 43 us (2.95 TB/s, two parts).  A call of 64 keys takes 3.4 us in a graph.
 //
 // p_j = 2^(s_j - r) with a reference r a head that follows the running maximum only
 // when some s_j - r passes a cap: p_j d_jg stays in fp16's normal range on both
@@ -25,7 +32,6 @@
 namespace dq {
 
 constexpr int KA_WARPS = 4;
-constexpr int KA_JOIN = 4;     // warps that join a head's splits
 constexpr int KA_STEP = 2;     // cache blocks a ring stage
 constexpr int KA_NS = 2;       // ring stages a warp
 constexpr int KA_RESIDENT = 3; // blocks an SM (4, at 128 registers: 96.5 against 94.0 us, 48 sequences)
@@ -513,13 +519,13 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
 }
 
 // The splits' results of one sequence and query head, four dims a lane: each warp adds
-// up every KA_JOIN-th split with a running maximum, four at a time so that their loads
+// up every JOIN-th split with a running maximum, four at a time so that their loads
 // are in flight together, then the warps' sums meet.
-template <typename T>
-__global__ void __launch_bounds__(32 * KA_JOIN) kv4_join_kernel(const Kv4AttnArgs a)
+template <typename T, int JOIN>
+__global__ void __launch_bounds__(32 * JOIN) kv4_join_kernel(const Kv4AttnArgs a)
 {
-    __shared__ float ml[KA_JOIN][2];
-    __shared__ float4 sums[KA_JOIN][32];
+    __shared__ float ml[JOIN][2];
+    __shared__ float4 sums[JOIN][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x / a.n_q, hq = blockIdx.x % a.n_q, g = hq / a.group, h = hq % a.group;
     int n = __ldg(a.n_keys + b);
@@ -531,13 +537,13 @@ __global__ void __launch_bounds__(32 * KA_JOIN) kv4_join_kernel(const Kv4AttnArg
     pdl_wait();
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = warp; c0 < splits; c0 += 4 * KA_JOIN) {
+    for (int c0 = warp; c0 < splits; c0 += 4 * JOIN) {
         float2 rl[4];
         float4 y[4];
         float top = m;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = c0 + KA_JOIN * i;
+            const int c = c0 + JOIN * i;
             rl[i] = make_float2(-INFINITY, 0.f);
             y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (c < splits) {
@@ -572,12 +578,12 @@ __global__ void __launch_bounds__(32 * KA_JOIN) kv4_join_kernel(const Kv4AttnArg
         return;
     float top = m;
 #pragma unroll
-    for (int w = 1; w < KA_JOIN; ++w)
+    for (int w = 1; w < JOIN; ++w)
         top = fmaxf(top, ml[w][0]);
     l = 0.f;
     v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < KA_JOIN; ++w) {
+    for (int w = 0; w < JOIN; ++w) {
         const float f = ml[w][0] == top ? 1.f : ex2(ml[w][0] - top);
         const float4 y = sums[w][lane];
         l = fmaf(f, ml[w][1], l);
@@ -680,14 +686,17 @@ DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, co
         // a dependent launch: its blocks are there when the last of the first kernel's end
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(n_seq) * n_q);
-        cfg.blockDim = dim3(32 * dq::KA_JOIN);
+        // many splits are those of few sequences, whose join has the card to itself (1 x 100001
+        // keys: 45.2 -> 43.4 us with 8 warps; 48 x 6000, 12 splits: 88.0 -> 89.4)
+        const int join = sp.splits > 16 ? 8 : 4;
+        cfg.blockDim = dim3(32 * join);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, dq::kv4_join_kernel<T>, a);
+        return cudaLaunchKernelEx(&cfg, join == 8 ? dq::kv4_join_kernel<T, 8> : dq::kv4_join_kernel<T, 4>, a);
     });
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }

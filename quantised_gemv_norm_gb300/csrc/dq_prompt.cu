@@ -18,6 +18,21 @@
 // used, P stays below 2^8 in fp16 and every sum is fp32, and the scaling of O,
 // which would wait for the last product, is rare after the first tiles.
 //
+// 8192 tokens, 32 heads on 8 KV heads, fp16: 385 us, 1430 TFLOP/s (0.75 of the
+// measured bf16 rate); 350 GB/s of DRAM.  A round (both query tiles against one key
+// tile) takes about 2900 clocks, its 32 products 2048: the rest is the chain S, softmax,
+// P, product, S of each tile, which the other tile's products do not quite cover, and
+// shared memory, whose 128 bytes a clock the products' operands and the copies need for
+// about as long as the products take.  A block's start and end (5 us) come on top: a
+// batch of twelve ragged prompts, 1432 blocks of 6 rounds on average, 140 us, 890
+// TFLOP/s.  Tried and not kept: blocks that fetch more work and copy the next tile
+// during the end of one (ragged batch 158 us), two product warps taking turns (8192
+// tokens 398 us), a product loop unrolled over the ring's slots (449 us).
+//
+// Where the query tiles are too few for the card, the keys of each are split over
+// several blocks and joined by a second kernel (64 queries over 16064 keys: 286 -> 27
+// us; the keys' 66 MB take 10).
+//
 // Key tiles that hold masked keys for some row (the diagonal's and a sequence's end)
 // have their infinities and NaNs in V replaced by zero before the product, since a
 // probability of 0 would not stop them; where such a key is seen by some row, the
@@ -33,7 +48,7 @@ namespace dq {
 
 constexpr int PR_HD = 128;
 constexpr int PR_KEYS = 128;                  // keys a tile
-constexpr int PR_STAGES = 5;                  // ring of key and value tiles, in turn (odd: see the products' loop)
+constexpr int PR_STAGES = 5;                  // ring of key and value tiles, in turn
 constexpr int PR_TILE = PR_KEYS * PR_HD * 2;  // bytes of a key, value or query tile
 constexpr int PR_PANEL = PR_TILE / 2;         // 64 dims of it
 // warps 0-7 softmax, then one that issues the products (of both query tiles: two warps

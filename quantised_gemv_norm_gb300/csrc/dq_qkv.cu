@@ -5,9 +5,10 @@
 // Half a warp takes one head, a warp eight heads of one row: lane i of 16 holds dims
 // 4 i .. 4 i + 3 and 64 + 4 i .., so a rotation's two dims are in one lane, the sum of
 // squares of two heads is four shuffles, and the row's angles are loaded once.  All
-// eight heads' loads are issued first.  Memory bounds it (8191 rows of 48 heads, 306
-// MB; one warp a head, with the partner dims 16 lanes away and divisions for the
-// index, was bound by its 150 instructions: 80 us).
+// eight heads' loads are issued first.  Memory bounds it: 8191 rows of 48 heads to
+// fp16, 306 MB, 55.8 us, 5.5 TB/s (0.81 of the measured copy rate; one warp a head, with
+// the partner dims 16 lanes away and divisions for the index, was bound by its 150
+// instructions: 80 us).
 #include "dq_attn.cuh"
 #include "dq_types.cuh"
 
