@@ -20,12 +20,12 @@
 //
 // 8192 tokens, 32 heads on 8 KV heads, fp16: 385 us, 1430 TFLOP/s (0.75 of the
 // measured bf16 rate); 350 GB/s of DRAM.  A round (both query tiles against one key
-// tile) takes about 2900 clocks, its 32 products 2048: the rest is the chain S, softmax,
-// P, product, S of each tile, which the other tile's products do not quite cover, and
-// shared memory, whose 128 bytes a clock the products' operands and the copies need for
-// about as long as the products take.  A block's start and end (5 us) come on top: a
-// batch of twelve ragged prompts, 1432 blocks of 6 rounds on average, 140 us, 890
-// TFLOP/s.  Tried and not kept: blocks that fetch more work and copy the next tile
+// tile) takes about 2900 clocks, its 32 products 2048.  The products bound it, not the
+// softmax: with P = S in place of the exponentials 382 us are left.  A product of 64
+// clocks reads 8 KB of shared memory for S and 4 KB for P V, and a round's copies write
+// 64 KB: 256 KB a round are the 128 bytes a clock that shared memory has for as long as
+// the products take.  A block's start and end (5 us) come on top: a batch of twelve
+// ragged prompts, 1432 blocks of 6 rounds on average, 140 us, 890 TFLOP/s.  Tried and not kept: blocks that fetch more work and copy the next tile
 // during the end of one (ragged batch 158 us), two product warps taking turns (8192
 // tokens 398 us), a product loop unrolled over the ring's slots (449 us).
 //
