@@ -36,7 +36,7 @@ constexpr int KA_STEP = 2;     // cache blocks a ring stage
 constexpr int KA_NS = 2;       // ring stages a warp
 constexpr int KA_RESIDENT = 3; // blocks an SM (4, at 128 registers: 96.5 against 94.0 us, 48 sequences)
 constexpr int KA_PART = 132;   // floats of a partial result: r, l, two unused, 128 sums
-constexpr float KA_CAP = 12.f;   // p_j <= 2^cap where every d <= 8
+constexpr float KA_CAP = 12.f;   // p_j <= 2^cap where every d <= 8 = 2^(15 - cap)
 constexpr float KA_HEAD = 3.f;   // log2 that the maximum may grow before r follows it
 
 struct Kv4AttnArgs {
@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
         for (int i = 0; i < 8; ++i)
             o[k][i >> 2][i & 3] = 0.f;
     float r = -INFINITY, cap = KA_CAP;
+    uint32_t lim = 0x48004800u;  // 2^(15 - cap) as an fp16 pair: 8 at first
 
     // the zero accumulator operand, kept in registers: as a constant it would be written
     // before every matrix instruction (64 moves a block)
@@ -354,13 +355,21 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
         }
         const float2 s0 = un2(s[0]), s1 = un2(s[1]);
         const float top = fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)) * unscale;
-        // d <= 8 keeps p d below 2^15 under the cap; a larger one lowers the cap
-        const bool wide = !__hble2(dmax, __half2half2(__ushort_as_half(0x4800)));
-        if (__any_sync(0xffffffffu, top - r > cap || (wide && cap == KA_CAP))) {
+        // d <= lim keeps p d at 2^15 or below under the cap.  A larger one lowers the cap, by no
+        // more than it takes: the lower it is, the fewer bits p d has above fp16's smallest
+        // number in groups with small scales (d of 1e-3 and the lowest cap: 2^-11 of them)
+        const bool wide = !__hble2(dmax, *reinterpret_cast<const __half2*>(&lim));
+        if (__any_sync(0xffffffffu, top - r > cap || wide)) {
             float t = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-            if (__any_sync(0xffffffffu, wide))
-                cap = 15.f - 16.f;  // from now on for the largest scale there is
+            if (__any_sync(0xffffffffu, wide)) {
+                // the power of two above the largest scale (an infinity counts as the largest)
+                const uint32_t d2 = *reinterpret_cast<const uint32_t*>(&dmax);
+                const uint32_t e = __reduce_max_sync(0xffffffffu, max(d2 & 0xffffu, d2 >> 16)) >> 10;
+                cap = fmaxf(29.f - static_cast<float>(e), -1.f);  // 15 - (e - 15 + 1)
+                lim = min(e + 1, 30u) << 10;
+                lim = (e >= 30 ? 0x7C00u : lim) * 0x10001u;  // no scale is above an infinity
+            }
             float f = 1.f;
             if (t - r > cap) {
                 const float rn = t - (cap - KA_HEAD);

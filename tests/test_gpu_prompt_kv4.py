@@ -512,6 +512,30 @@ def test_decode_peaked_and_shared_pages(dq):
     within(y, r, 2 * 8.2e-6 * 128 * 12 / 11.3 * size)
 
 
+def test_decode_small_values_beside_an_outlier_channel(dq):
+    # Equal scores: every p_j is the same 2^e, e = cap - 3 or more.  The outlier's scale is below 16, which lowers
+    # the cap of 12 to 11: 600 products p d of the small groups are off by at most half of 2^-24 (fp16's smallest, the
+    # second part's step) times |c - 8| <= 8 each, over a sum of 600 2^8: 2^-22 2^-8 = 2^-30 beside the usual bound.
+    # In the outlier's own group v is a difference: its bound goes by B = sum p (|v - z| + |z|) in place of A.
+    g = gen(51)
+    n, page = 600, 64
+    k, v = randn(g, n, 2, HD), randn(g, n, 2, HD) * 1e-4
+    v[:, :, 3] = 400 * torch.rand(n, 2, device="cuda", generator=g) - 200  # one a group: d = |v| / 15
+    pool, table = dq.kv4_pool(10, 2, page), torch.arange(10, device="cuda").int()[None]
+    slots = torch.arange(n, device="cuda").int()
+    dq.kv4_append(k, v, slots, pool)
+    kk, vv = (x.double() for x in dq.kv4_read(pool, slots, dtype=torch.float32))
+    d, z = quantise_ref(v.cpu().numpy())[:2]
+    assert 8 < float(d.max()) < 16
+    z = torch.from_numpy(z.astype(np.float64)).cuda().repeat_interleave(32, -1)
+    q = torch.zeros(1, 8, HD, device="cuda")
+    y = dq.attention_decode_kv4(q, pool, table, i32([n]), n)
+    r, size = decode_ref(q, [kk], [vv], [n])
+    parts = decode_ref(q, [kk], [(vv - z).abs() + z.abs()], [n])[0]
+    within(y[..., 32:], r[..., 32:], 2e-5 * size[..., 32:] + 2.0 ** -30)
+    within(y[..., :32], r[..., :32], 2e-5 * parts[..., :32])
+
+
 def test_decode_masked_rows_may_hold_anything(dq):
     pool, table, ks, vs, zs = build_cache(dq, 43, [70, 0, 5], 2, 64)  # unused rows: NaN scales, all codes 15
     q = randn(gen(44), 3, 4, HD)
