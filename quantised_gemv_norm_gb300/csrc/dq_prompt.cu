@@ -30,7 +30,7 @@
 // tokens 398 us), a product loop unrolled over the ring's slots (449 us).
 //
 // Where the query tiles are too few for the card, the keys of each are split over
-// several blocks and joined by a second kernel (64 queries over 16064 keys: 286 -> 27
+// several blocks and joined by a second kernel (64 queries over 16064 keys: 286 -> 25
 // us; the keys' 66 MB take 10).
 //
 // Key tiles that hold masked keys for some row (the diagonal's and a sequence's end)
@@ -91,65 +91,66 @@ struct PromptTile {
     int q0, k0, lq, lk, t0, live;
 };
 
-// Rows of sequence s; false where the offsets do not ascend within their totals.
-__device__ __forceinline__ bool prompt_seq(const PromptArgs& a, int s, int& q0, int& lq, int& k0, int& lk)
-{
-    const int qa = __ldg(a.cu_q + s), qb = __ldg(a.cu_q + s + 1);
-    const int ka = __ldg(a.cu_k + s), kb = __ldg(a.cu_k + s + 1);
-    q0 = qa;
-    k0 = ka;
-    const bool ok = qa >= 0 && qa <= qb && qb <= a.total_q && ka >= 0 && ka <= kb && kb <= a.total_k;
-    lq = ok ? qb - qa : 0;
-    lk = ok ? kb - ka : 0;
-    return ok;
-}
-
 // Block tile `idx`, counted from the last sequence's last tile (a causal sequence's
-// later tiles see more keys: they start first).  By one warp; `span` tokens a block.
+// later tiles see more keys: they start first).  By one warp, four sequences a lane, so
+// that the offsets of 128 are one wait for memory (256 sequences of 40 tokens: 162 us with
+// two passes of 32 at a time, 121 us); `span` tokens a block.
 __device__ __forceinline__ PromptTile prompt_find(const PromptArgs& a, int idx, int span, int lane)
 {
-    PromptTile t{0, 0, 0, 0, 0, 0};
-    int q0 = 0, lq = 0, k0 = 0, lk = 0;
-    auto load = [&](int s0) {
-        lq = lk = 0;
-        return s0 + lane >= a.n_seq || prompt_seq(a, s0 + lane, q0, lq, k0, lk);
-    };
-    int total = 0;
-    for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
-        if (!load(s0) && idx == 0)
-            set_error(a.err, DEVERR_BAD_ARG);
-        total += __reduce_add_sync(0xffffffffu, fast_div(lq + span - 1, a.by_span));
-    }
-    const int want = total - 1 - idx;
-    if (want < 0)
-        return t;
-    int before = 0;
-    for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
-        if (a.n_seq > 32)  // else they are in the registers
-            load(s0);
-        const int n = fast_div(lq + span - 1, a.by_span);
-        int incl = n;
+    int q0 = 0, k0 = 0, rows = 0, keys = 0, t0 = 0, live = 0;
+    int want = idx;  // tiles from the end of sequence s1 - 1
+    for (int s1 = a.n_seq; s1 > 0 && (!live || idx == 0); s1 -= 128) {
+        // sequences s1 - 1 - 4 lane - e; those below 0 have no rows
+        int cq[5], ck[5];
+#pragma unroll
+        for (int e = 0; e < 5; ++e) {
+            const int i = max(s1 - 4 * lane - e, 0);
+            cq[e] = __ldg(a.cu_q + i);
+            ck[e] = __ldg(a.cu_k + i);
+        }
+        int lq[4], n[4], sum = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // offsets that do not ascend within their totals: the first block reports them
+            const bool ok = cq[e + 1] >= 0 && cq[e + 1] <= cq[e] && cq[e] <= a.total_q && ck[e + 1] >= 0 &&
+                            ck[e + 1] <= ck[e] && ck[e] <= a.total_k;
+            if (!ok && idx == 0)
+                set_error(a.err, DEVERR_BAD_ARG);
+            lq[e] = ok ? cq[e] - cq[e + 1] : 0;
+            n[e] = fast_div(lq[e] + span - 1, a.by_span);
+            sum += n[e];
+        }
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o)
                 incl += x;
         }
-        const int mine = want - before - (incl - n);
-        const unsigned hit = __ballot_sync(0xffffffffu, mine >= 0 && mine < n);
-        if (hit) {
+        int mine = want - (incl - sum);
+        const unsigned hit = __ballot_sync(0xffffffffu, mine >= 0 && mine < sum);
+        if (hit && !live) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool it = mine >= 0 && mine < n[e];
+                q0 = it ? cq[e + 1] : q0;
+                k0 = it ? ck[e + 1] : k0;
+                rows = it ? lq[e] : rows;
+                keys = it ? ck[e] - ck[e + 1] : keys;
+                t0 = it ? (n[e] - 1 - mine) * span : t0;
+                mine -= n[e];
+            }
             const int src = __ffs(hit) - 1;
-            t.q0 = __shfl_sync(0xffffffffu, q0, src);
-            t.k0 = __shfl_sync(0xffffffffu, k0, src);
-            t.lq = __shfl_sync(0xffffffffu, lq, src);
-            t.lk = __shfl_sync(0xffffffffu, lk, src);
-            t.t0 = __shfl_sync(0xffffffffu, mine, src) * span;
-            t.live = 1;
-            return t;
+            q0 = __shfl_sync(0xffffffffu, q0, src);
+            k0 = __shfl_sync(0xffffffffu, k0, src);
+            rows = __shfl_sync(0xffffffffu, rows, src);
+            keys = __shfl_sync(0xffffffffu, keys, src);
+            t0 = __shfl_sync(0xffffffffu, t0, src);
+            live = 1;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        want -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    return t;
+    return PromptTile{q0, k0, rows, keys, t0, live};
 }
 
 // Key tiles of each of a block's two query tiles, its tokens, and the keys that all of
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         } else if (first_clean < 2 * n) {
             named_bar_sync(PR_CLEAN_BAR, 96);
             // infinities and NaNs of the value tiles with masked keys become zero
-                        for (int j = max(0, jclean); j < n; ++j) {
+            for (int j = max(0, jclean); j < n; ++j) {
                 wait(&v_full[j - jclean], 0, DEVERR_TIMEOUT_FULL);
                 uint8_t* vt = ring + (2 * j + 1) % PR_STAGES * PR_TILE;
                 bool seen = false;

@@ -198,6 +198,20 @@ def test_prompt_key_lengths(dq, lq, lk):
         at += a
 
 
+@pytest.mark.parametrize("n", [128, 129, 700])
+def test_prompt_many_sequences(dq, n):
+    # more sequences than one look at the offsets takes (128), some of them empty or without keys
+    g = gen(n)
+    lq, lk = [i * 7 % 5 for i in range(n)], [i * 5 % 11 for i in range(n)]
+    q, k, v = (randn(g, sum(x), h, HD, dtype=torch.float16) for x, h in ((lq, 4), (lk, 2), (lk, 2)))
+    check_prompt(dq, q, k, v, lq, lk)
+    assert dq.device_error() == 0
+    bad = starts(lq)
+    bad[3] = sum(lq) + 1  # far from the end, where the search begins: reported all the same
+    dq.attention_prompt(q, k, v, i32(bad), i32(starts(lk)))
+    assert dq.device_error() == BAD_ARG
+
+
 def test_prompt_over_cache_planes_and_into_a_strided_output(dq):
     g = gen(9)
     planes = randn(g, 2, 4, 700, HD, dtype=torch.float16)  # [k or v][n_kv][max_ctx][128]
