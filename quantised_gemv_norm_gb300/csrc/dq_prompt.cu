@@ -73,6 +73,10 @@ constexpr int PR_SMEM = (2 + PR_STAGES) * PR_TILE + 1024 /* alignment */ + 512;
 constexpr uint32_t PR_S0 = 0, PR_O0 = 256, PR_TCOLS = 512;  // tensor memory columns: S0 S1 O0 O1
 constexpr float PR_C = 0.08838834764831845f * 1.4426950408889634f;
 constexpr float PR_GROW = 8.0f;  // log2 of the growth of the maximum that is let pass
+// c s - c m in one fused step has the rounding of c m in it, the same for a whole row until m
+// moves: 2^-12 at this size of m, 2^13 at the largest that fp16 can give.  Past it m is
+// subtracted from s first.
+constexpr float PR_FAR = 32768.0f;
 
 struct PromptArgs {
     CUtensorMap tq, tk, tv;
@@ -350,7 +354,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
         const int tok = tile.t0 + t * a.tq_tokens + row_tok;  // within the sequence
         const bool mine = row_tok < sp.ntok[t];
         const int lim = min(tile.lk, max(0, tok + 1 + tile.lk - tile.lq));  // keys this row sees
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, base = 0.f;
+        bool far = false;  // |m| > PR_FAR for some row of the warp
         for (int j = 0; j < end; ++j) {
             wait(&s_full[t], j & 1, DEVERR_TIMEOUT_FULL);
             __syncwarp();
@@ -388,12 +393,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
             }
             const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
             const bool grow = (top - m) * PR_C > PR_GROW;
-            if (__any_sync(0xffffffffu, grow)) {
+            if (__any_sync(0xffffffffu, grow || far)) {
                 const float mn = grow ? top : m;
                 const float alpha = grow ? ex2((m - mn) * PR_C) : 1.0f;  // 0 from -infinity
                 m = mn;
                 l *= alpha;
-                if (j > 0) {
+                const float ref = m == -INFINITY ? 0.f : m;
+                far = __any_sync(0xffffffffu, fabsf(ref) > PR_FAR);
+                base = far ? 0.f : -ref * PR_C;
+                if (far) {
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        s[i] = __float_as_uint(__uint_as_float(s[i]) - ref);
+                }
+                if (j > 0 && __any_sync(0xffffffffu, grow)) {
                     wait(&o_full[t], (j - 1) & 1, DEVERR_TIMEOUT_FULL);
                     __syncwarp();
                     tc_fence_after_sync();
@@ -409,7 +422,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                     }
                 }
             }
-            const float base = m == -INFINITY ? 0.f : -m * PR_C;
             const uint64_t c2 = f2(PR_C, PR_C), b2 = f2(base, base);
             uint64_t sum0 = 0ull, sum1 = 0ull;
 #pragma unroll
