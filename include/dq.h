@@ -344,8 +344,10 @@ DQ_API int dq_qkv_rope(const float* qkv, long long row_stride, const int* positi
  * no copy.  total_q and total_k are the rows that q / out and k / v have; no other
  * row is read or written, and output rows of no sequence are left as they were.
  * Scores and sums are fp32; the probabilities are rounded to `type` for the product
- * with v, as the operands of the tensor cores are.  A masked key or value takes no
- * part whatever it holds, infinities and NaN included.  An offset array that
+ * with v, as the operands of the tensor cores are: in fp16 also to steps of 2^-31 of the
+ * row's largest one, below 2^-32 of it to zero.  A masked key or value takes no
+ * part whatever it holds, infinities and NaN included; an infinity in v that a query sees
+ * with a probability of zero gives NaN or that infinity.  An offset array that
  * decreases or leaves its total sets the bad-argument bit of the device's error
  * flag and its sequence is left out.
  * Strides are multiples of 8, the base pointers 16-byte aligned; out must not

@@ -7,16 +7,18 @@
 // of 128 keys, for each query tile:
 //   S = Q K^T     tcgen05.mma, 128 x 128 fp32 in tensor memory, operands in shared
 //                 memory (TMA, 128-byte swizzle);
-//   P = 2^(c S - c m), c = log2(e) / sqrt(128), by four warps, one row a thread, with
-//                 the row's running maximum m and sum l in fp32 registers; P goes
+//   P = 2^(c S - c m + b), c = log2(e) / sqrt(128), by four warps, one row a thread,
+//                 with the row's running maximum m and sum l in fp32 registers; P goes
 //                 back into tensor memory over S as 16-bit pairs;
 //   O += P V      tcgen05.mma, P from tensor memory, V N-major from shared memory,
 //                 128 x 128 fp32 in tensor memory.
 // While the tensor cores work on one query tile, the other tile's warps do their
 // exponentials.  m follows the true maximum only when that has grown by more than
-// 2^8 (then l and O are scaled): the ratio P / l does not depend on which m is
-// used, P stays below 2^8 in fp16 and every sum is fp32, and the scaling of O,
-// which would wait for the last product, is rare after the first tiles.
+// 2^8 (then l and O are scaled): the ratio P / l does not depend on which m and b are
+// used and every sum is fp32, and the scaling of O, which would wait for the last
+// product, is rare after the first tiles.  b is 7 in fp16, so that P fills its range up
+// to 2^15 and a key is lost only below 2^-32 of the largest probability (with b = 0,
+// 2^-25: 16000 keys of that size beside one key of value zero were gone); 0 in bf16.
 //
 // 8192 tokens, 32 heads on 8 KV heads, fp16: 385 us, 1430 TFLOP/s (0.75 of the
 // measured bf16 rate; 0.83 of the rate that the power limit leaves a library product
@@ -77,6 +79,9 @@ constexpr float PR_GROW = 8.0f;  // log2 of the growth of the maximum that is le
 // moves: 2^-12 at this size of m, 2^13 at the largest that fp16 can give.  Past it m is
 // subtracted from s first.
 constexpr float PR_FAR = 32768.0f;
+// b of a type: P <= 2^(b + PR_GROW)
+template <typename T>
+constexpr float PR_TOP = std::is_same<T, __nv_bfloat16>::value ? 0.f : 7.f;
 
 struct PromptArgs {
     CUtensorMap tq, tk, tv;
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 l *= alpha;
                 const float ref = m == -INFINITY ? 0.f : m;
                 far = __any_sync(0xffffffffu, fabsf(ref) > PR_FAR);
-                base = far ? 0.f : -ref * PR_C;
+                base = far ? PR_TOP<T> : fmaf(-ref, PR_C, PR_TOP<T>);
                 if (far) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)

@@ -14,6 +14,42 @@ pytestmark = pytest.mark.gpu
 assert dq  # the fixture
 
 
+def sink_inputs(g, below, n, queries, n_q, n_kv, dtype):
+    """q, k, v whose key 0 has a value of zero and 2^below times the usual probability of the n - 1 others."""
+    q, k, v = randn(g, queries, n_q, HD), 0.25 * randn(g, n, n_kv, HD), randn(g, n, n_kv, HD)
+    q[..., 0] = 16.0
+    k[..., 0] = 0.0
+    k[0] = 0.0
+    k[0, :, 0] = below * math.log(2.0) * math.sqrt(HD) / 16.0
+    v[0] = 0.0
+    return q.to(dtype), k.to(dtype), v.to(dtype)
+
+
+# One query tile's keys split over blocks (8 heads on 2), or not (80 blocks already).
+@pytest.mark.parametrize("n_q,n_kv", [(8, 2), (80, 80)])
+@pytest.mark.parametrize("below", [18, 24, 26])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_prompt_small_probabilities_beside_a_large_one(dq, below, n_q, n_kv, dtype):
+    # An fp16 probability is one of steps of 2^-24 below 2^-14, with the largest at 2^7: 2^-26 of it is 32 steps, each
+    # key's rounding half a step at most, 2^-32 of the largest.  The keys' probabilities spread over 8 steps and more,
+    # so the roundings are independent: six of their standard deviations, 2^-32 / sqrt(3) sqrt(sum v^2), are allowed.
+    n, queries = 16001, 3
+    q, k, v = sink_inputs(gen(below + n_q), below, n, queries, n_q, n_kv, dtype)
+    cu, ck = [0, queries], [0, n]
+    y = dq.attention_prompt(q, k, v, i32(cu), i32(ck))
+    r, size = prompt_ref(q, k, v, cu, ck)
+    spread = (v.double() ** 2).sum(0).sqrt().repeat_interleave(n_q // n_kv, 0)
+    slack = (U[dtype] + 4e-5) * size + 6 * 2.0 ** -32 / math.sqrt(3) * spread
+    within(y, r, slack)
+    # an infinity that a query sees with such a probability is there, whether or not its tile has masked keys
+    v[100, 0, 5], v[n - queries, 0, 6] = math.inf, -math.inf
+    y = dq.attention_prompt(q, k, v, i32(cu), i32(ck))
+    group = n_q // n_kv
+    assert bool((y[:, :group, 5] == math.inf).all()) and bool((y[:, :group, 6] == -math.inf).all())
+    r[:, :group, 5:7], y[:, :group, 5:7] = 0, 0
+    within(y, r, slack)
+
+
 def one_key_rows(scores, gap):
     """Rows [queries, heads] whose largest score leaves the next one behind by more than ``gap``."""
     top = scores.topk(2, -1).values
