@@ -24,7 +24,10 @@
 //
 // p_j = 2^(s_j - r) with a reference r a head that follows the running maximum only
 // when some s_j - r passes a cap: p_j d_jg stays in fp16's normal range on both
-// sides, and the outputs are scaled only a few times a sequence.
+// sides, and the outputs are scaled only a few times a sequence.  s_j is rounded once
+// more, to the unit of r, before r is subtracted (relative error at 100001 keys 8.5e-7, 8.4e-7
+// in one fused step): the largest score is then the same number in both, where the fused
+// step left out the rounding that r has and passed fp16's range at scores of 2^26.
 #include <algorithm>
 
 #include "dq_kv4.cuh"
@@ -234,8 +237,11 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
         int e = static_cast<int>(__float_as_uint(top) >> 23) - 127 - 6;
         e = max(-100, min(121, e));
         const float scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        // to scores in powers of two; from small codes they come in units of 2^-24
-        unscale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) *
+        // to scores in powers of two; from small codes they come in units of 2^-24.  Queries
+        // past the bound on e (2^95, 16-bit ones 2^71) take the bound's unit: two of their scores
+        // differ by 2^-48 (2^-72) or more before it, by 2^13 after it, or not at all, and no
+        // product with it passes fp32's range
+        unscale = __uint_as_float(static_cast<uint32_t>(127 + min(e, TWO ? 88 : 64)) << 23) *
                   ((TWO ? 1.f : 16777216.f) * 0.08838834764831845f * 1.4426950408889634f);
         float qsum[4];
 #pragma unroll
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
                 vs[1] = vs[3] = 0;
             __syncwarp();
         }
-        // scores of keys 8 nt + 2 tq, + 1 for head h, before `unscale`
+        // scores of keys 8 nt + 2 tq, + 1 for head h
         uint64_t s[2];
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -329,7 +335,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
                        t[2], t[3]);
                 acc = fma2(ka_both<TWO>(t2), half2_f2(dd[k]), acc);
             }
-            s[nt] = acc;
+            s[nt] = mul2(acc, f2(unscale, unscale));
         }
         if (TAIL) {
 #pragma unroll
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
                 dmax = __hmax2(dmax, *reinterpret_cast<const __half2*>(&vd[nt][k]));
         }
         const float2 s0 = un2(s[0]), s1 = un2(s[1]);
-        const float top = fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y)) * unscale;
+        const float top = fmaxf(fmaxf(s0.x, s0.y), fmaxf(s1.x, s1.y));
         // d <= lim keeps p d at 2^15 or below under the cap.  A larger one lowers the cap, by no
         // more than it takes: the lower it is, the fewer bits p d has above fp16's smallest
         // number in groups with small scales (d of 1e-3 and the lowest cap: 2^-11 of them)
@@ -372,7 +378,8 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             }
             float f = 1.f;
             if (t - r > cap) {
-                const float rn = t - (cap - KA_HEAD);
+                float rn = t - (cap - KA_HEAD);
+                rn = t - rn > cap ? t : rn;  // a score of 2^27 and more: rounded past the cap
                 f = ex2(r - rn);
                 r = rn;
             }
@@ -387,8 +394,8 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
                     o[k >> 1][k & 1][e] *= e & 1 ? f1 : f0;
             }
         }
-        const float2 e0 = un2(fma2(s[0], f2(unscale, unscale), f2(-r, -r)));
-        const float2 e1 = un2(fma2(s[1], f2(unscale, unscale), f2(-r, -r)));
+        const float2 e0 = un2(add2(s[0], f2(-r, -r)));
+        const float2 e1 = un2(add2(s[1], f2(-r, -r)));
         const uint64_t p0 = f2(ex2(e0.x), ex2(e0.y)), p1 = f2(ex2(e1.x), ex2(e1.y));
         lacc = add2(lacc, add2(p0, p1));
         {

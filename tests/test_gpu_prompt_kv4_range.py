@@ -8,7 +8,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_prompt_kv4 import dq, gen, HD, i32, prompt_ref, randn, U, within
+from test_gpu_prompt_kv4 import (build_cache, decode_ref, decode_slack, dq, gen, HD, i32, prompt_ref, quantise_ref,
+                                 randn, U, within)
 
 pytestmark = pytest.mark.gpu
 assert dq  # the fixture
@@ -77,3 +78,43 @@ def test_prompt_scores_far_from_zero(dq, lq, lk, dtype, scale):
     assert float(clear.double().mean()) > 0.9
     assert bool(torch.isfinite(y).all())
     within(y[clear], r[clear], U[dtype] * size[clear])
+
+
+@pytest.mark.parametrize("n", [200, 6000])
+@pytest.mark.parametrize("dtype,scale", [
+    (torch.float32, 1e5), (torch.float32, 1e9), (torch.float32, 1e20), (torch.float32, 1e37), (torch.float16, 15000.0),
+    (torch.bfloat16, 1e9), (torch.bfloat16, 1e20), (torch.bfloat16, 1e37),
+])
+def test_decode_scores_far_from_zero(dq, n, dtype, scale):
+    # Scores of +-4 scale, off by at most 6e-5 scale (two parts: (2^-21 + 128 2^-24) sum |q k| / sqrt(128); 16-bit
+    # queries: 2e-5): where the two largest are further apart than that, one key is the output.
+    pool, table, ks, vs, zs = build_cache(dq, n, [n], 2, 64)
+    q = randn(gen(n + 1), 1, 8, HD).mul(scale).to(dtype)
+    if dtype == torch.float16:
+        q = q.clamp(-65504, 65504)
+    y = dq.attention_decode_kv4(q, pool, table, i32([n]), n)
+    r, size = decode_ref(q, ks, vs, [n])
+    s = torch.einsum("hd,jhd->hj", q[0].double(), ks[0].repeat_interleave(4, 1)) / math.sqrt(HD)
+    clear = one_key_rows(s, 1e-3 * scale)[None]
+    assert float(clear.double().mean()) > 0.8
+    assert bool(torch.isfinite(y).all())
+    slack = decode_slack(q, ks, vs, zs, [n], size)
+    within(y[clear], r[clear], slack[clear])
+
+
+@pytest.mark.parametrize("n", [200, 6000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_decode_large_queries_over_equal_keys(dq, n, dtype):
+    # every score is zero, whatever the queries' size
+    g = gen(n)
+    k, v = torch.zeros(n, 2, HD, device="cuda"), randn(g, n, 2, HD)
+    pages = -(-n // 64)
+    pool, table = dq.kv4_pool(pages, 2, 64), torch.arange(pages, device="cuda").int()[None]
+    slots = torch.arange(n, device="cuda").int()
+    dq.kv4_append(k, v, slots, pool)
+    kk, vv = (x.double() for x in dq.kv4_read(pool, slots, dtype=torch.float32))
+    z = torch.from_numpy(quantise_ref(v.cpu().numpy())[1]).cuda().double().repeat_interleave(32, -1)
+    q = randn(g, 1, 8, HD).mul(1e37).to(dtype)
+    y = dq.attention_decode_kv4(q, pool, table, i32([n]), n)
+    r, size = decode_ref(torch.zeros_like(q), [kk], [vv], [n])
+    within(y, r, decode_slack(torch.zeros_like(q), [kk], [vv], [z], [n], size))
