@@ -48,7 +48,7 @@ struct Kv4AttnArgs {
     const unsigned char* pool;
     const int* pages;
     const int* n_keys;
-    float* part;       // [n_seq][n_kv][splits][8][KA_PART], or null: one block a sequence and KV head
+    float* part;       // [n_seq][n_kv][splits][group][KA_PART], or null: one block a sequence and KV head
     int n_seq, n_q, group, splits, chunk;  // chunk: 16-key blocks a thread block
     Kv4Shape s;
     int max_pages, max_keys;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             v.w += f * y.w;
         }
         if (a.part) {
-            float* pp = a.part + (((static_cast<size_t>(b) * a.s.n_kv + g) * a.splits + c) * 8 + hd) * KA_PART;
+            float* pp = a.part + (((static_cast<size_t>(b) * a.s.n_kv + g) * a.splits + c) * a.group + hd) * KA_PART;
             if (lane == 0) {
                 pp[0] = m;
                 pp[1] = l;
@@ -548,8 +548,8 @@ __global__ void __launch_bounds__(32 * JOIN) kv4_join_kernel(const Kv4AttnArgs a
     if (n < 0 || n > a.max_keys)
         n = 0;
     const int blocks = (n + KV4_ROWS - 1) / KV4_ROWS, splits = (blocks + a.chunk - 1) / a.chunk;
-    const float* base = a.part + ((static_cast<size_t>(b) * a.s.n_kv + g) * a.splits * 8 + h) * KA_PART;
-    constexpr size_t step = 8 * KA_PART;
+    const float* base = a.part + ((static_cast<size_t>(b) * a.s.n_kv + g) * a.splits * a.group + h) * KA_PART;
+    const size_t step = static_cast<size_t>(a.group) * KA_PART;
     pdl_wait();
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -623,6 +623,12 @@ struct Kv4Split {
     int chunk, splits;
 };
 
+static bool kv4_counts_fit(int n_seq, int n_q, int n_kv, int max_keys)
+{
+    return n_q / n_kv <= 8 && n_kv <= (1 << 16) && max_keys <= (1 << 30) &&
+           static_cast<long long>(n_seq) * n_q <= 0x7fffffffll;
+}
+
 // A thread block costs about two microseconds beside its keys, and a split's result
 // is written and read back.  So: 16 blocks (256 keys) or fewer are not split (1 x 256
 // keys: 5.5 us, 5.9 in two); where sequences and KV heads alone fill the card, splits
@@ -630,7 +636,10 @@ struct Kv4Split {
 // over two blocks an SM in splits of 128 to 512 keys (1 x 2000: 6.4 us, 9.8 with 512; 1
 // x 16000: 13.1 us with 512, 14.4 with 288), and more than that over the three that are
 // resident.  A batch's splits end at 1024 keys, so that sequences of different lengths
-// share the card evenly.
+// share the card evenly; where its sequences and KV heads fill the card several times
+// over, at as many times that, so that blocks and scratch go by max_keys and the card and
+// not by the batch as well (256 sequences, 32 heads on 8, a bound of 131072 keys: 1000 keys
+// each 332 -> 152 us, one of all 131072 among them 368 -> 182 us, scratch 1.1 GB -> 125 MB).
 static Kv4Split kv4_split(int n_seq, int n_kv, int max_keys)
 {
     const long long blocks = (static_cast<long long>(max_keys) + dq::KV4_ROWS - 1) / dq::KV4_ROWS;
@@ -642,7 +651,7 @@ static Kv4Split kv4_split(int n_seq, int n_kv, int max_keys)
         chunk = std::max((all + dq::KA_RESIDENT * sms - 1) / (dq::KA_RESIDENT * sms), 32ll);
     chunk = std::max(chunk, pairs >= sms ? 32ll : 8ll);
     if (n_seq > 1)
-        chunk = std::min(chunk, 64ll);
+        chunk = std::min(chunk, std::max(64ll, 64 * pairs / (dq::KA_RESIDENT * sms)));
     const long long round = dq::KA_WARPS * dq::KA_STEP;  // what the block's warps take at a time
     chunk = (chunk + round - 1) / round * round;
     return {static_cast<int>(chunk), static_cast<int>((blocks + chunk - 1) / chunk)};
@@ -654,10 +663,10 @@ extern "C" {
 
 DQ_API size_t dq_attention_decode_kv4_workspace_bytes(int n_seq, int n_q, int n_kv, int max_keys)
 {
-    if (n_seq < 1 || n_q < 1 || n_kv < 1 || max_keys < 1)
+    if (n_seq < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv || max_keys < 1 || !dqhost::kv4_counts_fit(n_seq, n_q, n_kv, max_keys))
         return 0;
     const dqhost::Kv4Split sp = dqhost::kv4_split(n_seq, n_kv, max_keys);
-    return sp.splits > 1 ? static_cast<size_t>(n_seq) * n_kv * sp.splits * 8 * dq::KA_PART * sizeof(float) : 0;
+    return sp.splits > 1 ? static_cast<size_t>(n_seq) * n_q * sp.splits * dq::KA_PART * sizeof(float) : 0;
 }
 
 DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, const int* pages, const int* n_keys,
@@ -673,13 +682,13 @@ DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, co
         return st;
     if (max_keys > static_cast<long long>(max_pages) * page_size)
         return DQ_ERR_SHAPE;
-    if (n_q / n_kv > 8 || max_keys > (1 << 30))
+    if (!dqhost::kv4_counts_fit(n_seq, n_q, n_kv, max_keys))
         return DQ_ERR_UNSUPPORTED;
     if (!dqhost::aligned16(q) || !dqhost::aligned16(pool) || !dqhost::aligned16(out))
         return DQ_ERR_ALIGN;
     const dqhost::Kv4Split sp = dqhost::kv4_split(n_seq, n_kv, max_keys);
     const long long blocks = static_cast<long long>(n_seq) * n_kv * sp.splits;
-    if (blocks > 0x7fffffffll || static_cast<long long>(n_seq) * n_q > 0x7fffffffll)
+    if (blocks > 0x7fffffffll)
         return DQ_ERR_UNSUPPORTED;
     if (sp.splits > 1) {
         if (!workspace)

@@ -118,3 +118,29 @@ def test_decode_large_queries_over_equal_keys(dq, n, dtype):
     y = dq.attention_decode_kv4(q, pool, table, i32([n]), n)
     r, size = decode_ref(torch.zeros_like(q), [kk], [vv], [n])
     within(y, r, decode_slack(torch.zeros_like(q), [kk], [vv], [z], [n], size))
+
+
+# ------------------------------------------------------------------ large batches
+
+
+def test_decode_scratch_of_a_large_batch(dq):
+    # one result of 132 numbers a query head for every 1024 keys of three blocks an SM, and one more a sequence
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for n_seq, n_q, n_kv, most in ((256, 32, 8, 131072), (1024, 32, 8, 131072), (64, 64, 64, 20000), (300, 8, 1, 1 << 20)):
+        need = dq.load().dq_attention_decode_kv4_workspace_bytes(n_seq, n_q, n_kv, most)
+        pairs = max(n_seq * n_kv, 3 * sms)
+        splits = most / 1024 * 3 * sms / pairs
+        assert need <= 528 * (n_q // n_kv) * n_seq * n_kv * (1.1 * splits + 1), (n_seq, n_q, n_kv, most)
+
+
+@pytest.mark.parametrize("n_q,n_kv,dtype", [(32, 8, torch.float16), (24, 8, torch.float32)])
+def test_decode_large_batch(dq, n_q, n_kv, dtype):
+    # 1600 pairs of a sequence and a KV head: the splits hold more than 1024 keys
+    lengths = [4000, 3333] + [1, 0, 17, 100, 257] * 39 + [2500, 16, 1100]
+    pool, table, ks, vs, zs = build_cache(dq, n_q, lengths, n_kv, 64)
+    q = randn(gen(n_q), len(lengths), n_q, HD, dtype=dtype)
+    r, size = decode_ref(q, ks, vs, lengths)
+    slack = decode_slack(q, ks, vs, zs, lengths, size)
+    for most in (4000, table.shape[1] * 64):
+        within(dq.attention_decode_kv4(q, pool, table, i32(lengths), most), r, slack)
+    assert dq.device_error() == 0
