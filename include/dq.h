@@ -430,9 +430,12 @@ DQ_API int dq_kv4_read(const void* pool, const int* slots, int type, void* k_out
  * sets the bad-argument bit of the device's error flag (the sequence's output is
  * then zero, a bad page's keys take no part).  max_keys: a bound on every n_keys,
  * known to the host (it sets the split), at most max_pages * page_size.  Scores,
- * softmax and sums are fp32.  For fp32 queries and outputs the queries and
- * probabilities enter the matrix instructions as two fp16 parts each (relative
- * error about 2^-22); for 16-bit ones a probability is one fp16 number.
+ * softmax and sums are fp32.  For fp32 queries and outputs the queries and the products
+ * p_j d_j and p_j of a probability enter the matrix instructions as two fp16 parts each
+ * (relative error about 2^-22); for 16-bit ones such a product is one fp16 number.  Either
+ * is also off by up to max(2^-34, D 2^-36) of the sequence's largest probability, D the KV
+ * head's largest value scale (times |c - 8| or |z| in the output): beside a channel of
+ * 1e5, values around 1e-3 may be off by 1e-3 of themselves.
  * workspace: dq_attention_decode_kv4_workspace_bytes(...) bytes of device scratch
  * for the same counts (NULL where that is 0), 16-byte aligned, its content before
  * and after the call of no meaning; calls that share one must not overlap in time.

@@ -23,8 +23,11 @@
 // MB, 43 us (2.95 TB/s, two parts).  A call of 64 keys takes 3.4 us in a graph.
 //
 // p_j = 2^(s_j - r) with a reference r a head that follows the running maximum only
-// when some s_j - r passes a cap: p_j d_jg stays in fp16's normal range on both
-// sides, and the outputs are scaled only a few times a sequence.  s_j is rounded once
+// when some s_j - r passes a cap: p_j d_jg stays below fp16's largest number, and the
+// outputs are scaled only a few times a sequence.  The cap is 12 where every value scale
+// d is 8 or less and falls with the largest one seen, to -1; the largest p is within 2^3 of
+// it.  Products below 2^-14 lose bits, each is off by half of fp16's smallest step (2^-25)
+// at most: 2^-34 max(1, D / 4) of the largest p, D the largest scale.  s_j is rounded once
 // more, to the unit of r, before r is subtracted (relative error at 100001 keys 8.5e-7, 8.4e-7
 // in one fused step): the largest score is then the same number in both, where the fused
 // step left out the rounding that r has and passed fp16's range at scores of 2^26.

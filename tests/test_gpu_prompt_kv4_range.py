@@ -120,6 +120,75 @@ def test_decode_large_queries_over_equal_keys(dq, n, dtype):
     within(y, r, decode_slack(torch.zeros_like(q), [kk], [vv], [z], [n], size))
 
 
+# ----------------------------------------------------- value scales of all sizes
+
+
+def scales_slack(q, keys, values, value_scales, value_z, lengths, dtype):
+    """The usual bound with B = sum p (|v - z| + |z|) in place of A, and what fp16's smallest step leaves of a key's
+    products: (8 + |z|) max(2^-34, D 2^-36) of the sequence's largest probability, D the KV head's largest scale."""
+    parts = [(v - z).abs() + z.abs() for v, z in zip(values, value_z)]
+    b = decode_ref(q, keys, parts, lengths)[0]
+    slack = 2e-5 * b if dtype == torch.float32 else (6e-5 + 2.0 ** -11) * b
+    for i, n in enumerate(lengths):
+        group = q.shape[1] // keys[i].shape[1]
+        s = torch.einsum("hd,jhd->hj", q[i].double(), keys[i].repeat_interleave(group, 1)) / math.sqrt(HD)
+        top = torch.softmax(s, 1).amax(1)[:, None]
+        most = value_scales[i].amax((0, 2)).repeat_interleave(group)[:, None]
+        step = torch.maximum(torch.full_like(most, 2.0 ** -34), most * 2.0 ** -36)
+        slack[i] += step * top * (8 + value_z[i].abs()).sum(0).repeat_interleave(group, 0)
+    return slack
+
+
+def decode_case(dq, k, v, q, copies):
+    """One sequence's rows, read by ``copies`` sequences with queries of their own."""
+    n, n_kv = k.shape[:2]
+    pages = -(-n // 64)
+    pool = dq.kv4_pool(pages, n_kv, 64)
+    table = torch.arange(pages, device="cuda").int()[None].repeat(copies, 1)
+    slots = torch.arange(n, device="cuda").int()
+    dq.kv4_append(k, v, slots, pool)
+    kk, vv = (x.double() for x in dq.kv4_read(pool, slots, dtype=torch.float32))
+    assert bool(torch.isfinite(vv).all())
+    d, z = (torch.from_numpy(x).cuda().double() for x in quantise_ref(v.cpu().numpy())[:2])
+    y = dq.attention_decode_kv4(q, pool, table, i32([n] * copies), n)
+    assert dq.device_error() == 0
+    keys, values, lengths = [kk] * copies, [vv] * copies, [n] * copies
+    r, _ = decode_ref(q, keys, values, lengths)
+    within(y, r, scales_slack(q, keys, values, [d] * copies, [z.repeat_interleave(32, -1)] * copies, lengths, q.dtype))
+
+
+# 240 keys: one block, whose warps each take cache blocks of the first and of the last keys; 600: splits of 128 keys;
+# 20 sequences of 8 KV heads: splits of 512 keys
+@pytest.mark.parametrize("n,copies,n_kv", [(240, 1, 2), (600, 1, 2), (1500, 20, 8)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("small", [1.0, 1e-3])
+def test_decode_scales_that_grow_along_the_keys(dq, n, copies, n_kv, dtype, small):
+    # ordinary values, then scales of 100, then one of 40000 (fp16's last binade), all in one KV head
+    g = gen(n + copies)
+    k, v = randn(g, n, n_kv, HD), randn(g, n, n_kv, HD) * small
+    a, b = 9 * n // 16, 14 * n // 16
+    v[a:b, 0, 3], v[a:b, 0, 4] = 750.0, -750.0
+    v[b:, 0, 70], v[b:, 0, 90] = 3e5, -3e5
+    decode_case(dq, k, v, (0.3 * randn(g, copies, 4 * n_kv, HD)).to(dtype), copies)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+def test_decode_scales_that_fall_along_the_keys(dq, dtype):
+    # the largest scale first: the later keys' products stay under its lower cap
+    g = gen(7)
+    k, v = randn(g, 250, 2, HD), randn(g, 250, 2, HD)
+    v[0, :, 3], v[0, :, 4] = 3e5, -3e5
+    decode_case(dq, k, v, randn(g, 1, 8, HD).to(dtype), 1)
+
+
+@pytest.mark.parametrize("n", [250, 6000])
+@pytest.mark.parametrize("below", [12, 20])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_decode_small_probabilities_beside_a_large_one(dq, n, below, dtype):
+    q, k, v = sink_inputs(gen(below + n), below, n, 1, 8, 2, torch.float32)
+    decode_case(dq, k, v, q.to(dtype), 1)
+
+
 # ------------------------------------------------------------------ large batches
 
 
