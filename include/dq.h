@@ -349,7 +349,8 @@ DQ_API int dq_qkv_rope(const float* qkv, long long row_stride, const int* positi
  * part whatever it holds, infinities and NaN included; an infinity in v that a query sees
  * with a probability of zero gives NaN or that infinity.  An offset array that
  * decreases or leaves its total sets the bad-argument bit of the device's error
- * flag and its sequence is left out.
+ * flag; the output rows below total_q are then undefined (sequences may be left out, or
+ * overlap), and nothing else is touched.
  * Strides are multiples of 8, the base pointers 16-byte aligned; out must not
  * overlap the inputs.
  * workspace: device scratch of dq_attention_prompt_workspace_bytes(...) bytes for

@@ -8,8 +8,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_prompt_kv4 import (build_cache, decode_ref, decode_slack, dq, gen, HD, i32, prompt_ref, quantise_ref,
-                                 randn, U, within)
+from test_gpu_prompt_kv4 import (BAD_ARG, build_cache, decode_ref, decode_slack, dq, gen, HD, i32, prompt_ref,
+                                 quantise_ref, randn, U, within)
 
 pytestmark = pytest.mark.gpu
 assert dq  # the fixture
@@ -213,3 +213,27 @@ def test_decode_large_batch(dq, n_q, n_kv, dtype):
     for most in (4000, table.shape[1] * 64):
         within(dq.attention_decode_kv4(q, pool, table, i32(lengths), most), r, slack)
     assert dq.device_error() == 0
+
+
+# ------------------------------------------------------------------- bad offsets
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [
+    ([0, 600, 100, 1000], None),  # rows of two sequences, more block tiles than valid offsets can need
+    ([0, 600, 100, 1000], [0, 600, 100, 1000]), ([0, 1000, 0, 1000, 0, 1000, 0], None), ([0, 300, 1001, 1000], None),
+    ([-5, 300, 600, 1000], None), ([0, 300, 600, 1000], [0, 300, 1001, 1000]), ([0, 300, 600, 1000], [0, 700, 2, 1000]),
+    ([0, 300, 600, 1000], [-2147483648, 2147483647, 0, 1000]),
+])
+def test_prompt_bad_offsets_touch_nothing_outside(dq, cu_q, cu_k):
+    g = gen(17)
+    n = 1000
+    q, k, v = (randn(g, n, h, HD, dtype=torch.float16) for h in (8, 2, 2))
+    wide = torch.full((n + 400, 10, HD), 5.0, dtype=torch.float16, device="cuda")
+    dq.attention_prompt(q, k, v, i32(cu_q), None if cu_k is None else i32(cu_k), out=wide[200:-200, 1:9])
+    assert dq.device_error() == BAD_ARG
+    assert bool((wide[:200] == 5).all()) and bool((wide[-200:] == 5).all())
+    assert bool((wide[:, 0] == 5).all()) and bool((wide[:, 9] == 5).all())
+    # the next call is not affected
+    y = dq.attention_prompt(q, k, v, i32([0, 300, 600, 1000]))
+    r, size = prompt_ref(q, k, v, [0, 300, 600, 1000], [0, 300, 600, 1000])
+    within(y, r, (U[q.dtype] + 4e-5) * size)
