@@ -6,9 +6,9 @@
 // and scales together) into a ring of its own in shared memory with bulk copies and
 // keeps its own running reference exponent, sum and output, all in registers;
 // the block's warps meet once at the end, the blocks of one sequence in a second
-// kernel.  The cache bytes bound it, so the arithmetic goes to the (warp-level)
-// matrix instructions m16n8k16, whose 16 rows hold the group's up to 8 query heads
-// twice: the fp16 part of a query in row h and, for fp32 results, the rest of it in row
+// kernel.  Its floor is the cache's bytes, so the arithmetic goes to the
+// (warp-level) matrix instructions m16n8k16, whose 16 rows hold the group's up to 8 query
+// heads twice: the fp16 part of a query in row h and, for fp32 results, the rest of it in row
 // 8 + h, which gives 22 bits for the price of 11 with so few rows.  The codes c - 8 are
 // exact in fp16 and need no scale before the product:
 //   s_j   = sum_g d_jg (sum_{n in g} q_n (c_jn - 8)) + z_jg (sum_{n in g} q_n)
@@ -16,11 +16,12 @@
 // with g the groups of 32 dims; p_j d_jg is again two fp16 parts for fp32 results and
 // one for 16-bit ones.
 //
-// A cache block takes a warp 405 instructions with one part (half of them codes and
-// scales made into operands) and 450 with two; with 12 warps an SM these are issued at
-// 0.6 a clock and scheduler, and that, not the memory, bounds it: 48 sequences of 1 to
-// 12000 keys, 325 MB, 85 us (3.8 TB/s; 48 us at the memory's rate), one of 100001, 128
-// MB, 43 us (2.95 TB/s, two parts).  A call of 64 keys takes 3.4 us in a graph.
+// What bounds it is the latency of its chains of instructions: a cache block takes a warp
+// 405 of them with one part (half of them codes and scales made into operands) and 450
+// with two, each warp's largely in sequence, and the 12 warps an SM that 168 registers
+// leave issue 0.60 (0.54) a clock and scheduler.  48 sequences of 1 to 12000 keys, 325 MB:
+// 85 us (3.8 TB/s; 48 us at the memory's rate), one of 100001, 128 MB, two parts: 44 us
+// (2.9 TB/s; 19 us).  A call of 64 keys takes 3.4 us in a graph.
 //
 // p_j = 2^(s_j - r) with a reference r a head that follows the running maximum only
 // when some s_j - r passes a cap: p_j d_jg stays below fp16's largest number, and the
@@ -105,7 +106,12 @@ __device__ __forceinline__ void ka_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// The same in place.
+// The same from zero, and in place.
+__device__ __forceinline__ void ka_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1)
+{
+    ka_mma(d, a0, a1, a2, a3, b0, b1, 0.f, 0.f, 0.f, 0.f);
+}
 __device__ __forceinline__ void ka_mma_add(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                            uint32_t b1)
 {
@@ -288,11 +294,6 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
     float r = -INFINITY, cap = KA_CAP;
     uint32_t lim = 0x48004800u;  // 2^(15 - cap) as an fp16 pair: 8 at first
 
-    // the zero accumulator operand, kept in registers: as a constant it would be written
-    // before every matrix instruction (64 moves a block)
-    const float zz[4] = {__uint_as_float(ka_opaque(0u)), __uint_as_float(ka_opaque(0u)), __uint_as_float(ka_opaque(0u)),
-                         __uint_as_float(ka_opaque(0u))};
-
     // One cache block, `left` (1 or more) of its keys seen; all of them without TAIL.
     auto block = [&](auto tail, unsigned char* kb, int left) {
         constexpr bool TAIL = decltype(tail)::value;
@@ -319,8 +320,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             const uint4 zs = lds128(kb + KV4_KSCALES + 32 * (4 * nt + (h >> 1)) + 16 * (tq & 1));
             const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w}, dd[4] = {sc0.x, sc0.z, sc1.x, sc1.z};
             float m[4];
-            ka_mma(m, qz, 0u, qd, 0u, __byte_perm(zs.y, zs.w, odd), TWO ? 0u : __byte_perm(zs.x, zs.z, odd), zz[0], zz[1],
-                   zz[2], zz[3]);
+            ka_mma(m, qz, 0u, qd, 0u, __byte_perm(zs.y, zs.w, odd), TWO ? 0u : __byte_perm(zs.x, zs.z, odd));
             const float u24 = 1.f / 16777216.f;
             uint64_t acc = TWO ? f2(m[0], m[1]) : mul2(f2(m[0], m[1]), f2(u24, u24));
 #pragma unroll
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
                 else
                     ka_small_codes(words[k], p);
                 float t[4], t2[4];
-                ka_mma(t, qa[2 * k][0], qa[2 * k][1], qa[2 * k][2], qa[2 * k][3], p[0], p[1], zz[0], zz[1], zz[2], zz[3]);
+                ka_mma(t, qa[2 * k][0], qa[2 * k][1], qa[2 * k][2], qa[2 * k][3], p[0], p[1]);
                 ka_mma(t2, qa[2 * k + 1][0], qa[2 * k + 1][1], qa[2 * k + 1][2], qa[2 * k + 1][3], p[2], p[3], t[0], t[1],
                        t[2], t[3]);
                 acc = fma2(ka_both<TWO>(t2), half2_f2(dd[k]), acc);
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
             const uint32_t z0 = lds32(zs), z1 = lds32(zs + 128);
             if (TWO) {
                 float m[4], m2[4];
-                ka_mma(m, z0, z0, z1, z1, h0, h1, zz[0], zz[1], zz[2], zz[3]);
+                ka_mma(m, z0, z0, z1, z1, h0, h1);
                 ka_mma(m2, z0, z0, z1, z1, l0, l1, m[0], m[1], m[2], m[3]);
                 ka_add(zacc, m2);
             } else {
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(32 * KA_WARPS, KA_RESIDENT) kv4_attn_kernel(co
                 // 1.6e-6 with it, 4.1e-7 so)
                 if (TWO) {
                     float m[4], m2[4];
-                    ka_mma(m, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], h0, h1, zz[0], zz[1], zz[2], zz[3]);
+                    ka_mma(m, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], h0, h1);
                     ka_mma(m2, b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], l0, l1, m[0], m[1], m[2], m[3]);
                     ka_add(o[k][j], m2);
                 } else {
