@@ -403,13 +403,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1) prompt_kernel(const __grid_cons
                 const float alpha = grow ? ex2((m - mn) * PR_C) : 1.0f;  // 0 from -infinity
                 m = mn;
                 l *= alpha;
-                const float ref = m == -INFINITY ? 0.f : m;
-                far = __any_sync(0xffffffffu, fabsf(ref) > PR_FAR);
-                base = far ? PR_TOP<T> : fmaf(-ref, PR_C, PR_TOP<T>);
+                // a row's own m alone decides: its result is the same whatever the other rows hold
+                const float ref = m == -INFINITY ? 0.f : m, off = fabsf(ref) > PR_FAR ? ref : 0.f;
+                far = __any_sync(0xffffffffu, off != 0.f);
+                base = fmaf(off - ref, PR_C, PR_TOP<T>);
                 if (far) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
-                        s[i] = __float_as_uint(__uint_as_float(s[i]) - ref);
+                        s[i] = __float_as_uint(__uint_as_float(s[i]) - off);
                 }
                 if (j > 0 && __any_sync(0xffffffffu, grow)) {
                     wait(&o_full[t], (j - 1) & 1, DEVERR_TIMEOUT_FULL);

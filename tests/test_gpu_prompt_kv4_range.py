@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from test_gpu_prompt_kv4 import (BAD_ARG, build_cache, decode_ref, decode_slack, dq, gen, HD, i32, prompt_ref,
-                                 quantise_ref, randn, U, within)
+                                 quantise_ref, randn, starts, U, within)
 
 pytestmark = pytest.mark.gpu
 assert dq  # the fixture
@@ -80,6 +80,23 @@ def test_prompt_scores_far_from_zero(dq, lq, lk, dtype, scale):
     within(y[clear], r[clear], U[dtype] * size[clear])
 
 
+@pytest.mark.parametrize("n_q,lq,lk", [(4, 70, 70), (127, 3, 3), (4, 5, 3000)])
+def test_prompt_a_row_far_from_zero_changes_no_other(dq, n_q, lq, lk):
+    g = gen(n_q + lk)
+    q, k, v = (randn(g, n, h, HD, dtype=torch.float16) for n, h in ((lq, n_q), (lk, 1), (lk, 1)))
+    cu, ck = i32([0, lq]), i32([0, lk])
+    want = dq.attention_prompt(q, k, v, cu, ck)
+    q2 = q.clone()
+    q2[1, 2] *= 16000
+    y = dq.attention_prompt(q2, k, v, cu, ck)
+    assert not torch.equal(y[1, 2], want[1, 2])
+    y[1, 2] = want[1, 2]
+    assert torch.equal(y, want)
+    for _ in range(10):  # whatever an earlier call left in shared memory
+        dq.attention_prompt(q2.flip(0).contiguous(), k, v, cu, ck)
+        assert torch.equal(dq.attention_prompt(q, k, v, cu, ck), want)
+
+
 @pytest.mark.parametrize("n", [200, 6000])
 @pytest.mark.parametrize("dtype,scale", [
     (torch.float32, 1e5), (torch.float32, 1e9), (torch.float32, 1e20), (torch.float32, 1e37), (torch.float16, 15000.0),
@@ -118,6 +135,24 @@ def test_decode_large_queries_over_equal_keys(dq, n, dtype):
     y = dq.attention_decode_kv4(q, pool, table, i32([n]), n)
     r, size = decode_ref(torch.zeros_like(q), [kk], [vv], [n])
     within(y, r, decode_slack(torch.zeros_like(q), [kk], [vv], [z], [n], size))
+
+
+def test_calls_repeat_to_the_bit(dq):
+    g = gen(91)
+    lq = [300, 1, 900, 40]
+    q, k, v = (randn(g, sum(lq), h, HD, dtype=torch.bfloat16) for h in (8, 2, 2))
+    pool, table, _, _, _ = build_cache(dq, 92, [5000, 3, 800], 2, 64)
+    x, n = randn(g, 3, 8, HD, dtype=torch.float16), i32([5000, 3, 800])
+    few, fk = randn(g, 6, 8, HD, dtype=torch.float16), randn(g, 9000, 2, HD, dtype=torch.float16)
+
+    def all_three():
+        return (dq.attention_prompt(q, k, v, i32(starts(lq))), dq.attention_prompt(few, fk, fk, i32([0, 6]), i32([0, 9000])),
+                dq.attention_decode_kv4(x, pool, table, n, 5000))
+
+    want = all_three()
+    for _ in range(20):
+        for a, b in zip(all_three(), want):
+            assert torch.equal(a, b)
 
 
 # ----------------------------------------------------- value scales of all sizes
