@@ -272,3 +272,32 @@ def test_prompt_bad_offsets_touch_nothing_outside(dq, cu_q, cu_k):
     y = dq.attention_prompt(q, k, v, i32([0, 300, 600, 1000]))
     r, size = prompt_ref(q, k, v, [0, 300, 600, 1000], [0, 300, 600, 1000])
     within(y, r, (U[q.dtype] + 4e-5) * size)
+
+
+# ------------------------------------------------ into the decode step's fp16 planes
+
+
+def test_prompt_into_the_fp16_planes_and_a_token_after_it(dq):
+    # a prompt's keys and values copied into a layer's planes: the prompt attention reads them there, and the
+    # single-token attention goes on from them (fp64 form: normwise 1e-4, that call's own bound)
+    g = gen(19)
+    n, n_q, n_kv, ctx = 90, 32, 8, 128
+    table = dq.rope_table(ctx)
+    wq, wk = 1 + 0.1 * randn(g, HD), 1 + 0.1 * randn(g, HD)
+    norms = dict(q_norm=wq, k_norm=wk)
+    x = randn(g, n + 1, (n_q + 2 * n_kv) * HD)
+    pos = torch.arange(n + 1, device="cuda").int()
+    q, k, v = dq.qkv_rope(x[:n], pos[:n], table, n_q, n_kv, **norms)
+    planes = torch.full((2, n_kv, ctx, HD), math.nan, dtype=torch.float16, device="cuda")
+    planes[0, :, :n], planes[1, :, :n] = k.transpose(0, 1), v.transpose(0, 1)
+    cu = i32([0, n])
+    rows = planes.transpose(1, 2)
+    assert torch.equal(dq.attention_prompt(q, rows[0][:n], rows[1][:n], cu), dq.attention_prompt(q, k, v, cu))
+    new = x[n].reshape(-1, HD)
+    planes[1, :, n] = new[n_q + n_kv:].half()
+    y = dq.attention_decode_rope(new[:n_q].contiguous(), new[n_q:n_q + n_kv].contiguous(), planes[0], planes[1], wq, wk,
+                                 table, n + 1)
+    q1, _, _ = dq.qkv_rope(x[n:], pos[n:], table, n_q, n_kv, dtype=torch.float32, **norms)
+    r, _ = decode_ref(q1, [rows[0][:n + 1].double()], [rows[1][:n + 1].double()], [n + 1])
+    assert float((y.double() - r[0]).norm() / r.norm()) <= 1e-4
+    assert dq.device_error() == 0
