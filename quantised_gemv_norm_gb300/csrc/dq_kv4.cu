@@ -71,8 +71,8 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], float& d, 
         hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
     // (hi - lo) / 15 as IEEE division rounds it: the product with 1 / 15, corrected once by
-    // its exact remainder (P. Markstein, IBM Journal of Research and Development 34(1), 1990,
-    // section on division); the tests go through every fp32 mantissa
+    // its exact remainder (the method of P. Markstein, IBM Journal of Research and Development
+    // 34(1), 1990); the tests go through every fp32 mantissa
     const float range = __fsub_rn(hi, lo), part = __fmul_rn(range, 1.f / 15.f);
     d = __half2float(__float2half_rn(__fmaf_rn(__fmaf_rn(-15.f, part, range), 1.f / 15.f, part)));
     z = __half2float(__float2half_rn(__fadd_rn(lo, 8.0f * d)));

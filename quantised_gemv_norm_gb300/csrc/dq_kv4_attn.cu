@@ -17,9 +17,9 @@
 // one for 16-bit ones.
 //
 // What bounds it is the latency of its chains of instructions: a cache block takes a warp
-// 405 of them with one part (half of them codes and scales made into operands) and 450
+// 402 of them with one part (half of them codes and scales made into operands) and 451
 // with two, each warp's largely in sequence, and the 12 warps an SM that 168 registers
-// leave issue 0.60 (0.54) a clock and scheduler.  48 sequences of 1 to 12000 keys, 325 MB:
+// leave issue 0.59 (0.54) a clock and scheduler.  48 sequences of 1 to 12000 keys, 325 MB:
 // 85 us (3.8 TB/s; 48 us at the memory's rate), one of 100001, 128 MB, two parts: 44 us
 // (2.9 TB/s; 19 us).  A call of 64 keys takes 3.4 us in a graph.
 //
@@ -643,6 +643,8 @@ static bool kv4_counts_fit(int n_seq, int n_q, int n_kv, int max_keys)
 // over, at as many times that, so that blocks and scratch go by max_keys and the card and
 // not by the batch as well (256 sequences, 32 heads on 8, a bound of 131072 keys: 1000 keys
 // each 332 -> 152 us, one of all 131072 among them 368 -> 182 us, scratch 1.1 GB -> 125 MB).
+// The splits under either limit are of one size (100 x 2000 keys: 72 us, 81 with one of 1792
+// and one of 208).
 static Kv4Split kv4_split(int n_seq, int n_kv, int max_keys)
 {
     const long long blocks = (static_cast<long long>(max_keys) + dq::KV4_ROWS - 1) / dq::KV4_ROWS;
@@ -653,8 +655,11 @@ static Kv4Split kv4_split(int n_seq, int n_kv, int max_keys)
     if (chunk > 32)
         chunk = std::max((all + dq::KA_RESIDENT * sms - 1) / (dq::KA_RESIDENT * sms), 32ll);
     chunk = std::max(chunk, pairs >= sms ? 32ll : 8ll);
-    if (n_seq > 1)
-        chunk = std::min(chunk, std::max(64ll, 64 * pairs / (dq::KA_RESIDENT * sms)));
+    const long long most = std::max(64ll, 64 * pairs / (dq::KA_RESIDENT * sms));
+    if (n_seq > 1 && chunk > most) {
+        const long long splits = (blocks + most - 1) / most;
+        chunk = (blocks + splits - 1) / splits;
+    }
     const long long round = dq::KA_WARPS * dq::KA_STEP;  // what the block's warps take at a time
     chunk = (chunk + round - 1) / round * round;
     return {static_cast<int>(chunk), static_cast<int>((blocks + chunk - 1) / chunk)};
