@@ -20,25 +20,32 @@
 // to 2^15 and a key is lost only below 2^-32 of the largest probability (with b = 0,
 // 2^-25: 16000 keys of that size beside one key of value zero were gone); 0 in bf16.
 //
-// 8192 tokens, 32 heads on 8 KV heads, fp16: 385 us, 1430 TFLOP/s (0.75 of the
-// measured bf16 rate; 0.83 of the rate that the power limit leaves a library product
+// The running maximum and sum are M. Milakov and N. Gimelshein's online softmax (2018); the
+// order of the work, tiles that take turns with a reference that moves rarely, follows what
+// T. Dao, J. Shah and others have published on attention in one pass.
+//
+// 8192 tokens, 32 heads on 8 KV heads, fp16: 381 us, 1445 TFLOP/s (0.76 of the
+// measured bf16 rate; 0.84 of the rate that the power limit leaves a library product
 // over seconds, and the limit holds here too: 1.8 of 2.07 GHz at 1300 W; alone, from a
 // rested card, 350 us); 350 GB/s of DRAM.  The products bound it, not the softmax: with
-// P = S in place of the exponentials 382 us are left.  A round (both query tiles against
-// one key tile, 32 products of 64 clocks: 1.02 us at 2 GHz) takes 1.22 us with no
+// P = S in place of the exponentials 382 of 385 us were left.  A round (both query tiles
+// against one key tile, 32 products of 64 clocks: 1.02 us at 2 GHz) takes 1.22 us with no
 // softmax at all and 1.31 whole: a product of 64 clocks reads 8 KB of shared memory for
 // S and 4 KB for P V, and a round's copies write 64 KB; 256 KB are the 128 bytes a clock
 // that shared memory has for as long as the products take.  A block's start and end (5
 // us) come on top: a batch of twelve ragged prompts, 1432 blocks of 6 rounds on average,
-// 140 us, 890 TFLOP/s.  Tried and not kept: blocks that fetch more work and copy the
+// 142 us, 880 TFLOP/s; short prompts are nothing else: 256 of 40 tokens 121 us (bytes: 31),
+// 1000 of 8 tokens 427 us (24).  Tried and not kept: blocks that fetch more work and copy the
 // next tile during the end of one (ragged batch 158 us), one query tile a block and two
 // blocks an SM (8192 tokens 419 us, ragged batch 147; 256 prompts of 40 tokens 121 ->
-// 105), two product warps taking turns (398 us), a product loop unrolled over the ring's
-// slots (449 us), P handed over in quarters (16% more).
+// 105, 1000 of 8 tokens 427 -> 257), two product warps taking turns (398 us), a product
+// loop unrolled over the ring's slots (449 us), P handed over in quarters (16% more).
 //
 // Where the query tiles are too few for the card, the keys of each are split over
-// several blocks and joined by a second kernel (64 queries over 16064 keys: 286 -> 25
-// us; the keys' 66 MB take 10).
+// several blocks and joined by a second kernel (64 queries over 16064 keys: 286 -> 26
+// us; the keys' 66 MB take 10).  Above half the card's blocks nothing is split, and the
+// last wave may be nearly empty: 1280 queries after 16000 keys are 160 equal blocks on 152
+// SMs, 352 us (184 of products), 2048 queries 377 us (302).
 //
 // Key tiles that hold masked keys for some row (the diagonal's and a sequence's end)
 // have their infinities and NaNs in V replaced by zero before the product, since a
