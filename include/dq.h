@@ -449,6 +449,156 @@ DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, co
                                    void* out, int n_seq, int n_q, int n_kv, int head_dim, int n_pages, int page_size,
                                    int max_pages, int max_keys, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------- speculative decode step
+ * Several tokens of each sequence at once: a tree of drafted tokens (or a chain, or
+ * the one token of an ordinary decode step) whose root is the last token that was
+ * decided.  A step runs the projections of all nodes (dq_matmul_q4k takes up to 64),
+ * dq_kv16_append and dq_attention_tree in each layer, dq_verify_draft on the logits
+ * and dq_kv16_keep on the accepted nodes' cache rows.
+ *
+ * The cache is paged, in 16 bits.  pool: fp16 or bf16 [n_pages][2][n_kv][page_size][128]
+ * (keys, then values), page_size a multiple of 16.  A row's slot is page * page_size +
+ * its offset in the page.  Row j of sequence s is in page pages[s][j / page_size] at
+ * offset j % page_size; a sequence has n_past[s] rows, and its new tokens' rows follow
+ * them in the order of its nodes. */
+
+/* Projections into the cache: for row r of qkv (in_type DQ_TYPE_*, rows of
+ * (n_q + 2 n_kv) * 128, row_stride elements apart), with rope and the head norms as
+ * dq_qkv_rope, q_out[r] (contiguous [rows][n_q][128] of `type`) = the turned queries,
+ * and the turned keys and the values of the row go into slot slots[r] of the pool (of
+ * the same `type`), each computed in fp32 and rounded once.  positions, slots: int32
+ * [rows] (device).  A negative position is padding: nothing of the row is written; a
+ * negative slot leaves the cache alone.  A position >= max_ctx (nothing of the row is
+ * written) or a slot past the pool (its key and value are not) sets the bad-argument
+ * bit of the device's error flag.  Non-negative slots of one call must differ from
+ * one another.  q_norm and k_norm may both be NULL.
+ * Errors: NULL -> DQ_ERR_NULL; a count < 1, a type (the cache's has 16 bits), an
+ * epsilon, page_size not a multiple of 16, row_stride < the heads -> DQ_ERR_SHAPE;
+ * head_dim != 128, n_q or n_kv > 65536, n_pages * page_size >= 2^31 or that times
+ * 2 n_kv >= 2^31 -> DQ_ERR_UNSUPPORTED; a pointer not 16-byte aligned (positions and
+ * slots: 4), row_stride not a multiple of 8 (fp32: 4) -> DQ_ERR_ALIGN. */
+DQ_API int dq_kv16_append(const void* qkv, int in_type, long long row_stride, const int* positions, const int* slots,
+                          const float* q_norm, const float* k_norm, const float* rope_table, float eps, int rows,
+                          int n_q, int n_kv, int head_dim, int max_ctx, int type, void* q_out, void* pool, int n_pages,
+                          int page_size, void* stream);
+
+/* Attention of every sequence's new tokens over its cache.  Sequence s has the rows
+ * cu_new[s] .. cu_new[s + 1] - 1 of q and out (int32 [n_seq + 1], device; NULL: max_new
+ * rows each), T of them; its row i sees the keys j < n_past[s] and, of the new tokens'
+ * keys j = n_past[s] + t (t < T), those with bit t of seen[row] (64-bit words [total_new],
+ * device; NULL: the bits 0 .. i, a chain).  A row's own bit counts like any other.
+ *   out[row][h] = sum_j softmax_j(q[row][h] . k_j / sqrt(128)) v_j,  KV head h / (n_q / n_kv)
+ * Scores, softmax and sums are fp32; a probability is rounded to `type` before it
+ * multiplies a value.  A row that sees no key (or only scores of -infinity) is zero.
+ * What lies in keys and values that a row does not see, infinities and NaN too, does
+ * not reach it.  Rows of no sequence are left as they were; out may equal q.
+ * pages: int32 [n_seq][max_pages], entries past a sequence's last page are not looked
+ * at; a page outside the pool sets the bad-argument bit and its keys take no part.
+ * n_past: int32 [n_seq]; one that is negative or leaves no room for the new tokens in
+ * max_pages pages sets the bit, and the sequence's rows are zero.  cu_new that does not
+ * ascend within total_new, or T > max_new, sets the bit and the sequence has no rows.
+ * The work is spread over the card by the lengths it finds: a captured call may be
+ * replayed after n_past, cu_new, seen and pages have changed.
+ * workspace: dq_attention_tree_workspace_bytes(...) bytes of device scratch for the
+ * same counts, 16-byte aligned, its content before and after the call of no meaning;
+ * calls that share one must not overlap in time. */
+typedef struct {
+    const void* q;
+    void* out;
+    long long q_row_stride, q_head_stride, out_row_stride, out_head_stride; /* elements */
+    const void* pool;
+    const int* pages;
+    const int* n_past;
+    const int* cu_new;
+    const unsigned long long* seen;
+    int type; /* DQ_TYPE_F16 or DQ_TYPE_BF16: of q, out and pool */
+    int n_seq, total_new, max_new, n_q, n_kv, head_dim, n_pages, page_size, max_pages;
+    void* workspace;
+    size_t workspace_bytes;
+} dq_tree;
+
+/* Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, the type, page_size not a
+ * multiple of 16, a stride < 128 where its count exceeds 1, total_new != n_seq * max_new
+ * without cu_new, a workspace too small -> DQ_ERR_SHAPE; head_dim != 128, max_new > 64,
+ * n_q / n_kv > 64, total_new or max_pages * page_size > 2^30, n_seq * n_kv >= 2^24, a
+ * pool as in dq_kv16_append -> DQ_ERR_UNSUPPORTED; strides not multiples of 8, a pointer
+ * not 16-byte aligned -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
+DQ_API size_t dq_attention_tree_workspace_bytes(int n_seq, int max_new, int n_q, int n_kv);
+DQ_API int dq_attention_tree(const dq_tree* t, void* stream);
+
+/* Drafted tokens against the target's logits.  Sequence s has the nodes cu_new[s] ..
+ * cu_new[s + 1] - 1 (NULL: max_new each).  Node 0 of a sequence is its root; node i > 0
+ * is the drafted token tokens[node] after node parents[node] < i of the same sequence
+ * (NULL: after node i - 1, a chain).  logits[node] (DQ_TYPE_*, `vocab` contiguous
+ * elements) are the target's for the token after the node.  With p = softmax(logits /
+ * temperature[s]) at the current node, the root at first, its children x in ascending
+ * order are accepted if
+ *   uniform[x] * draft_probs[x][token] < p(token)     where draft_probs is given: the
+ *                     distribution that x was drawn from (chains only), or
+ *   uniform[x] * (1 - p(rejected)) < p(token)         where it is NULL: candidates that
+ *                     were chosen without chance; p(rejected) is the sum over the tokens
+ *                     of the node's children before, each counted once and never taken
+ *                     a second time
+ * and an accepted child is the new current node.  Where none is left, the next token is
+ *   argmax_v r(v) / noise[s][v],  ties to the lowest v,
+ * with r = max(p - draft_probs[x], 0) for the rejected x, else p without the rejected
+ * tokens.  With uniform from [0, 1) and noise from the exponential distribution the
+ * tokens are distributed as if drawn from p one by one.  Where r is zero everywhere, and
+ * where temperature[s] is not above 0 (a child is then accepted if its token is it), the
+ * token of the largest logit (the lowest of equal ones).  temperature NULL: 1.
+ * A NaN among the logits counts as -infinity, the weight of a -infinity is 0, the
+ * largest one's 1 even where it is infinite; a row of none but those accepts nothing and
+ * gives the token -1.  uniform and draft_probs are >= 0, noise > 0, none NaN.
+ * Out: path int32 [n_seq][max_new]: the accepted nodes, the root first, then -1; n_path
+ * int32 [n_seq]: how many (0 for a sequence without nodes); next int32 [n_seq]: the
+ * token (-1 without nodes).
+ * A token outside 0 .. vocab - 1 is never accepted.  A parent that is not below its node,
+ * cu_new that does not ascend within total_new, or more than max_new nodes (the sequence
+ * then has none) sets the bad-argument bit of the device's error flag. */
+typedef struct {
+    const void* logits;
+    long long logits_stride; /* elements between nodes, >= vocab */
+    const float* draft_probs;
+    long long draft_stride;
+    const float* noise; /* fp32 [n_seq][vocab], noise_stride elements apart */
+    long long noise_stride;
+    const int* tokens;
+    const int* parents;
+    const float* uniform;
+    const float* temperature;
+    const int* cu_new;
+    int* path;
+    int* n_path;
+    int* next;
+    int type, n_seq, total_new, max_new, vocab;
+    void* workspace; /* dq_verify_draft_workspace_bytes(total_new, vocab), 16-byte aligned, as dq_tree's */
+    size_t workspace_bytes;
+} dq_verify;
+
+/* Errors: NULL -> DQ_ERR_NULL; a count < 1, the type, a stride below vocab, total_new !=
+ * n_seq * max_new without cu_new, a workspace too small -> DQ_ERR_SHAPE; max_new > 64,
+ * draft_probs with parents, vocab or total_new > 2^24, more than 2^30 pieces of 8192
+ * logits -> DQ_ERR_UNSUPPORTED; a pointer not aligned to its elements (workspace: 16
+ * bytes) -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
+DQ_API size_t dq_verify_draft_workspace_bytes(int total_new, int vocab);
+DQ_API int dq_verify_draft(const dq_verify* v, void* stream);
+
+/* The accepted nodes' cache rows to where the sequence goes on: row n_past[s] + path[s][i]
+ * of the cache becomes row n_past[s] + i for i < n_path[s], as if all were read before any
+ * is written, in n_layers pools of the same layout, layer_stride bytes apart (a multiple
+ * of 16; ignored for one).  path: int32 [n_seq][max_new], n_path: int32 [n_seq], as
+ * dq_verify_draft writes them.  Sequences must not share the pages that hold their new
+ * rows.  A node outside 0 .. max_new - 1, a row past max_pages pages or a page outside
+ * the pool sets the bad-argument bit of the device's error flag and the row is not
+ * moved; n_path outside 0 .. max_new or a negative n_past the same for the sequence.
+ * Errors: NULL -> DQ_ERR_NULL; a count < 1, the type, page_size not a multiple of 16,
+ * layer_stride smaller than a pool -> DQ_ERR_SHAPE; max_new > 64, head_dim != 128, a
+ * pool as in dq_kv16_append, 2^31 or more (sequence, layer, head) triples ->
+ * DQ_ERR_UNSUPPORTED; DQ_ERR_ALIGN. */
+DQ_API int dq_kv16_keep(void* pool, int type, const int* pages, const int* n_past, const int* path, const int* n_path,
+                        int n_layers, long long layer_stride, int n_seq, int max_new, int n_kv, int head_dim,
+                        int n_pages, int page_size, int max_pages, void* stream);
+
 /* ------------------------------------------------------------ M-token sweep
  * "The roofline holds on a second GPU", section "The Math": M tokens share one
  * read of the weights; below M* = (w/16)(R/BW) memory bounds the product, above

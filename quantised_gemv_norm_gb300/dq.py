@@ -54,6 +54,12 @@ SIGNATURES = {
     "dq_kv4_read": (I, [P, P, I, P, P, I, I, I, I, I, P]),
     "dq_attention_decode_kv4_workspace_bytes": (SZ, [I, I, I, I]),
     "dq_attention_decode_kv4": (I, [P, I, P, P, P, P, I, I, I, I, I, I, I, I, P, SZ, P]),
+    "dq_kv16_append": (I, [P, I, LL, P, P, P, P, P, F, I, I, I, I, I, I, P, P, I, I, P]),
+    "dq_attention_tree_workspace_bytes": (SZ, [I, I, I, I]),
+    "dq_attention_tree": (I, [P, P]),
+    "dq_verify_draft_workspace_bytes": (SZ, [I, I]),
+    "dq_verify_draft": (I, [P, P]),
+    "dq_kv16_keep": (I, [P, I, P, P, P, P, I, LL, I, I, I, I, I, I, I, P]),
     "dq_matmul_q4k": (I, [P, P, P, I, I, I, P]),
     "dq_matmul_q4k_path": (I, [P, P, P, I, I, I, I, P]),
     "dq_matmul_q4k_split": (I, [P, P, P, I, I, I, P, LL, P]),
@@ -588,6 +594,235 @@ def attention_decode_kv4(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tenso
     if st:
         raise DQError("dq_attention_decode_kv4", st)
     return out
+
+
+# --------------------------------------------------- speculative decode step
+
+
+def kv16_pool(n_pages: int, n_kv: int, page_size: int, dtype=torch.float16, n_layers: int | None = None, device=None):
+    """A zero-filled 16-bit cache pool: [n_pages, 2 (keys, values), n_kv, page_size, 128], with ``n_layers`` one for
+    each layer in front of one another: [n_layers, ...] (see include/dq.h)."""
+    if page_size < 1 or page_size % 16:
+        raise ValueError("page_size must be a multiple of 16")
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("a 16-bit cache is fp16 or bf16")
+    shape = (n_pages, 2, n_kv, page_size, 128)
+    return torch.zeros(shape if n_layers is None else (n_layers,) + shape, dtype=dtype, device=device or "cuda")
+
+
+def _kv16(pool, dims=5):
+    shape = pool.shape
+    if len(shape) != dims or shape[dims - 4] != 2 or shape[-1] != 128 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous [n_pages, 2, n_kv, page_size, 128] tensor")
+    if pool.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("pool must be fp16 or bf16")
+    return shape[-5], shape[-3], shape[-2]
+
+
+def kv16_append(qkv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, rope: torch.Tensor, pool: torch.Tensor,
+                n_q: int, q_norm=None, k_norm=None, eps: float = 1e-6, out=None):
+    """qkv: fp32, fp16 or bf16 [rows, >= (n_q + 2 n_kv) 128] (a row stride is fine); positions (negative: a padding row)
+    and slots (page * page_size + offset; negative: the cache is left alone) int32 [rows]; rope from rope_table.  The
+    turned keys and the values go into the pool; returns the turned queries [rows, n_q, 128] of its dtype."""
+    lib = _lib or load()
+    n_pages, n_kv, page = _kv16(pool)
+    if qkv.dim() != 2:
+        raise ValueError("qkv must be a 2-D tensor")
+    rows, width = qkv.shape
+    stride, one = qkv.stride()
+    if width < (n_q + 2 * n_kv) * 128 or one != 1:
+        raise ValueError("qkv must have contiguous rows of %d heads of 128" % (n_q + 2 * n_kv))
+    if rope.dtype is not torch.float32 or rope.shape[1:] != (64, 2) or not rope.is_contiguous():
+        raise ValueError("rope must be a contiguous fp32 [max_ctx, 64, 2] table")
+    _int32("positions", positions, (rows,))
+    _int32("slots", slots, (rows,))
+    wq = wk = None
+    if q_norm is not None or k_norm is not None:
+        for w in (q_norm, k_norm):
+            if w is None or w.dtype is not torch.float32 or w.numel() != 128 or not w.is_contiguous():
+                raise ValueError("both head norms' weights must be fp32 [128], or both None")
+        _device(q_norm, k_norm)
+        wq, wk = q_norm.data_ptr(), k_norm.data_ptr()
+    t = _type(qkv.dtype)
+    dtype, shape = pool.dtype, (rows, n_q, 128)
+    out = torch.empty(shape, dtype=dtype, device=qkv.device) if out is None else _checked_out("out", out, shape, dtype)
+    dev = _device(qkv, positions, slots, rope, pool, out)
+    st = lib.dq_kv16_append(qkv.data_ptr(), t, stride if rows > 1 else -(-width // 8) * 8, positions.data_ptr(),
+                            slots.data_ptr(), wq, wk, rope.data_ptr(), eps, rows, n_q, n_kv, 128, rope.shape[0],
+                            _TYPES[dtype], out.data_ptr(), pool.data_ptr(), n_pages, page, _raw_stream(dev))
+    if st:
+        raise DQError("dq_kv16_append", st)
+    return out
+
+
+class _Tree(ctypes.Structure):
+    _fields_ = ([(n, P) for n in ("q", "out")]
+                + [(n, LL) for n in ("q_row_stride", "q_head_stride", "out_row_stride", "out_head_stride")]
+                + [(n, P) for n in ("pool", "pages", "n_past", "cu_new", "seen")]
+                + [(n, I) for n in ("type", "n_seq", "total_new", "max_new", "n_q", "n_kv", "head_dim", "n_pages",
+                                    "page_size", "max_pages")]
+                + [("workspace", P), ("workspace_bytes", SZ)])
+
+
+def attention_tree_workspace(n_seq: int, max_new: int, n_q: int, n_kv: int, device=None):
+    """Scratch for attention_tree calls of these counts, whatever the lengths."""
+    n = load().dq_attention_tree_workspace_bytes(n_seq, max_new, n_q, n_kv)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def attention_tree(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tensor, n_past: torch.Tensor, cu_new=None, seen=None,
+                   max_new: int | None = None, workspace=None, out=None):
+    """The new tokens of every sequence over its paged 16-bit cache, their own rows included: q [total_new, n_q, 128] of
+    the pool's dtype (any row and head strides), pages int32 [n_seq, max_pages], n_past int32 [n_seq] (rows before the
+    new ones), cu_new int32 [n_seq + 1] (None: as many rows in every sequence), seen int64 [total_new], bit t of a row's:
+    it sees its sequence's new token t (None: those up to itself).  ``max_new``: a bound on a sequence's rows known to
+    the host, at most 64 (where it is not given: 64, or total_new if that is less).  -> [total_new, n_q, 128]."""
+    lib = _lib or load()
+    n_pages, n_kv, page = _kv16(pool)
+    dtype = pool.dtype
+    q_row, q_head = _rows("q", q, dtype)
+    total, n_q, _ = q.shape
+    if pages.dim() != 2:
+        raise ValueError("pages must be [n_seq, max_pages]")
+    n_seq, max_pages = pages.shape
+    _int32("pages", pages, (n_seq, max_pages))
+    _int32("n_past", n_past, (n_seq,))
+    if cu_new is not None:
+        _int32("cu_new", cu_new, (n_seq + 1,))
+        if max_new is None:
+            max_new = min(64, total)
+    else:
+        each = total // n_seq if n_seq else 0
+        if each * n_seq != total or (max_new is not None and max_new != each):
+            raise ValueError("without cu_new every sequence has the same number of rows, max_new")
+        max_new = each
+    if seen is not None and (seen.dtype is not torch.int64 or seen.shape != (total,) or not seen.is_contiguous()):
+        raise ValueError("seen must be a contiguous int64 tensor of shape (%d,)" % total)
+    if out is None:
+        out = torch.empty((total, n_q, 128), dtype=dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    o_row, o_head = _rows("out", out, dtype)
+    dev = _device(q, pool, pages, n_past, out)
+    if cu_new is not None:
+        _device(cu_new)
+    if seen is not None:
+        _device(seen)
+    need = lib.dq_attention_tree_workspace_bytes(n_seq, max_new, n_q, n_kv) if workspace is None else 0
+    pw, nw, workspace = _scratch(workspace, need, q.device)
+    d = _Tree(q.data_ptr(), out.data_ptr(), q_row, q_head, o_row, o_head, pool.data_ptr(), pages.data_ptr(),
+              n_past.data_ptr(), None if cu_new is None else cu_new.data_ptr(), None if seen is None else seen.data_ptr(),
+              _TYPES[dtype], n_seq, total, max_new, n_q, n_kv, 128, n_pages, page, max_pages, pw, nw)
+    st = lib.dq_attention_tree(ctypes.addressof(d), _raw_stream(dev))
+    if st:
+        raise DQError("dq_attention_tree", st)
+    return out
+
+
+class _Verify(ctypes.Structure):
+    _fields_ = ([("logits", P), ("logits_stride", LL), ("draft_probs", P), ("draft_stride", LL), ("noise", P),
+                 ("noise_stride", LL)]
+                + [(n, P) for n in ("tokens", "parents", "uniform", "temperature", "cu_new", "path", "n_path", "next")]
+                + [(n, I) for n in ("type", "n_seq", "total_new", "max_new", "vocab")]
+                + [("workspace", P), ("workspace_bytes", SZ)])
+
+
+def verify_draft_workspace(total_new: int, vocab: int, device=None):
+    """Scratch for verify_draft calls of these counts."""
+    n = load().dq_verify_draft_workspace_bytes(total_new, vocab)
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _float_rows(name, t, rows, vocab):
+    if t.dtype is not torch.float32 or t.shape != (rows, vocab) or t.stride(1) != 1:
+        raise ValueError("%s must be an fp32 tensor of shape (%d, %d) with contiguous rows" % (name, rows, vocab))
+    return t.stride(0) if rows > 1 else vocab
+
+
+def _float32(name, t, n):
+    if t.dtype is not torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous fp32 tensor of shape (%d,)" % (name, n))
+
+
+def verify_draft(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tensor, noise: torch.Tensor, cu_new=None,
+                 max_new: int | None = None, parents=None, draft_probs=None, temperature=None, workspace=None, out=None):
+    """Drafted tokens against the target's logits [total_new, vocab] (fp32, fp16 or bf16), the root's among them.
+    tokens, parents (None: chains) int32 [total_new], uniform fp32 [total_new] from [0, 1), noise fp32 [n_seq, vocab]
+    from the exponential distribution, cu_new int32 [n_seq + 1] (None: as many nodes in every sequence), draft_probs
+    fp32 [total_new, vocab]: what each token of a chain was drawn from (None: candidates chosen without chance),
+    temperature fp32 [n_seq] (None: 1; not above 0: the largest logit).  -> (path int32 [n_seq, max_new]: the accepted
+    nodes, the root first, then -1; n_path int32 [n_seq]; the next token int32 [n_seq]).  The rules are in include/dq.h."""
+    lib = _lib or load()
+    if logits.dim() != 2 or logits.stride(1) != 1:
+        raise ValueError("logits must be [total_new, vocab] with contiguous rows")
+    total, vocab = logits.shape
+    n_seq = noise.shape[0]
+    noise_stride = _float_rows("noise", noise, n_seq, vocab)
+    _int32("tokens", tokens, (total,))
+    _float32("uniform", uniform, total)
+    if cu_new is not None:
+        _int32("cu_new", cu_new, (n_seq + 1,))
+        if max_new is None:
+            max_new = min(64, total)
+    else:
+        each = total // n_seq if n_seq else 0
+        if each * n_seq != total or (max_new is not None and max_new != each):
+            raise ValueError("without cu_new every sequence has the same number of nodes, max_new")
+        max_new = each
+    if parents is not None:
+        _int32("parents", parents, (total,))
+    draft_stride = 0 if draft_probs is None else _float_rows("draft_probs", draft_probs, total, vocab)
+    if temperature is not None:
+        _float32("temperature", temperature, n_seq)
+    t = _type(logits.dtype)
+    if out is None:
+        dev = logits.device
+        path = torch.empty((n_seq, max_new), dtype=torch.int32, device=dev)
+        n_path = torch.empty((n_seq,), dtype=torch.int32, device=dev)
+        after = torch.empty((n_seq,), dtype=torch.int32, device=dev)
+    else:
+        path, n_path, after = out
+        _int32("path", path, (n_seq, max_new))
+        _int32("n_path", n_path, (n_seq,))
+        _int32("next", after, (n_seq,))
+    dev = _device(logits, tokens, uniform, noise, path, n_path, after,
+                  *(x for x in (cu_new, parents, draft_probs, temperature) if x is not None))
+    need = lib.dq_verify_draft_workspace_bytes(total, vocab) if workspace is None else 0
+    pw, nw, workspace = _scratch(workspace, need, logits.device)
+
+    def ptr(x):
+        return None if x is None else x.data_ptr()
+
+    d = _Verify(logits.data_ptr(), logits.stride(0) if total > 1 else vocab, ptr(draft_probs), draft_stride,
+                noise.data_ptr(), noise_stride, tokens.data_ptr(), ptr(parents), uniform.data_ptr(), ptr(temperature),
+                ptr(cu_new), path.data_ptr(), n_path.data_ptr(), after.data_ptr(), t, n_seq, total, max_new, vocab, pw, nw)
+    st = lib.dq_verify_draft(ctypes.addressof(d), _raw_stream(dev))
+    if st:
+        raise DQError("dq_verify_draft", st)
+    return path, n_path, after
+
+
+def kv16_keep(pool: torch.Tensor, pages: torch.Tensor, n_past: torch.Tensor, path: torch.Tensor, n_path: torch.Tensor):
+    """The accepted nodes' cache rows to where their sequences go on: row n_past + path[s, i] becomes row n_past + i for
+    i < n_path[s], in a pool of one layer or of several ([n_layers, n_pages, 2, n_kv, page_size, 128])."""
+    lib = _lib or load()
+    dims = pool.dim()
+    n_pages, n_kv, page = _kv16(pool, 6 if dims == 6 else 5)
+    layers = pool.shape[0] if dims == 6 else 1
+    if path.dim() != 2 or pages.dim() != 2:
+        raise ValueError("path must be [n_seq, max_new] and pages [n_seq, max_pages]")
+    n_seq, max_new = path.shape
+    max_pages = pages.shape[1]
+    _int32("pages", pages, (n_seq, max_pages))
+    _int32("n_past", n_past, (n_seq,))
+    _int32("path", path, (n_seq, max_new))
+    _int32("n_path", n_path, (n_seq,))
+    dev = _device(pool, pages, n_past, path, n_path)
+    st = lib.dq_kv16_keep(pool.data_ptr(), _TYPES[pool.dtype], pages.data_ptr(), n_past.data_ptr(), path.data_ptr(),
+                          n_path.data_ptr(), layers, n_pages * page * n_kv * 512, n_seq, max_new, n_kv, 128, n_pages,
+                          page, max_pages, _raw_stream(dev))
+    if st:
+        raise DQError("dq_kv16_keep", st)
 
 
 # --------------------------------------------------------------- model
