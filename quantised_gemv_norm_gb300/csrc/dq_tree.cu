@@ -1,32 +1,45 @@
 // dq_tree.cu -- attention of a few new tokens of each sequence, a drafted tree, a chain
 // or one, over a paged 16-bit cache (dq_attention_tree).
 #include <algorithm>
+#include <mutex>
 
 #include "dq_kv16.cuh"
+#include "dq_tma_host.h"
 
 namespace dq {
 
 constexpr float TR_C = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr int TR_MAX_NEW = 64, TR_MAX_GROUP = 64;
+// log2 of the growth of a row's maximum that is let pass before its sums are scaled: a
+// probability is up to 2^8 (fp16: of 2^7 at the maximum, up to 2^15)
+constexpr float TR_GROW = 8.f;
+
+struct TreeJoin;
 
 struct TreeArgs {
+    CUtensorMap map;  // the pool as [2 halves of a row][rows][64]
     const void* q;
     void* out;
     long long q_row, q_head, o_row, o_head;
-    const void* pool;
     const int* pages;
     const int* n_past;
     const int* cu_new;
     const unsigned long long* seen;
-    int n_seq, total_new, max_new, n_q, group, max_pages;
+    float* part;      // [blocks][2: first and last segment][rows a block][128], unscaled sums
+    float2* part_ml;  // their maxima and sums of probabilities
+    TreeJoin* join;   // [blocks]
+    long long room;   // rows that max_pages pages hold
+    int n_seq, total_new, max_new, group, max_pages, box, least;
     Kv16Shape s;
+    FastDiv by_group, by_boxes;  // boxes of a page
     int* err;
 };
 
-// A sequence's new rows, and the keys before them; no rows where cu_new is not in order.
+// A sequence's new rows, and the keys before them; no rows where cu_new is not in order,
+// no keys where n_past does not fit.
 struct TreeSeq {
-    int row0, rows, past;
-    bool bad;  // no keys: n_past does not fit
+    int row0, rows, past, keys;
+    bool bad;
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s)
@@ -43,72 +56,714 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s)
     t.past = __ldg(a.n_past + s);
     const bool in_order = t.row0 >= 0 && r1 >= t.row0 && r1 <= a.total_new && r1 - t.row0 <= a.max_new;
     t.rows = in_order ? r1 - t.row0 : 0;
-    t.bad = t.past < 0 || static_cast<long long>(t.past) + t.rows > static_cast<long long>(a.max_pages) * a.s.page_rows;
-    if (t.bad || !in_order)
-        set_error(a.err, DEVERR_BAD_ARG);
-    if (t.bad)
+    const bool fits = t.past >= 0 && static_cast<long long>(t.past) + t.rows <= a.room;
+    t.bad = !in_order || !fits;
+    if (!fits)
         t.past = 0;
+    t.keys = fits ? t.past + t.rows : 0;
     return t;
 }
 
-// One block a new token and query head; a warp takes every fourth key, four dims a lane.
-template <typename T>
-__global__ void __launch_bounds__(128) tree_simple_kernel(const TreeArgs a)
+// The work is counted in units: one key tile of one item, an item being a row tile of one
+// sequence and KV head.  Sequence by sequence, item by item, tile by tile they are one
+// long row, of which every block takes an equal stretch; a stretch is cut into segments
+// where items change.
+template <int R, int KT>
+struct TreeCursor {
+    TreeSeq t;
+    int s, items, tiles;    // of the sequence
+    int item, tile;
+    long long left;         // units of the block's stretch
+
+    __device__ __forceinline__ long long units(const TreeArgs& a)
+    {
+        const int row_tiles = (t.rows * a.group + R - 1) / R;
+        items = a.s.n_kv * row_tiles;
+        tiles = max(1, (t.keys + KT - 1) / KT);
+        return static_cast<long long>(items) * tiles;
+    }
+    __device__ __forceinline__ void load(const TreeArgs& a, int seq)
+    {
+        s = seq;
+        t = tree_seq(a, seq);
+        units(a);
+    }
+    __device__ __forceinline__ int end() const { return static_cast<int>(min(static_cast<long long>(tiles), tile + left)); }
+    // to the next segment
+    __device__ __forceinline__ void next(const TreeArgs& a)
+    {
+        left -= end() - tile;
+        tile = 0;
+        ++item;
+        while (left > 0 && item >= items) {
+            item = 0;
+            load(a, s + 1);
+        }
+    }
+};
+
+// The block's stretch, by one warp: where it starts and how many units it has.
+struct TreeStart {
+    long long offset, left;  // units within the sequence; 0 left: none
+    int s;
+};
+
+template <int R, int KT>
+__device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int lane)
 {
-    __shared__ float ml[4][2];
-    __shared__ float4 sums[4][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x / a.max_new, i = blockIdx.x % a.max_new, h = blockIdx.y, g = h / a.group;
-    const TreeSeq t = tree_seq(a, s);
-    if (i >= t.rows)
+    constexpr int E = 4;  // sequences a lane and round
+    long long total = 0;
+    long long u[E];
+    auto round = [&](int s0, bool report) {
+        TreeCursor<R, KT> c;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int s = s0 + 32 * e + lane;
+            u[e] = 0;
+            if (s < a.n_seq) {
+                c.t = tree_seq(a, s);
+                u[e] = c.units(a);
+                if (report && c.t.bad)
+                    set_error(a.err, DEVERR_BAD_ARG);
+            }
+        }
+    };
+    auto sum = [](long long v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    for (int s0 = 0; s0 < a.n_seq; s0 += 32 * E) {
+        round(s0, blockIdx.x == 0);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            total += sum(u[e]);
+    }
+    const long long each = max(static_cast<long long>(a.least), (total + gridDim.x - 1) / gridDim.x);
+    TreeStart st{0, 0, 0};
+    long long want = each * blockIdx.x;
+    st.left = min(each, total - want);
+    if (st.left <= 0) {
+        st.left = 0;
+        return st;
+    }
+    for (int s0 = 0; s0 < a.n_seq; s0 += 32 * E) {
+        if (a.n_seq > 32 * E)
+            round(s0, false);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            long long incl = u[e];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, want >= incl - u[e] && want < incl);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                st.offset = __shfl_sync(0xffffffffu, want - (incl - u[e]), src);
+                st.s = s0 + 32 * e + src;
+                return st;
+            }
+            want -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    st.left = 0;  // not reached: want is below the total
+    return st;
+}
+
+template <int R, int KT>
+__device__ __forceinline__ TreeCursor<R, KT> tree_cursor(const TreeArgs& a, const TreeStart& st)
+{
+    TreeCursor<R, KT> c;
+    c.left = st.left;
+    c.load(a, st.s);
+    c.item = static_cast<int>(st.offset / c.tiles);
+    c.tile = static_cast<int>(st.offset - static_cast<long long>(c.item) * c.tiles);
+    return c;
+}
+
+// What a block leaves for the join: its last segment began an item that later blocks go
+// on with, the last of them `last`; -1: nothing to join.
+struct TreeJoin {
+    int row0, rows, kv, row_tile, last;
+};
+
+__device__ __forceinline__ void tree_load(void* dst, const CUtensorMap* map, int y, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(at)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void tree_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ float tree_one(uint32_t bits)
+{
+    return std::is_same<T, __half>::value ? half_bits_to_float(bits) : bf16lo(bits);
+}
+
+// 0xffff in the halves of a pair that are an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t tree_non_finite(uint32_t w)
+{
+    constexpr bool half = std::is_same<T, __half>::value;
+    constexpr uint32_t mask = half ? 0x7C007C00u : 0x7F807F80u, one = half ? 0x04000400u : 0x00800080u;
+    return ((((w & mask) + one) & 0x80008000u) >> 15) * 0xffffu;
+}
+
+// The rest of a wait whose first poll found nothing; once one has run out the others
+// return at once and the block writes nothing.
+__device__ __forceinline__ void tree_wait_on(uint64_t* bar, uint32_t parity, volatile int* fail, int* err, int code)
+{
+    const unsigned long long t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+        if (*fail)
+            return;
+        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            *fail = 1;
+            set_error(err, code);
+            return;
+        }
+    }
+}
+
+// ---- up to 64 rows a block: warp-level matrix instructions
+
+constexpr int TM_KEYS = 64;                     // keys a tile
+constexpr int TM_SLOT = TM_KEYS * ATT_HD * 2;   // bytes of a tile of keys or values
+constexpr int TM_SLOTS = 6;                     // ring: keys, values, keys, ...
+constexpr int TM_WARPS = 4, TM_THREADS = 32 * (TM_WARPS + 1), TM_RESIDENT = 2;
+constexpr int TM_MEET = 2 * 16 * ATT_HD * 4;    // two warps' sums
+constexpr int TM_SMEM = TM_SLOTS * TM_SLOT + TM_MEET + 512;
+
+struct TreeMiscM {
+    uint64_t full[TM_SLOTS], freed[TM_SLOTS];
+    uint32_t absent[TM_SLOTS];  // runs of 16 keys whose page is outside the pool
+    float ml[2][16][2];
+    TreeStart start;
+    int fail;
+};
+static_assert(sizeof(TreeMiscM) <= 512, "fits behind the ring");
+
+template <typename T, int WR>
+__global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const __grid_constant__ TreeArgs a)
+{
+    constexpr int R = 16 * WR, WK = TM_WARPS / WR, NK = TM_KEYS / WK;  // rows a block; warps along the keys; keys a warp
+    constexpr float TOP = std::is_same<T, __half>::value ? 7.f : 0.f;
+    extern __shared__ __align__(1024) uint8_t ring[];
+    float2* meet = reinterpret_cast<float2*>(ring + TM_SLOTS * TM_SLOT);
+    TreeMiscM& sh = *reinterpret_cast<TreeMiscM*>(ring + TM_SLOTS * TM_SLOT + TM_MEET);
+    volatile int* fail = &sh.fail;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_trigger();
+    if (warp == TM_WARPS) {
+        if (lane == 0) {
+            for (int i = 0; i < TM_SLOTS; ++i) {
+                mbar_init(&sh.full[i], 1);
+                mbar_init(&sh.freed[i], TM_WARPS);
+            }
+            fence_mbar_init();
+            sh.fail = 0;
+        }
+        const TreeStart st = tree_start<R, TM_KEYS>(a, lane);
+        if (lane == 0)
+            sh.start = st;
+    }
+    __syncthreads();
+    const TreeStart st = sh.start;
+    TreeJoin join{0, 0, 0, 0, -1};
+    if (st.left > 0) {
+        auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
+            if (!mbar_try_wait(bar, parity))
+                tree_wait_on(bar, parity, fail, a.err, code);
+        };
+        TreeCursor<R, TM_KEYS> c = tree_cursor<R, TM_KEYS>(a, st);
+        int slot = 0;
+        uint32_t phase = 0;
+        auto turn = [&] {
+            if (++slot == TM_SLOTS) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        if (warp == TM_WARPS) {
+            // ---- copies: a lane takes one of a tile's boxes (16, 32 or 64 rows of a page)
+            const int box = a.box, per_tile = TM_KEYS / box, ahead = 32 / per_tile;
+            long long issued = 0;
+            for (; c.left > 0 && !__any_sync(0xffffffffu, *fail); c.next(a)) {
+                const int row_tiles = c.items / a.s.n_kv, g = c.item / row_tiles;
+                const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
+                // lane i has the page of box `first + i`, and of box `first + 32 + i`
+                auto page_of = [&](int x) {
+                    return static_cast<long long>(x) * box < c.t.keys ? __ldg(pages + fast_div(x, a.by_boxes)) : 0;
+                };
+                int first = c.tile, now = page_of(first * per_tile + lane), then = page_of((first + ahead) * per_tile + lane);
+                const int end = c.end();
+                for (int k = c.tile; k < end; ++k) {
+                    if (k - first == ahead) {
+                        first = k;
+                        now = then;
+                        then = page_of((first + ahead) * per_tile + lane);
+                    }
+                    const int page = __shfl_sync(0xffffffffu, now, (k - first) * per_tile + lane & 31);
+                    const int x = k * per_tile + lane;
+                    const bool mine = lane < per_tile && static_cast<long long>(x) * box < c.t.keys;
+                    const bool there = mine && page >= 0 && page < a.s.n_pages;
+                    const unsigned have = __ballot_sync(0xffffffffu, there), lack = __ballot_sync(0xffffffffu, mine && !there);
+                    uint32_t absent = 0;
+                    if (lack) {
+                        for (int i = 0; i < per_tile; ++i)
+                            if (lack >> i & 1)
+                                absent |= ((1u << (box / 16)) - 1) << (i * (box / 16));
+                        if (lane == 0)
+                            set_error(a.err, DEVERR_BAD_ARG);
+                    }
+                    const uint32_t bytes = static_cast<uint32_t>(__popc(have) * box * 256);
+                    const int off = (x - static_cast<int>(fast_div(x, a.by_boxes) * a.by_boxes.d)) * box;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        wait(&sh.freed[slot], phase ^ 1, DEVERR_TIMEOUT_EMPTY);
+                        __syncwarp();
+                        if (__any_sync(0xffffffffu, *fail))
+                            continue;
+                        if (lane == 0) {
+                            sh.absent[slot] = absent;
+                            mbar_arrive_expect_tx(&sh.full[slot], bytes);
+                        }
+                        __syncwarp();
+                        if (there)
+                            tree_load(ring + slot * TM_SLOT + lane * box * 256, &a.map,
+                                      static_cast<int>(kv16_row(a.s, page, kv, g)) + off, &sh.full[slot]);
+                        ++issued;
+                        turn();
+                    }
+                }
+            }
+            // every copy has landed before the block ends
+            for (long long i = max(0ll, issued - TM_SLOTS); i < issued; ++i)
+                if (!mbar_wait(&sh.full[i % TM_SLOTS], static_cast<uint32_t>(i / TM_SLOTS) & 1) && lane == 0)
+                    set_error(a.err, DEVERR_TIMEOUT_DRAIN);
+        } else {
+            const int wr = warp % WR, wk = warp / WR, r8 = lane >> 2, q4 = lane & 3;
+            const uint32_t panel = static_cast<uint32_t>(a.box) * 128;
+            // byte offset of key block i (16 keys, from the warp's first) in a slot
+            uint32_t block_at[NK / 16];
+#pragma unroll
+            for (int i = 0; i < NK / 16; ++i) {
+                const int key = wk * NK + 16 * i, b = key / a.box;
+                block_at[i] = static_cast<uint32_t>(b * a.box * 256 + (key - b * a.box) * 128);
+            }
+            // this lane's row and 16-byte piece of the four 8 x 8 matrices: of keys (two runs of 8,
+            // two of dims), of values (the same, transposed)
+            const uint32_t sw = lane & 7;
+            const uint32_t k_at = ((lane >> 4) * 8 + sw) * 128 + (((lane >> 3 & 1) ^ sw) << 4);
+            const uint32_t v_at = ((lane >> 3 & 1) * 8 + sw) * 128 + (((lane >> 4) ^ sw) << 4);
+            const uint32_t base = smem_addr(ring);
+            for (; c.left > 0; c.next(a)) {
+                const int row_tiles = c.items / a.s.n_kv, g = c.item / row_tiles, rt = c.item - g * row_tiles;
+                const TreeSeq t = c.t;
+                // this lane's two rows
+                const T* qp[2];
+                uint64_t seen[2];
+                bool live[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = rt * R + 16 * wr + r8 + 8 * h, node = static_cast<int>(fast_div(r, a.by_group));
+                    live[h] = node < t.rows;
+                    const int row = t.row0 + (live[h] ? node : 0);
+                    qp[h] = static_cast<const T*>(a.q) + static_cast<long long>(row) * a.q_row +
+                            static_cast<long long>(g * a.group + r - node * a.group) * a.q_head;
+                    seen[h] = !live[h] ? 0ull : a.seen ? __ldg(a.seen + row) : (2ull << node) - 1;
+                    if (t.rows < 64)
+                        seen[h] &= (1ull << t.rows) - 1;
+                }
+                uint32_t q[8][4];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            q[k][h + 2 * e] = live[h] ? __ldg(reinterpret_cast<const uint32_t*>(qp[h] + 16 * k + 8 * e + 2 * q4)) : 0u;
+                float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+                const int end = c.end();
+
+                auto tile = [&](auto tail, int k) {
+                    constexpr bool TAIL = decltype(tail)::value;
+                    float s[NK / 8][4];
+#pragma unroll
+                    for (int i = 0; i < NK / 8; ++i)
+                        s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+                    const uint32_t kb = base + slot * TM_SLOT;
+#pragma unroll
+                    for (int d = 0; d < 8; ++d)
+#pragma unroll
+                        for (int i = 0; i < NK / 16; ++i) {
+                            uint32_t b[4];
+                            ldsm4(b, ((kb + block_at[i] + k_at) ^ ((d & 3) * 32)) + (d >> 2) * panel);
+                            tree_mma<T>(s[2 * i], q[d], b[0], b[1]);
+                            tree_mma<T>(s[2 * i + 1], q[d], b[2], b[3]);
+                        }
+                    const uint32_t absent = !TAIL ? 0u : t.keys ? sh.absent[slot] : 0xfu;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.freed[slot]);
+                    turn();
+                    // new token of this lane's first key
+                    const int node0 = k * TM_KEYS + wk * NK + 2 * q4 - t.past;
+                    if (TAIL) {
+#pragma unroll
+                        for (int i = 0; i < NK / 8; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int node = node0 + 8 * i + e;
+                                const bool gone = absent >> ((wk * NK + 8 * i) / 16) & 1;
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (gone || node >= 64 || (node >= 0 && !(seen[h] >> (node & 63) & 1)))
+                                        s[i][2 * h + e] = -INFINITY;
+                            }
+                    }
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < NK / 8; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            top[h] = fmaxf(top[h], fmaxf(s[i][2 * h], s[i][2 * h + 1]));
+                    if (__any_sync(0xffffffffu, (top[0] - m[0]) * TR_C > TR_GROW || (top[1] - m[1]) * TR_C > TR_GROW)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float x = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                            float f = 1.f;
+                            if ((x - m[h]) * TR_C > TR_GROW) {
+                                f = ex2((m[h] - x) * TR_C);  // 0 from -infinity
+                                m[h] = x;
+                            }
+                            l[h] *= f;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                o[i][2 * h] *= f;
+                                o[i][2 * h + 1] *= f;
+                            }
+                        }
+                    }
+                    uint32_t p[NK / 16][4];
+                    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+                    for (int i = 0; i < NK / 8; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float x = ex2(fmaf(s[i][2 * h] - ref[h], TR_C, TOP)), y = ex2(fmaf(s[i][2 * h + 1] - ref[h], TR_C, TOP));
+                            l[h] += x + y;
+                            p[i >> 1][(i & 1) * 2 + h] = pack2(x, y, static_cast<const T*>(nullptr));
+                        }
+                    wait(&sh.full[slot], phase, DEVERR_TIMEOUT_FULL);
+                    __syncwarp();
+                    const uint32_t vb = base + slot * TM_SLOT;
+                    bool poison = false;
+#pragma unroll
+                    for (int i = 0; i < NK / 16; ++i) {
+                        uint32_t keep[2], fresh[2];  // keys 2 q4, + 1 and 8 more: those that exist, those that are new
+                        if (TAIL) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int node = node0 + 16 * i + 8 * e;
+                                const bool gone = absent >> ((wk * NK + 16 * i) / 16) & 1;
+                                keep[e] = gone ? 0u : (node < t.rows ? 0xffffu : 0u) | (node + 1 < t.rows ? 0xffff0000u : 0u);
+                                fresh[e] = (node >= 0 ? 0xffffu : 0u) | (node + 1 >= 0 ? 0xffff0000u : 0u);
+                            }
+                        }
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) {
+                            uint32_t b[4];
+                            ldsm4_trans(b, ((vb + block_at[i] + v_at) ^ ((d & 3) * 32)) + (d >> 2) * panel);
+                            if (TAIL) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    b[e] &= keep[e & 1];
+                                    const uint32_t nf = tree_non_finite<T>(b[e]) & fresh[e & 1];
+                                    poison |= nf != 0;
+                                    b[e] &= ~nf;
+                                }
+                            }
+                            tree_mma<T>(o[2 * d], p[i], b[0], b[1]);
+                            tree_mma<T>(o[2 * d + 1], p[i], b[2], b[3]);
+                        }
+                    }
+                    if (TAIL && __any_sync(0xffffffffu, poison)) {
+                        // new tokens' infinities and NaNs, which the products left out: to the rows that see them
+                        for (int key = 0; key < NK; ++key) {
+                            const int node = k * TM_KEYS + wk * NK + key - t.past;
+                            if (node < 0 || node >= t.rows || (absent >> ((wk * NK + key) / 16) & 1))
+                                continue;
+                            const int first = wk * NK + key & ~15, b = first / a.box;
+                            const uint32_t at = b * a.box * 256 + (first - b * a.box + (key & 15)) * 128;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const uint32_t w = *reinterpret_cast<const uint32_t*>(
+                                    ring + slot * TM_SLOT + at + (i >> 3) * panel + (((i & 7) ^ (key & 7)) << 4) + 4 * q4);
+                                const uint32_t nf = tree_non_finite<T>(w);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (seen[h] >> node & 1) {
+                                        if (nf & 0xffffu)
+                                            o[i][2 * h] += tree_one<T>(w & 0xffffu);
+                                        if (nf >> 16)
+                                            o[i][2 * h + 1] += tree_one<T>(w >> 16);
+                                    }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.freed[slot]);
+                    turn();
+                };
+
+                for (int k = c.tile; k < end; ++k) {
+                    wait(&sh.full[slot], phase, DEVERR_TIMEOUT_FULL);
+                    __syncwarp();
+                    if ((k + 1) * TM_KEYS > t.past || sh.absent[slot])
+                        tile(std::true_type{}, k);
+                    else
+                        tile(std::false_type{}, k);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                }
+                // ---- the warps along the keys meet: half of them give, the others take
+#pragma unroll
+                for (int half = WK / 2; half > 0; half /= 2) {
+                    const int place = wr + WR * (wk % half);
+                    if (wk >= half && wk < 2 * half) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                meet[place * 1024 + (2 * i + h) * 32 + lane] = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                        if (q4 == 0)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                sh.ml[place][r8 + 8 * h][0] = m[h];
+                                sh.ml[place][r8 + 8 * h][1] = l[h];
+                            }
+                    }
+                    named_bar_sync(1, 32 * TM_WARPS);
+                    if (wk < half) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float m2 = sh.ml[place][r8 + 8 * h][0], l2 = sh.ml[place][r8 + 8 * h][1];
+                            const float mn = fmaxf(m[h], m2);
+                            const float f = m[h] == mn ? 1.f : ex2((m[h] - mn) * TR_C), f2 = m2 == mn ? 1.f : ex2((m2 - mn) * TR_C);
+                            m[h] = mn;
+                            l[h] = l[h] * f + l2 * f2;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 y = meet[place * 1024 + (2 * i + h) * 32 + lane];
+                                o[i][2 * h] = o[i][2 * h] * f + y.x * f2;
+                                o[i][2 * h + 1] = o[i][2 * h + 1] * f + y.y * f2;
+                            }
+                        }
+                    }
+                    named_bar_sync(1, 32 * TM_WARPS);
+                }
+                const bool whole = c.tile == 0 && end == c.tiles;
+                if (!whole && c.tile == 0 && warp == 0) {
+                    // the blocks that go on with the item: each has as many units as this one
+                    const long long each = st.left;
+                    join = TreeJoin{t.row0, t.rows, g, rt,
+                                    static_cast<int>(blockIdx.x + (c.tiles - end + each - 1) / each)};
+                }
+                if (wk == 0 && !*fail) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int rr = 16 * wr + r8 + 8 * h, r = rt * R + rr, node = static_cast<int>(fast_div(r, a.by_group));
+                        if (!live[h])
+                            continue;
+                        if (whole) {
+                            const float inv = l[h] == 0.f ? 0.f : 1.f / l[h];
+                            T* out = static_cast<T*>(a.out) + static_cast<long long>(t.row0 + node) * a.o_row +
+                                     static_cast<long long>(g * a.group + r - node * a.group) * a.o_head + 2 * q4;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                *reinterpret_cast<uint32_t*>(out + 8 * i) =
+                                    l[h] == 0.f ? 0u : pack2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv, static_cast<const T*>(nullptr));
+                        } else {
+                            const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0)) * R + rr;
+                            if (q4 == 0)
+                                a.part_ml[at] = make_float2(m[h], l[h]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                *reinterpret_cast<float2*>(a.part + at * ATT_HD + 8 * i + 2 * q4) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (tid == 0)
+        a.join[blockIdx.x] = *fail ? TreeJoin{0, 0, 0, 0, -1} : join;
+}
+
+// A row of an item that several blocks had a part of: one warp, four dims a lane.
+template <typename T, int R>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, rr = blockIdx.y * 8 + warp;
+    pdl_wait();
+    const TreeJoin j = a.join[b];
+    const int r = j.row_tile * R + rr, node = static_cast<int>(fast_div(r, a.by_group));
+    if (j.last < 0 || node >= j.rows)
         return;
-    const int row = t.row0 + i;
-    const unsigned long long seen = a.seen ? a.seen[row] : (2ull << i) - 1;
-    const float4 q = load4(static_cast<const T*>(a.q) + row * a.q_row + h * a.q_head + 4 * lane);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int keys = t.bad ? 0 : t.past + t.rows;
-    for (int j = warp; j < keys; j += 4) {
-        if (j >= t.past && !(seen >> (j - t.past) & 1))
-            continue;
-        const int page = a.pages[static_cast<size_t>(s) * a.max_pages + j / a.s.page_rows];
-        if (page < 0 || page >= a.s.n_pages) {
-            set_error(a.err, DEVERR_BAD_ARG);
-            continue;
+    constexpr int E = 4;
+    for (int b0 = b; b0 <= j.last; b0 += E) {
+        float2 ml[E];
+        float4 y[E];
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            ml[e] = make_float2(-INFINITY, 0.f);
+            y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (b0 + e <= j.last) {
+                const size_t at = (static_cast<size_t>(b0 + e) * 2 + (b0 + e == b)) * R + rr;
+                ml[e] = __ldcg(a.part_ml + at);
+                y[e] = __ldcg(reinterpret_cast<const float4*>(a.part + at * ATT_HD) + lane);
+            }
+            top = fmaxf(top, ml[e].x);
         }
-        const T* pool = static_cast<const T*>(a.pool);
-        const float4 k = load4(pool + (kv16_row(a.s, page, 0, g) + j % a.s.page_rows) * ATT_HD + 4 * lane);
-        const float4 v = load4(pool + (kv16_row(a.s, page, 1, g) + j % a.s.page_rows) * ATT_HD + 4 * lane);
-        const float x = warp_sum(q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w);
-        const float mn = fmaxf(m, x), f = mn == m ? 1.f : ex2((m - mn) * TR_C), p = mn == -INFINITY ? 0.f : ex2((x - mn) * TR_C);
-        m = mn;
-        l = l * f + p;
-        o = make_float4(o.x * f + p * v.x, o.y * f + p * v.y, o.z * f + p * v.z, o.w * f + p * v.w);
-    }
-    if (lane == 0) {
-        ml[warp][0] = m;
-        ml[warp][1] = l;
-    }
-    sums[warp][lane] = o;
-    __syncthreads();
-    if (warp)
-        return;
-    for (int w = 1; w < 4; ++w)
-        m = fmaxf(m, ml[w][0]);
-    l = 0.f;
-    o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = 0; w < 4; ++w) {
-        const float f = ml[w][0] == m ? 1.f : ex2((ml[w][0] - m) * TR_C);
-        const float4 y = sums[w][lane];
-        l += f * ml[w][1];
-        o = make_float4(o.x + f * y.x, o.y + f * y.y, o.z + f * y.z, o.w + f * y.w);
+        const float f = m == top ? 1.f : ex2((m - top) * TR_C);
+        m = top;
+        l *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float w = ml[e].x == m ? 1.f : ex2((ml[e].x - m) * TR_C);
+            l = fmaf(w, ml[e].y, l);
+            o = make_float4(fmaf(w, y[e].x, o.x), fmaf(w, y[e].y, o.y), fmaf(w, y[e].z, o.z), fmaf(w, y[e].w, o.w));
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4(static_cast<T*>(a.out) + row * a.o_row + h * a.o_head + 4 * lane,
+    store4(static_cast<T*>(a.out) + static_cast<long long>(j.row0 + node) * a.o_row +
+               static_cast<long long>(j.kv * a.group + r - node * a.group) * a.o_head + 4 * lane,
            l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
 }  // namespace dq
+
+namespace dqhost {
+
+// Rows a block, and blocks: two of up to 64 rows an SM.
+struct TreeCut {
+    int rows, blocks;
+};
+
+static TreeCut tree_cut(int max_new, int group)
+{
+    const int rows = max_new * group;
+    return {rows <= 16 ? 16 : rows <= 32 ? 32 : 64, dq::TM_RESIDENT * sm_count()};
+}
+
+static size_t tree_bytes(const TreeCut& c)
+{
+    const size_t rows = static_cast<size_t>(c.blocks) * 2 * c.rows;
+    return rows * (dq::ATT_HD + 2) * sizeof(float) + (c.blocks * sizeof(dq::TreeJoin) + 15) / 16 * 16;
+}
+
+// The pool in boxes of `box` rows, both halves of 64 dims, with the 128-byte swizzle.
+static bool tree_map(CUtensorMap* m, int type, const void* pool, long long rows, int box)
+{
+    const EncodeTiled enc = encode_tiled();
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 2};
+    const cuuint64_t strides[2] = {dq::ATT_HD * 2, 128};
+    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 2};
+    const cuuint32_t ones[3] = {1, 1, 1};
+    return enc && enc(m, type == DQ_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                      const_cast<void*>(pool), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A kernel's shared memory, asked for once per device.
+template <typename K>
+static cudaError_t tree_prepare(K kernel, int bytes, bool (&done)[64])
+{
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && dev >= 0 && dev < 64)
+            done[dev] = true;
+    }
+    return e;
+}
+
+template <typename T, int WR>
+static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaStream_t s)
+{
+    static bool done[64] = {};
+    cudaError_t e = tree_prepare(dq::tree_mma_kernel<T, WR>, dq::TM_SMEM, done);
+    if (e != cudaSuccess)
+        return e;
+    dq::tree_mma_kernel<T, WR><<<cut.blocks, dq::TM_THREADS, dq::TM_SMEM, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.blocks), 2 * WR);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, dq::tree_join_kernel<T, 16 * WR>, a);
+}
+
+}  // namespace dqhost
 
 extern "C" {
 
@@ -117,7 +772,7 @@ DQ_API size_t dq_attention_tree_workspace_bytes(int n_seq, int max_new, int n_q,
     if (n_seq < 1 || max_new < 1 || max_new > dq::TR_MAX_NEW || n_q < 1 || n_kv < 1 || n_q % n_kv ||
         n_q / n_kv > dq::TR_MAX_GROUP)
         return 0;
-    return 16;
+    return dqhost::tree_bytes(dqhost::tree_cut(max_new, n_q / n_kv));
 }
 
 DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
@@ -152,14 +807,43 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         return DQ_ERR_ALIGN;
     if (t->workspace_bytes < dq_attention_tree_workspace_bytes(t->n_seq, t->max_new, t->n_q, t->n_kv))
         return DQ_ERR_SHAPE;
-    const dq::TreeArgs a{t->q, t->out, rows[0], heads[0], rows[1], heads[1], t->pool, t->pages, t->n_past, t->cu_new, t->seen,
-                         t->n_seq, t->total_new, t->max_new, t->n_q, t->n_q / t->n_kv, t->max_pages,
-                         {t->n_kv, t->n_pages, t->page_size}, dqhost::device_error_flag()};
+    const int group = t->n_q / t->n_kv, box = t->page_size % 64 == 0 ? 64 : t->page_size % 32 == 0 ? 32 : 16;
+    const dqhost::TreeCut cut = dqhost::tree_cut(t->max_new, group);
+    dq::TreeArgs a{};
+    if (!dqhost::tree_map(&a.map, t->type, t->pool, 2ll * t->n_pages * t->n_kv * t->page_size, box))
+        return DQ_ERR_UNSUPPORTED;
+    a.q = t->q;
+    a.out = t->out;
+    a.q_row = rows[0];
+    a.q_head = heads[0];
+    a.o_row = rows[1];
+    a.o_head = heads[1];
+    a.pages = t->pages;
+    a.n_past = t->n_past;
+    a.cu_new = t->cu_new;
+    a.seen = t->seen;
+    const size_t part_rows = static_cast<size_t>(cut.blocks) * 2 * cut.rows;
+    a.part = static_cast<float*>(t->workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part + part_rows * dq::ATT_HD);
+    a.join = reinterpret_cast<dq::TreeJoin*>(a.part_ml + part_rows);
+    a.room = static_cast<long long>(t->max_pages) * t->page_size;
+    a.n_seq = t->n_seq;
+    a.total_new = t->total_new;
+    a.max_new = t->max_new;
+    a.group = group;
+    a.max_pages = t->max_pages;
+    a.box = box;
+    a.least = 4;
+    a.s = {t->n_kv, t->n_pages, t->page_size};
+    a.by_group = dqhost::fast_divisor(group);
+    a.by_boxes = dqhost::fast_divisor(t->page_size / box);
+    a.err = dqhost::device_error_flag();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = dqhost::with_type16(t->type, [&](auto* p) {
-        dq::tree_simple_kernel<std::remove_pointer_t<decltype(p)>>
-            <<<dim3(static_cast<unsigned>(t->n_seq) * t->max_new, t->n_q), 128, 0, s>>>(a);
-        return cudaGetLastError();
+        using T = std::remove_pointer_t<decltype(p)>;
+        return cut.rows == 16   ? dqhost::tree_launch<T, 1>(a, cut, s)
+               : cut.rows == 32 ? dqhost::tree_launch<T, 2>(a, cut, s)
+                                : dqhost::tree_launch<T, 4>(a, cut, s);
     });
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }
