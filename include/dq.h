@@ -548,7 +548,8 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream);
  * token of the largest logit (the lowest of equal ones).  temperature NULL: 1.
  * A NaN among the logits counts as -infinity, the weight of a -infinity is 0, the
  * largest one's 1 even where it is infinite; a row of none but those accepts nothing and
- * gives the token -1.  uniform and draft_probs are >= 0, noise > 0, none NaN.
+ * gives the token -1.  uniform and draft_probs are >= 0, noise > 0, none NaN; a
+ * temperature above 0 is kept within 2^-60 .. 2^60.
  * Out: path int32 [n_seq][max_new]: the accepted nodes, the root first, then -1; n_path
  * int32 [n_seq]: how many (0 for a sequence without nodes); next int32 [n_seq]: the
  * token (-1 without nodes).

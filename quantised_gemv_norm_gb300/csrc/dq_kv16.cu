@@ -126,66 +126,98 @@ struct Kv16KeepArgs {
     const int* n_path;
     int max_new, max_pages;
     Kv16Shape s;
-    FastDiv by_page, by_planes, by_layers;
+    FastDiv by_page, by_layers;
     int* err;
 };
 
-constexpr int KV16_KEEP_THREADS = 128;
+constexpr int KV16_KEEP_THREADS = 256;
+constexpr int KV16_KEEP_EACH = 4;  // 16-byte pieces a thread has in registers
 constexpr int KV16_MAX_NEW = 64;
+static_assert(KV16_KEEP_THREADS * KV16_KEEP_EACH >= KV16_MAX_NEW * 16, "a plane's rows are moved at once");
 
-// One block a sequence, layer and plane (a head's keys or values): all its rows are in
-// registers before the first is written.
+// One block a sequence, layer and half (its keys or its values).  The moved rows' places are
+// found once, a thread a row; then as many heads at a time as the block's registers hold go
+// through them, all their rows read before the first is written (a row may be another's
+// place).  64 sequences' 6 rows or so in 36 layers of 8 heads: a block a head, each finding
+// the rows for itself, took 59 us.
 __global__ void __launch_bounds__(KV16_KEEP_THREADS) kv16_keep_kernel(const Kv16KeepArgs a)
 {
-    constexpr int EACH = KV16_MAX_NEW * 16 / KV16_KEEP_THREADS;
-    const uint32_t x = fast_div(blockIdx.x, a.by_planes), plane = blockIdx.x - x * a.by_planes.d;
+    __shared__ long long from[KV16_MAX_NEW], to[KV16_MAX_NEW];  // in rows from the pool's start, of head 0
+    __shared__ int moved;
+    const int tid = threadIdx.x, lane = tid & 31, kv = blockIdx.x & 1;
+    const uint32_t x = blockIdx.x >> 1;
     const uint32_t b = fast_div(x, a.by_layers), layer = x - b * a.by_layers.d;
-    const int n = __ldg(a.n_path + b), past = __ldg(a.n_past + b);
-    if (n < 0 || n > a.max_new || past < 0) {
-        if (threadIdx.x == 0)
+    if (tid < 32) {
+        const int n = __ldg(a.n_path + b), past = __ldg(a.n_past + b);
+        const bool bad = n < 0 || n > a.max_new || past < 0;
+        if (bad && lane == 0)
             set_error(a.err, DEVERR_BAD_ARG);
-        return;
-    }
-    uint4* base = reinterpret_cast<uint4*>(a.pool + layer * a.layer);
-    const int* pages = a.pages + static_cast<size_t>(b) * a.max_pages;
-    // a row's first 16 bytes in this plane, null where the row does not exist
-    auto at = [&](int j) -> uint4* {
-        if (j < 0)
-            return nullptr;  // past the range of a row's number
-        const int k = static_cast<int>(fast_div(static_cast<uint32_t>(j), a.by_page));
-        if (k >= a.max_pages)
-            return nullptr;
-        const int page = __ldg(pages + k);
-        if (page < 0 || page >= a.s.n_pages)
-            return nullptr;
-        return base + (kv16_row(a.s, page, 0, static_cast<int>(plane)) + (j - k * a.s.page_rows)) * 16;
-    };
-    uint4 v[EACH];
-    uint4* to[EACH];
+        const int* pages = a.pages + static_cast<size_t>(b) * a.max_pages;
+        // a row's place, below 0 where it does not exist
+        auto at = [&](uint32_t j) -> long long {
+            if (j > 0x7fffffffu)
+                return -1;
+            const int k = static_cast<int>(fast_div(j, a.by_page));
+            if (k >= a.max_pages)
+                return -1;
+            const int page = __ldg(pages + k);
+            return page < 0 || page >= a.s.n_pages ? -1 : kv16_row(a.s, page, kv, 0) + (static_cast<int>(j) - k * a.s.page_rows);
+        };
+        int count = 0;
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-        const int i = static_cast<int>(threadIdx.x >> 4) + e * (KV16_KEEP_THREADS / 16);
-        to[e] = nullptr;
-        if (i >= n)
-            continue;
-        const int node = __ldg(a.path + static_cast<size_t>(b) * a.max_new + i);
-        if (node == i)
-            continue;
-        const bool fits = node >= 0 && node < a.max_new;
-        const uint4* from = fits ? at(static_cast<int>(static_cast<uint32_t>(past) + node)) : nullptr;
-        to[e] = at(static_cast<int>(static_cast<uint32_t>(past) + i));
-        if (!from || !to[e]) {
-            set_error(a.err, DEVERR_BAD_ARG);
-            to[e] = nullptr;
-            continue;
+        for (int e = 0; e < KV16_MAX_NEW / 32; ++e) {
+            const int i = 32 * e + lane;
+            bool go = !bad && i < n;
+            long long f = -1, t = -1;
+            if (go) {
+                const int node = __ldg(a.path + static_cast<size_t>(b) * a.max_new + i);
+                go = node != i;
+                if (go) {
+                    if (node >= 0 && node < a.max_new)
+                        f = at(static_cast<uint32_t>(past) + node);
+                    t = at(static_cast<uint32_t>(past) + i);
+                    if (f < 0 || t < 0) {
+                        set_error(a.err, DEVERR_BAD_ARG);
+                        go = false;
+                    }
+                }
+            }
+            const unsigned who = __ballot_sync(0xffffffffu, go);
+            if (go) {
+                const int place = count + __popc(who & ((1u << lane) - 1));
+                from[place] = f;
+                to[place] = t;
+            }
+            count += __popc(who);
         }
-        v[e] = from[threadIdx.x & 15];
+        if (lane == 0)
+            moved = count;
     }
     __syncthreads();
+    const int n = moved;
+    if (n == 0)
+        return;
+    uint4* base = reinterpret_cast<uint4*>(a.pool + layer * a.layer);
+    const int pieces = 16 * n, heads = KV16_KEEP_THREADS * KV16_KEEP_EACH / pieces;  // at a time
+    for (int h0 = 0; h0 < a.s.n_kv; h0 += heads) {
+        uint4 v[KV16_KEEP_EACH];
+        long long dst[KV16_KEEP_EACH];
 #pragma unroll
-    for (int e = 0; e < EACH; ++e)
-        if (to[e])
-            to[e][threadIdx.x & 15] = v[e];
+        for (int e = 0; e < KV16_KEEP_EACH; ++e) {
+            const int i = tid + e * KV16_KEEP_THREADS, h = i / pieces, row = (i - h * pieces) >> 4;
+            dst[e] = -1;
+            if (h < heads && h0 + h < a.s.n_kv) {
+                const long long head = static_cast<long long>(h0 + h) * a.s.page_rows;
+                v[e] = __ldcg(base + (from[row] + head) * 16 + (i & 15));
+                dst[e] = (to[row] + head) * 16 + (i & 15);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < KV16_KEEP_EACH; ++e)
+            if (dst[e] >= 0)
+                base[dst[e]] = v[e];
+    }
 }
 
 }  // namespace dq
@@ -253,10 +285,9 @@ DQ_API int dq_kv16_keep(void* pool, int type, const int* pages, const int* n_pas
         (reinterpret_cast<uintptr_t>(n_past) & 3) || (reinterpret_cast<uintptr_t>(path) & 3) ||
         (reinterpret_cast<uintptr_t>(n_path) & 3))
         return DQ_ERR_ALIGN;
-    const unsigned grid = static_cast<unsigned>(static_cast<long long>(n_seq) * n_layers * 2 * n_kv);
+    const unsigned grid = static_cast<unsigned>(static_cast<long long>(n_seq) * n_layers * 2);
     const dq::Kv16KeepArgs a{static_cast<unsigned char*>(pool), layer_stride, pages, n_past, path, n_path, max_new, max_pages,
-                             {n_kv, n_pages, page_size}, dqhost::fast_divisor(page_size), dqhost::fast_divisor(2 * n_kv),
-                             dqhost::fast_divisor(n_layers), dqhost::device_error_flag()};
+                             {n_kv, n_pages, page_size}, dqhost::fast_divisor(page_size), dqhost::fast_divisor(n_layers), dqhost::device_error_flag()};
     dq::kv16_keep_kernel<<<grid, dq::KV16_KEEP_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);

@@ -23,6 +23,8 @@ constexpr int VF_PIECE = 8192;   // logits a block of the first kernel
 constexpr int VF_THREADS = 256;
 constexpr int VF_EACH = VF_PIECE / VF_THREADS;
 constexpr int VF_CLUSTER = 8;    // blocks a sequence
+constexpr int VF_PICK = 512;     // threads each
+constexpr int VF_BATCH = 8;      // places a thread has in flight there
 constexpr int VF_MAX_NEW = 64;
 
 struct VerifyArgs {
@@ -62,26 +64,36 @@ __device__ __forceinline__ float verify_one(const __half* p) { return __half2flo
 __device__ __forceinline__ float verify_one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // A logit as the definition takes it: NaN counts as -infinity.
-__device__ __forceinline__ float verify_clean(float x) { return x == x ? x : -INFINITY; }
+__device__ __forceinline__ float verify_clean(float x) { return fmaxf(x, -INFINITY); }
 
-// log2(e) / temperature in two parts.
+// What exp((x - m) / temperature) needs: log2(e) / temperature in two parts, and the
+// difference beyond which it is 0 (2^-200).  The temperature is kept within 2^-60 .. 2^60.
 struct VerifyScale {
-    float hi, lo;
+    float hi, lo, least;
 };
 __device__ __forceinline__ VerifyScale verify_scale(float temperature)
 {
     constexpr float L = 1.4426950408889634f, REST = static_cast<float>(1.4426950408889634 - static_cast<double>(L));
-    const float hi = __fdiv_rn(L, temperature);
-    const float lo = __fdiv_rn(fmaf(-hi, temperature, L) + REST, temperature);
-    return {hi, hi > 0.f && hi < INFINITY ? lo : 0.f};
+    const float t = fminf(fmaxf(temperature, 8.673617e-19f), 1.1529215e18f);
+    const float hi = __fdiv_rn(L, t);
+    return {hi, __fdiv_rn(fmaf(-hi, t, L) + REST, t), __fdiv_rn(-200.f, hi)};
 }
-// exp((x - m) / temperature) for x <= m, m > -infinity: 1 at m even where m is infinite, 0
-// at -infinity.  The product's rounding error goes back in as a factor 1 + e ln 2.
-__device__ __forceinline__ float verify_exp(float x, float m, VerifyScale c)
+// exp((x - m) / temperature) of two x <= m, m finite: exactly 1 at m, 0 at -infinity.  The
+// product's rounding error goes back in as a factor 1 + e ln 2 (ex2 itself: 2^-22).
+__device__ __forceinline__ uint64_t verify_exp2(float x, float y, float m, const VerifyScale& c)
 {
-    const float d = x - m, t = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -t));
-    const float w = ex2(t);
-    return x == m ? 1.f : w == 0.f || x == -INFINITY ? 0.f : fmaf(w, e * 0.6931471805599453f, w);
+    const float2 d0 = un2(add2(f2(x, y), f2(-m, -m)));
+    const uint64_t d = f2(fmaxf(d0.x, c.least), fmaxf(d0.y, c.least)), hi = f2(c.hi, c.hi);
+    const uint64_t t = mul2(d, hi), minus = mul2(t, f2(-1.f, -1.f));
+    const uint64_t e = fma2(d, f2(c.lo, c.lo), fma2(d, hi, minus));
+    const float2 p = un2(t);
+    const uint64_t w = f2(ex2(p.x), ex2(p.y));
+    return fma2(w, mul2(e, f2(0.6931471805599453f, 0.6931471805599453f)), w);
+}
+// The same of one, 1 at m even where m is infinite.
+__device__ __forceinline__ float verify_exp(float x, float m, const VerifyScale& c)
+{
+    return x == m ? 1.f : isinf(m) ? 0.f : un2(verify_exp2(x, x, m, c)).x;
 }
 
 struct Best {
@@ -101,105 +113,140 @@ __device__ __forceinline__ Best warp_best(Best x)
     return x;
 }
 
-template <typename T, bool VEC>
+// The sequence that a row belongs to, by one warp; -1: none.
+__device__ __forceinline__ int verify_seq(const VerifyArgs& a, int row, int lane)
+{
+    if (!a.cu)
+        return row / a.max_new;
+    for (int s0 = 0; s0 < a.n_seq; s0 += 128) {
+        unsigned hit[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int s = s0 + 32 * e + lane;
+            bool ok = false;
+            int2 n = make_int2(0, 0);
+            if (s < a.n_seq)
+                n = verify_nodes(a, s, ok);
+            hit[e] = __ballot_sync(0xffffffffu, ok && row >= n.x && row < n.x + n.y);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (hit[e])
+                return s0 + 32 * e + __ffs(hit[e]) - 1;
+    }
+    return -1;
+}
+
+template <typename T>
 __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyArgs a)
 {
-    __shared__ Best tops[VF_THREADS / 32];
-    __shared__ float sums[VF_THREADS / 32];
-    __shared__ int seq_of;
+    constexpr int WARPS = VF_THREADS / 32;
+    __shared__ Best tops[WARPS];
+    __shared__ float sums[WARPS];
     const int row = blockIdx.x / a.pieces, piece = blockIdx.x - row * a.pieces;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_trigger();
     const T* src = static_cast<const T*>(a.logits) + row * a.ld;
-    constexpr int W = VEC ? 16 / static_cast<int>(sizeof(T)) : 1;  // elements an access
+    // 16-byte accesses wherever the row begins: element 0 of a row is element `skew` of its
+    // first one; element i = W k + e of a thread is at first + W VF_THREADS k + e
+    constexpr int W = 16 / static_cast<int>(sizeof(T));
+    const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+    const int first = piece * VF_PIECE + W * tid - skew;
     float x[VF_EACH];
-    // element i = W k + e of a thread is at base + W VF_THREADS k + W tid + e: ascending in i
-    const int base = piece * VF_PIECE + W * tid;
+    if (piece * VF_PIECE >= skew && piece * VF_PIECE - skew + VF_PIECE <= a.vocab) {
+        uint4 u[VF_EACH / W];
 #pragma unroll
-    for (int k = 0; k < VF_EACH / W; ++k) {
-        const int at = base + W * VF_THREADS * k;
-        if (VEC && at + W <= a.vocab) {
-            const uint4 u = __ldcg(reinterpret_cast<const uint4*>(src + at));
-            const T* e = reinterpret_cast<const T*>(&u);
+        for (int k = 0; k < VF_EACH / W; ++k)
+            u[k] = __ldcg(reinterpret_cast<const uint4*>(src + first + W * VF_THREADS * k));
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                x[W * k + i] = verify_clean(verify_one(e + i));
-        } else {
+        for (int k = 0; k < VF_EACH / W; ++k)
 #pragma unroll
             for (int i = 0; i < W; ++i)
-                x[W * k + i] = at + i < a.vocab ? verify_clean(verify_one(src + at + i)) : -INFINITY;
-        }
-    }
-    if (tid == 0)
-        seq_of = -1;
-    __syncthreads();
-    if (!a.cu) {
-        if (tid == 0)
-            seq_of = row / a.max_new;
+                x[W * k + i] = verify_one(reinterpret_cast<const T*>(&u[k]) + i);
     } else {
-        for (int s = tid; s < a.n_seq; s += VF_THREADS) {
-            bool ok;
-            const int2 n = verify_nodes(a, s, ok);
-            if (row >= n.x && row < n.x + n.y)
-                seq_of = s;
+#pragma unroll
+        for (int k = 0; k < VF_EACH / W; ++k) {
+            const int at = first + W * VF_THREADS * k;
+            if (at >= 0 && at + W <= a.vocab) {
+                const uint4 u = __ldcg(reinterpret_cast<const uint4*>(src + at));
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    x[W * k + i] = verify_one(reinterpret_cast<const T*>(&u) + i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    x[W * k + i] = at + i >= 0 && at + i < a.vocab ? verify_one(src + at + i) : -INFINITY;
+            }
         }
     }
-    Best top{-INFINITY, -1};
-#pragma unroll
-    for (int i = 0; i < VF_EACH; ++i)
-        if (x[i] > top.v)
-            top = {x[i], base + W * VF_THREADS * (i / W) + i % W};
-    top = warp_best(top);
-    if (lane == 0)
-        tops[warp] = top;
-    __syncthreads();
-    const int s = seq_of;
+    const int s = verify_seq(a, row, lane);
     if (s < 0)
         return;  // a row of no sequence
-    top = tops[0];
-#pragma unroll
-    for (int w = 1; w < VF_THREADS / 32; ++w)
-        top = better(top, tops[w]);
     const float temp = a.temperature ? __ldg(a.temperature + s) : 1.f;
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < VF_EACH; ++i)
+        m4[i & 3] = fmaxf(m4[i & 3], x[i]);  // NaN is passed over
+    const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), m = warp_max(mine);
+    int at = 0x7fffffff;
+    if (mine == m && m > -INFINITY) {
+#pragma unroll
+        for (int i = VF_EACH - 1; i >= 0; --i)
+            if (x[i] == m)
+                at = first + W * VF_THREADS * (i / W) + i % W;
+    }
+    at = __reduce_min_sync(0xffffffffu, at);
     float sum = 0.f;
-    if (temp > 0.f && top.at >= 0) {
+    if (temp > 0.f && m > -INFINITY) {
         const VerifyScale c = verify_scale(temp);
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        if (m < INFINITY) {
+            uint64_t part[2] = {0ull, 0ull};
 #pragma unroll
-        for (int i = 0; i < VF_EACH; ++i)
-            part[i & 3] += verify_exp(x[i], top.v, c);
-        sum = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+            for (int i = 0; i < VF_EACH / 2; ++i)
+                part[i & 1] = add2(part[i & 1], verify_exp2(verify_clean(x[2 * i]), verify_clean(x[2 * i + 1]), m, c));
+            const float2 p = un2(add2(part[0], part[1]));
+            sum = p.x + p.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < VF_EACH; ++i)
+                sum += x[i] == m ? 1.f : 0.f;
+        }
+        sum = warp_sum(sum);
     }
-    if (lane == 0)
+    if (lane == 0) {
+        tops[warp] = Best{m, m > -INFINITY ? at : -1};
         sums[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        float z = 0.f;
-#pragma unroll
-        for (int w = 0; w < VF_THREADS / 32; ++w)
-            z += sums[w];
-        a.part[static_cast<size_t>(row) * a.pieces + piece] = make_float4(top.v, __int_as_float(top.at), z, 0.f);
     }
+    __syncthreads();
+    if (warp)
+        return;
+    Best b = lane < WARPS ? tops[lane] : Best{-INFINITY, -1};
+    const Best top = warp_best(b);
+    if (top.at >= 0 && temp > 0.f)
+        sum = warp_sum(lane < WARPS && b.at >= 0 ? sums[lane] * verify_exp(b.v, top.v, verify_scale(temp)) : 0.f);
+    if (lane == 0)
+        a.part[static_cast<size_t>(row) * a.pieces + piece] = make_float4(top.v, __int_as_float(top.at), sum, 0.f);
 }
 
 struct VerifyShared {
-    Best top[VF_MAX_NEW];      // a node's largest logit
-    double sum[VF_MAX_NEW];    // of its weights
-    double p[VF_MAX_NEW];      // of a node's token at its parent
+    Best top[VF_MAX_NEW];        // a node's largest logit
+    double sum[VF_MAX_NEW];      // of its weights
+    float w[VF_MAX_NEW];         // the weight of a node's token at its parent
     float u[VF_MAX_NEW], q[VF_MAX_NEW];
     int parent[VF_MAX_NEW], token[VF_MAX_NEW];
+    int path[VF_MAX_NEW], len;
     int gone[VF_MAX_NEW], n_gone;  // rejected tokens at the last node
     int last, turned_down;         // the rejected node of a chain, or 0
-    Best warp[VF_THREADS / 32];
-    double exact_v[VF_THREADS / 32];
-    int exact_at[VF_THREADS / 32];
-    float best;          // the block's
+    Best warp[VF_PICK / 32];
+    double exact_v[VF_PICK / 32];
+    int exact_at[VF_PICK / 32];
+    float best;  // the block's
     double best_exact;
     int best_at;
 };
 
 template <typename T>
-__global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS) verify_pick_kernel(const VerifyArgs a)
+__global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) verify_pick_kernel(const VerifyArgs a)
 {
     namespace cg = cooperative_groups;
     __shared__ VerifyShared sh;
@@ -249,50 +296,64 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
         sh.token[tid] = token;
     }
     pdl_wait();
-    // four threads a node join its pieces
-    {
-        const int node = tid >> 2, k0 = tid & 3;
+    // eight threads a node join its pieces: the largest logit first, then the sums in two
+    // parts (the second has what the first loses)
+    if (warp < 4 * ((n + 15) / 16)) {
+        const int node = tid >> 3, k0 = tid & 7;
+        const float4* part = a.part + static_cast<size_t>(row0 + min(node, n - 1)) * a.pieces;
+        constexpr int E = 4;
+        float4 x[E];
         Best top{-INFINITY, -1};
-        double sum = 0.0;
-        if (node < n) {
-            const float4* part = a.part + static_cast<size_t>(row0 + node) * a.pieces;
-            for (int k = k0; k < a.pieces; k += 4) {
-                const float4 x = __ldcg(part + k);
-                const Best b{x.x, __float_as_int(x.y)};
-                if (b.at < 0)
-                    continue;
-                const Best t = better(top, b);
-                sum = (top.at < 0 ? 0.0 : sum * verify_exp(top.v, t.v, c)) +
-                      static_cast<double>(x.z) * verify_exp(b.v, t.v, c);
-                top = t;
+        for (int k = k0; k < a.pieces; k += 8 * E) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[e] = k + 8 * e < a.pieces ? __ldcg(part + k + 8 * e) : make_float4(-INFINITY, __int_as_float(-1), 0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                top = better(top, Best{x[e].x, __float_as_int(x[e].y)});
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+            top = better(top, Best{__shfl_xor_sync(0xffffffffu, top.v, o), __shfl_xor_sync(0xffffffffu, top.at, o)});
+        float hi = 0.f, lo = 0.f;
+        auto add = [&](float v) {
+            const float t = hi + v, z = t - hi;
+            lo += (hi - (t - z)) + (v - z);
+            hi = t;
+        };
+        for (int k = k0; k < a.pieces; k += 8 * E) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (a.pieces > 8 * E)
+                    x[e] = k + 8 * e < a.pieces ? __ldcg(part + k + 8 * e) : make_float4(0.f, __int_as_float(-1), 0.f, 0.f);
+                if (__float_as_int(x[e].y) >= 0)
+                    add(x[e].z * verify_exp(x[e].x, top.v, c));
             }
         }
 #pragma unroll
-        for (int o = 2; o > 0; o >>= 1) {
-            const Best b{__shfl_xor_sync(0xffffffffu, top.v, o), __shfl_xor_sync(0xffffffffu, top.at, o)};
-            const double z = __shfl_xor_sync(0xffffffffu, sum, o);
-            const Best t = better(top, b);
-            sum = (top.at < 0 ? 0.0 : sum * verify_exp(top.v, t.v, c)) + (b.at < 0 ? 0.0 : z * verify_exp(b.v, t.v, c));
-            top = t;
+        for (int o = 4; o > 0; o >>= 1) {
+            const float h2 = __shfl_xor_sync(0xffffffffu, hi, o), l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+            add(h2);
+            lo += l2;
         }
         if (node < n && k0 == 0) {
             sh.top[node] = top;
-            sh.sum[node] = sum;
+            sh.sum[node] = static_cast<double>(hi) + lo;
         }
     }
     __syncthreads();
     if (tid < n && parent >= 0) {
         const Best t = sh.top[parent];
-        sh.p[tid] = token < 0 || t.at < 0 || greedy ? 0.0 : verify_exp(own, t.v, c) / sh.sum[parent];
+        sh.w[tid] = token < 0 || t.at < 0 || greedy ? 0.f : verify_exp(own, t.v, c);
     }
     __syncthreads();
 
-    // ---- the walk: a node's children are above it, so one pass in ascending order
+    // ---- the walk, by one thread: a node's children are above it, so one pass in ascending
+    // order; probabilities in units of 1 / the node's sum
     if (tid == 0) {
         int cur = 0, len = 1, gone = 0, down = 0;
-        double left = 1.0;
-        if (rank == 0)
-            path[0] = 0;
+        double left = sh.sum[0];
+        sh.path[0] = 0;
         for (int j = 1; j < n; ++j) {
             if (sh.parent[j] != cur)
                 continue;
@@ -301,37 +362,37 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
             if (greedy) {
                 take = x >= 0 && x == sh.top[cur].at;
             } else if (a.draft) {
-                take = x >= 0 && static_cast<double>(sh.u[j]) * sh.q[j] < sh.p[j];
+                take = x >= 0 && static_cast<double>(sh.u[j]) * sh.q[j] * left < sh.w[j];
                 down = take ? 0 : j;
             } else {
                 bool again = x < 0;
                 for (int k = 0; k < gone; ++k)
                     again |= sh.gone[k] == x;
-                take = !again && sh.u[j] * left < sh.p[j];
+                take = !again && sh.u[j] * left < sh.w[j];
                 if (!again && !take) {
                     sh.gone[gone++] = x;
-                    left -= sh.p[j];
+                    left -= sh.w[j];
                 }
             }
             if (take) {
-                if (rank == 0)
-                    path[len] = j;
+                sh.path[len++] = j;
                 cur = j;
-                ++len;
                 gone = 0;
-                left = 1.0;
+                left = sh.sum[j];
             }
         }
         sh.last = cur;
         sh.n_gone = gone;
         sh.turned_down = down;
-        if (rank == 0) {
-            a.n_path[s] = len;
-            for (int k = len; k < a.max_new; ++k)
-                path[k] = -1;
-        }
+        sh.len = len;
     }
     __syncthreads();
+    if (rank == 0) {
+        if (tid < a.max_new)
+            path[tid] = tid < sh.len ? sh.path[tid] : -1;
+        if (tid == 0)
+            a.n_path[s] = sh.len;
+    }
     const int last = sh.last, n_gone = sh.n_gone, down = sh.turned_down;
     const Best top = sh.top[last];
     if (greedy || top.at < 0) {
@@ -348,16 +409,27 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
     const int slice = (a.vocab + VF_CLUSTER - 1) / VF_CLUSTER, v0 = rank * slice, v1 = min(a.vocab, v0 + slice);
     Best best{0.f, -1};
     float size = 0.f;  // of the numbers that the best's r is a difference of, over its noise
-    for (int v = v0 + tid; v < v1; v += VF_THREADS) {
-        const float w = verify_exp(verify_clean(verify_one(row + v)), top.v, c), q = draft ? z * draft[v] : 0.f;
-        const float e = noise[v], score = (w - q) / e;
-        if (score > best.v) {
-            bool out = false;
-            for (int k = 0; k < n_gone; ++k)
-                out |= sh.gone[k] == v;
-            if (!out) {
-                best = {score, v};
-                size = (w + q) / e;
+    for (int b0 = v0 + tid; b0 < v1; b0 += VF_PICK * VF_BATCH) {
+        float x[VF_BATCH], q[VF_BATCH], e[VF_BATCH];
+#pragma unroll
+        for (int i = 0; i < VF_BATCH; ++i) {
+            const int v = b0 + i * VF_PICK;
+            x[i] = v < v1 ? verify_clean(verify_one(row + v)) : -INFINITY;
+            e[i] = v < v1 ? __ldcs(noise + v) : 1.f;
+            q[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < VF_BATCH; ++i) {
+            const int v = b0 + i * VF_PICK;
+            const float w = verify_exp(x[i], top.v, c), score = __fdividef(w - z * q[i], e[i]);
+            if (score > best.v) {
+                bool out = false;
+                for (int k = 0; k < n_gone; ++k)
+                    out |= sh.gone[k] == v;
+                if (!out) {
+                    best = {score, v};
+                    size = (w + z * q[i]) / e[i];
+                }
             }
         }
     }
@@ -366,31 +438,34 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
         sh.warp[warp] = b;
     __syncthreads();
     cg::cluster_group cluster = cg::this_cluster();
-    if (tid == 0) {
-        for (int w = 1; w < VF_THREADS / 32; ++w)
-            b = better(b, sh.warp[w]);
-        sh.best = b.at < 0 ? 0.f : b.v;
+    if (warp == 0) {
+        b = warp_best(lane < VF_PICK / 32 ? sh.warp[lane] : Best{0.f, -1});
+        if (lane == 0)
+            sh.best = b.at < 0 ? 0.f : b.v;
     }
     cluster.sync();
     float most = 0.f;
+#pragma unroll
     for (int k = 0; k < VF_CLUSTER; ++k)
         most = fmaxf(most, *cluster.map_shared_rank(&sh.best, k));
     double v64 = 0.0;
     int at64 = -1;
-    if (best.at >= 0 && best.v + 1e-5f * size >= most * (1.f - 1e-5f)) {
-        const float x = verify_one(row + best.at);
-        const double w = x == top.v ? 1.0 : exp((static_cast<double>(x) - top.v) / temp);
-        v64 = (w - (draft ? sh.sum[last] * draft[best.at] : 0.0)) / noise[best.at];
-        at64 = best.at;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const double v = __shfl_xor_sync(0xffffffffu, v64, o);
-        const int at = __shfl_xor_sync(0xffffffffu, at64, o);
+    auto larger = [&](double v, int at) {
         if (at >= 0 && (at64 < 0 || v > v64 || (v == v64 && at < at64))) {
             v64 = v;
             at64 = at;
         }
+    };
+    if (best.at >= 0 && best.v + 1e-5f * size >= most * (1.f - 1e-5f)) {
+        const float x = verify_one(row + best.at);
+        const double t = fmin(fmax(static_cast<double>(temp), 8.673617379884035e-19), 1.152921504606847e18);
+        const double w = x == top.v ? 1.0 : exp((static_cast<double>(x) - top.v) / t);
+        larger((w - (draft ? sh.sum[last] * draft[best.at] : 0.0)) / noise[best.at], best.at);
+    }
+    if (__any_sync(0xffffffffu, at64 >= 0)) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            larger(__shfl_xor_sync(0xffffffffu, v64, o), __shfl_xor_sync(0xffffffffu, at64, o));
     }
     if (lane == 0) {
         sh.exact_v[warp] = v64;
@@ -398,24 +473,15 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
     }
     __syncthreads();
     if (tid == 0) {
-        for (int w = 1; w < VF_THREADS / 32; ++w)
-            if (sh.exact_at[w] >= 0 && (at64 < 0 || sh.exact_v[w] > v64 || (sh.exact_v[w] == v64 && sh.exact_at[w] < at64))) {
-                v64 = sh.exact_v[w];
-                at64 = sh.exact_at[w];
-            }
+        for (int w = 1; w < VF_PICK / 32; ++w)
+            larger(sh.exact_v[w], sh.exact_at[w]);
         sh.best_exact = v64;
         sh.best_at = at64;
     }
     cluster.sync();
     if (rank == 0 && tid == 0) {
-        for (int k = 1; k < VF_CLUSTER; ++k) {
-            const double v = *cluster.map_shared_rank(&sh.best_exact, k);
-            const int at = *cluster.map_shared_rank(&sh.best_at, k);
-            if (at >= 0 && (at64 < 0 || v > v64 || (v == v64 && at < at64))) {
-                v64 = v;
-                at64 = at;
-            }
-        }
+        for (int k = 1; k < VF_CLUSTER; ++k)
+            larger(*cluster.map_shared_rank(&sh.best_exact, k), *cluster.map_shared_rank(&sh.best_at, k));
         a.next[s] = at64 >= 0 ? at64 : top.at;
     }
     cluster.sync();  // a block's shared memory is read by the first until here
@@ -425,7 +491,8 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_THREADS)
 
 namespace dqhost {
 
-static int verify_pieces(int vocab) { return (vocab + dq::VF_PIECE - 1) / dq::VF_PIECE; }
+// Pieces of a row, which may begin up to 7 elements into its first 16 bytes.
+static int verify_pieces(int vocab) { return (vocab + 7 + dq::VF_PIECE - 1) / dq::VF_PIECE; }
 
 }  // namespace dqhost
 
@@ -467,21 +534,17 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
                            v->n_seq, v->total_new, v->max_new, v->vocab, pieces, static_cast<float4*>(v->workspace),
                            dqhost::device_error_flag()};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool vec = dqhost::aligned16(v->logits) && (v->total_new == 1 || v->logits_stride * size % 16 == 0);
     cudaError_t e = dqhost::with_type(v->type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
         const unsigned grid = static_cast<unsigned>(v->total_new) * pieces;
-        if (vec)
-            dq::verify_stats_kernel<T, true><<<grid, dq::VF_THREADS, 0, s>>>(a);
-        else
-            dq::verify_stats_kernel<T, false><<<grid, dq::VF_THREADS, 0, s>>>(a);
+        dq::verify_stats_kernel<T><<<grid, dq::VF_THREADS, 0, s>>>(a);
         const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess)
             return err;
         // a dependent launch: it gathers the tree's numbers while the last pieces run
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(v->n_seq) * dq::VF_CLUSTER);
-        cfg.blockDim = dim3(dq::VF_THREADS);
+        cfg.blockDim = dim3(dq::VF_PICK);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -488,6 +488,8 @@ def verify_reference(logits, tokens, uniform, noise, new, parents=None, draft=No
     vocab = logits.shape[1]
     for s, n in enumerate(new):
         temp = 1.0 if temperature is None else float(temperature[s])
+        if temp > 0:
+            temp = min(max(temp, 2.0 ** -60), 2.0 ** 60)
         cur, path, gone, down = 0, [0][:n], [], 0
 
         def weights(node):
