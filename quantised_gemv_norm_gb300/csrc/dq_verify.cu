@@ -22,9 +22,9 @@ namespace dq {
 constexpr int VF_PIECE = 8192;   // logits a block of the first kernel
 constexpr int VF_THREADS = 256;
 constexpr int VF_EACH = VF_PIECE / VF_THREADS;
-constexpr int VF_CLUSTER = 8;    // blocks a sequence
+constexpr int VF_CLUSTER = 8;    // blocks a sequence, at most
 constexpr int VF_PICK = 512;     // threads each
-constexpr int VF_BATCH = 8;      // places a thread has in flight there
+constexpr int VF_BATCH = 10;     // places a thread has in flight there
 constexpr int VF_MAX_NEW = 64;
 
 struct VerifyArgs {
@@ -78,22 +78,21 @@ __device__ __forceinline__ VerifyScale verify_scale(float temperature)
     const float hi = __fdiv_rn(L, t);
     return {hi, __fdiv_rn(fmaf(-hi, t, L) + REST, t), __fdiv_rn(-200.f, hi)};
 }
-// exp((x - m) / temperature) of two x <= m, m finite: exactly 1 at m, 0 at -infinity.  The
-// product's rounding error goes back in as a factor 1 + e ln 2 (ex2 itself: 2^-22).
-__device__ __forceinline__ uint64_t verify_exp2(float x, float y, float m, const VerifyScale& c)
+// exp((x - m) / temperature) of two x <= m, m finite: exactly 1 at m, 0 at -infinity and
+// for a NaN.  Off by 2^-24 of the exponent, where a weight is large less than ex2's 2^-22.
+__device__ __forceinline__ uint64_t verify_exp2(uint64_t x, uint64_t minus_m, const VerifyScale& c)
 {
-    const float2 d0 = un2(add2(f2(x, y), f2(-m, -m)));
-    const uint64_t d = f2(fmaxf(d0.x, c.least), fmaxf(d0.y, c.least)), hi = f2(c.hi, c.hi);
-    const uint64_t t = mul2(d, hi), minus = mul2(t, f2(-1.f, -1.f));
-    const uint64_t e = fma2(d, f2(c.lo, c.lo), fma2(d, hi, minus));
-    const float2 p = un2(t);
-    const uint64_t w = f2(ex2(p.x), ex2(p.y));
-    return fma2(w, mul2(e, f2(0.6931471805599453f, 0.6931471805599453f)), w);
+    const float2 d0 = un2(add2(x, minus_m));
+    const uint64_t d = f2(fmaxf(d0.x, c.least), fmaxf(d0.y, c.least));
+    const float2 t = un2(fma2(d, f2(c.lo, c.lo), mul2(d, f2(c.hi, c.hi))));
+    return f2(ex2(t.x), ex2(t.y));
 }
-// The same of one, 1 at m even where m is infinite.
+// The same of one, 1 at m even where m is infinite; the product's rounding error goes back
+// in as a factor 1 + e ln 2.
 __device__ __forceinline__ float verify_exp(float x, float m, const VerifyScale& c)
 {
-    return x == m ? 1.f : isinf(m) ? 0.f : un2(verify_exp2(x, x, m, c)).x;
+    const float d = fmaxf(x - m, c.least), t = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -t)), w = ex2(t);
+    return x == m ? 1.f : isinf(m) ? 0.f : fmaf(w, e * 0.6931471805599453f, w);
 }
 
 struct Best {
@@ -141,8 +140,8 @@ template <typename T>
 __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyArgs a)
 {
     constexpr int WARPS = VF_THREADS / 32;
-    __shared__ Best tops[WARPS];
-    __shared__ float sums[WARPS];
+    __shared__ float tops[WARPS], sums[WARPS];
+    __shared__ int place;
     const int row = blockIdx.x / a.pieces, piece = blockIdx.x - row * a.pieces;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_trigger();
@@ -179,6 +178,8 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
             }
         }
     }
+    if (tid == 0)
+        place = 0x7fffffff;
     const int s = verify_seq(a, row, lane);
     if (s < 0)
         return;  // a row of no sequence
@@ -187,23 +188,16 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
 #pragma unroll
     for (int i = 0; i < VF_EACH; ++i)
         m4[i & 3] = fmaxf(m4[i & 3], x[i]);  // NaN is passed over
-    const float mine = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), m = warp_max(mine);
-    int at = 0x7fffffff;
-    if (mine == m && m > -INFINITY) {
-#pragma unroll
-        for (int i = VF_EACH - 1; i >= 0; --i)
-            if (x[i] == m)
-                at = first + W * VF_THREADS * (i / W) + i % W;
-    }
-    at = __reduce_min_sync(0xffffffffu, at);
+    const float m = warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
     float sum = 0.f;
+    const VerifyScale c = verify_scale(temp > 0.f ? temp : 1.f);
     if (temp > 0.f && m > -INFINITY) {
-        const VerifyScale c = verify_scale(temp);
         if (m < INFINITY) {
             uint64_t part[2] = {0ull, 0ull};
+            const uint64_t minus = f2(-m, -m);
 #pragma unroll
             for (int i = 0; i < VF_EACH / 2; ++i)
-                part[i & 1] = add2(part[i & 1], verify_exp2(verify_clean(x[2 * i]), verify_clean(x[2 * i + 1]), m, c));
+                part[i & 1] = add2(part[i & 1], verify_exp2(f2(x[2 * i], x[2 * i + 1]), minus, c));
             const float2 p = un2(add2(part[0], part[1]));
             sum = p.x + p.y;
         } else {
@@ -214,18 +208,29 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
         sum = warp_sum(sum);
     }
     if (lane == 0) {
-        tops[warp] = Best{m, m > -INFINITY ? at : -1};
+        tops[warp] = m;
         sums[warp] = sum;
+    }
+    __syncthreads();
+    const float theirs = lane < WARPS ? tops[lane] : -INFINITY, top = warp_max(theirs);
+    // the lowest place of the largest logit: by the warps that have it
+    if (m == top && top > -INFINITY) {
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int i = VF_EACH - 1; i >= 0; --i)
+            if (x[i] == top)
+                at = first + W * VF_THREADS * (i / W) + i % W;
+        at = __reduce_min_sync(0xffffffffu, at);
+        if (lane == 0)
+            atomicMin(&place, at);
     }
     __syncthreads();
     if (warp)
         return;
-    Best b = lane < WARPS ? tops[lane] : Best{-INFINITY, -1};
-    const Best top = warp_best(b);
-    if (top.at >= 0 && temp > 0.f)
-        sum = warp_sum(lane < WARPS && b.at >= 0 ? sums[lane] * verify_exp(b.v, top.v, verify_scale(temp)) : 0.f);
+    sum = warp_sum(lane < WARPS && theirs > -INFINITY ? sums[lane] * verify_exp(theirs, top, c) : 0.f);
     if (lane == 0)
-        a.part[static_cast<size_t>(row) * a.pieces + piece] = make_float4(top.v, __int_as_float(top.at), sum, 0.f);
+        a.part[static_cast<size_t>(row) * a.pieces + piece] =
+            make_float4(top, __int_as_float(top > -INFINITY ? place : -1), sum, 0.f);
 }
 
 struct VerifyShared {
@@ -241,16 +246,17 @@ struct VerifyShared {
     double exact_v[VF_PICK / 32];
     int exact_at[VF_PICK / 32];
     float best;  // the block's
-    double best_exact;
-    int best_at;
+    int near[VF_PICK * VF_CLUSTER], n_near;  // in the first block: places near the cluster's best
 };
 
 template <typename T>
-__global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) verify_pick_kernel(const VerifyArgs a)
+__global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArgs a)
 {
     namespace cg = cooperative_groups;
     __shared__ VerifyShared sh;
-    const int s = blockIdx.x / VF_CLUSTER, rank = blockIdx.x % VF_CLUSTER;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int s = blockIdx.x / blocks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     bool ok;
     const int2 nodes = verify_nodes(a, s, ok);
@@ -406,7 +412,8 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) ve
     const float* noise = a.noise + s * a.noise_ld;
     const float* draft = down ? a.draft + (row0 + down) * a.draft_ld : nullptr;
     const float z = static_cast<float>(sh.sum[last]);
-    const int slice = (a.vocab + VF_CLUSTER - 1) / VF_CLUSTER, v0 = rank * slice, v1 = min(a.vocab, v0 + slice);
+    const int slice = (a.vocab + blocks - 1) / blocks, v0 = rank * slice, v1 = min(a.vocab, v0 + slice);
+    const uint64_t minus = f2(-top.v, -top.v);
     Best best{0.f, -1};
     float size = 0.f;  // of the numbers that the best's r is a difference of, over its noise
     for (int b0 = v0 + tid; b0 < v1; b0 += VF_PICK * VF_BATCH) {
@@ -414,14 +421,15 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) ve
 #pragma unroll
         for (int i = 0; i < VF_BATCH; ++i) {
             const int v = b0 + i * VF_PICK;
-            x[i] = v < v1 ? verify_clean(verify_one(row + v)) : -INFINITY;
+            x[i] = v < v1 ? verify_one(row + v) : -INFINITY;
             e[i] = v < v1 ? __ldcs(noise + v) : 1.f;
             q[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < VF_BATCH; ++i) {
             const int v = b0 + i * VF_PICK;
-            const float w = verify_exp(x[i], top.v, c), score = __fdividef(w - z * q[i], e[i]);
+            const float w = isinf(top.v) ? (x[i] == top.v ? 1.f : 0.f) : un2(verify_exp2(f2(x[i], x[i]), minus, c)).x;
+            const float score = __fdividef(w - z * q[i], e[i]);
             if (score > best.v) {
                 bool out = false;
                 for (int k = 0; k < n_gone; ++k)
@@ -437,17 +445,30 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) ve
     if (lane == 0)
         sh.warp[warp] = b;
     __syncthreads();
-    cg::cluster_group cluster = cg::this_cluster();
     if (warp == 0) {
         b = warp_best(lane < VF_PICK / 32 ? sh.warp[lane] : Best{0.f, -1});
-        if (lane == 0)
+        if (lane == 0) {
             sh.best = b.at < 0 ? 0.f : b.v;
+            sh.n_near = 0;
+        }
     }
     cluster.sync();
     float most = 0.f;
-#pragma unroll
-    for (int k = 0; k < VF_CLUSTER; ++k)
+    for (int k = 0; k < blocks; ++k)
         most = fmaxf(most, *cluster.map_shared_rank(&sh.best, k));
+    if (best.at >= 0 && best.v + 1e-5f * size >= most * (1.f - 1e-5f)) {
+        VerifyShared* head = cluster.map_shared_rank(&sh, 0);
+        head->near[atomicAdd(&head->n_near, 1)] = best.at;
+    }
+    cluster.sync();
+    if (rank)
+        return;
+    const int near = sh.n_near;
+    if (near <= 1) {
+        if (tid == 0)
+            a.next[s] = near ? sh.near[0] : top.at;
+        return;
+    }
     double v64 = 0.0;
     int at64 = -1;
     auto larger = [&](double v, int at) {
@@ -456,17 +477,16 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) ve
             at64 = at;
         }
     };
-    if (best.at >= 0 && best.v + 1e-5f * size >= most * (1.f - 1e-5f)) {
-        const float x = verify_one(row + best.at);
+    for (int k = tid; k < near; k += VF_PICK) {
+        const int at = sh.near[k];
+        const float x = verify_one(row + at);
         const double t = fmin(fmax(static_cast<double>(temp), 8.673617379884035e-19), 1.152921504606847e18);
         const double w = x == top.v ? 1.0 : exp((static_cast<double>(x) - top.v) / t);
-        larger((w - (draft ? sh.sum[last] * draft[best.at] : 0.0)) / noise[best.at], best.at);
+        larger((w - (draft ? sh.sum[last] * draft[at] : 0.0)) / noise[at], at);
     }
-    if (__any_sync(0xffffffffu, at64 >= 0)) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            larger(__shfl_xor_sync(0xffffffffu, v64, o), __shfl_xor_sync(0xffffffffu, at64, o));
-    }
+    for (int o = 16; o > 0; o >>= 1)
+        larger(__shfl_xor_sync(0xffffffffu, v64, o), __shfl_xor_sync(0xffffffffu, at64, o));
     if (lane == 0) {
         sh.exact_v[warp] = v64;
         sh.exact_at[warp] = at64;
@@ -475,16 +495,8 @@ __global__ void __cluster_dims__(VF_CLUSTER, 1, 1) __launch_bounds__(VF_PICK) ve
     if (tid == 0) {
         for (int w = 1; w < VF_PICK / 32; ++w)
             larger(sh.exact_v[w], sh.exact_at[w]);
-        sh.best_exact = v64;
-        sh.best_at = at64;
+        a.next[s] = at64;
     }
-    cluster.sync();
-    if (rank == 0 && tid == 0) {
-        for (int k = 1; k < VF_CLUSTER; ++k)
-            larger(*cluster.map_shared_rank(&sh.best_exact, k), *cluster.map_shared_rank(&sh.best_at, k));
-        a.next[s] = at64 >= 0 ? at64 : top.at;
-    }
-    cluster.sync();  // a block's shared memory is read by the first until here
 }
 
 }  // namespace dq
@@ -542,15 +554,22 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
         if (err != cudaSuccess)
             return err;
         // a dependent launch: it gathers the tree's numbers while the last pieces run
+        // as many blocks a sequence as are resident together, two an SM (1, 2, 4 or 8)
+        int blocks = dq::VF_CLUSTER;
+        while (blocks > 1 && static_cast<long long>(v->n_seq) * blocks > 2 * dqhost::sm_count())
+            blocks /= 2;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(v->n_seq) * dq::VF_CLUSTER);
+        cfg.gridDim = dim3(static_cast<unsigned>(v->n_seq) * blocks);
         cfg.blockDim = dim3(dq::VF_PICK);
         cfg.stream = s;
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = blocks;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, dq::verify_pick_kernel<T>, a);
     });
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
