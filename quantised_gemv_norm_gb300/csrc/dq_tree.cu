@@ -3,202 +3,9 @@
 #include <algorithm>
 #include <mutex>
 
-#include "dq_kv16.cuh"
-#include "dq_tma_host.h"
+#include "dq_tree.cuh"
 
 namespace dq {
-
-constexpr float TR_C = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
-constexpr int TR_MAX_NEW = 64, TR_MAX_GROUP = 64;
-// log2 of the growth of a row's maximum that is let pass before its sums are scaled: a
-// probability is up to 2^8 (fp16: of 2^7 at the maximum, up to 2^15)
-constexpr float TR_GROW = 8.f;
-
-struct TreeJoin;
-
-struct TreeArgs {
-    CUtensorMap map;  // the pool as [2 halves of a row][rows][64]
-    const void* q;
-    void* out;
-    long long q_row, q_head, o_row, o_head;
-    const int* pages;
-    const int* n_past;
-    const int* cu_new;
-    const unsigned long long* seen;
-    float* part;      // [blocks][2: first and last segment][rows a block][128], unscaled sums
-    float2* part_ml;  // their maxima and sums of probabilities
-    TreeJoin* join;   // [blocks]
-    long long room;   // rows that max_pages pages hold
-    int n_seq, total_new, max_new, group, max_pages, box, least;
-    Kv16Shape s;
-    FastDiv by_group, by_boxes;  // boxes of a page
-    int* err;
-};
-
-// A sequence's new rows, and the keys before them; no rows where cu_new is not in order,
-// no keys where n_past does not fit.
-struct TreeSeq {
-    int row0, rows, past, keys;
-    bool bad;
-};
-
-__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s)
-{
-    TreeSeq t;
-    int r1;
-    if (a.cu_new) {
-        t.row0 = __ldg(a.cu_new + s);
-        r1 = __ldg(a.cu_new + s + 1);
-    } else {
-        t.row0 = s * a.max_new;
-        r1 = t.row0 + a.max_new;
-    }
-    t.past = __ldg(a.n_past + s);
-    const bool in_order = t.row0 >= 0 && r1 >= t.row0 && r1 <= a.total_new && r1 - t.row0 <= a.max_new;
-    t.rows = in_order ? r1 - t.row0 : 0;
-    const bool fits = t.past >= 0 && static_cast<long long>(t.past) + t.rows <= a.room;
-    t.bad = !in_order || !fits;
-    if (!fits)
-        t.past = 0;
-    t.keys = fits ? t.past + t.rows : 0;
-    return t;
-}
-
-// The work is counted in units: one key tile of one item, an item being a row tile of one
-// sequence and KV head.  Sequence by sequence, item by item, tile by tile they are one
-// long row, of which every block takes an equal stretch; a stretch is cut into segments
-// where items change.
-template <int R, int KT>
-struct TreeCursor {
-    TreeSeq t;
-    int s, items, tiles;    // of the sequence
-    int item, tile;
-    long long left;         // units of the block's stretch
-
-    __device__ __forceinline__ long long units(const TreeArgs& a)
-    {
-        const int row_tiles = (t.rows * a.group + R - 1) / R;
-        items = a.s.n_kv * row_tiles;
-        tiles = max(1, (t.keys + KT - 1) / KT);
-        return static_cast<long long>(items) * tiles;
-    }
-    __device__ __forceinline__ void load(const TreeArgs& a, int seq)
-    {
-        s = seq;
-        t = tree_seq(a, seq);
-        units(a);
-    }
-    __device__ __forceinline__ int end() const { return static_cast<int>(min(static_cast<long long>(tiles), tile + left)); }
-    // to the next segment
-    __device__ __forceinline__ void next(const TreeArgs& a)
-    {
-        left -= end() - tile;
-        tile = 0;
-        ++item;
-        while (left > 0 && item >= items) {
-            item = 0;
-            load(a, s + 1);
-        }
-    }
-};
-
-// The block's stretch, by one warp: where it starts and how many units it has.
-struct TreeStart {
-    long long offset, left;  // units within the sequence; 0 left: none
-    int s;
-};
-
-template <int R, int KT>
-__device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int lane)
-{
-    constexpr int E = 4;  // sequences a lane and round
-    long long total = 0;
-    long long u[E];
-    auto round = [&](int s0, bool report) {
-        TreeCursor<R, KT> c;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int s = s0 + 32 * e + lane;
-            u[e] = 0;
-            if (s < a.n_seq) {
-                c.t = tree_seq(a, s);
-                u[e] = c.units(a);
-                if (report && c.t.bad)
-                    set_error(a.err, DEVERR_BAD_ARG);
-            }
-        }
-    };
-    auto sum = [](long long v) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
-    };
-    for (int s0 = 0; s0 < a.n_seq; s0 += 32 * E) {
-        round(s0, blockIdx.x == 0);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            total += sum(u[e]);
-    }
-    const long long each = max(static_cast<long long>(a.least), (total + gridDim.x - 1) / gridDim.x);
-    TreeStart st{0, 0, 0};
-    long long want = each * blockIdx.x;
-    st.left = min(each, total - want);
-    if (st.left <= 0) {
-        st.left = 0;
-        return st;
-    }
-    for (int s0 = 0; s0 < a.n_seq; s0 += 32 * E) {
-        if (a.n_seq > 32 * E)
-            round(s0, false);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            long long incl = u[e];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, want >= incl - u[e] && want < incl);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                st.offset = __shfl_sync(0xffffffffu, want - (incl - u[e]), src);
-                st.s = s0 + 32 * e + src;
-                return st;
-            }
-            want -= __shfl_sync(0xffffffffu, incl, 31);
-        }
-    }
-    st.left = 0;  // not reached: want is below the total
-    return st;
-}
-
-template <int R, int KT>
-__device__ __forceinline__ TreeCursor<R, KT> tree_cursor(const TreeArgs& a, const TreeStart& st)
-{
-    TreeCursor<R, KT> c;
-    c.left = st.left;
-    c.load(a, st.s);
-    c.item = static_cast<int>(st.offset / c.tiles);
-    c.tile = static_cast<int>(st.offset - static_cast<long long>(c.item) * c.tiles);
-    return c;
-}
-
-// What a block leaves for the join: its last segment began an item that later blocks go
-// on with, the last of them `last`; -1: nothing to join.
-struct TreeJoin {
-    int row0, rows, kv, row_tile, last;
-};
-
-__device__ __forceinline__ void tree_load(void* dst, const CUtensorMap* map, int y, uint64_t* bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(0), "r"(smem_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at)
 {
@@ -226,37 +33,6 @@ __device__ __forceinline__ void tree_mma(float (&d)[4], const uint32_t (&a)[4], 
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <typename T>
-__device__ __forceinline__ float tree_one(uint32_t bits)
-{
-    return std::is_same<T, __half>::value ? half_bits_to_float(bits) : bf16lo(bits);
-}
-
-// 0xffff in the halves of a pair that are an infinity or NaN.
-template <typename T>
-__device__ __forceinline__ uint32_t tree_non_finite(uint32_t w)
-{
-    constexpr bool half = std::is_same<T, __half>::value;
-    constexpr uint32_t mask = half ? 0x7C007C00u : 0x7F807F80u, one = half ? 0x04000400u : 0x00800080u;
-    return ((((w & mask) + one) & 0x80008000u) >> 15) * 0xffffu;
-}
-
-// The rest of a wait whose first poll found nothing; once one has run out the others
-// return at once and the block writes nothing.
-__device__ __forceinline__ void tree_wait_on(uint64_t* bar, uint32_t parity, volatile int* fail, int* err, int code)
-{
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-        if (*fail)
-            return;
-        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
-            *fail = 1;
-            set_error(err, code);
-            return;
-        }
-    }
 }
 
 // ---- up to 64 rows a block: warp-level matrix instructions
@@ -323,7 +99,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             const int box = a.box, per_tile = TM_KEYS / box, ahead = 32 / per_tile;
             long long issued = 0;
             for (; c.left > 0 && !__any_sync(0xffffffffu, *fail); c.next(a)) {
-                const int row_tiles = c.items / a.s.n_kv, g = c.item / row_tiles;
+                const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles;
                 const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
                 // lane i has the page of box `first + i`, and of box `first + 32 + i`
                 auto page_of = [&](int x) {
@@ -364,8 +140,8 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                         }
                         __syncwarp();
                         if (there)
-                            tree_load(ring + slot * TM_SLOT + lane * box * 256, &a.map,
-                                      static_cast<int>(kv16_row(a.s, page, kv, g)) + off, &sh.full[slot]);
+                            tree_load(ring + slot * TM_SLOT + lane * box * 256, &a.map, 0,
+                                      static_cast<int>(kv16_row(a.s, page, kv, g)) + off, 0, &sh.full[slot]);
                         ++issued;
                         turn();
                     }
@@ -392,7 +168,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             const uint32_t v_at = ((lane >> 3 & 1) * 8 + sw) * 128 + (((lane >> 4) ^ sw) << 4);
             const uint32_t base = smem_addr(ring);
             for (; c.left > 0; c.next(a)) {
-                const int row_tiles = c.items / a.s.n_kv, g = c.item / row_tiles, rt = c.item - g * row_tiles;
+                const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles;
                 const TreeSeq t = c.t;
                 // this lane's two rows
                 const T* qp[2];
@@ -650,7 +426,16 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, rr = blockIdx.y * 8 + warp;
     pdl_wait();
     const TreeJoin j = a.join[b];
-    const int r = j.row_tile * R + rr, node = static_cast<int>(fast_div(r, a.by_group));
+    int node, head;
+    if (a.nodes) {  // 128 rows for as many whole tokens as they hold
+        const int in_tile = rr & 127, token = static_cast<int>(fast_div(in_tile, a.by_group)), tokens = a.nodes / (R / 128);
+        head = in_tile - token * a.group;
+        node = token < tokens ? j.row_tile * a.nodes + (rr >> 7) * tokens + token : 0x7fffffff;
+    } else {
+        const int r = j.row_tile * R + rr;
+        node = static_cast<int>(fast_div(r, a.by_group));
+        head = r - node * a.group;
+    }
     if (j.last < 0 || node >= j.rows)
         return;
     float m = -INFINITY, l = 0.f;
@@ -684,7 +469,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     store4(static_cast<T*>(a.out) + static_cast<long long>(j.row0 + node) * a.o_row +
-               static_cast<long long>(j.kv * a.group + r - node * a.group) * a.o_head + 4 * lane,
+               static_cast<long long>(j.kv * a.group + head) * a.o_head + 4 * lane,
            l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
@@ -692,14 +477,20 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 
 namespace dqhost {
 
-// Rows a block, and blocks: two of up to 64 rows an SM.
+constexpr int TREE_MMA_ROWS = 48;
+
+// Rows a block and blocks: two of up to 64 rows an SM, or one of 128 or 256 on the tensor
+// cores of the 5th generation.
 struct TreeCut {
     int rows, blocks;
+    bool tc() const { return rows >= 128; }
 };
 
 static TreeCut tree_cut(int max_new, int group)
 {
     const int rows = max_new * group;
+    if (rows > TREE_MMA_ROWS)
+        return {(max_new + 128 / group - 1) / (128 / group) > 1 ? 256 : 128, sm_count()};
     return {rows <= 16 ? 16 : rows <= 32 ? 32 : 64, dq::TM_RESIDENT * sm_count()};
 }
 
@@ -707,20 +498,6 @@ static size_t tree_bytes(const TreeCut& c)
 {
     const size_t rows = static_cast<size_t>(c.blocks) * 2 * c.rows;
     return rows * (dq::ATT_HD + 2) * sizeof(float) + (c.blocks * sizeof(dq::TreeJoin) + 15) / 16 * 16;
-}
-
-// The pool in boxes of `box` rows, both halves of 64 dims, with the 128-byte swizzle.
-static bool tree_map(CUtensorMap* m, int type, const void* pool, long long rows, int box)
-{
-    const EncodeTiled enc = encode_tiled();
-    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 2};
-    const cuuint64_t strides[2] = {dq::ATT_HD * 2, 128};
-    const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(box), 2};
-    const cuuint32_t ones[3] = {1, 1, 1};
-    return enc && enc(m, type == DQ_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                      const_cast<void*>(pool), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A kernel's shared memory, asked for once per device.
@@ -749,10 +526,15 @@ static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaSt
     if (e != cudaSuccess)
         return e;
     dq::tree_mma_kernel<T, WR><<<cut.blocks, dq::TM_THREADS, dq::TM_SMEM, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess)
-        return e;
+    return cudaGetLastError();
+}
+
+// The join: a dependent launch.
+template <typename T, int R>
+static cudaError_t tree_join(const dq::TreeArgs& a, const TreeCut& cut, cudaStream_t s)
+{
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cut.blocks), 2 * WR);
+    cfg.gridDim = dim3(static_cast<unsigned>(cut.blocks), R / 8);
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -760,7 +542,7 @@ static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dq::tree_join_kernel<T, 16 * WR>, a);
+    return cudaLaunchKernelEx(&cfg, dq::tree_join_kernel<T, R>, a);
 }
 
 }  // namespace dqhost
@@ -807,11 +589,25 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         return DQ_ERR_ALIGN;
     if (t->workspace_bytes < dq_attention_tree_workspace_bytes(t->n_seq, t->max_new, t->n_q, t->n_kv))
         return DQ_ERR_SHAPE;
-    const int group = t->n_q / t->n_kv, box = t->page_size % 64 == 0 ? 64 : t->page_size % 32 == 0 ? 32 : 16;
+    const int group = t->n_q / t->n_kv;
     const dqhost::TreeCut cut = dqhost::tree_cut(t->max_new, group);
+    int box = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS;  // rows of a copy: what divides a tile and a page
+    while (t->page_size % box)
+        box /= 2;
     dq::TreeArgs a{};
-    if (!dqhost::tree_map(&a.map, t->type, t->pool, 2ll * t->n_pages * t->n_kv * t->page_size, box))
+    if (!dqhost::tree_map(&a.map, t->type, t->pool, {64, 2ll * t->n_pages * t->n_kv * t->page_size, 2}, {dq::ATT_HD * 2, 128},
+                          box, cut.tc() ? 1 : 2))
         return DQ_ERR_UNSUPPORTED;
+    if (cut.tc()) {
+        const int tokens = 128 / group;
+        a.nodes = tokens * (cut.rows / 128);
+        // a stride of a dimension of one is never used, but has to be one that the encoder takes
+        if (!dqhost::tree_map(&a.tq, t->type, t->q, {dq::ATT_HD, t->n_q, t->total_new},
+                              {2 * (t->n_q > 1 ? heads[0] : dq::ATT_HD), 2 * (t->total_new > 1 ? rows[0] : dq::ATT_HD)}, group,
+                              tokens))
+            return DQ_ERR_UNSUPPORTED;
+    }
+    a.pool = t->pool;
     a.q = t->q;
     a.out = t->out;
     a.q_row = rows[0];
@@ -841,9 +637,17 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = dqhost::with_type16(t->type, [&](auto* p) {
         using T = std::remove_pointer_t<decltype(p)>;
-        return cut.rows == 16   ? dqhost::tree_launch<T, 1>(a, cut, s)
-               : cut.rows == 32 ? dqhost::tree_launch<T, 2>(a, cut, s)
-                                : dqhost::tree_launch<T, 4>(a, cut, s);
+        cudaError_t err = cut.tc()         ? dqhost::tree_tc_launch(t->type, cut.rows == 256, a, cut.blocks, s)
+                          : cut.rows == 16 ? dqhost::tree_launch<T, 1>(a, cut, s)
+                          : cut.rows == 32 ? dqhost::tree_launch<T, 2>(a, cut, s)
+                                           : dqhost::tree_launch<T, 4>(a, cut, s);
+        if (err != cudaSuccess)
+            return err;
+        return cut.rows == 16    ? dqhost::tree_join<T, 16>(a, cut, s)
+               : cut.rows == 32  ? dqhost::tree_join<T, 32>(a, cut, s)
+               : cut.rows == 64  ? dqhost::tree_join<T, 64>(a, cut, s)
+               : cut.rows == 128 ? dqhost::tree_join<T, 128>(a, cut, s)
+                                 : dqhost::tree_join<T, 256>(a, cut, s);
     });
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }
