@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
 
 namespace dqhost {
 
-constexpr int TREE_MMA_ROWS = 48;
+constexpr int TREE_MMA_ROWS = 32;
 
 // Rows a block and blocks: two of up to 64 rows an SM, or one of 128 or 256 on the tensor
 // cores of the 5th generation.

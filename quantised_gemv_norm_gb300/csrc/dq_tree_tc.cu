@@ -44,6 +44,7 @@ struct TreeMiscT {
     uint64_t drain;
     uint32_t absent[8];                  // of a key tile, by its number: runs of 16 keys whose page is outside the pool
     float ml[2][128][2];
+    TreeCursor<256, TT_KEYS> parked[8];  // the softmax warps' cursors while registers are short
     TreeStart start;
     uint32_t tmem;
     int fail, poison;                    // poison: a new token's value is an infinity or NaN
@@ -70,19 +71,21 @@ template <int NS>
 struct TreePlace {
     int s;
     uint32_t phase;
-    __device__ __forceinline__ void step()  // to the next tile's: keys and values take turns
+    __device__ __forceinline__ TreePlace after(int copies) const
     {
-        if ((s += 2) >= NS) {
-            s -= NS;
-            phase ^= 1;
-        }
-    }
-    __device__ __forceinline__ TreePlace after(int tiles) const
-    {
-        const int at = s + 2 * tiles;
+        const int at = s + copies;
         return TreePlace{at % NS, phase ^ (at / NS & 1)};
     }
 };
+
+// The order in which a segment of n tiles goes through the ring is the order of its use.
+// PAIR: K0 V0 K1 V1 ...; one query tile, whose two chains have two tiles' scores under way:
+// K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
+template <bool PAIR>
+__device__ __forceinline__ int tree_values_at(int j, int n)
+{
+    return PAIR ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1);
+}
 
 template <typename T, bool PAIR>
 __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_constant__ TreeArgs a)
@@ -141,22 +144,26 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tbase + lanes + TT_S0 + 128 * t, to = tbase + lanes + TT_O0;
         const int token = static_cast<int>(fast_div(r, a.by_group)), head = r - token * a.group;
-        uint32_t before = 0, count[2] = {0, 0};  // key tiles of earlier segments, and of each chain
-        for (TreeCursor<R, TT_KEYS> c = tree_cursor<R, TT_KEYS>(a, st); c.left > 0; c.next(a)) {
-            const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles;
-            const int node = rt * a.nodes + (PAIR ? t * tokens : 0) + token;
-            const bool live = token < tokens && node < c.t.rows;
-            const int row = c.t.row0 + node, end = c.end(), n = end - c.tile;
+        uint32_t before = 0, mine = 0;  // key tiles of earlier segments, and of this chain so far
+        using Cursor = TreeCursor<256, TT_KEYS>;
+        for (Cursor c = tree_cursor<256, TT_KEYS>(a, st); c.left > 0; c.next(a)) {
+            if (lane == 0)
+                sh.parked[warp] = c;
+            const int n = c.end() - c.tile;
+            int node = c.item - c.item / c.row_tiles(a, c.t.rows) * c.row_tiles(a, c.t.rows);
+            node = node * a.nodes + (PAIR ? t * tokens : 0) + token;
+            bool live = token < tokens && node < c.t.rows;
+            int row = c.t.row0 + node;
             uint64_t seen = !live || c.t.keys == 0 ? 0ull : a.seen ? __ldg(a.seen + row) : (2ull << node) - 1;
             if (c.t.rows < 64)
                 seen &= (1ull << c.t.rows) - 1;
             const bool any = __any_sync(0xffffffffu, live);
-            const int from_new = c.t.keys ? c.t.past / TT_KEYS : 0;
+            // of the segment's first tile: a new token's key in a tile, and the first tile with one
+            const int past = c.t.past - c.tile * TT_KEYS, from_new = c.t.keys ? c.t.past / TT_KEYS - c.tile : -0x7fffffff;
             float m = -INFINITY, l = 0.f, base = 0.f;
             bool far = false;  // |m| > TT_FAR for some row of the warp
-            uint32_t i_chain = count[t];
-            for (int j = PAIR ? 0 : t; j < n; j += PAIR ? 1 : 2, ++i_chain) {
-                const uint32_t parity = i_chain & 1;
+            for (int j = PAIR ? 0 : t; j < n; j += PAIR ? 1 : 2, ++mine) {
+                const uint32_t parity = mine & 1;
                 wait(&sh.s_full[t], parity, DEVERR_TIMEOUT_FULL);
                 __syncwarp();
                 tc_fence_after_sync();
@@ -167,9 +174,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     }
                     continue;
                 }
-                const int k = c.tile + j;
                 const uint32_t absent = sh.absent[(before + j) & 7];
-                const bool tail = k >= from_new || absent;
+                const bool tail = j >= from_new || absent;
                 uint32_t s[128];
                 // the maximum of the first half while the second is on its way
                 float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -187,7 +193,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     if (tail) {
 #pragma unroll
                         for (int w = 2 * q; w < 2 * q + 2; ++w) {
-                            uint32_t word = c.t.keys ? tree_word(seen, c.t.past - k * TT_KEYS, w) : 0u;
+                            uint32_t word = from_new > -0x7fffffff ? tree_word(seen, past - j * TT_KEYS, w) : 0u;
                             if (absent >> (2 * w) & 1)
                                 word &= 0xffff0000u;
                             if (absent >> (2 * w + 1) & 1)
@@ -263,26 +269,31 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             }
 
             // ---- the segment's end
-            const int tiles[2] = {PAIR ? n : (n + 1) / 2, PAIR ? n : n / 2};
-            if (tiles[t])
-                wait(&sh.o_full[t], (count[t] + tiles[t] - 1) & 1, DEVERR_TIMEOUT_FULL);
             __syncwarp();
-            float f[2] = {1.f, 1.f};  // of the two chains' sums
+            c = sh.parked[warp];
+            const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles, end = c.tile + n;
+            node = rt * a.nodes + (PAIR ? t * tokens : 0) + token;
+            live = token < tokens && node < c.t.rows;
+            row = c.t.row0 + node;
+            if (n > (PAIR ? 0 : t))
+                wait(&sh.o_full[t], (mine - 1) & 1, DEVERR_TIMEOUT_FULL);
+            __syncwarp();
+            float f0 = 1.f, f1 = 1.f;  // of the two chains' sums
             if (!PAIR) {
                 sh.ml[t][r][0] = m;
                 sh.ml[t][r][1] = l;
                 named_bar_sync(TT_MEET_BAR, 256);
                 const float m0 = sh.ml[0][r][0], l0 = sh.ml[0][r][1], m1 = sh.ml[1][r][0], l1 = sh.ml[1][r][1];
                 m = fmaxf(m0, m1);
-                f[0] = m0 == m ? 1.f : ex2((m0 - m) * TR_C);
-                f[1] = m1 == m ? 1.f : ex2((m1 - m) * TR_C);
-                l = l0 * f[0] + l1 * f[1];
+                f0 = m0 == m ? 1.f : ex2((m0 - m) * TR_C);
+                f1 = m1 == m ? 1.f : ex2((m1 - m) * TR_C);
+                l = l0 * f0 + l1 * f1;
             }
             tc_fence_after_sync();
             const bool whole = c.tile == 0 && end == c.tiles, ok = __all_sync(0xffffffffu, !*fail), bad = sh.poison;
             if (!whole && c.tile == 0)
                 join = TreeJoin{c.t.row0, c.t.rows, g, rt,
-                                static_cast<int>(blockIdx.x + (c.tiles - end + st.left - 1) / st.left)};
+                                static_cast<int>(blockIdx.x + (c.tiles - end + sh.start.left - 1) / sh.start.left)};
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0)) * R + (PAIR ? 128 * t : 0) + r;
             if (!whole && live && ok && (PAIR || t == 0))
@@ -293,19 +304,19 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     float o[32];
                     {
                         uint32_t x[32];
-                        if (PAIR || tiles[0]) {
+                        {
                             tmem_ld32(to + (PAIR ? 128 * t : 0) + 32 * q, x);
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                o[i] = __uint_as_float(x[i]) * f[0];
+                                o[i] = PAIR ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * f0;
                         }
-                        if (!PAIR && tiles[1]) {
+                        if (!PAIR && n > 1) {
                             tmem_ld32(to + 128 + 32 * q, x);
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                o[i] = fmaf(__uint_as_float(x[i]), f[1], o[i]);
+                                o[i] = fmaf(__uint_as_float(x[i]), f1, o[i]);
                         }
                     }
                     if (bad) {
@@ -359,8 +370,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             if (!PAIR)
                 named_bar_sync(TT_MEET_BAR, 256);  // both chains' sums and numbers are read
             before += n;
-            count[0] += tiles[0];
-            count[1] += tiles[1];
         }
     } else if (st.left > 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TT_OTHER_REGS));
@@ -393,7 +402,45 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                                       c.t.row0 + rt * a.nodes + q * tokens, &sh.q_full);
                 }
                 __syncwarp();
-                const int end = c.end();
+                // one tile of keys (kv = 0) or values; y: the lane's row of the pool, below 0 without one
+                auto copy = [&](int kv, int k, int y, uint32_t bytes, uint32_t absent) {
+                    wait(&sh.freed[slot], phase ^ 1, DEVERR_TIMEOUT_EMPTY);
+                    __syncwarp();
+                    if (__any_sync(0xffffffffu, *fail))
+                        return;
+                    uint8_t* to = ring + slot * TT_TILE;
+                    if (absent && kv) {  // their probabilities are zero, so their values have to be finite
+                        for (int i = lane; i < TT_TILE / 16; i += 32)
+                            if (absent >> ((i & 1023) / 8 / 16) & 1)
+                                *reinterpret_cast<uint4*>(to + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const bool clean = kv && k >= from_new;
+                    uint64_t* bar = clean ? &sh.v_full[slot] : &sh.full[slot];
+                    if (lane == 0) {
+                        if (kv == 0)
+                            sh.absent[number & 7] = absent;
+                        mbar_arrive_expect_tx(bar, bytes);
+                        if (clean)
+                            mbar_arrive(&sh.full[slot]);  // the slot's phase goes on
+                    }
+                    if (clean) {
+                        v_phase ^= 1u << slot;
+                        v_used |= 1u << slot;
+                    }
+                    __syncwarp();
+                    if (y >= 0)
+                        tree_load(to + panel * TT_PANEL + u * box * 128, &a.map, 0, y, panel, bar);
+                    ++issued;
+                    if (++slot == NS) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                };
+                const int end = c.end(), to_values = a.s.n_kv * a.s.page_rows;
+                int y = -1, y_last = -1;
+                uint32_t bytes = 0, absent = 0, bytes_last = 0, absent_last = 0;
                 for (int k = c.tile; k < end; ++k, ++number) {
                     if (k - first == ahead) {
                         first = k;
@@ -406,7 +453,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     const bool there = mine && page >= 0 && page < a.s.n_pages;
                     const unsigned have = __ballot_sync(0xffffffffu, there);
                     const unsigned lack = __ballot_sync(0xffffffffu, mine && !there && panel == 0);
-                    uint32_t absent = 0;
+                    absent = 0;
                     if (lack) {
                         for (int i = 0; i < boxes; ++i)
                             if (lack >> i & 1)
@@ -414,46 +461,21 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                         if (lane == 0)
                             set_error(a.err, DEVERR_BAD_ARG);
                     }
-                    const uint32_t bytes = static_cast<uint32_t>(__popc(have) * box * 128);
-                    const int off = (x - static_cast<int>(fast_div(x, a.by_boxes) * a.by_boxes.d)) * box;
-#pragma unroll 1
-                    for (int kv = 0; kv < 2; ++kv) {
-                        wait(&sh.freed[slot], phase ^ 1, DEVERR_TIMEOUT_EMPTY);
-                        __syncwarp();
-                        if (__any_sync(0xffffffffu, *fail))
-                            continue;
-                        uint8_t* to = ring + slot * TT_TILE;
-                        if (absent && kv) {  // their probabilities are zero, so their values have to be finite
-                            for (int i = lane; i < TT_TILE / 16; i += 32)
-                                if (absent >> ((i & 1023) / 8 / 16) & 1)
-                                    *reinterpret_cast<uint4*>(to + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                        const bool clean = kv && k >= from_new;
-                        uint64_t* bar = clean ? &sh.v_full[slot] : &sh.full[slot];
-                        if (lane == 0) {
-                            if (kv == 0)
-                                sh.absent[number & 7] = absent;
-                            mbar_arrive_expect_tx(bar, bytes);
-                            if (clean)
-                                mbar_arrive(&sh.full[slot]);  // the slot's phase goes on
-                        }
-                        if (clean) {
-                            v_phase ^= 1u << slot;
-                            v_used |= 1u << slot;
-                        }
-                        __syncwarp();
-                        if (there)
-                            tree_load(to + panel * TT_PANEL + u * box * 128, &a.map, 0,
-                                      static_cast<int>(kv16_row(a.s, page, kv, g)) + off, panel, bar);
-                        ++issued;
-                        if (++slot == NS) {
-                            slot = 0;
-                            phase ^= 1;
-                        }
-                    }
+                    bytes = static_cast<uint32_t>(__popc(have) * box * 128);
+                    y = there ? static_cast<int>(kv16_row(a.s, page, 0, g)) +
+                                    (x - static_cast<int>(fast_div(x, a.by_boxes) * a.by_boxes.d)) * box
+                              : -1;
+                    copy(0, k, y, bytes, absent);
+                    if (PAIR)
+                        copy(1, k, y < 0 ? y : y + to_values, bytes, absent);
+                    else if (k > c.tile)
+                        copy(1, k - 1, y_last < 0 ? y_last : y_last + to_values, bytes_last, absent_last);
+                    y_last = y;
+                    bytes_last = bytes;
+                    absent_last = absent;
                 }
+                if (!PAIR)
+                    copy(1, end - 1, y_last < 0 ? y_last : y_last + to_values, bytes_last, absent_last);
             }
             // every copy has landed before the block ends
             bool landed = true;
@@ -500,17 +522,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                 }
                 umma_commit_warp(&sh.o_full[t]);
             };
-            TreePlace<NS> pk{0, 0}, pv_at{1, 0};
-            uint32_t count[2] = {0, 0}, segment = 0, clean_phase = 0;
+            TreePlace<NS> at{0, 0};  // of the next tile in the ring
+            uint32_t count0 = 0, count1 = 0, segment = 0, clean_phase = 0;  // tiles of the chains so far
             for (TreeCursor<R, TT_KEYS> c = tree_cursor<R, TT_KEYS>(a, st); c.left > 0; c.next(a), ++segment) {
                 const int n = c.end() - c.tile, from_new = c.t.keys ? c.t.past / TT_KEYS : 0;
-                auto keys = [&] {
-                    wait(&sh.full[pk.s], pk.phase, DEVERR_TIMEOUT_FULL);
+                auto landed = [&](const TreePlace<NS>& x) {
+                    wait(&sh.full[x.s], x.phase, DEVERR_TIMEOUT_FULL);
                     __syncwarp();
-                };
-                auto keys_done = [&] {
-                    umma_commit_warp(&sh.freed[pk.s]);
-                    pk.step();
                 };
                 wait(&sh.q_full, segment & 1, DEVERR_TIMEOUT_FULL);
                 __syncwarp();
@@ -519,52 +537,56 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     if (!PAIR && t >= n)
                         continue;
                     if (!PAIR || t == 0)
-                        keys();
-                    qk(t, pk.s);
-                    if (!PAIR || t == 1)
-                        keys_done();
+                        landed(at);
+                    qk(t, at.s);
+                    if (!PAIR || t == 1) {
+                        umma_commit_warp(&sh.freed[at.s]);
+                        at = at.after(1);
+                    }
                 }
                 if (n <= (PAIR ? 1 : 2))
                     umma_commit_warp(&sh.q_free);
                 for (int j = 0; j < n; ++j) {
+                    const TreePlace<NS> keys = at.after(1);  // the ones that come after these values
                     if (c.tile + j >= from_new) {
-                        wait(&sh.cleaned[pv_at.s], clean_phase >> pv_at.s & 1, DEVERR_TIMEOUT_FULL);
-                        clean_phase ^= 1u << pv_at.s;
+                        wait(&sh.cleaned[at.s], clean_phase >> at.s & 1, DEVERR_TIMEOUT_FULL);
+                        clean_phase ^= 1u << at.s;
+                        __syncwarp();
                     } else {
-                        wait(&sh.full[pv_at.s], pv_at.phase, DEVERR_TIMEOUT_FULL);
+                        landed(at);
                     }
-                    __syncwarp();
                     if (PAIR) {
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            pv(t, pv_at.s, (count[0] + j) & 1, j == 0);
+                            pv(t, at.s, (count0 + j) & 1, j == 0);
                             if (j + 1 < n) {
                                 if (t == 0)
-                                    keys();
-                                qk(t, pk.s);
+                                    landed(keys);
+                                qk(t, keys.s);
                             }
                         }
-                        umma_commit_warp(&sh.freed[pv_at.s]);
+                        umma_commit_warp(&sh.freed[at.s]);
                         if (j + 1 < n)
-                            keys_done();
+                            umma_commit_warp(&sh.freed[keys.s]);
                         if (j + 2 == n)
                             umma_commit_warp(&sh.q_free);
+                        at = j + 1 < n ? keys.after(1) : keys;
                     } else {
                         const int t = j & 1;
-                        pv(t, pv_at.s, (count[t] + (j >> 1)) & 1, j < 2);
-                        umma_commit_warp(&sh.freed[pv_at.s]);
+                        pv(t, at.s, ((t ? count1 : count0) + (j >> 1)) & 1, j < 2);
+                        umma_commit_warp(&sh.freed[at.s]);
                         if (j + 2 < n) {
-                            keys();
-                            qk(t, pk.s);
-                            keys_done();
+                            landed(keys);
+                            qk(t, keys.s);
+                            umma_commit_warp(&sh.freed[keys.s]);
                         }
                         if (j + 3 == n)
                             umma_commit_warp(&sh.q_free);
+                        at = j + 2 < n ? keys.after(1) : keys;
                     }
-                    pv_at.step();
                 }
-                count[0] += PAIR ? n : (n + 1) / 2;
-                count[1] += PAIR ? n : n / 2;
+                count0 += PAIR ? n : (n + 1) / 2;
+                count1 += PAIR ? n : n / 2;
             }
             umma_commit_warp(&sh.drain);  // every product is done before the block ends
             if (!mbar_wait(&sh.drain, 0) && lane == 0)
@@ -572,12 +594,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             __syncwarp();
         } else {
             // ---- infinities and NaNs of new tokens' values, and of what lies behind them, become zero
-            TreePlace<NS> at{1, 0};
+            TreePlace<NS> at{0, 0};
             uint32_t v_phase = 0;
             for (TreeCursor<R, TT_KEYS> c = tree_cursor<R, TT_KEYS>(a, st); c.left > 0; c.next(a)) {
                 const int n = c.end() - c.tile, from_new = c.t.keys ? c.t.past / TT_KEYS : 0;
                 for (int j = max(0, from_new - c.tile); j < n; ++j) {
-                    const TreePlace<NS> here = at.after(j);
+                    const TreePlace<NS> here = at.after(tree_values_at<PAIR>(j, n));
                     wait(&sh.v_full[here.s], v_phase >> here.s & 1, DEVERR_TIMEOUT_FULL);
                     v_phase ^= 1u << here.s;
                     __syncwarp();
@@ -604,7 +626,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     if (lane == 0)
                         mbar_arrive(&sh.cleaned[here.s]);
                 }
-                at = at.after(n);
+                at = at.after(2 * n);
             }
         }
     }
