@@ -35,7 +35,7 @@ __device__ __forceinline__ void tree_mma(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// ---- up to 64 rows a block: warp-level matrix instructions
+// ---- up to 32 rows a block: warp-level matrix instructions
 
 constexpr int TM_KEYS = 64;                     // keys a tile
 constexpr int TM_SLOT = TM_KEYS * ATT_HD * 2;   // bytes of a tile of keys or values
@@ -48,7 +48,7 @@ struct TreeMiscM {
     uint64_t full[TM_SLOTS], freed[TM_SLOTS];
     uint32_t absent[TM_SLOTS];  // runs of 16 keys whose page is outside the pool
     float ml[2][16][2];
-    TreeStart start;
+    TreeCursor<16, TM_KEYS> start;
     int fail;
 };
 static_assert(sizeof(TreeMiscM) <= 512, "fits behind the ring");
@@ -72,20 +72,21 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             }
             fence_mbar_init();
             sh.fail = 0;
+            tree_fetch_map(&a.map);
         }
-        const TreeStart st = tree_start<R, TM_KEYS>(a, lane);
+        const TreeCursor<R, TM_KEYS> first = tree_start<R, TM_KEYS>(a, lane);
         if (lane == 0)
-            sh.start = st;
+            reinterpret_cast<TreeCursor<R, TM_KEYS>&>(sh.start) = first;
     }
     __syncthreads();
-    const TreeStart st = sh.start;
-    TreeJoin join{0, 0, 0, 0, -1};
-    if (st.left > 0) {
+    TreeCursor<R, TM_KEYS> c = reinterpret_cast<const TreeCursor<R, TM_KEYS>&>(sh.start);
+    const long long each = c.left;
+    TreeShared join{0, 0, 0, 0, -1};
+    if (each > 0) {
         auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
             if (!mbar_try_wait(bar, parity))
                 tree_wait_on(bar, parity, fail, a.err, code);
         };
-        TreeCursor<R, TM_KEYS> c = tree_cursor<R, TM_KEYS>(a, st);
         int slot = 0;
         uint32_t phase = 0;
         auto turn = [&] {
@@ -384,9 +385,8 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                 const bool whole = c.tile == 0 && end == c.tiles;
                 if (!whole && c.tile == 0 && warp == 0) {
                     // the blocks that go on with the item: each has as many units as this one
-                    const long long each = st.left;
-                    join = TreeJoin{t.row0, t.rows, g, rt,
-                                    static_cast<int>(blockIdx.x + (c.tiles - end + each - 1) / each)};
+                    join = TreeShared{t.row0, t.rows, g, rt,
+                                    static_cast<int>(blockIdx.x + tree_blocks(c.tiles - end, each))};
                 }
                 if (wk == 0 && !*fail) {
 #pragma unroll
@@ -403,12 +403,13 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                                 *reinterpret_cast<uint32_t*>(out + 8 * i) =
                                     l[h] == 0.f ? 0u : pack2(o[i][2 * h] * inv, o[i][2 * h + 1] * inv, static_cast<const T*>(nullptr));
                         } else {
-                            const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0)) * R + rr;
+                            const size_t at = static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0);
                             if (q4 == 0)
-                                a.part_ml[at] = make_float2(m[h], l[h]);
+                                a.part_ml[at * R + rr] = make_float2(m[h], l[h]);
+                            float2* part = reinterpret_cast<float2*>(a.part + (at * 32 + (q4 >> 1)) * R + rr) + (q4 & 1);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                *reinterpret_cast<float2*>(a.part + at * ATT_HD + 8 * i + 2 * q4) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                                part[4 * i * R] = make_float2(o[i][2 * h], o[i][2 * h + 1]);
                         }
                     }
                 }
@@ -416,19 +417,71 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
         }
     }
     if (tid == 0)
-        a.join[blockIdx.x] = *fail ? TreeJoin{0, 0, 0, 0, -1} : join;
+        a.join[blockIdx.x] = *fail ? TreeJoin{0, 0, 0, -1} : join.packed();
 }
 
-// A row of an item that several blocks had a part of: one warp, four dims a lane.
-template <typename T, int R>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a)
+// Items that several blocks had a part of.  A unit of work is 32 lanes' rows (of 16-row
+// items: their rows twice, the next four dims) and four dims each, over all the blocks' sums.
+// P = 1: one row of the grid a block of the first kernel, which has left the item that it
+// began and did not end, and a warp a unit.  Where items are few and each had many blocks,
+// one row an item, whose blocks are worked out while the first kernel still runs, and P warps
+// a unit, each every P-th block's sums, which then meet.
+constexpr int TJ_WARPS = 8, TJ_BATCH = 10;
+
+template <typename T, int R, int KT, int P>
+__global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_constant__ TreeArgs a, int blocks, int per_seq)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x, rr = blockIdx.y * 8 + warp;
-    pdl_wait();
-    const TreeJoin j = a.join[b];
+    constexpr int ROWS = R < 32 ? R : 32;
+    __shared__ float2 meet_ml[P > 1 ? TJ_WARPS : 1][32];
+    __shared__ float4 meet_o[P > 1 ? TJ_WARPS : 1][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    TreeShared j;
+    int b = blockIdx.x;
+    if (P == 1) {
+        pdl_wait();
+        const int4 x = __ldcg(reinterpret_cast<const int4*>(a.join + b));
+        j = TreeShared{x.x, x.y >> 8, x.z, x.y & 0xff, x.w};
+        if (j.last < 0)
+            return;
+    } else {
+        // every warp for itself
+        TreeCursor<(R < 128 ? R : 0), KT> c;
+        const int s = blockIdx.x / per_seq, item = blockIdx.x - s * per_seq;
+        long long before = 0, total = 0;
+        for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
+            long long u = 0;
+            if (s0 + lane < a.n_seq) {
+                c.t = tree_seq(a, s0 + lane);
+                u = c.units(a);
+            }
+            long long low = s0 + lane < s ? u : 0;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                u += __shfl_xor_sync(0xffffffffu, u, o);
+                low += __shfl_xor_sync(0xffffffffu, low, o);
+            }
+            total += u;
+            before += low;
+        }
+        c.load(a, s);
+        if (item >= c.items)
+            return;
+        const long long each = max(static_cast<long long>(a.least), tree_div_up(total, blocks));
+        const long long start = before + static_cast<long long>(item) * c.tiles;
+        b = tree_div(start, each);
+        const int row_tiles = c.row_tiles(a, c.t.rows);
+        j = TreeShared{c.t.row0, c.t.rows, item / row_tiles, item % row_tiles, tree_div(start + c.tiles - 1, each)};
+        if (j.last == b)
+            return;
+        pdl_wait();
+        if (__ldcg(&a.join[b].last) < 0)
+            return;  // a wait ran out
+    }
+    const int n = j.last - b + 1, part = warp % P, u = blockIdx.y * (TJ_WARPS / P) + warp / P;
+    const int rr = u % (R / ROWS) * ROWS + lane % ROWS, four = u / (R / ROWS) * (32 / ROWS) + lane / ROWS;
     int node, head;
-    if (a.nodes) {  // 128 rows for as many whole tokens as they hold
-        const int in_tile = rr & 127, token = static_cast<int>(fast_div(in_tile, a.by_group)), tokens = a.nodes / (R / 128);
+    if (R >= 128) {  // 128 rows for as many whole tokens as they hold
+        const int in_tile = rr & 127, token = static_cast<int>(fast_div(in_tile, a.by_group)), tokens = a.nodes / (R < 128 ? 1 : R / 128);
         head = in_tile - token * a.group;
         node = token < tokens ? j.row_tile * a.nodes + (rr >> 7) * tokens + token : 0x7fffffff;
     } else {
@@ -436,41 +489,48 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
         node = static_cast<int>(fast_div(r, a.by_group));
         head = r - node * a.group;
     }
-    if (j.last < 0 || node >= j.rows)
-        return;
+    const bool live = node < j.rows;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int E = 4;
-    for (int b0 = b; b0 <= j.last; b0 += E) {
-        float2 ml[E];
-        float4 y[E];
-        float top = m;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            ml[e] = make_float2(-INFINITY, 0.f);
-            y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (b0 + e <= j.last) {
-                const size_t at = (static_cast<size_t>(b0 + e) * 2 + (b0 + e == b)) * R + rr;
-                ml[e] = __ldcg(a.part_ml + at);
-                y[e] = __ldcg(reinterpret_cast<const float4*>(a.part + at * ATT_HD) + lane);
-            }
-            top = fmaxf(top, ml[e].x);
-        }
-        const float f = m == top ? 1.f : ex2((m - top) * TR_C);
+    auto add = [&](float2 ml, float4 y) {
+        const float top = fmaxf(m, ml.x), f = m == top ? 1.f : ex2((m - top) * TR_C), w = ml.x == top ? 1.f : ex2((ml.x - top) * TR_C);
         m = top;
-        l *= f;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+        l = fmaf(w, ml.y, l * f);
+        o = make_float4(fmaf(w, y.x, o.x * f), fmaf(w, y.y, o.y * f), fmaf(w, y.z, o.z * f), fmaf(w, y.w, o.w * f));
+    };
+    for (int k0 = part; k0 < n && live; k0 += P * TJ_BATCH) {
+        float2 ml[TJ_BATCH];
+        float4 y[TJ_BATCH];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float w = ml[e].x == m ? 1.f : ex2((ml[e].x - m) * TR_C);
-            l = fmaf(w, ml[e].y, l);
-            o = make_float4(fmaf(w, y[e].x, o.x), fmaf(w, y[e].y, o.y), fmaf(w, y[e].z, o.z), fmaf(w, y[e].w, o.w));
+        for (int e = 0; e < TJ_BATCH; ++e) {
+            const int k = k0 + e * P;
+            if (k < n) {
+                const size_t at = static_cast<size_t>(b + k) * 2 + (k == 0);
+                ml[e] = __ldcg(a.part_ml + at * R + rr);
+                y[e] = __ldcg(a.part + (at * 32 + four) * R + rr);
+            }
         }
+#pragma unroll
+        for (int e = 0; e < TJ_BATCH; ++e)
+            if (k0 + e * P < n)
+                add(ml[e], y[e]);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    store4(static_cast<T*>(a.out) + static_cast<long long>(j.row0 + node) * a.o_row +
-               static_cast<long long>(j.kv * a.group + head) * a.o_head + 4 * lane,
-           l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (P > 1) {
+        meet_ml[warp][lane] = make_float2(m, l);
+        meet_o[warp][lane] = o;
+        __syncthreads();
+        if (part)
+            return;
+#pragma unroll
+        for (int w = 1; w < P; ++w)
+            add(meet_ml[warp + w][lane], meet_o[warp + w][lane]);
+    }
+    if (live) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store4(static_cast<T*>(a.out) + static_cast<long long>(j.row0 + node) * a.o_row +
+                   static_cast<long long>(j.kv * a.group + head) * a.o_head + 4 * four,
+               l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
 }
 
 }  // namespace dq
@@ -479,7 +539,7 @@ namespace dqhost {
 
 constexpr int TREE_MMA_ROWS = 32;
 
-// Rows a block and blocks: two of up to 64 rows an SM, or one of 128 or 256 on the tensor
+// Rows a block and blocks: two of up to 32 rows an SM, or one of 128 or 256 on the tensor
 // cores of the 5th generation.
 struct TreeCut {
     int rows, blocks;
@@ -491,7 +551,7 @@ static TreeCut tree_cut(int max_new, int group)
     const int rows = max_new * group;
     if (rows > TREE_MMA_ROWS)
         return {(max_new + 128 / group - 1) / (128 / group) > 1 ? 256 : 128, sm_count()};
-    return {rows <= 16 ? 16 : rows <= 32 ? 32 : 64, dq::TM_RESIDENT * sm_count()};
+    return {rows <= 16 ? 16 : 32, dq::TM_RESIDENT * sm_count()};
 }
 
 static size_t tree_bytes(const TreeCut& c)
@@ -500,9 +560,9 @@ static size_t tree_bytes(const TreeCut& c)
     return rows * (dq::ATT_HD + 2) * sizeof(float) + (c.blocks * sizeof(dq::TreeJoin) + 15) / 16 * 16;
 }
 
-// A kernel's shared memory, asked for once per device.
+// A kernel's attribute, set once per device.
 template <typename K>
-static cudaError_t tree_prepare(K kernel, int bytes, bool (&done)[64])
+static cudaError_t tree_prepare(K kernel, cudaFuncAttribute what, int value, bool (&done)[64])
 {
     static std::mutex mu;
     int dev = 0;
@@ -511,7 +571,7 @@ static cudaError_t tree_prepare(K kernel, int bytes, bool (&done)[64])
         return e;
     std::lock_guard<std::mutex> lock(mu);
     if (dev < 0 || dev >= 64 || !done[dev]) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(kernel, what, value);
         if (e == cudaSuccess && dev >= 0 && dev < 64)
             done[dev] = true;
     }
@@ -522,7 +582,7 @@ template <typename T, int WR>
 static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaStream_t s)
 {
     static bool done[64] = {};
-    cudaError_t e = tree_prepare(dq::tree_mma_kernel<T, WR>, dq::TM_SMEM, done);
+    cudaError_t e = tree_prepare(dq::tree_mma_kernel<T, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq::TM_SMEM, done);
     if (e != cudaSuccess)
         return e;
     dq::tree_mma_kernel<T, WR><<<cut.blocks, dq::TM_THREADS, dq::TM_SMEM, s>>>(a);
@@ -530,19 +590,31 @@ static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaSt
 }
 
 // The join: a dependent launch.
-template <typename T, int R>
+template <typename T, int R, int KT>
 static cudaError_t tree_join(const dq::TreeArgs& a, const TreeCut& cut, cudaStream_t s)
 {
+    const int per_seq = a.s.n_kv * (a.nodes ? (a.max_new + a.nodes - 1) / a.nodes : (a.max_new * a.group + R - 1) / R);
+    const long long items = static_cast<long long>(a.n_seq) * per_seq;
+    // warps a unit: an item has about blocks / items blocks' sums
+    int parts = 1;
+    if (items * 8 <= cut.blocks)
+        while (parts < 8 && items * parts * dq::TJ_BATCH < cut.blocks)
+            parts *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cut.blocks), R / 8);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(static_cast<unsigned>(parts == 1 ? cut.blocks : items), static_cast<unsigned>(R * parts / dq::TJ_WARPS));
+    cfg.blockDim = dim3(32 * dq::TJ_WARPS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dq::tree_join_kernel<T, R>, a);
+    return cudaLaunchKernelEx(&cfg,
+                              parts == 1   ? dq::tree_join_kernel<T, R, KT, 1>
+                              : parts == 2 ? dq::tree_join_kernel<T, R, KT, 2>
+                              : parts == 4 ? dq::tree_join_kernel<T, R, KT, 4>
+                                           : dq::tree_join_kernel<T, R, KT, 8>,
+                              a, cut.blocks, per_seq);
 }
 
 }  // namespace dqhost
@@ -619,8 +691,8 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
     a.cu_new = t->cu_new;
     a.seen = t->seen;
     const size_t part_rows = static_cast<size_t>(cut.blocks) * 2 * cut.rows;
-    a.part = static_cast<float*>(t->workspace);
-    a.part_ml = reinterpret_cast<float2*>(a.part + part_rows * dq::ATT_HD);
+    a.part = static_cast<float4*>(t->workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part + part_rows * (dq::ATT_HD / 4));
     a.join = reinterpret_cast<dq::TreeJoin*>(a.part_ml + part_rows);
     a.room = static_cast<long long>(t->max_pages) * t->page_size;
     a.n_seq = t->n_seq;
@@ -639,15 +711,13 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         using T = std::remove_pointer_t<decltype(p)>;
         cudaError_t err = cut.tc()         ? dqhost::tree_tc_launch(t->type, cut.rows == 256, a, cut.blocks, s)
                           : cut.rows == 16 ? dqhost::tree_launch<T, 1>(a, cut, s)
-                          : cut.rows == 32 ? dqhost::tree_launch<T, 2>(a, cut, s)
-                                           : dqhost::tree_launch<T, 4>(a, cut, s);
+                                           : dqhost::tree_launch<T, 2>(a, cut, s);
         if (err != cudaSuccess)
             return err;
-        return cut.rows == 16    ? dqhost::tree_join<T, 16>(a, cut, s)
-               : cut.rows == 32  ? dqhost::tree_join<T, 32>(a, cut, s)
-               : cut.rows == 64  ? dqhost::tree_join<T, 64>(a, cut, s)
-               : cut.rows == 128 ? dqhost::tree_join<T, 128>(a, cut, s)
-                                 : dqhost::tree_join<T, 256>(a, cut, s);
+        return cut.rows == 16    ? dqhost::tree_join<T, 16, dq::TM_KEYS>(a, cut, s)
+               : cut.rows == 32  ? dqhost::tree_join<T, 32, dq::TM_KEYS>(a, cut, s)
+               : cut.rows == 128 ? dqhost::tree_join<T, 128, dqhost::TREE_TC_KEYS>(a, cut, s)
+                                 : dqhost::tree_join<T, 256, dqhost::TREE_TC_KEYS>(a, cut, s);
     });
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
 }

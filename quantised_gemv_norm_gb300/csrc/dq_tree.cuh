@@ -26,8 +26,10 @@ struct TreeArgs {
     const int* n_past;
     const int* cu_new;
     const unsigned long long* seen;
-    float* part;      // [blocks][2: first and last segment][rows a block][128], unscaled sums
-    float2* part_ml;  // their maxima and sums of probabilities
+    // unscaled sums, and their maxima and sums of probabilities, of each block's first and last
+    // segment: [blocks][2][32 fours of dims][rows a block], [blocks][2][rows a block]
+    float4* part;
+    float2* part_ml;
     TreeJoin* join;   // [blocks]
     long long room;   // rows that max_pages pages hold
     int n_seq, total_new, max_new, group, max_pages, box, least;
@@ -79,8 +81,8 @@ struct TreeCursor {
 
     static __device__ __forceinline__ int row_tiles(const TreeArgs& a, int rows)
     {
-        // with `nodes` an item has whole tokens, else R rows whatever tokens they are of
-        return a.nodes ? (rows + a.nodes - 1) / a.nodes : (rows * a.group + R - 1) / R;
+        // R rows whatever tokens they are of, or (R = 0) a.nodes whole tokens
+        return R ? (rows * a.group + R - 1) / (R ? R : 1) : (rows + a.nodes - 1) / a.nodes;
     }
     __device__ __forceinline__ long long units(const TreeArgs& a)
     {
@@ -108,23 +110,39 @@ struct TreeCursor {
     }
 };
 
-// The block's stretch, by one warp: where it starts and how many units it has.
-struct TreeStart {
-    long long offset, left;  // units within the sequence; 0 left: none
-    int s;
-};
-
-template <int R, int KT>
-__device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int lane)
+// n / d rounded up, n >= 0, d > 0; rarely in 64 bits, which takes long.
+__device__ __forceinline__ long long tree_div_up(long long n, int d)
 {
-    constexpr int E = 4;  // sequences a lane and round
-    long long total = 0;
-    long long u[E];
+    const unsigned long long m = static_cast<unsigned long long>(n) + (d - 1);
+    return m >> 32 ? static_cast<long long>(m / d) : static_cast<long long>(static_cast<uint32_t>(m) / static_cast<uint32_t>(d));
+}
+
+// n / d below 2^31, n >= 0, d > 0.
+__device__ __forceinline__ int tree_div(long long n, long long d)
+{
+    return static_cast<int>((n | d) >> 32 ? n / d : static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
+}
+
+// Blocks that `units` more units of an item take, `each` a block.
+__device__ __forceinline__ int tree_blocks(int units, long long each)
+{
+    return each > 0x7fffffffll ? 1 : static_cast<int>((static_cast<uint32_t>(units) + static_cast<uint32_t>(each) - 1) / static_cast<uint32_t>(each));
+}
+
+// Where the block's stretch begins, by one warp; left = 0: it has none.  A lane has four
+// consecutive sequences at a time, so that the lengths of 128 are one wait for memory.
+template <int R, int KT>
+__device__ __forceinline__ TreeCursor<R, KT> tree_start(const TreeArgs& a, int lane)
+{
+    constexpr int E = 4;
+    TreeCursor<R, KT> c;
+    long long u[E], mine = 0, incl = 0, total = 0;
+    // sequences s0 ..: the lane's units, and those of all lanes up to it
     auto round = [&](int s0, bool report) {
-        TreeCursor<R, KT> c;
+        mine = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int s = s0 + 32 * e + lane;
+            const int s = s0 + E * lane + e;
             u[e] = 0;
             if (s < a.n_seq) {
                 c.t = tree_seq(a, s);
@@ -132,70 +150,68 @@ __device__ __forceinline__ TreeStart tree_start(const TreeArgs& a, int lane)
                 if (report && c.t.bad)
                     set_error(a.err, DEVERR_BAD_ARG);
             }
+            mine += u[e];
         }
-    };
-    auto sum = [](long long v) {
+        incl = mine;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += x;
+        }
     };
     for (int s0 = 0; s0 < a.n_seq; s0 += 32 * E) {
         round(s0, blockIdx.x == 0);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            total += sum(u[e]);
+        total += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const long long each = max(static_cast<long long>(a.least), (total + gridDim.x - 1) / gridDim.x);
-    TreeStart st{0, 0, 0};
+    const long long each = max(static_cast<long long>(a.least), tree_div_up(total, static_cast<int>(gridDim.x)));
     long long want = each * blockIdx.x;
-    st.left = min(each, total - want);
-    if (st.left <= 0) {
-        st.left = 0;
-        return st;
-    }
+    const long long left = min(each, total - want);
+    c.left = 0;
+    if (left <= 0)
+        return c;
     for (int s0 = 0; s0 < a.n_seq; s0 += 32 * E) {
         if (a.n_seq > 32 * E)
             round(s0, false);
+        const unsigned hit = __ballot_sync(0xffffffffu, want >= incl - mine && want < incl);
+        if (hit) {
+            long long off = want - (incl - mine);
+            int s = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            long long incl = u[e];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, want >= incl - u[e] && want < incl);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                st.offset = __shfl_sync(0xffffffffu, want - (incl - u[e]), src);
-                st.s = s0 + 32 * e + src;
-                return st;
-            }
-            want -= __shfl_sync(0xffffffffu, incl, 31);
+            for (int e = 0; e < E - 1; ++e)
+                if (s == e && off >= u[e]) {
+                    off -= u[e];
+                    ++s;
+                }
+            const int src = __ffs(hit) - 1;
+            off = __shfl_sync(0xffffffffu, off, src);
+            s = s0 + E * src + __shfl_sync(0xffffffffu, s, src);
+            c.load(a, s);
+            c.item = static_cast<int>(off >> 32 ? off / c.tiles : static_cast<uint32_t>(off) / static_cast<uint32_t>(c.tiles));
+            c.tile = static_cast<int>(off - static_cast<long long>(c.item) * c.tiles);
+            c.left = left;
+            return c;
         }
+        want -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    st.left = 0;  // not reached: want is below the total
-    return st;
-}
-
-template <int R, int KT>
-__device__ __forceinline__ TreeCursor<R, KT> tree_cursor(const TreeArgs& a, const TreeStart& st)
-{
-    TreeCursor<R, KT> c;
-    c.left = st.left;
-    c.load(a, st.s);
-    c.item = static_cast<int>(st.offset / c.tiles);
-    c.tile = static_cast<int>(st.offset - static_cast<long long>(c.item) * c.tiles);
-    return c;
+    return c;  // not reached: want is below the total
 }
 
 // What a block leaves for the join: its last segment began an item that later blocks go
 // on with, the last of them `last`; -1: nothing to join.
-struct TreeJoin {
-    int row0, rows, kv, row_tile, last;
+struct __align__(16) TreeJoin {
+    int row0, rows_tile, kv, last;
 };
+struct TreeShared {
+    int row0, rows, kv, row_tile, last;
+    __device__ __forceinline__ TreeJoin packed() const { return TreeJoin{row0, rows << 8 | row_tile, kv, last}; }
+};
+static_assert(TR_MAX_NEW <= 128 && TR_MAX_GROUP * TR_MAX_NEW / 16 <= 256, "a row tile's number has eight bits");
+
+__device__ __forceinline__ void tree_fetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 
 __device__ __forceinline__ void tree_load(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {

@@ -34,6 +34,8 @@ template <bool PAIR>
 constexpr int TT_SLOTS = PAIR ? 5 : 6;  // ring of key and value tiles in turn, beside the query tiles
 constexpr int TT_RING = 7 * TT_TILE;    // either way
 
+using Cursor = TreeCursor<0, TT_KEYS>;  // items of whole tokens
+
 struct TreeMiscT {
     uint64_t q_full, q_free;             // the segment's queries landed; its last S is done
     uint64_t full[6], freed[6];          // a ring tile landed; its products are done
@@ -44,8 +46,8 @@ struct TreeMiscT {
     uint64_t drain;
     uint32_t absent[8];                  // of a key tile, by its number: runs of 16 keys whose page is outside the pool
     float ml[2][128][2];
-    TreeCursor<256, TT_KEYS> parked[8];  // the softmax warps' cursors while registers are short
-    TreeStart start;
+    Cursor parked[8];  // the softmax warps' cursors while registers are short
+    Cursor start;
     uint32_t tmem;
     int fail, poison;                    // poison: a new token's value is an infinity or NaN
 };
@@ -118,10 +120,12 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             mbar_init(&sh.drain, 1);
             fence_mbar_init();
             sh.fail = sh.poison = 0;
+            tree_fetch_map(&a.map);
+            tree_fetch_map(&a.tq);
         }
-        const TreeStart st = tree_start<R, TT_KEYS>(a, lane);
+        const Cursor first = tree_start<0, TT_KEYS>(a, lane);
         if (lane == 0)
-            sh.start = st;
+            sh.start = first;
         __syncwarp();
     } else if (warp == TT_MMA_WARP) {
         tmem_alloc(&sh.tmem, TT_TCOLS);
@@ -129,15 +133,15 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const TreeStart st = sh.start;
+    const bool some = sh.start.left > 0;
     const uint32_t tbase = sh.tmem;
-    TreeJoin join{0, 0, 0, 0, -1};
+    TreeShared join{0, 0, 0, 0, -1};
 
     auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
         if (!mbar_try_wait(bar, parity))
             tree_wait_on(bar, parity, fail, a.err, code);
     };
-    if (st.left > 0 && warp < TT_MMA_WARP) {
+    if (some && warp < TT_MMA_WARP) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TT_SOFTMAX_REGS));
         // ---- softmax and epilogue: thread r of chain t has row r of its query tile
         const int t = warp >> 2, r = tid & 127;
@@ -145,8 +149,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
         const uint32_t ts = tbase + lanes + TT_S0 + 128 * t, to = tbase + lanes + TT_O0;
         const int token = static_cast<int>(fast_div(r, a.by_group)), head = r - token * a.group;
         uint32_t before = 0, mine = 0;  // key tiles of earlier segments, and of this chain so far
-        using Cursor = TreeCursor<256, TT_KEYS>;
-        for (Cursor c = tree_cursor<256, TT_KEYS>(a, st); c.left > 0; c.next(a)) {
+        for (Cursor c = sh.start; c.left > 0; c.next(a)) {
             if (lane == 0)
                 sh.parked[warp] = c;
             const int n = c.end() - c.tile;
@@ -292,12 +295,13 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             tc_fence_after_sync();
             const bool whole = c.tile == 0 && end == c.tiles, ok = __all_sync(0xffffffffu, !*fail), bad = sh.poison;
             if (!whole && c.tile == 0)
-                join = TreeJoin{c.t.row0, c.t.rows, g, rt,
-                                static_cast<int>(blockIdx.x + (c.tiles - end + sh.start.left - 1) / sh.start.left)};
+                join = TreeShared{c.t.row0, c.t.rows, g, rt,
+                                static_cast<int>(blockIdx.x + tree_blocks(c.tiles - end, sh.start.left))};
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t at = (static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0)) * R + (PAIR ? 128 * t : 0) + r;
+            const size_t at = static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0);
+            const int rr = (PAIR ? 128 * t : 0) + r;
             if (!whole && live && ok && (PAIR || t == 0))
-                a.part_ml[at] = make_float2(m, l);
+                a.part_ml[at * R + rr] = make_float2(m, l);
             if (any) {
 #pragma unroll 1
                 for (int q = PAIR ? 0 : 2 * t; q < (PAIR ? 4 : 2 * t + 2); ++q) {
@@ -359,10 +363,10 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                             out[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else {
-                        float4* part = reinterpret_cast<float4*>(a.part + at * ATT_HD + 32 * q);
+                        float4* part = a.part + (at * 32 + 8 * q) * R + rr;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            part[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            part[i * R] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
             }
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                 named_bar_sync(TT_MEET_BAR, 256);  // both chains' sums and numbers are read
             before += n;
         }
-    } else if (st.left > 0) {
+    } else if (some) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TT_OTHER_REGS));
         if (warp == TT_TMA_WARP) {
             // ---- copies: a lane takes one panel of one of a tile's boxes of rows
@@ -380,7 +384,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             int slot = 0;
             uint32_t phase = 0, number = 0, segment = 0, v_phase = 0, v_used = 0;  // v_: a bit a slot
             long long issued = 0;
-            for (TreeCursor<R, TT_KEYS> c = tree_cursor<R, TT_KEYS>(a, st); c.left > 0 && !__any_sync(0xffffffffu, *fail);
+            for (Cursor c = sh.start; c.left > 0 && !__any_sync(0xffffffffu, *fail);
                  c.next(a), ++segment) {
                 const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles;
                 const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             };
             TreePlace<NS> at{0, 0};  // of the next tile in the ring
             uint32_t count0 = 0, count1 = 0, segment = 0, clean_phase = 0;  // tiles of the chains so far
-            for (TreeCursor<R, TT_KEYS> c = tree_cursor<R, TT_KEYS>(a, st); c.left > 0; c.next(a), ++segment) {
+            for (Cursor c = sh.start; c.left > 0; c.next(a), ++segment) {
                 const int n = c.end() - c.tile, from_new = c.t.keys ? c.t.past / TT_KEYS : 0;
                 auto landed = [&](const TreePlace<NS>& x) {
                     wait(&sh.full[x.s], x.phase, DEVERR_TIMEOUT_FULL);
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             // ---- infinities and NaNs of new tokens' values, and of what lies behind them, become zero
             TreePlace<NS> at{0, 0};
             uint32_t v_phase = 0;
-            for (TreeCursor<R, TT_KEYS> c = tree_cursor<R, TT_KEYS>(a, st); c.left > 0; c.next(a)) {
+            for (Cursor c = sh.start; c.left > 0; c.next(a)) {
                 const int n = c.end() - c.tile, from_new = c.t.keys ? c.t.past / TT_KEYS : 0;
                 for (int j = max(0, from_new - c.tile); j < n; ++j) {
                     const TreePlace<NS> here = at.after(tree_values_at<PAIR>(j, n));
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     uint8_t* vt = ring + here.s * TT_TILE;
                     const int key0 = (c.tile + j) * TT_KEYS;
                     bool seen = false;
-#pragma unroll 4
+#pragma unroll 8
                     for (int i = tid - 32 * TT_CLEAN_WARP; i < TT_TILE / 16; i += 64) {
                         const int key = key0 + (i & 1023) / 8;  // a panel's rows are 8 of these
                         if (key < c.t.past)
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
     if (warp == TT_MMA_WARP)
         tmem_dealloc(tbase, TT_TCOLS);
     if (tid == 0)
-        a.join[blockIdx.x] = *fail ? TreeJoin{0, 0, 0, 0, -1} : join;
+        a.join[blockIdx.x] = *fail ? TreeJoin{0, 0, 0, -1} : join.packed();
 }
 
 }  // namespace dq
