@@ -63,7 +63,6 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
     TreeMiscM& sh = *reinterpret_cast<TreeMiscM*>(ring + TM_SLOTS * TM_SLOT + TM_MEET);
     volatile int* fail = &sh.fail;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_trigger();
     if (warp == TM_WARPS) {
         if (lane == 0) {
             for (int i = 0; i < TM_SLOTS; ++i) {
@@ -74,10 +73,13 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             sh.fail = 0;
             tree_fetch_map(&a.map);
         }
+        pdl_wait();
         const TreeCursor<R, TM_KEYS> first = tree_start<R, TM_KEYS>(a, lane);
         if (lane == 0)
             reinterpret_cast<TreeCursor<R, TM_KEYS>&>(sh.start) = first;
     }
+    pdl_wait();
+    pdl_trigger();  // only now: the join reads lengths before this kernel ends
     __syncthreads();
     TreeCursor<R, TM_KEYS> c = reinterpret_cast<const TreeCursor<R, TM_KEYS>&>(sh.start);
     const long long each = c.left;
@@ -426,15 +428,16 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
 // began and did not end, and a warp a unit.  Where items are few and each had many blocks,
 // one row an item, whose blocks are worked out while the first kernel still runs, and P warps
 // a unit, each every P-th block's sums, which then meet.
-constexpr int TJ_WARPS = 8, TJ_BATCH = 10;
+constexpr int TJ_WARPS = 8, TJ_BATCH = 5;
 
 template <typename T, int R, int KT, int P>
 __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_constant__ TreeArgs a, int blocks, int per_seq)
 {
     constexpr int ROWS = R < 32 ? R : 32;
     __shared__ float2 meet_ml[P > 1 ? TJ_WARPS : 1][32];
-    __shared__ float4 meet_o[P > 1 ? TJ_WARPS : 1][32];
+    __shared__ float4 meet_o[P > 1 ? TJ_WARPS : 1][2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
     TreeShared j;
     int b = blockIdx.x;
     if (P == 1) {
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
             return;  // a wait ran out
     }
     const int n = j.last - b + 1, part = warp % P, u = blockIdx.y * (TJ_WARPS / P) + warp / P;
-    const int rr = u % (R / ROWS) * ROWS + lane % ROWS, four = u / (R / ROWS) * (32 / ROWS) + lane / ROWS;
+    const int rr = u % (R / ROWS) * ROWS + lane % ROWS, pair = u / (R / ROWS) * (32 / ROWS) + lane / ROWS;
     int node, head;
     if (R >= 128) {  // 128 rows for as many whole tokens as they hold
         const int in_tile = rr & 127, token = static_cast<int>(fast_div(in_tile, a.by_group)), tokens = a.nodes / (R < 128 ? 1 : R / 128);
@@ -491,23 +494,28 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
     }
     const bool live = node < j.rows;
     float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 y) {
+    float4 o[2] = {};
+    auto add = [&](float2 ml, const float4 (&y)[2]) {
         const float top = fmaxf(m, ml.x), f = m == top ? 1.f : ex2((m - top) * TR_C), w = ml.x == top ? 1.f : ex2((ml.x - top) * TR_C);
         m = top;
         l = fmaf(w, ml.y, l * f);
-        o = make_float4(fmaf(w, y.x, o.x * f), fmaf(w, y.y, o.y * f), fmaf(w, y.z, o.z * f), fmaf(w, y.w, o.w * f));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            o[h] = make_float4(fmaf(w, y[h].x, o[h].x * f), fmaf(w, y[h].y, o[h].y * f), fmaf(w, y[h].z, o[h].z * f),
+                               fmaf(w, y[h].w, o[h].w * f));
     };
     for (int k0 = part; k0 < n && live; k0 += P * TJ_BATCH) {
         float2 ml[TJ_BATCH];
-        float4 y[TJ_BATCH];
+        float4 y[TJ_BATCH][2];
 #pragma unroll
         for (int e = 0; e < TJ_BATCH; ++e) {
             const int k = k0 + e * P;
             if (k < n) {
                 const size_t at = static_cast<size_t>(b + k) * 2 + (k == 0);
                 ml[e] = __ldcg(a.part_ml + at * R + rr);
-                y[e] = __ldcg(a.part + (at * 32 + four) * R + rr);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    y[e][h] = __ldcg(a.part + (at * 32 + 2 * pair + h) * R + rr);
             }
         }
 #pragma unroll
@@ -517,19 +525,28 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
     }
     if (P > 1) {
         meet_ml[warp][lane] = make_float2(m, l);
-        meet_o[warp][lane] = o;
+        meet_o[warp][0][lane] = o[0];
+        meet_o[warp][1][lane] = o[1];
         __syncthreads();
         if (part)
             return;
 #pragma unroll
-        for (int w = 1; w < P; ++w)
-            add(meet_ml[warp + w][lane], meet_o[warp + w][lane]);
+        for (int w = 1; w < P; ++w) {
+            const float4 y[2] = {meet_o[warp + w][0][lane], meet_o[warp + w][1][lane]};
+            add(meet_ml[warp + w][lane], y);
+        }
     }
     if (live) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        store4(static_cast<T*>(a.out) + static_cast<long long>(j.row0 + node) * a.o_row +
-                   static_cast<long long>(j.kv * a.group + head) * a.o_head + 4 * four,
-               l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w[2 * h] = l == 0.f ? 0u : pack2(o[h].x * inv, o[h].y * inv, static_cast<const T*>(nullptr));
+            w[2 * h + 1] = l == 0.f ? 0u : pack2(o[h].z * inv, o[h].w * inv, static_cast<const T*>(nullptr));
+        }
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<long long>(j.row0 + node) * a.o_row +
+                                  static_cast<long long>(j.kv * a.group + head) * a.o_head + 8 * pair) =
+            make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -585,8 +602,7 @@ static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaSt
     cudaError_t e = tree_prepare(dq::tree_mma_kernel<T, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq::TM_SMEM, done);
     if (e != cudaSuccess)
         return e;
-    dq::tree_mma_kernel<T, WR><<<cut.blocks, dq::TM_THREADS, dq::TM_SMEM, s>>>(a);
-    return cudaGetLastError();
+    return tree_dependent(dq::tree_mma_kernel<T, WR>, dim3(cut.blocks), dq::TM_THREADS, dq::TM_SMEM, s, a);
 }
 
 // The join: a dependent launch.
@@ -600,21 +616,12 @@ static cudaError_t tree_join(const dq::TreeArgs& a, const TreeCut& cut, cudaStre
     if (items * 8 <= cut.blocks)
         while (parts < 8 && items * parts * dq::TJ_BATCH < cut.blocks)
             parts *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(parts == 1 ? cut.blocks : items), static_cast<unsigned>(R * parts / dq::TJ_WARPS));
-    cfg.blockDim = dim3(32 * dq::TJ_WARPS);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg,
-                              parts == 1   ? dq::tree_join_kernel<T, R, KT, 1>
-                              : parts == 2 ? dq::tree_join_kernel<T, R, KT, 2>
-                              : parts == 4 ? dq::tree_join_kernel<T, R, KT, 4>
-                                           : dq::tree_join_kernel<T, R, KT, 8>,
-                              a, cut.blocks, per_seq);
+    return tree_dependent(parts == 1   ? dq::tree_join_kernel<T, R, KT, 1>
+                          : parts == 2 ? dq::tree_join_kernel<T, R, KT, 2>
+                          : parts == 4 ? dq::tree_join_kernel<T, R, KT, 4>
+                                       : dq::tree_join_kernel<T, R, KT, 8>,
+                          dim3(static_cast<unsigned>(parts == 1 ? cut.blocks : items), static_cast<unsigned>(R / 2 * parts / dq::TJ_WARPS)),
+                          32 * dq::TJ_WARPS, 0, s, a, cut.blocks, per_seq);
 }
 
 }  // namespace dqhost

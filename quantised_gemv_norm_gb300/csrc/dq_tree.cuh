@@ -272,6 +272,23 @@ inline bool tree_map(CUtensorMap* m, int type, const void* p, const long long (&
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A dependent launch: the kernel sets itself up while the one before it ends.
+template <typename... P, typename... A>
+cudaError_t tree_dependent(void (*kernel)(P...), dim3 grid, int threads, int shared, cudaStream_t s, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(shared);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The tensor-core kernel (dq_tree_tc.cu): one query tile of 128 rows a block, or two.
 constexpr int TREE_TC_KEYS = 128;  // keys a tile
 cudaError_t tree_tc_launch(int type, bool pair, const dq::TreeArgs& a, int blocks, cudaStream_t s);

@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
     volatile int* fail = &sh.fail;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tokens = a.nodes / QT;  // a query tile
-    pdl_trigger();
     if (warp == TT_TMA_WARP) {
         if (lane == 0) {
             mbar_init(&sh.q_full, 1);
@@ -123,6 +122,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             tree_fetch_map(&a.map);
             tree_fetch_map(&a.tq);
         }
+        pdl_wait();
         const Cursor first = tree_start<0, TT_KEYS>(a, lane);
         if (lane == 0)
             sh.start = first;
@@ -130,6 +130,8 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
     } else if (warp == TT_MMA_WARP) {
         tmem_alloc(&sh.tmem, TT_TCOLS);
     }
+    pdl_wait();
+    pdl_trigger();  // only now: the join reads lengths before this kernel ends
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -666,8 +668,7 @@ static cudaError_t tree_tc(const dq::TreeArgs& a, int blocks, cudaStream_t s)
                 done[dev] = true;
         }
     }
-    dq::tree_tc_kernel<T, PAIR><<<blocks, dq::TT_THREADS, dq::TT_SMEM, s>>>(a);
-    return cudaGetLastError();
+    return tree_dependent(dq::tree_tc_kernel<T, PAIR>, dim3(blocks), dq::TT_THREADS, dq::TT_SMEM, s, a);
 }
 
 cudaError_t tree_tc_launch(int type, bool pair, const dq::TreeArgs& a, int blocks, cudaStream_t s)
