@@ -35,8 +35,9 @@ __device__ __forceinline__ void tree_mma(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// ---- up to 32 rows a block: warp-level matrix instructions
+// ---- up to 16 rows a KV head: warp-level matrix instructions
 
+constexpr int TM_ROWS = 16;                     // rows an item
 constexpr int TM_KEYS = 64;                     // keys a tile
 constexpr int TM_SLOT = TM_KEYS * ATT_HD * 2;   // bytes of a tile of keys or values
 constexpr int TM_SLOTS = 6;                     // ring: keys, values, keys, ...
@@ -48,15 +49,16 @@ struct TreeMiscM {
     uint64_t full[TM_SLOTS], freed[TM_SLOTS];
     uint32_t absent[TM_SLOTS];  // runs of 16 keys whose page is outside the pool
     float ml[2][16][2];
-    TreeCursor<16, TM_KEYS> start;
+    TreeCursor<TM_ROWS, TM_KEYS> start;
     int fail;
 };
 static_assert(sizeof(TreeMiscM) <= 512, "fits behind the ring");
 
-template <typename T, int WR>
+template <typename T>
 __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const __grid_constant__ TreeArgs a)
 {
-    constexpr int R = 16 * WR, WK = TM_WARPS / WR, NK = TM_KEYS / WK;  // rows a block; warps along the keys; keys a warp
+    constexpr int R = TM_ROWS, NK = TM_KEYS / TM_WARPS;  // keys a warp
+    static_assert(NK == 16, "one step of the matrix instruction");
     constexpr float TOP = std::is_same<T, __half>::value ? 7.f : 0.f;
     extern __shared__ __align__(1024) uint8_t ring[];
     float2* meet = reinterpret_cast<float2*>(ring + TM_SLOTS * TM_SLOT);
@@ -74,15 +76,15 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             tree_fetch_map(&a.map);
         }
         pdl_wait();
-        const TreeCursor<R, TM_KEYS> first = tree_start<R, TM_KEYS>(a, lane);
+        const TreeCursor<TM_ROWS, TM_KEYS> first = tree_start<TM_ROWS, TM_KEYS>(a, lane);
         if (lane == 0)
-            reinterpret_cast<TreeCursor<R, TM_KEYS>&>(sh.start) = first;
+            sh.start = first;
     }
     pdl_wait();
     pdl_trigger();  // only now: the join reads lengths before this kernel ends
     __syncthreads();
-    TreeCursor<R, TM_KEYS> c = reinterpret_cast<const TreeCursor<R, TM_KEYS>&>(sh.start);
-    const long long each = c.left;
+    TreeCursor<TM_ROWS, TM_KEYS> c = sh.start;
+    const int each = c.left;
     TreeShared join{0, 0, 0, 0, -1};
     if (each > 0) {
         auto wait = [&](uint64_t* bar, uint32_t parity, int code) {
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             const int box = a.box, per_tile = TM_KEYS / box, ahead = 32 / per_tile;
             long long issued = 0;
             for (; c.left > 0 && !__any_sync(0xffffffffu, *fail); c.next(a)) {
-                const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles;
+                const int g = c.g;
                 const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
                 // lane i has the page of box `first + i`, and of box `first + 32 + i`
                 auto page_of = [&](int x) {
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                 if (!mbar_wait(&sh.full[i % TM_SLOTS], static_cast<uint32_t>(i / TM_SLOTS) & 1) && lane == 0)
                     set_error(a.err, DEVERR_TIMEOUT_DRAIN);
         } else {
-            const int wr = warp % WR, wk = warp / WR, r8 = lane >> 2, q4 = lane & 3;
+            const int wk = warp, r8 = lane >> 2, q4 = lane & 3;
             const uint32_t panel = static_cast<uint32_t>(a.box) * 128;
             // byte offset of key block i (16 keys, from the warp's first) in a slot
             uint32_t block_at[NK / 16];
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
             const uint32_t v_at = ((lane >> 3 & 1) * 8 + sw) * 128 + (((lane >> 4) ^ sw) << 4);
             const uint32_t base = smem_addr(ring);
             for (; c.left > 0; c.next(a)) {
-                const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles;
+                const int g = c.g, rt = c.rt;
                 const TreeSeq t = c.t;
                 // this lane's two rows
                 const T* qp[2];
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                 bool live[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int r = rt * R + 16 * wr + r8 + 8 * h, node = static_cast<int>(fast_div(r, a.by_group));
+                    const int r = rt * R + r8 + 8 * h, node = static_cast<int>(fast_div(r, a.by_group));
                     live[h] = node < t.rows;
                     const int row = t.row0 + (live[h] ? node : 0);
                     qp[h] = static_cast<const T*>(a.q) + static_cast<long long>(row) * a.q_row +
@@ -350,8 +352,8 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                 }
                 // ---- the warps along the keys meet: half of them give, the others take
 #pragma unroll
-                for (int half = WK / 2; half > 0; half /= 2) {
-                    const int place = wr + WR * (wk % half);
+                for (int half = TM_WARPS / 2; half > 0; half /= 2) {
+                    const int place = wk % half;
                     if (wk >= half && wk < 2 * half) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -388,12 +390,12 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                 if (!whole && c.tile == 0 && warp == 0) {
                     // the blocks that go on with the item: each has as many units as this one
                     join = TreeShared{t.row0, t.rows, g, rt,
-                                    static_cast<int>(blockIdx.x + tree_blocks(c.tiles - end, each))};
+                                    static_cast<int>(blockIdx.x) + (c.tiles - end + each - 1) / each};
                 }
                 if (wk == 0 && !*fail) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int rr = 16 * wr + r8 + 8 * h, r = rt * R + rr, node = static_cast<int>(fast_div(r, a.by_group));
+                        const int rr = r8 + 8 * h, r = rt * R + rr, node = static_cast<int>(fast_div(r, a.by_group));
                         if (!live[h])
                             continue;
                         if (whole) {
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
 constexpr int TJ_WARPS = 8, TJ_BATCH = 5;
 
 template <typename T, int R, int KT, int P>
-__global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_constant__ TreeArgs a, int blocks, int per_seq)
+__global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_constant__ TreeArgs a, int per_seq)
 {
     constexpr int ROWS = R < 32 ? R : 32;
     __shared__ float2 meet_ml[P > 1 ? TJ_WARPS : 1][32];
@@ -450,30 +452,22 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
         // every warp for itself
         TreeCursor<(R < 128 ? R : 0), KT> c;
         const int s = blockIdx.x / per_seq, item = blockIdx.x - s * per_seq;
-        long long before = 0, total = 0;
+        int before = 0, total = 0;
         for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
-            long long u = 0;
+            int u = 0;
             if (s0 + lane < a.n_seq) {
                 c.t = tree_seq(a, s0 + lane);
                 u = c.units(a);
             }
-            long long low = s0 + lane < s ? u : 0;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                u += __shfl_xor_sync(0xffffffffu, u, o);
-                low += __shfl_xor_sync(0xffffffffu, low, o);
-            }
-            total += u;
-            before += low;
+            before += __reduce_add_sync(0xffffffffu, s0 + lane < s ? u : 0);
+            total += __reduce_add_sync(0xffffffffu, u);
         }
         c.load(a, s);
-        if (item >= c.items)
+        if (item >= a.s.n_kv * c.row_tiles)
             return;
-        const long long each = max(static_cast<long long>(a.least), tree_div_up(total, blocks));
-        const long long start = before + static_cast<long long>(item) * c.tiles;
-        b = tree_div(start, each);
-        const int row_tiles = c.row_tiles(a, c.t.rows);
-        j = TreeShared{c.t.row0, c.t.rows, item / row_tiles, item % row_tiles, tree_div(start + c.tiles - 1, each)};
+        const int each = tree_each(a, total), start = before + item * c.tiles;
+        b = start / each;
+        j = TreeShared{c.t.row0, c.t.rows, item / c.row_tiles, item % c.row_tiles, (start + c.tiles - 1) / each};
         if (j.last == b)
             return;
         pdl_wait();
@@ -554,9 +548,7 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
 
 namespace dqhost {
 
-constexpr int TREE_MMA_ROWS = 32;
-
-// Rows a block and blocks: two of up to 32 rows an SM, or one of 128 or 256 on the tensor
+// Rows a block and blocks: two of 16 rows an SM, or one of 128 or 256 on the tensor
 // cores of the 5th generation.
 struct TreeCut {
     int rows, blocks;
@@ -566,9 +558,9 @@ struct TreeCut {
 static TreeCut tree_cut(int max_new, int group)
 {
     const int rows = max_new * group;
-    if (rows > TREE_MMA_ROWS)
+    if (rows > dq::TM_ROWS)
         return {(max_new + 128 / group - 1) / (128 / group) > 1 ? 256 : 128, sm_count()};
-    return {rows <= 16 ? 16 : 32, dq::TM_RESIDENT * sm_count()};
+    return {dq::TM_ROWS, dq::TM_RESIDENT * sm_count()};
 }
 
 static size_t tree_bytes(const TreeCut& c)
@@ -595,14 +587,14 @@ static cudaError_t tree_prepare(K kernel, cudaFuncAttribute what, int value, boo
     return e;
 }
 
-template <typename T, int WR>
+template <typename T>
 static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaStream_t s)
 {
     static bool done[64] = {};
-    cudaError_t e = tree_prepare(dq::tree_mma_kernel<T, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq::TM_SMEM, done);
+    cudaError_t e = tree_prepare(dq::tree_mma_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq::TM_SMEM, done);
     if (e != cudaSuccess)
         return e;
-    return tree_dependent(dq::tree_mma_kernel<T, WR>, dim3(cut.blocks), dq::TM_THREADS, dq::TM_SMEM, s, a);
+    return tree_dependent(dq::tree_mma_kernel<T>, dim3(cut.blocks), dq::TM_THREADS, dq::TM_SMEM, s, a);
 }
 
 // The join: a dependent launch.
@@ -621,7 +613,7 @@ static cudaError_t tree_join(const dq::TreeArgs& a, const TreeCut& cut, cudaStre
                           : parts == 4 ? dq::tree_join_kernel<T, R, KT, 4>
                                        : dq::tree_join_kernel<T, R, KT, 8>,
                           dim3(static_cast<unsigned>(parts == 1 ? cut.blocks : items), static_cast<unsigned>(R / 2 * parts / dq::TJ_WARPS)),
-                          32 * dq::TJ_WARPS, 0, s, a, cut.blocks, per_seq);
+                          32 * dq::TJ_WARPS, 0, s, a, per_seq);
 }
 
 }  // namespace dqhost
@@ -670,6 +662,11 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         return DQ_ERR_SHAPE;
     const int group = t->n_q / t->n_kv;
     const dqhost::TreeCut cut = dqhost::tree_cut(t->max_new, group);
+    // units of work, at most
+    const long long tile = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS, tiles = (static_cast<long long>(t->max_pages) * t->page_size + tile - 1) / tile;
+    const long long row_tiles = (static_cast<long long>(t->max_new) * group + cut.rows - 1) / cut.rows + 1;
+    if (tiles * row_tiles > 0x7fffffffll / (static_cast<long long>(t->n_seq) * t->n_kv))
+        return DQ_ERR_UNSUPPORTED;
     int box = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS;  // rows of a copy: what divides a tile and a page
     while (t->page_size % box)
         box /= 2;
@@ -708,21 +705,24 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
     a.group = group;
     a.max_pages = t->max_pages;
     a.box = box;
-    a.least = 4;
+    // a block's units where there are few: a tile costs less than starting a block and joining
+    // its sums, but they run side by side (one token after 2000 keys: 8.8 us with 1 or 2, 9.2
+    // with 4; 64 tokens: 17.4 us with 1, 20.3 with 2, 23.6 with 4)
+    a.least = cut.tc() ? 1 : 2;
     a.s = {t->n_kv, t->n_pages, t->page_size};
     a.by_group = dqhost::fast_divisor(group);
+    a.by_nodes = dqhost::fast_divisor(std::max(1, a.nodes));
+    a.by_blocks = dqhost::fast_divisor(cut.blocks);
     a.by_boxes = dqhost::fast_divisor(t->page_size / box);
     a.err = dqhost::device_error_flag();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = dqhost::with_type16(t->type, [&](auto* p) {
         using T = std::remove_pointer_t<decltype(p)>;
-        cudaError_t err = cut.tc()         ? dqhost::tree_tc_launch(t->type, cut.rows == 256, a, cut.blocks, s)
-                          : cut.rows == 16 ? dqhost::tree_launch<T, 1>(a, cut, s)
-                                           : dqhost::tree_launch<T, 2>(a, cut, s);
+        cudaError_t err = cut.tc() ? dqhost::tree_tc_launch(t->type, cut.rows == 256, a, cut.blocks, s)
+                                   : dqhost::tree_launch<T>(a, cut, s);
         if (err != cudaSuccess)
             return err;
-        return cut.rows == 16    ? dqhost::tree_join<T, 16, dq::TM_KEYS>(a, cut, s)
-               : cut.rows == 32  ? dqhost::tree_join<T, 32, dq::TM_KEYS>(a, cut, s)
+        return !cut.tc()         ? dqhost::tree_join<T, dq::TM_ROWS, dq::TM_KEYS>(a, cut, s)
                : cut.rows == 128 ? dqhost::tree_join<T, 128, dqhost::TREE_TC_KEYS>(a, cut, s)
                                  : dqhost::tree_join<T, 256, dqhost::TREE_TC_KEYS>(a, cut, s);
     });

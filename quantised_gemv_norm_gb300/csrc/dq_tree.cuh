@@ -35,7 +35,7 @@ struct TreeArgs {
     int n_seq, total_new, max_new, group, max_pages, box, least;
     int nodes;        // tokens an item where it has whole ones, else 0
     Kv16Shape s;
-    FastDiv by_group, by_boxes;  // boxes of a page
+    FastDiv by_group, by_boxes, by_nodes, by_blocks;  // boxes of a page; blocks of the first kernel
     int* err;
 };
 
@@ -68,27 +68,30 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s)
     return t;
 }
 
+// Units a block.
+__device__ __forceinline__ int tree_each(const TreeArgs& a, int total)
+{
+    const int each = static_cast<int>(fast_div(total, a.by_blocks));
+    return max(a.least, each + (each * static_cast<int>(a.by_blocks.d) < total));
+}
+
 // The work is counted in units: one key tile of one item, an item being a row tile of one
 // sequence and KV head.  Sequence by sequence, item by item, tile by tile they are one
 // long row, of which every block takes an equal stretch; a stretch is cut into segments
-// where items change.
+// where items change.  The host has seen that the units are fewer than 2^31.
 template <int R, int KT>
 struct TreeCursor {
     TreeSeq t;
-    int s, items, tiles;    // of the sequence
-    int item, tile;
-    long long left;         // units of the block's stretch
+    int s, row_tiles, tiles;  // of the sequence
+    int g, rt, tile;          // the item's KV head and row tile, the segment's first key tile
+    int left;                 // units of the block's stretch
 
-    static __device__ __forceinline__ int row_tiles(const TreeArgs& a, int rows)
+    __device__ __forceinline__ int units(const TreeArgs& a)
     {
         // R rows whatever tokens they are of, or (R = 0) a.nodes whole tokens
-        return R ? (rows * a.group + R - 1) / (R ? R : 1) : (rows + a.nodes - 1) / a.nodes;
-    }
-    __device__ __forceinline__ long long units(const TreeArgs& a)
-    {
-        items = a.s.n_kv * row_tiles(a, t.rows);
+        row_tiles = R ? (t.rows * a.group + R - 1) / (R ? R : 1) : static_cast<int>(fast_div(t.rows + a.nodes - 1, a.by_nodes));
         tiles = max(1, (t.keys + KT - 1) / KT);
-        return static_cast<long long>(items) * tiles;
+        return a.s.n_kv * row_tiles * tiles;
     }
     __device__ __forceinline__ void load(const TreeArgs& a, int seq)
     {
@@ -96,38 +99,23 @@ struct TreeCursor {
         t = tree_seq(a, seq);
         units(a);
     }
-    __device__ __forceinline__ int end() const { return static_cast<int>(min(static_cast<long long>(tiles), tile + left)); }
+    __device__ __forceinline__ int end() const { return min(tiles, tile + left); }
     // to the next segment
     __device__ __forceinline__ void next(const TreeArgs& a)
     {
         left -= end() - tile;
         tile = 0;
-        ++item;
-        while (left > 0 && item >= items) {
-            item = 0;
+        if (left <= 0 || ++rt < row_tiles)
+            return;
+        rt = 0;
+        if (++g < a.s.n_kv)
+            return;
+        g = 0;
+        do
             load(a, s + 1);
-        }
+        while (row_tiles == 0);  // there are units left, so there is a sequence with some
     }
 };
-
-// n / d rounded up, n >= 0, d > 0; rarely in 64 bits, which takes long.
-__device__ __forceinline__ long long tree_div_up(long long n, int d)
-{
-    const unsigned long long m = static_cast<unsigned long long>(n) + (d - 1);
-    return m >> 32 ? static_cast<long long>(m / d) : static_cast<long long>(static_cast<uint32_t>(m) / static_cast<uint32_t>(d));
-}
-
-// n / d below 2^31, n >= 0, d > 0.
-__device__ __forceinline__ int tree_div(long long n, long long d)
-{
-    return static_cast<int>((n | d) >> 32 ? n / d : static_cast<uint32_t>(n) / static_cast<uint32_t>(d));
-}
-
-// Blocks that `units` more units of an item take, `each` a block.
-__device__ __forceinline__ int tree_blocks(int units, long long each)
-{
-    return each > 0x7fffffffll ? 1 : static_cast<int>((static_cast<uint32_t>(units) + static_cast<uint32_t>(each) - 1) / static_cast<uint32_t>(each));
-}
 
 // Where the block's stretch begins, by one warp; left = 0: it has none.  A lane has four
 // consecutive sequences at a time, so that the lengths of 128 are one wait for memory.
@@ -136,7 +124,7 @@ __device__ __forceinline__ TreeCursor<R, KT> tree_start(const TreeArgs& a, int l
 {
     constexpr int E = 4;
     TreeCursor<R, KT> c;
-    long long u[E], mine = 0, incl = 0, total = 0;
+    int u[E], mine = 0, incl = 0, total = 0;
     // sequences s0 ..: the lane's units, and those of all lanes up to it
     auto round = [&](int s0, bool report) {
         mine = 0;
@@ -155,7 +143,7 @@ __device__ __forceinline__ TreeCursor<R, KT> tree_start(const TreeArgs& a, int l
         incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o)
                 incl += x;
         }
@@ -164,9 +152,9 @@ __device__ __forceinline__ TreeCursor<R, KT> tree_start(const TreeArgs& a, int l
         round(s0, blockIdx.x == 0);
         total += __shfl_sync(0xffffffffu, incl, 31);
     }
-    const long long each = max(static_cast<long long>(a.least), tree_div_up(total, static_cast<int>(gridDim.x)));
-    long long want = each * blockIdx.x;
-    const long long left = min(each, total - want);
+    const int each = tree_each(a, total);
+    int want = each * static_cast<int>(blockIdx.x);
+    const int left = min(each, total - want);
     c.left = 0;
     if (left <= 0)
         return c;
@@ -175,8 +163,7 @@ __device__ __forceinline__ TreeCursor<R, KT> tree_start(const TreeArgs& a, int l
             round(s0, false);
         const unsigned hit = __ballot_sync(0xffffffffu, want >= incl - mine && want < incl);
         if (hit) {
-            long long off = want - (incl - mine);
-            int s = 0;
+            int off = want - (incl - mine), s = 0;
 #pragma unroll
             for (int e = 0; e < E - 1; ++e)
                 if (s == e && off >= u[e]) {
@@ -187,8 +174,10 @@ __device__ __forceinline__ TreeCursor<R, KT> tree_start(const TreeArgs& a, int l
             off = __shfl_sync(0xffffffffu, off, src);
             s = s0 + E * src + __shfl_sync(0xffffffffu, s, src);
             c.load(a, s);
-            c.item = static_cast<int>(off >> 32 ? off / c.tiles : static_cast<uint32_t>(off) / static_cast<uint32_t>(c.tiles));
-            c.tile = static_cast<int>(off - static_cast<long long>(c.item) * c.tiles);
+            const int item = off / c.tiles;
+            c.g = c.row_tiles > 1 ? item / c.row_tiles : item;
+            c.rt = item - c.g * c.row_tiles;
+            c.tile = off - item * c.tiles;
             c.left = left;
             return c;
         }

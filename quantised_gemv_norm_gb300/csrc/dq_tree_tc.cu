@@ -155,8 +155,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             if (lane == 0)
                 sh.parked[warp] = c;
             const int n = c.end() - c.tile;
-            int node = c.item - c.item / c.row_tiles(a, c.t.rows) * c.row_tiles(a, c.t.rows);
-            node = node * a.nodes + (PAIR ? t * tokens : 0) + token;
+            int node = c.rt * a.nodes + (PAIR ? t * tokens : 0) + token;
             bool live = token < tokens && node < c.t.rows;
             int row = c.t.row0 + node;
             uint64_t seen = !live || c.t.keys == 0 ? 0ull : a.seen ? __ldg(a.seen + row) : (2ull << node) - 1;
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             // ---- the segment's end
             __syncwarp();
             c = sh.parked[warp];
-            const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles, end = c.tile + n;
+            const int g = c.g, rt = c.rt, end = c.tile + n;
             node = rt * a.nodes + (PAIR ? t * tokens : 0) + token;
             live = token < tokens && node < c.t.rows;
             row = c.t.row0 + node;
@@ -298,7 +297,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             const bool whole = c.tile == 0 && end == c.tiles, ok = __all_sync(0xffffffffu, !*fail), bad = sh.poison;
             if (!whole && c.tile == 0)
                 join = TreeShared{c.t.row0, c.t.rows, g, rt,
-                                static_cast<int>(blockIdx.x + tree_blocks(c.tiles - end, sh.start.left))};
+                                static_cast<int>(blockIdx.x) + (c.tiles - end + sh.start.left - 1) / sh.start.left};
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t at = static_cast<size_t>(blockIdx.x) * 2 + (c.tile == 0);
             const int rr = (PAIR ? 128 * t : 0) + r;
@@ -388,7 +387,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             long long issued = 0;
             for (Cursor c = sh.start; c.left > 0 && !__any_sync(0xffffffffu, *fail);
                  c.next(a), ++segment) {
-                const int row_tiles = c.row_tiles(a, c.t.rows), g = c.item / row_tiles, rt = c.item - g * row_tiles;
+                const int g = c.g, rt = c.rt;
                 const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
                 // lane i has the page of box `first + i`, and of box `first + 32 + i`
                 auto page_of = [&](int x) {
