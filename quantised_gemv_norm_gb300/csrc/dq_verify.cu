@@ -15,16 +15,18 @@
 // 64 bits, and those decide.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "dq_types.cuh"
 
 namespace dq {
 
-constexpr int VF_PIECE = 8192;   // logits a block of the first kernel
 constexpr int VF_THREADS = 256;
-constexpr int VF_EACH = VF_PIECE / VF_THREADS;
+constexpr int VF_EACH = 16;      // logits a thread has of a step of the first kernel
+constexpr int VF_STEP = VF_THREADS * VF_EACH;
 constexpr int VF_CLUSTER = 8;    // blocks a sequence, at most
 constexpr int VF_PICK = 512;     // threads each
-constexpr int VF_BATCH = 10;     // places a thread has in flight there
+constexpr int VF_BATCH = 12;     // places a thread has in flight there
 constexpr int VF_MAX_NEW = 64;
 
 struct VerifyArgs {
@@ -42,7 +44,7 @@ struct VerifyArgs {
     int* path;
     int* n_path;
     int* next;
-    int n_seq, total_new, max_new, vocab, pieces;
+    int n_seq, total_new, max_new, vocab, pieces, steps;  // pieces of a row, a block each; steps a piece
     float4* part;  // [total_new][pieces]: largest logit, its place, sum
     int* err;
 };
@@ -136,109 +138,138 @@ __device__ __forceinline__ int verify_seq(const VerifyArgs& a, int row, int lane
     return -1;
 }
 
+// One step's logits of a thread, in 16-byte accesses wherever the row begins: element 0 of a
+// row is element `skew` of its first one; element W k + e of a thread is at first + W
+// VF_THREADS k + e.
+template <typename T>
+struct VerifyStep {
+    static constexpr int W = 16 / static_cast<int>(sizeof(T)), N = VF_EACH / W;
+    uint4 u[N];
+    // `whole`: the block's step lies within the row
+    __device__ __forceinline__ void load(const T* src, int first, int vocab, bool whole)
+    {
+        if (whole) {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                u[k] = __ldcg(reinterpret_cast<const uint4*>(src + first + W * VF_THREADS * k));
+            return;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int at = first + W * VF_THREADS * k;
+            if (at >= 0 && at + W <= vocab) {
+                u[k] = __ldcg(reinterpret_cast<const uint4*>(src + at));
+            } else {
+                T x[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    x[i] = at + i >= 0 && at + i < vocab ? src[at + i] : static_cast<T>(-INFINITY);
+                memcpy(&u[k], x, 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[VF_EACH]) const
+    {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                x[W * k + i] = verify_one(reinterpret_cast<const T*>(&u[k]) + i);
+    }
+};
+
+// The largest logit with its lowest place and the sum of weights of a piece: `steps` steps
+// of one row, the next one's logits on their way while one is added up.  A warp has a
+// running maximum of its own; the block's warps meet at the end.
 template <typename T>
 __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyArgs a)
 {
-    constexpr int WARPS = VF_THREADS / 32;
-    __shared__ float tops[WARPS], sums[WARPS];
-    __shared__ int place;
+    constexpr int WARPS = VF_THREADS / 32, W = VerifyStep<T>::W;
+    __shared__ Best tops[WARPS];
+    __shared__ float sums[WARPS], row_temp;
+    __shared__ VerifyScale row_scale;
+    __shared__ int row_seq;
     const int row = blockIdx.x / a.pieces, piece = blockIdx.x - row * a.pieces;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_trigger();
     const T* src = static_cast<const T*>(a.logits) + row * a.ld;
-    // 16-byte accesses wherever the row begins: element 0 of a row is element `skew` of its
-    // first one; element i = W k + e of a thread is at first + W VF_THREADS k + e
-    constexpr int W = 16 / static_cast<int>(sizeof(T));
     const int skew = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
-    const int first = piece * VF_PIECE + W * tid - skew;
-    float x[VF_EACH];
-    if (piece * VF_PIECE >= skew && piece * VF_PIECE - skew + VF_PIECE <= a.vocab) {
-        uint4 u[VF_EACH / W];
+    int base = piece * a.steps * VF_STEP - skew;  // the step's first element
+    auto whole = [&](int b) { return b >= 0 && b + VF_STEP <= a.vocab; };
+    const int steps = min(a.steps, (a.vocab + skew + VF_STEP - 1) / VF_STEP - piece * a.steps);
+    VerifyStep<T> next;
+    next.load(src, base + W * tid, a.vocab, whole(base));
+    if (warp == 0) {
+        const int s = verify_seq(a, row, lane);
+        if (lane == 0) {
+            row_temp = s < 0 ? -1.f : a.temperature ? __ldg(a.temperature + s) : 1.f;
+            row_seq = s;
+            row_scale = verify_scale(row_temp > 0.f ? row_temp : 1.f);
+        }
+    }
+    __syncthreads();
+    if (row_seq < 0)
+        return;  // a row of no sequence
+    const float temp = row_temp;
+    const VerifyScale c = row_scale;
+    Best top{-INFINITY, -1};  // the warp's
+    float sum = 0.f;          // the lane's
+    for (int k = 0; k < steps; ++k, base += VF_STEP) {
+        float x[VF_EACH];
+        next.get(x);
+        if (k + 1 < steps)
+            next.load(src, base + VF_STEP + W * tid, a.vocab, whole(base + VF_STEP));
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < VF_EACH / W; ++k)
-            u[k] = __ldcg(reinterpret_cast<const uint4*>(src + first + W * VF_THREADS * k));
+        for (int i = 0; i < VF_EACH; ++i)
+            m4[i & 3] = fmaxf(m4[i & 3], x[i]);  // NaN is passed over
+        const float m = warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+        if (m > top.v) {  // the same in the whole warp
+            int at = 0x7fffffff;
 #pragma unroll
-        for (int k = 0; k < VF_EACH / W; ++k)
+            for (int i = VF_EACH - 1; i >= 0; --i)
+                if (x[i] == m)
+                    at = base + W * tid + W * VF_THREADS * (i / W) + i % W;
+            sum = top.at < 0 ? 0.f : sum * verify_exp(top.v, m, c);
+            top = Best{m, static_cast<int>(__reduce_min_sync(0xffffffffu, at))};
+        }
+        if (temp > 0.f && top.at >= 0) {
+            if (top.v < INFINITY) {
+                uint64_t part[2] = {0ull, 0ull};
+                const uint64_t minus = f2(-top.v, -top.v);
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                x[W * k + i] = verify_one(reinterpret_cast<const T*>(&u[k]) + i);
-    } else {
-#pragma unroll
-        for (int k = 0; k < VF_EACH / W; ++k) {
-            const int at = first + W * VF_THREADS * k;
-            if (at >= 0 && at + W <= a.vocab) {
-                const uint4 u = __ldcg(reinterpret_cast<const uint4*>(src + at));
-#pragma unroll
-                for (int i = 0; i < W; ++i)
-                    x[W * k + i] = verify_one(reinterpret_cast<const T*>(&u) + i);
+                for (int i = 0; i < VF_EACH / 2; ++i)
+                    part[i & 1] = add2(part[i & 1], verify_exp2(f2(x[2 * i], x[2 * i + 1]), minus, c));
+                const float2 p = un2(add2(part[0], part[1]));
+                sum += p.x + p.y;
             } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i)
-                    x[W * k + i] = at + i >= 0 && at + i < a.vocab ? verify_one(src + at + i) : -INFINITY;
+                for (int i = 0; i < VF_EACH; ++i)
+                    sum += x[i] == top.v ? 1.f : 0.f;
             }
         }
     }
-    if (tid == 0)
-        place = 0x7fffffff;
-    const int s = verify_seq(a, row, lane);
-    if (s < 0)
-        return;  // a row of no sequence
-    const float temp = a.temperature ? __ldg(a.temperature + s) : 1.f;
-    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-    for (int i = 0; i < VF_EACH; ++i)
-        m4[i & 3] = fmaxf(m4[i & 3], x[i]);  // NaN is passed over
-    const float m = warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-    float sum = 0.f;
-    const VerifyScale c = verify_scale(temp > 0.f ? temp : 1.f);
-    if (temp > 0.f && m > -INFINITY) {
-        if (m < INFINITY) {
-            uint64_t part[2] = {0ull, 0ull};
-            const uint64_t minus = f2(-m, -m);
-#pragma unroll
-            for (int i = 0; i < VF_EACH / 2; ++i)
-                part[i & 1] = add2(part[i & 1], verify_exp2(f2(x[2 * i], x[2 * i + 1]), minus, c));
-            const float2 p = un2(add2(part[0], part[1]));
-            sum = p.x + p.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < VF_EACH; ++i)
-                sum += x[i] == m ? 1.f : 0.f;
-        }
-        sum = warp_sum(sum);
-    }
+    sum = warp_sum(sum);
     if (lane == 0) {
-        tops[warp] = m;
+        tops[warp] = top;
         sums[warp] = sum;
-    }
-    __syncthreads();
-    const float theirs = lane < WARPS ? tops[lane] : -INFINITY, top = warp_max(theirs);
-    // the lowest place of the largest logit: by the warps that have it
-    if (m == top && top > -INFINITY) {
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int i = VF_EACH - 1; i >= 0; --i)
-            if (x[i] == top)
-                at = first + W * VF_THREADS * (i / W) + i % W;
-        at = __reduce_min_sync(0xffffffffu, at);
-        if (lane == 0)
-            atomicMin(&place, at);
     }
     __syncthreads();
     if (warp)
         return;
-    sum = warp_sum(lane < WARPS && theirs > -INFINITY ? sums[lane] * verify_exp(theirs, top, c) : 0.f);
+    const Best b = lane < WARPS ? tops[lane] : Best{-INFINITY, -1};
+    top = warp_best(b);
+    sum = warp_sum(b.at >= 0 ? sums[lane] * verify_exp(b.v, top.v, c) : 0.f);
     if (lane == 0)
-        a.part[static_cast<size_t>(row) * a.pieces + piece] =
-            make_float4(top, __int_as_float(top > -INFINITY ? place : -1), sum, 0.f);
+        a.part[static_cast<size_t>(row) * a.pieces + piece] = make_float4(top.v, __int_as_float(top.at), sum, 0.f);
 }
 
 struct VerifyShared {
     Best top[VF_MAX_NEW];        // a node's largest logit
     double sum[VF_MAX_NEW];      // of its weights
     float w[VF_MAX_NEW];         // the weight of a node's token at its parent
-    float u[VF_MAX_NEW], q[VF_MAX_NEW];
     int parent[VF_MAX_NEW], token[VF_MAX_NEW];
+    unsigned long long taken[VF_MAX_NEW];  // the children of a node that are accepted if their turn comes
     int path[VF_MAX_NEW], len;
     int gone[VF_MAX_NEW], n_gone;  // rejected tokens at the last node
     int last, turned_down;         // the rejected node of a chain, or 0
@@ -249,6 +280,13 @@ struct VerifyShared {
     int near[VF_PICK * VF_CLUSTER], n_near;  // in the first block: places near the cluster's best
 };
 
+// Four consecutive logits from an address that is a multiple of their size.
+template <typename T>
+__device__ __forceinline__ float4 verify_four(const T* p)
+{
+    return load4(p);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArgs a)
 {
@@ -258,6 +296,7 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int s = blockIdx.x / blocks;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const float temp = a.temperature ? __ldg(a.temperature + s) : 1.f;
     bool ok;
     const int2 nodes = verify_nodes(a, s, ok);
     const int row0 = nodes.x, n = nodes.y;
@@ -277,15 +316,31 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
         return;
     }
     const T* logits = static_cast<const T*>(a.logits);
-    const float temp = a.temperature ? __ldg(a.temperature + s) : 1.f;
     const bool greedy = !(temp > 0.f);
     const VerifyScale c = verify_scale(greedy ? 1.f : temp);
 
-    float own = -INFINITY;  // a node's token's logit at its parent
+    // the tree's numbers and the random ones are on their way while the sums are still made
     int parent = -1, token = -1;
+    float u = 0.f, q = 1.f;
     if (tid < n) {
         token = __ldg(a.tokens + row0 + tid);
         parent = tid == 0 ? -1 : a.parents ? __ldg(a.parents + row0 + tid) : tid - 1;
+        u = __ldg(a.uniform + row0 + tid);
+    }
+    const int slice = ((a.vocab + blocks - 1) / blocks + 3) & ~3, v0 = rank * slice, v1 = min(a.vocab, v0 + slice);
+    const float* noise = a.noise + s * a.noise_ld;
+    if (!greedy)
+        for (int v = v0 + 32 * tid; v < v1; v += 32 * VF_PICK)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + v));
+    pdl_wait();
+    // eight threads a node join its pieces: the largest logit first, then the sums in two
+    // parts (the second has what the first loses)
+    const int node = tid >> 3;
+    const float4* part = a.part + static_cast<size_t>(row0 + min(node, n - 1)) * a.pieces;
+    const float4 none = make_float4(-INFINITY, __int_as_float(-1), 0.f, 0.f);
+    const float4 mine = (tid & 7) < a.pieces ? __ldcg(part + (tid & 7)) : none;
+    float own = -INFINITY;  // a node's token's logit at its parent
+    if (tid < n) {
         if (tid > 0 && (parent < 0 || parent >= tid)) {
             parent = -1;
             if (rank == 0)
@@ -295,46 +350,32 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
             token = -1;
         if (parent >= 0 && token >= 0) {
             own = verify_clean(verify_one(logits + (row0 + parent) * a.ld + token));
-            sh.u[tid] = __ldg(a.uniform + row0 + tid);
-            sh.q[tid] = a.draft ? __ldg(a.draft + (row0 + tid) * a.draft_ld + token) : 1.f;
+            if (a.draft)
+                q = __ldg(a.draft + (row0 + tid) * a.draft_ld + token);
         }
         sh.parent[tid] = parent;
         sh.token[tid] = token;
+        sh.taken[tid] = 0ull;
     }
-    pdl_wait();
-    // eight threads a node join its pieces: the largest logit first, then the sums in two
-    // parts (the second has what the first loses)
     if (warp < 4 * ((n + 15) / 16)) {
-        const int node = tid >> 3, k0 = tid & 7;
-        const float4* part = a.part + static_cast<size_t>(row0 + min(node, n - 1)) * a.pieces;
-        constexpr int E = 4;
-        float4 x[E];
-        Best top{-INFINITY, -1};
-        for (int k = k0; k < a.pieces; k += 8 * E) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[e] = k + 8 * e < a.pieces ? __ldcg(part + k + 8 * e) : make_float4(-INFINITY, __int_as_float(-1), 0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                top = better(top, Best{x[e].x, __float_as_int(x[e].y)});
+        Best top{mine.x, __float_as_int(mine.y)};
+        for (int k = (tid & 7) + 8; k < a.pieces; k += 8) {
+            const float4 x = __ldcg(part + k);
+            top = better(top, Best{x.x, __float_as_int(x.y)});
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1)
             top = better(top, Best{__shfl_xor_sync(0xffffffffu, top.v, o), __shfl_xor_sync(0xffffffffu, top.at, o)});
-        float hi = 0.f, lo = 0.f;
+        float hi = __float_as_int(mine.y) >= 0 ? mine.z * verify_exp(mine.x, top.v, c) : 0.f, lo = 0.f;
         auto add = [&](float v) {
             const float t = hi + v, z = t - hi;
             lo += (hi - (t - z)) + (v - z);
             hi = t;
         };
-        for (int k = k0; k < a.pieces; k += 8 * E) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (a.pieces > 8 * E)
-                    x[e] = k + 8 * e < a.pieces ? __ldcg(part + k + 8 * e) : make_float4(0.f, __int_as_float(-1), 0.f, 0.f);
-                if (__float_as_int(x[e].y) >= 0)
-                    add(x[e].z * verify_exp(x[e].x, top.v, c));
-            }
+        for (int k = (tid & 7) + 8; k < a.pieces; k += 8) {
+            const float4 x = __ldcg(part + k);
+            if (__float_as_int(x.y) >= 0)
+                add(x.z * verify_exp(x.x, top.v, c));
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
@@ -342,105 +383,153 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
             add(h2);
             lo += l2;
         }
-        if (node < n && k0 == 0) {
+        if (node < n && (tid & 7) == 0) {
             sh.top[node] = top;
             sh.sum[node] = static_cast<double>(hi) + lo;
         }
     }
     __syncthreads();
-    if (tid < n && parent >= 0) {
-        const Best t = sh.top[parent];
-        sh.w[tid] = token < 0 || t.at < 0 || greedy ? 0.f : verify_exp(own, t.v, c);
-    }
+    const Best above = parent >= 0 ? sh.top[parent] : Best{-INFINITY, -1};
+    const float w = parent < 0 || token < 0 || above.at < 0 || greedy ? 0.f : verify_exp(own, above.v, c);
+    if (tid < n)
+        sh.w[tid] = w;
     __syncthreads();
 
-    // ---- the walk, by one thread: a node's children are above it, so one pass in ascending
-    // order; probabilities in units of 1 / the node's sum
-    if (tid == 0) {
-        int cur = 0, len = 1, gone = 0, down = 0;
-        double left = sh.sum[0];
-        sh.path[0] = 0;
-        for (int j = 1; j < n; ++j) {
-            if (sh.parent[j] != cur)
-                continue;
-            const int x = sh.token[j];
-            bool take;
-            if (greedy) {
-                take = x >= 0 && x == sh.top[cur].at;
-            } else if (a.draft) {
-                take = x >= 0 && static_cast<double>(sh.u[j]) * sh.q[j] * left < sh.w[j];
-                down = take ? 0 : j;
-            } else {
-                bool again = x < 0;
-                for (int k = 0; k < gone; ++k)
-                    again |= sh.gone[k] == x;
-                take = !again && sh.u[j] * left < sh.w[j];
-                if (!again && !take) {
-                    sh.gone[gone++] = x;
-                    left -= sh.w[j];
+    // ---- each node's test, should its turn come: the children of a node are tried in ascending
+    // order, so all its siblings before it were rejected; probabilities in units of 1 / the
+    // node's sum
+    if (parent >= 0 && token >= 0) {
+        bool take;
+        if (greedy) {
+            take = token == above.at;
+        } else {
+            double left = sh.sum[parent];
+            bool again = false;
+            if (a.parents && !a.draft) {
+                for (int i = parent + 1; i < tid; ++i) {
+                    if (sh.parent[i] != parent || sh.token[i] < 0)
+                        continue;
+                    again |= sh.token[i] == token;
+                    bool counted = false;  // a token counts once
+                    for (int k = parent + 1; k < i; ++k)
+                        counted |= sh.parent[k] == parent && sh.token[k] == sh.token[i];
+                    if (!counted)
+                        left -= sh.w[i];
                 }
             }
-            if (take) {
-                sh.path[len++] = j;
-                cur = j;
-                gone = 0;
-                left = sh.sum[j];
-            }
+            take = !again && static_cast<double>(u) * q * left < w;
         }
-        sh.last = cur;
-        sh.n_gone = gone;
-        sh.turned_down = down;
-        sh.len = len;
+        if (take)
+            atomicOr(&sh.taken[parent], 1ull << tid);
     }
     __syncthreads();
+    if (tid == 0) {
+        int cur = 0, len = 1;
+        sh.path[0] = 0;
+        while (sh.taken[cur]) {
+            cur = __ffsll(static_cast<long long>(sh.taken[cur])) - 1;
+            sh.path[len++] = cur;
+        }
+        sh.last = cur;
+        sh.len = len;
+        sh.n_gone = sh.turned_down = 0;
+    }
+    __syncthreads();
+    const int last = sh.last;
+    if (parent == last && tid < n) {  // the last node's children were all rejected
+        if (a.draft)
+            sh.turned_down = tid;  // a chain's one
+        else if (token >= 0)
+            sh.gone[atomicAdd(&sh.n_gone, 1)] = token;
+    }
     if (rank == 0) {
         if (tid < a.max_new)
             path[tid] = tid < sh.len ? sh.path[tid] : -1;
         if (tid == 0)
             a.n_path[s] = sh.len;
     }
-    const int last = sh.last, n_gone = sh.n_gone, down = sh.turned_down;
     const Best top = sh.top[last];
     if (greedy || top.at < 0) {
         if (rank == 0 && tid == 0)
             a.next[s] = top.at;
         return;
     }
+    __syncthreads();
+    const int n_gone = sh.n_gone, down = sh.turned_down;
 
     // ---- the next token
     const T* row = logits + (row0 + last) * a.ld;
-    const float* noise = a.noise + s * a.noise_ld;
     const float* draft = down ? a.draft + (row0 + down) * a.draft_ld : nullptr;
     const float z = static_cast<float>(sh.sum[last]);
-    const int slice = (a.vocab + blocks - 1) / blocks, v0 = rank * slice, v1 = min(a.vocab, v0 + slice);
     const uint64_t minus = f2(-top.v, -top.v);
+    const bool infinite = isinf(top.v);
     Best best{0.f, -1};
-    float size = 0.f;  // of the numbers that the best's r is a difference of, over its noise
-    for (int b0 = v0 + tid; b0 < v1; b0 += VF_PICK * VF_BATCH) {
-        float x[VF_BATCH], q[VF_BATCH], e[VF_BATCH];
+    auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int v) {
+        float2 p = un2(verify_exp2(f2(x, y), minus, c));
+        if (infinite)
+            p = make_float2(x == top.v ? 1.f : 0.f, y == top.v ? 1.f : 0.f);
+        const float sx = __fdividef(fmaf(-z, qx, p.x), ex), sy = __fdividef(fmaf(-z, qy, p.y), ey);
+        if (n_gone) {
+            for (int e = 0; e < 2; ++e) {
+                if (!((e ? sy : sx) > best.v))
+                    continue;
+                bool out = false;
+                for (int k = 0; k < n_gone; ++k)
+                    out |= sh.gone[k] == v + e;
+                if (!out)
+                    best = Best{e ? sy : sx, v + e};
+            }
+        } else {
+            best.at = sx > best.v ? v : best.at;
+            best.v = fmaxf(sx, best.v);
+            best.at = sy > best.v ? v + 1 : best.at;
+            best.v = fmaxf(sy, best.v);
+        }
+    };
+    const bool vec = !((reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) | (reinterpret_cast<uintptr_t>(noise) & 15) |
+                       (reinterpret_cast<uintptr_t>(draft) & 15));
+    const int v4 = vec ? v0 + (max(0, v1 - v0) & ~3) : v0;
+    constexpr int N = VF_BATCH / 4;
+    for (int b0 = v0 + 4 * tid; b0 < v4; b0 += 4 * VF_PICK * N) {
+        float4 x[N], e[N], d[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = b0 + 4 * VF_PICK * i;
+            x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            e[i] = make_float4(1.f, 1.f, 1.f, 1.f);
+            d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (v < v4) {
+                x[i] = verify_four(row + v);
+                e[i] = __ldcs(reinterpret_cast<const float4*>(noise + v));
+                if (draft)
+                    d[i] = __ldcs(reinterpret_cast<const float4*>(draft + v));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = b0 + 4 * VF_PICK * i;
+            look(x[i].x, x[i].y, d[i].x, d[i].y, e[i].x, e[i].y, v);
+            look(x[i].z, x[i].w, d[i].z, d[i].w, e[i].z, e[i].w, v + 2);
+        }
+    }
+    // rows that do not begin alike, and what four do not divide
+    for (int b0 = v4 + tid; b0 < v1; b0 += VF_PICK * VF_BATCH) {
+        float x[VF_BATCH], d[VF_BATCH], e[VF_BATCH];
 #pragma unroll
         for (int i = 0; i < VF_BATCH; ++i) {
             const int v = b0 + i * VF_PICK;
             x[i] = v < v1 ? verify_one(row + v) : -INFINITY;
             e[i] = v < v1 ? __ldcs(noise + v) : 1.f;
-            q[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
+            d[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < VF_BATCH; ++i) {
-            const int v = b0 + i * VF_PICK;
-            const float w = isinf(top.v) ? (x[i] == top.v ? 1.f : 0.f) : un2(verify_exp2(f2(x[i], x[i]), minus, c)).x;
-            const float score = __fdividef(w - z * q[i], e[i]);
-            if (score > best.v) {
-                bool out = false;
-                for (int k = 0; k < n_gone; ++k)
-                    out |= sh.gone[k] == v;
-                if (!out) {
-                    best = {score, v};
-                    size = (w + z * q[i]) / e[i];
-                }
-            }
-        }
+        for (int i = 0; i < VF_BATCH; ++i)
+            look(x[i], -INFINITY, d[i], 0.f, e[i], 1.f, b0 + i * VF_PICK);
     }
+    // the numbers that the best's r is a difference of, over its noise
+    float size = 0.f;
+    if (best.at >= 0)
+        size = best.v + 2.f * (draft ? z * draft[best.at] : 0.f) / noise[best.at];
     Best b = warp_best(best);
     if (lane == 0)
         sh.warp[warp] = b;
@@ -503,8 +592,19 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
 
 namespace dqhost {
 
-// Pieces of a row, which may begin up to 7 elements into its first 16 bytes.
-static int verify_pieces(int vocab) { return (vocab + 7 + dq::VF_PIECE - 1) / dq::VF_PIECE; }
+// How the first kernel cuts a row: into pieces of so many steps that the card has two
+// rounds of blocks, five an SM, to do (a row may begin up to 7 elements into its first 16
+// bytes).
+struct VerifyCut {
+    int pieces, steps;
+};
+static VerifyCut verify_cut(int total_new, int vocab)
+{
+    const int all = (vocab + 7 + dq::VF_STEP - 1) / dq::VF_STEP;
+    const long long steps = std::min<long long>(16, std::max(1ll, static_cast<long long>(total_new) * all / (10ll * sm_count())));
+    const int pieces = static_cast<int>((all + steps - 1) / steps);
+    return {pieces, (all + pieces - 1) / pieces};
+}
 
 }  // namespace dqhost
 
@@ -514,7 +614,7 @@ DQ_API size_t dq_verify_draft_workspace_bytes(int total_new, int vocab)
 {
     if (total_new < 1 || vocab < 1 || total_new > (1 << 24) || vocab > (1 << 24))
         return 0;
-    return static_cast<size_t>(total_new) * dqhost::verify_pieces(vocab) * sizeof(float4);
+    return static_cast<size_t>(total_new) * dqhost::verify_cut(total_new, vocab).pieces * sizeof(float4);
 }
 
 DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
@@ -527,9 +627,9 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
         (v->draft_probs && v->total_new > 1 && v->draft_stride < v->vocab) ||
         (!v->cu_new && v->total_new != static_cast<long long>(v->n_seq) * v->max_new))
         return DQ_ERR_SHAPE;
-    const int pieces = dqhost::verify_pieces(v->vocab);
+    const long long steps = (static_cast<long long>(v->vocab) + 7 + dq::VF_STEP - 1) / dq::VF_STEP;
     if (v->max_new > dq::VF_MAX_NEW || (v->draft_probs && v->parents) || v->vocab > (1 << 24) || v->total_new > (1 << 24) ||
-        v->n_seq > (1 << 24) || static_cast<long long>(v->total_new) * pieces > (1 << 30))
+        v->n_seq > (1 << 24) || v->total_new * steps > (1 << 30))
         return DQ_ERR_UNSUPPORTED;
     const void* words[11] = {v->draft_probs, v->noise, v->tokens, v->parents, v->uniform, v->temperature, v->cu_new,
                              v->path, v->n_path, v->next, nullptr};
@@ -541,14 +641,15 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
         return DQ_ERR_ALIGN;
     if (v->workspace_bytes < dq_verify_draft_workspace_bytes(v->total_new, v->vocab))
         return DQ_ERR_SHAPE;
+    const dqhost::VerifyCut cut = dqhost::verify_cut(v->total_new, v->vocab);
     const dq::VerifyArgs a{v->logits, v->logits_stride, v->draft_probs, v->draft_stride, v->noise, v->noise_stride,
                            v->tokens, v->parents, v->uniform, v->temperature, v->cu_new, v->path, v->n_path, v->next,
-                           v->n_seq, v->total_new, v->max_new, v->vocab, pieces, static_cast<float4*>(v->workspace),
+                           v->n_seq, v->total_new, v->max_new, v->vocab, cut.pieces, cut.steps, static_cast<float4*>(v->workspace),
                            dqhost::device_error_flag()};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = dqhost::with_type(v->type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        const unsigned grid = static_cast<unsigned>(v->total_new) * pieces;
+        const unsigned grid = static_cast<unsigned>(v->total_new) * cut.pieces;
         dq::verify_stats_kernel<T><<<grid, dq::VF_THREADS, 0, s>>>(a);
         const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess)
