@@ -16,6 +16,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "dq_types.cuh"
 
@@ -24,7 +25,7 @@ namespace dq {
 constexpr int VF_THREADS = 256;
 constexpr int VF_EACH = 16;      // logits a thread has of a step of the first kernel
 constexpr int VF_STEP = VF_THREADS * VF_EACH;
-constexpr int VF_CLUSTER = 8;    // blocks a sequence, at most
+constexpr int VF_CLUSTER = 16;   // blocks a sequence, at most (8 is the portable limit)
 constexpr int VF_PICK = 512;     // threads each
 constexpr int VF_BATCH = 12;     // places a thread has in flight there
 constexpr int VF_MAX_NEW = 64;
@@ -337,8 +338,16 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
     // parts (the second has what the first loses)
     const int node = tid >> 3;
     const float4* part = a.part + static_cast<size_t>(row0 + min(node, n - 1)) * a.pieces;
-    const float4 none = make_float4(-INFINITY, __int_as_float(-1), 0.f, 0.f);
-    const float4 mine = (tid & 7) < a.pieces ? __ldcg(part + (tid & 7)) : none;
+    constexpr int E = 5;  // pieces a thread has in registers: 40 a row
+    float4 x[E];
+    auto pieces = [&](int k0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int k = k0 + (tid & 7) + 8 * e;
+            x[e] = k < a.pieces ? __ldcg(part + k) : make_float4(-INFINITY, __int_as_float(-1), 0.f, 0.f);
+        }
+    };
+    pieces(0);
     float own = -INFINITY;  // a node's token's logit at its parent
     if (tid < n) {
         if (tid > 0 && (parent < 0 || parent >= tid)) {
@@ -358,24 +367,33 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
         sh.taken[tid] = 0ull;
     }
     if (warp < 4 * ((n + 15) / 16)) {
-        Best top{mine.x, __float_as_int(mine.y)};
-        for (int k = (tid & 7) + 8; k < a.pieces; k += 8) {
-            const float4 x = __ldcg(part + k);
-            top = better(top, Best{x.x, __float_as_int(x.y)});
+        Best top{-INFINITY, -1};
+        auto largest = [&] {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                top = better(top, Best{x[e].x, __float_as_int(x[e].y)});
+        };
+        largest();
+        for (int k = 8 * E; k < a.pieces; k += 8 * E) {
+            pieces(k);
+            largest();
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1)
             top = better(top, Best{__shfl_xor_sync(0xffffffffu, top.v, o), __shfl_xor_sync(0xffffffffu, top.at, o)});
-        float hi = __float_as_int(mine.y) >= 0 ? mine.z * verify_exp(mine.x, top.v, c) : 0.f, lo = 0.f;
+        float hi = 0.f, lo = 0.f;
         auto add = [&](float v) {
             const float t = hi + v, z = t - hi;
             lo += (hi - (t - z)) + (v - z);
             hi = t;
         };
-        for (int k = (tid & 7) + 8; k < a.pieces; k += 8) {
-            const float4 x = __ldcg(part + k);
-            if (__float_as_int(x.y) >= 0)
-                add(x.z * verify_exp(x.x, top.v, c));
+        for (int k = 0; k < a.pieces; k += 8 * E) {
+            if (a.pieces > 8 * E)
+                pieces(k);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (__float_as_int(x[e].y) >= 0)
+                    add(x[e].z * verify_exp(x[e].x, top.v, c));
         }
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) {
@@ -592,6 +610,24 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
 
 namespace dqhost {
 
+// More than eight blocks a cluster, allowed once per device.
+template <typename K>
+static cudaError_t verify_prepare(K kernel, bool (&done)[64])
+{
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && dev >= 0 && dev < 64)
+            done[dev] = true;
+    }
+    return e;
+}
+
 // How the first kernel cuts a row: into pieces of so many steps that the card has two
 // rounds of blocks, five an SM, to do (a row may begin up to 7 elements into its first 16
 // bytes).
@@ -655,7 +691,11 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
         if (err != cudaSuccess)
             return err;
         // a dependent launch: it gathers the tree's numbers while the last pieces run
-        // as many blocks a sequence as are resident together, two an SM (1, 2, 4 or 8)
+        static bool done[64] = {};
+        const cudaError_t wide = dqhost::verify_prepare(dq::verify_pick_kernel<T>, done);
+        if (wide != cudaSuccess)
+            return wide;
+        // as many blocks a sequence as are resident together, two an SM (1, 2, 4, 8 or 16)
         int blocks = dq::VF_CLUSTER;
         while (blocks > 1 && static_cast<long long>(v->n_seq) * blocks > 2 * dqhost::sm_count())
             blocks /= 2;
