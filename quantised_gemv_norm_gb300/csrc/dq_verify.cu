@@ -198,8 +198,13 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
     int base = piece * a.steps * VF_STEP - skew;  // the step's first element
     auto whole = [&](int b) { return b >= 0 && b + VF_STEP <= a.vocab; };
     const int steps = min(a.steps, (a.vocab + skew + VF_STEP - 1) / VF_STEP - piece * a.steps);
-    VerifyStep<T> next;
-    next.load(src, base + W * tid, a.vocab, whole(base));
+    // 64 bytes a thread on their way
+    constexpr int DEPTH = 4 / static_cast<int>(sizeof(T));
+    VerifyStep<T> next[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        if (d == 0 || d < steps)
+            next[d].load(src, base + d * VF_STEP + W * tid, a.vocab, whole(base + d * VF_STEP));
     if (warp == 0) {
         const int s = verify_seq(a, row, lane);
         if (lane == 0) {
@@ -217,9 +222,12 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
     float sum = 0.f;          // the lane's
     for (int k = 0; k < steps; ++k, base += VF_STEP) {
         float x[VF_EACH];
-        next.get(x);
-        if (k + 1 < steps)
-            next.load(src, base + VF_STEP + W * tid, a.vocab, whole(base + VF_STEP));
+        next[0].get(x);
+#pragma unroll
+        for (int d = 0; d + 1 < DEPTH; ++d)
+            next[d] = next[d + 1];
+        if (k + DEPTH < steps)
+            next[DEPTH - 1].load(src, base + DEPTH * VF_STEP + W * tid, a.vocab, whole(base + DEPTH * VF_STEP));
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int i = 0; i < VF_EACH; ++i)
