@@ -2,10 +2,15 @@
 // embedding on the way (dq_kv16_append), and accepted rows moved within it
 // (dq_kv16_keep).
 //
-// The store is dq_qkv.cu's: half a warp takes one head, a warp eight heads of one row;
-// lane i of 16 holds dims 4 i .. 4 i + 3 and 64 + 4 i .., so a rotation's two dims are in
-// one lane and all eight heads' loads are issued first.  Only where a key or value row
-// goes differs: to its slot.
+// The store: half a warp takes one head, a warp four heads of one row; lane i of 16 holds
+// dims 4 i .. 4 i + 3 and 64 + 4 i .., so a rotation's two dims are in one lane, the sum of
+// squares of two heads is four shuffles, the row's angles are loaded once and all four heads'
+// loads are issued first.  Memory bounds it: 8191 rows of 48 heads from fp32, 306 MB, 48.3
+// us, 6.3 TB/s (0.95 of the measured copy rate).  The stores are streaming ones: written
+// back late, as plain stores are, the rows took 55.8 us.  Eight heads a warp 50.1 us (one row
+// 3.1 us, with four heads 2.6), blocks of 16 warps 54.3.
+#include <algorithm>
+
 #include "dq_kv16.cuh"
 
 namespace dq {
@@ -27,8 +32,8 @@ struct Kv16AppendArgs {
     int* err;
 };
 
-constexpr int KV16_WARPS = 8;
-constexpr int KV16_PAIRS = 4;  // pairs of heads a warp
+constexpr int KV16_WARPS = 4;
+constexpr int KV16_PAIRS = 2;  // pairs of heads a warp
 
 // Four consecutive elements, read once.
 __device__ __forceinline__ float4 stream4(const float* p) { return __ldcs(reinterpret_cast<const float4*>(p)); }
@@ -39,6 +44,13 @@ __device__ __forceinline__ float4 stream4(const T* p)
     const float2 a = un2(std::is_same<T, __half>::value ? half2_f2(u.x) : f2(bf16lo(u.x), bf16hi(u.x)));
     const float2 b = un2(std::is_same<T, __half>::value ? half2_f2(u.y) : f2(bf16lo(u.y), bf16hi(u.y)));
     return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Four elements to where they are not read again soon.
+template <typename T>
+__device__ __forceinline__ void stream_store4(T* p, float4 v)
+{
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack2(v.x, v.y, p), pack2(v.z, v.w, p)));
 }
 
 template <typename In, typename T>
@@ -112,8 +124,8 @@ __global__ void __launch_bounds__(32 * KV16_WARPS) kv16_append_kernel(const Kv16
             // heads n_q .. are the pool's planes [2][n_kv] in order
             out = static_cast<T*>(a.pool) + (first + static_cast<long long>(h - a.n_q) * a.s.page_rows) * ATT_HD;
         }
-        store4(out + 4 * i, x[p]);
-        store4(out + 64 + 4 * i, y[p]);
+        stream_store4(out + 4 * i, x[p]);
+        stream_store4(out + 64 + 4 * i, y[p]);
     }
 }
 
@@ -124,9 +136,9 @@ struct Kv16KeepArgs {
     const int* n_past;
     const int* path;
     const int* n_path;
-    int max_new, max_pages;
+    int max_new, max_pages, n_layers, each;  // layers a block
     Kv16Shape s;
-    FastDiv by_page, by_layers;
+    FastDiv by_page, by_groups;  // groups of layers
     int* err;
 };
 
@@ -135,20 +147,26 @@ constexpr int KV16_KEEP_EACH = 4;  // 16-byte pieces a thread has in registers
 constexpr int KV16_MAX_NEW = 64;
 static_assert(KV16_KEEP_THREADS * KV16_KEEP_EACH >= KV16_MAX_NEW * 16, "a plane's rows are moved at once");
 
-// One block a sequence, layer and half (its keys or its values).  The moved rows' places are
-// found once, a thread a row; then as many heads at a time as the block's registers hold go
-// through them, all their rows read before the first is written (a row may be another's
-// place).  64 sequences' 6 rows or so in 36 layers of 8 heads: a block a head, each finding
-// the rows for itself, took 59 us.
+// One block a sequence, group of layers and half (keys or values).  The moved rows' places
+// are found once, a thread a row; then, layer by layer, as many heads at a time as the
+// block's registers hold go through them, all their rows read before the first is written (a
+// row may be another's place).  A block has as many layers as leave eight blocks an SM:
+// finding the places is three waits for memory in a row.  64 sequences' rows in 36 layers, 113
+// MB: 23.3 us (one layer a block 25.5, a block a head, each finding the rows for itself, 59);
+// the rows' bytes take 17.
 __global__ void __launch_bounds__(KV16_KEEP_THREADS) kv16_keep_kernel(const Kv16KeepArgs a)
 {
     __shared__ long long from[KV16_MAX_NEW], to[KV16_MAX_NEW];  // in rows from the pool's start, of head 0
     __shared__ int moved;
     const int tid = threadIdx.x, lane = tid & 31, kv = blockIdx.x & 1;
     const uint32_t x = blockIdx.x >> 1;
-    const uint32_t b = fast_div(x, a.by_layers), layer = x - b * a.by_layers.d;
+    const uint32_t b = fast_div(x, a.by_groups), group = x - b * a.by_groups.d;
     if (tid < 32) {
         const int n = __ldg(a.n_path + b), past = __ldg(a.n_past + b);
+        int nodes[KV16_MAX_NEW / 32];
+#pragma unroll
+        for (int e = 0; e < KV16_MAX_NEW / 32; ++e)
+            nodes[e] = 32 * e + lane < a.max_new ? __ldg(a.path + static_cast<size_t>(b) * a.max_new + 32 * e + lane) : 0;
         const bool bad = n < 0 || n > a.max_new || past < 0;
         if (bad && lane == 0)
             set_error(a.err, DEVERR_BAD_ARG);
@@ -170,7 +188,7 @@ __global__ void __launch_bounds__(KV16_KEEP_THREADS) kv16_keep_kernel(const Kv16
             bool go = !bad && i < n;
             long long f = -1, t = -1;
             if (go) {
-                const int node = __ldg(a.path + static_cast<size_t>(b) * a.max_new + i);
+                const int node = nodes[e];
                 go = node != i;
                 if (go) {
                     if (node >= 0 && node < a.max_new)
@@ -197,26 +215,29 @@ __global__ void __launch_bounds__(KV16_KEEP_THREADS) kv16_keep_kernel(const Kv16
     const int n = moved;
     if (n == 0)
         return;
-    uint4* base = reinterpret_cast<uint4*>(a.pool + layer * a.layer);
     const int pieces = 16 * n, heads = KV16_KEEP_THREADS * KV16_KEEP_EACH / pieces;  // at a time
-    for (int h0 = 0; h0 < a.s.n_kv; h0 += heads) {
-        uint4 v[KV16_KEEP_EACH];
-        long long dst[KV16_KEEP_EACH];
+    const int last = min(a.n_layers, static_cast<int>(group + 1) * a.each);
+    for (int layer = static_cast<int>(group) * a.each; layer < last; ++layer) {
+        uint4* base = reinterpret_cast<uint4*>(a.pool + layer * a.layer);
+        for (int h0 = 0; h0 < a.s.n_kv; h0 += heads) {
+            uint4 v[KV16_KEEP_EACH];
+            long long dst[KV16_KEEP_EACH];
 #pragma unroll
-        for (int e = 0; e < KV16_KEEP_EACH; ++e) {
-            const int i = tid + e * KV16_KEEP_THREADS, h = i / pieces, row = (i - h * pieces) >> 4;
-            dst[e] = -1;
-            if (h < heads && h0 + h < a.s.n_kv) {
-                const long long head = static_cast<long long>(h0 + h) * a.s.page_rows;
-                v[e] = __ldcg(base + (from[row] + head) * 16 + (i & 15));
-                dst[e] = (to[row] + head) * 16 + (i & 15);
+            for (int e = 0; e < KV16_KEEP_EACH; ++e) {
+                const int i = tid + e * KV16_KEEP_THREADS, h = i / pieces, row = (i - h * pieces) >> 4;
+                dst[e] = -1;
+                if (h < heads && h0 + h < a.s.n_kv) {
+                    const long long head = static_cast<long long>(h0 + h) * a.s.page_rows;
+                    v[e] = __ldcg(base + (from[row] + head) * 16 + (i & 15));
+                    dst[e] = (to[row] + head) * 16 + (i & 15);
+                }
             }
-        }
-        __syncthreads();
+            __syncthreads();
 #pragma unroll
-        for (int e = 0; e < KV16_KEEP_EACH; ++e)
-            if (dst[e] >= 0)
-                base[dst[e]] = v[e];
+            for (int e = 0; e < KV16_KEEP_EACH; ++e)
+                if (dst[e] >= 0)
+                    base[dst[e]] = v[e];
+        }
     }
 }
 
@@ -285,9 +306,12 @@ DQ_API int dq_kv16_keep(void* pool, int type, const int* pages, const int* n_pas
         (reinterpret_cast<uintptr_t>(n_past) & 3) || (reinterpret_cast<uintptr_t>(path) & 3) ||
         (reinterpret_cast<uintptr_t>(n_path) & 3))
         return DQ_ERR_ALIGN;
-    const unsigned grid = static_cast<unsigned>(static_cast<long long>(n_seq) * n_layers * 2);
+    const long long each = std::min<long long>(n_layers, std::max(1ll, 2ll * n_seq * n_layers / (8ll * dqhost::sm_count())));
+    const int groups = static_cast<int>((n_layers + each - 1) / each);
+    const unsigned grid = static_cast<unsigned>(2ll * n_seq * groups);
     const dq::Kv16KeepArgs a{static_cast<unsigned char*>(pool), layer_stride, pages, n_past, path, n_path, max_new, max_pages,
-                             {n_kv, n_pages, page_size}, dqhost::fast_divisor(page_size), dqhost::fast_divisor(n_layers), dqhost::device_error_flag()};
+                             n_layers, static_cast<int>(each), {n_kv, n_pages, page_size}, dqhost::fast_divisor(page_size),
+                             dqhost::fast_divisor(groups), dqhost::device_error_flag()};
     dq::kv16_keep_kernel<<<grid, dq::KV16_KEEP_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? DQ_OK : dqhost::set_cuda_error(e);
