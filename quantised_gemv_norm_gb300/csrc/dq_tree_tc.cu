@@ -304,6 +304,16 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             if (!whole && live && ok && (PAIR || t == 0))
                 a.part_ml[at * R + rr] = make_float2(m, l);
             if (any) {
+                // the rows that this lane helps to write: those of its four, below
+                uint64_t to_row[4];
+                {
+                    const uint64_t mine_at = live && ok ? reinterpret_cast<uint64_t>(static_cast<T*>(a.out) + static_cast<long long>(row) * a.o_row +
+                                                                                     static_cast<long long>(g * a.group + head) * a.o_head)
+                                                        : 0ull;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        to_row[i] = __shfl_sync(0xffffffffu, mine_at, (lane & ~3) + i);
+                }
 #pragma unroll 1
                 for (int q = PAIR ? 0 : 2 * t; q < (PAIR ? 4 : 2 * t + 2); ++q) {
                     float o[32];
@@ -350,20 +360,36 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                         }
                         __syncwarp();
                     }
-                    if (!live || !ok)
-                        continue;
                     if (whole) {
-                        uint4* out = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + static_cast<long long>(row) * a.o_row +
-                                                              static_cast<long long>(g * a.group + head) * a.o_head + 32 * q);
+                        // 64 bytes of each row, in pieces of 16: four lanes trade theirs so that each has
+                        // one piece of four rows and a store fills whole sectors (a piece a lane and row
+                        // took four times the store's cycles)
+                        uint32_t w[4][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
+                        for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                w[e] = l == 0.f ? 0u : pack2(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv, static_cast<const T*>(nullptr));
-                            out[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
+                                w[i][e] = l == 0.f ? 0u : pack2(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv, static_cast<const T*>(nullptr));
+#pragma unroll
+                        for (int d = 1; d < 4; d *= 2)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (i & d)
+                                    continue;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & d ? w[i][e] : w[i + d][e], d);
+                                    if (lane & d)
+                                        w[i][e] = got;
+                                    else
+                                        w[i + d][e] = got;
+                                }
+                            }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (to_row[i])
+                                *reinterpret_cast<uint4*>(to_row[i] + 64 * q + 16 * (lane & 3)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+                    } else if (live && ok) {
                         float4* part = a.part + (at * 32 + 8 * q) * R + rr;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -610,18 +636,27 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                     __syncwarp();
                     uint8_t* vt = ring + here.s * TT_TILE;
                     const int key0 = (c.tile + j) * TT_KEYS;
+                    // 16-byte pieces of the rows from the first new key on, eight a row and panel
+                    const int row0 = max(0, c.t.past - key0), each = 8 * (TT_KEYS - row0);
                     bool seen = false;
-#pragma unroll 8
-                    for (int i = tid - 32 * TT_CLEAN_WARP; i < TT_TILE / 16; i += 64) {
-                        const int key = key0 + (i & 1023) / 8;  // a panel's rows are 8 of these
-                        if (key < c.t.past)
-                            continue;
-                        uint4 w = *reinterpret_cast<const uint4*>(vt + 16 * i);
-                        const uint32_t nx = tree_non_finite<T>(w.x), ny = tree_non_finite<T>(w.y), nz = tree_non_finite<T>(w.z),
-                                       nw = tree_non_finite<T>(w.w);
-                        if (nx | ny | nz | nw) {
-                            *reinterpret_cast<uint4*>(vt + 16 * i) = make_uint4(w.x & ~nx, w.y & ~ny, w.z & ~nz, w.w & ~nw);
-                            seen |= key < c.t.keys;
+                    for (int i0 = tid - 32 * TT_CLEAN_WARP; i0 < 2 * each; i0 += 64 * 8) {
+                        uint4 w[8];
+                        int at[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = min(i0 + 64 * e, 2 * each - 1), second = i >= each;
+                            at[e] = second * TT_PANEL + 16 * (8 * row0 + i - second * each);
+                            w[e] = *reinterpret_cast<const uint4*>(vt + at[e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t nx = tree_non_finite<T>(w[e].x), ny = tree_non_finite<T>(w[e].y),
+                                           nz = tree_non_finite<T>(w[e].z), nw = tree_non_finite<T>(w[e].w);
+                            if (nx | ny | nz | nw) {
+                                *reinterpret_cast<uint4*>(vt + at[e]) =
+                                    make_uint4(w[e].x & ~nx, w[e].y & ~ny, w[e].z & ~nz, w[e].w & ~nw);
+                                seen |= key0 + (at[e] % TT_PANEL) / 128 < c.t.keys;
+                            }
                         }
                     }
                     if (seen)
