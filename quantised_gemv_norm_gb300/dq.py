@@ -610,6 +610,20 @@ def kv16_pool(n_pages: int, n_kv: int, page_size: int, dtype=torch.float16, n_la
     return torch.zeros(shape if n_layers is None else (n_layers,) + shape, dtype=dtype, device=device or "cuda")
 
 
+_sizes: dict = {}
+
+
+def _size(fn, dev, *counts):
+    """A workspace's size, which goes by the counts and the device: asked for once."""
+    key = (fn, dev, *counts)
+    n = _sizes.get(key)
+    if n is None:
+        if len(_sizes) > 4096:
+            _sizes.clear()
+        n = _sizes[key] = getattr(_lib, fn)(*counts)
+    return n
+
+
 def _kv16(pool, dims=5):
     shape = pool.shape
     if len(shape) != dims or shape[dims - 4] != 2 or shape[-1] != 128 or not pool.is_contiguous():
@@ -682,10 +696,11 @@ def attention_tree(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tensor, n_p
     dtype = pool.dtype
     q_row, q_head = _rows("q", q, dtype)
     total, n_q, _ = q.shape
-    if pages.dim() != 2:
+    table = pages.shape
+    if len(table) != 2:
         raise ValueError("pages must be [n_seq, max_pages]")
-    n_seq, max_pages = pages.shape
-    _int32("pages", pages, (n_seq, max_pages))
+    n_seq, max_pages = table
+    _int32("pages", pages, table)
     _int32("n_past", n_past, (n_seq,))
     if cu_new is not None:
         _int32("cu_new", cu_new, (n_seq + 1,))
@@ -698,17 +713,19 @@ def attention_tree(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tensor, n_p
         max_new = each
     if seen is not None and (seen.dtype is not torch.int64 or seen.shape != (total,) or not seen.is_contiguous()):
         raise ValueError("seen must be a contiguous int64 tensor of shape (%d,)" % total)
+    dev = _device(q, pool, pages, n_past)
     if out is None:
-        out = torch.empty((total, n_q, 128), dtype=dtype, device=q.device)
+        out, o_row, o_head = torch.empty((total, n_q, 128), dtype=dtype, device=q.device), n_q * 128, 128
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    o_row, o_head = _rows("out", out, dtype)
-    dev = _device(q, pool, pages, n_past, out)
+    else:
+        o_row, o_head = _rows("out", out, dtype)
+        _device(out)
     if cu_new is not None:
         _device(cu_new)
     if seen is not None:
         _device(seen)
-    need = lib.dq_attention_tree_workspace_bytes(n_seq, max_new, n_q, n_kv) if workspace is None else 0
+    need = _size("dq_attention_tree_workspace_bytes", dev, n_seq, max_new, n_q, n_kv) if workspace is None else 0
     pw, nw, workspace = _scratch(workspace, need, q.device)
     d = _Tree(q.data_ptr(), out.data_ptr(), q_row, q_head, o_row, o_head, pool.data_ptr(), pages.data_ptr(),
               n_past.data_ptr(), None if cu_new is None else cu_new.data_ptr(), None if seen is None else seen.data_ptr(),
@@ -775,19 +792,22 @@ def verify_draft(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tens
     if temperature is not None:
         _float32("temperature", temperature, n_seq)
     t = _type(logits.dtype)
+    dev = _device(logits, tokens, uniform, noise)
+    for x in (cu_new, parents, draft_probs, temperature):
+        if x is not None:
+            _device(x)
     if out is None:
-        dev = logits.device
-        path = torch.empty((n_seq, max_new), dtype=torch.int32, device=dev)
-        n_path = torch.empty((n_seq,), dtype=torch.int32, device=dev)
-        after = torch.empty((n_seq,), dtype=torch.int32, device=dev)
+        where = logits.device
+        path = torch.empty((n_seq, max_new), dtype=torch.int32, device=where)
+        n_path = torch.empty((n_seq,), dtype=torch.int32, device=where)
+        after = torch.empty((n_seq,), dtype=torch.int32, device=where)
     else:
         path, n_path, after = out
         _int32("path", path, (n_seq, max_new))
         _int32("n_path", n_path, (n_seq,))
         _int32("next", after, (n_seq,))
-    dev = _device(logits, tokens, uniform, noise, path, n_path, after,
-                  *(x for x in (cu_new, parents, draft_probs, temperature) if x is not None))
-    need = lib.dq_verify_draft_workspace_bytes(total, vocab) if workspace is None else 0
+        _device(path, n_path, after)
+    need = _size("dq_verify_draft_workspace_bytes", dev, total, vocab) if workspace is None else 0
     pw, nw, workspace = _scratch(workspace, need, logits.device)
 
     def ptr(x):
