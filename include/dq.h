@@ -520,7 +520,7 @@ typedef struct {
 /* Errors: NULL -> DQ_ERR_NULL; a count < 1, n_q % n_kv, the type, page_size not a
  * multiple of 16, a stride < 128 where its count exceeds 1, total_new != n_seq * max_new
  * without cu_new, a workspace too small -> DQ_ERR_SHAPE; head_dim != 128, max_new > 64,
- * n_q / n_kv > 64, total_new or max_pages * page_size > 2^30, n_seq * n_kv >= 2^24, 2^31
+ * n_q / n_kv > 64, total_new or max_pages * page_size > 2^30, n_seq * n_kv >= 2^24, 2^30
  * tiles of work or more (n_seq * n_kv * max_pages * page_size / 64 and the like), a
  * pool as in dq_kv16_append -> DQ_ERR_UNSUPPORTED; strides not multiples of 8, a pointer
  * not 16-byte aligned -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                 const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
                 // lane i has the page of box `first + i`, and of box `first + 32 + i`
                 auto page_of = [&](int x) {
-                    return static_cast<long long>(x) * box < c.t.keys ? __ldg(pages + fast_div(x, a.by_boxes)) : 0;
+                    return static_cast<long long>(x) * box < c.t.keys ? __ldcg(pages + fast_div(x, a.by_boxes)) : 0;
                 };
                 int first = c.tile, now = page_of(first * per_tile + lane), then = page_of((first + ahead) * per_tile + lane);
                 const int end = c.end();
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                         now = then;
                         then = page_of((first + ahead) * per_tile + lane);
                     }
-                    const int page = __shfl_sync(0xffffffffu, now, (k - first) * per_tile + lane & 31);
+                    const int page = __shfl_sync(0xffffffffu, now, ((k - first) * per_tile + lane) & 31);
                     const int x = k * per_tile + lane;
                     const bool mine = lane < per_tile && static_cast<long long>(x) * box < c.t.keys;
                     const bool there = mine && page >= 0 && page < a.s.n_pages;
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                     const int row = t.row0 + (live[h] ? node : 0);
                     qp[h] = static_cast<const T*>(a.q) + static_cast<long long>(row) * a.q_row +
                             static_cast<long long>(g * a.group + r - node * a.group) * a.q_head;
-                    seen[h] = !live[h] ? 0ull : a.seen ? __ldg(a.seen + row) : (2ull << node) - 1;
+                    seen[h] = !live[h] ? 0ull : a.seen ? __ldcg(a.seen + row) : (2ull << node) - 1;
                     if (t.rows < 64)
                         seen[h] &= (1ull << t.rows) - 1;
                 }
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            q[k][h + 2 * e] = live[h] ? __ldg(reinterpret_cast<const uint32_t*>(qp[h] + 16 * k + 8 * e + 2 * q4)) : 0u;
+                            q[k][h + 2 * e] = live[h] ? __ldcg(reinterpret_cast<const uint32_t*>(qp[h] + 16 * k + 8 * e + 2 * q4)) : 0u;
                 float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                             const int node = k * TM_KEYS + wk * NK + key - t.past;
                             if (node < 0 || node >= t.rows || (absent >> ((wk * NK + key) / 16) & 1))
                                 continue;
-                            const int first = wk * NK + key & ~15, b = first / a.box;
+                            const int first = (wk * NK + key) & ~15, b = first / a.box;
                             const uint32_t at = b * a.box * 256 + (first - b * a.box + (key & 15)) * 128;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
 }
 
 // Items that several blocks had a part of.  A unit of work is 32 lanes' rows (of 16-row
-// items: their rows twice, the next four dims) and four dims each, over all the blocks' sums.
+// items: their rows twice, the next eight dims) and eight dims each, over all the blocks' sums.
 // P = 1: one row of the grid a block of the first kernel, which has left the item that it
 // began and did not end, and a warp a unit.  Where items are few and each had many blocks,
 // one row an item, whose blocks are worked out while the first kernel still runs, and P warps
@@ -463,6 +463,7 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
             total += __reduce_add_sync(0xffffffffu, u);
         }
         c.load(a, s);
+        pdl_wait();  // before any return: this kernel ends after the first one
         if (item >= a.s.n_kv * c.row_tiles)
             return;
         const int each = tree_each(a, total), start = before + item * c.tiles;
@@ -470,7 +471,6 @@ __global__ void __launch_bounds__(32 * TJ_WARPS) tree_join_kernel(const __grid_c
         j = TreeShared{c.t.row0, c.t.rows, item / c.row_tiles, item % c.row_tiles, (start + c.tiles - 1) / each};
         if (j.last == b)
             return;
-        pdl_wait();
         if (__ldcg(&a.join[b].last) < 0)
             return;  // a wait ran out
     }
@@ -662,10 +662,10 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         return DQ_ERR_SHAPE;
     const int group = t->n_q / t->n_kv;
     const dqhost::TreeCut cut = dqhost::tree_cut(t->max_new, group);
-    // units of work, at most
+    // units of work, at most: they are counted in 32 bits
     const long long tile = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS, tiles = (static_cast<long long>(t->max_pages) * t->page_size + tile - 1) / tile;
     const long long row_tiles = (static_cast<long long>(t->max_new) * group + cut.rows - 1) / cut.rows + 1;
-    if (tiles * row_tiles > 0x7fffffffll / (static_cast<long long>(t->n_seq) * t->n_kv))
+    if (tiles * row_tiles > (1 << 30) / (static_cast<long long>(t->n_seq) * t->n_kv))
         return DQ_ERR_UNSUPPORTED;
     int box = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS;  // rows of a copy: what divides a tile and a page
     while (t->page_size % box)

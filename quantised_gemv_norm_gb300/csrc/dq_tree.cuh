@@ -46,18 +46,20 @@ struct TreeSeq {
     bool bad;
 };
 
+// Loads of inputs go past L1, here and in the kernels: a dependent launch may have started
+// before they were written.
 __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s)
 {
     TreeSeq t;
     int r1;
     if (a.cu_new) {
-        t.row0 = __ldg(a.cu_new + s);
-        r1 = __ldg(a.cu_new + s + 1);
+        t.row0 = __ldcg(a.cu_new + s);
+        r1 = __ldcg(a.cu_new + s + 1);
     } else {
         t.row0 = s * a.max_new;
         r1 = t.row0 + a.max_new;
     }
-    t.past = __ldg(a.n_past + s);
+    t.past = __ldcg(a.n_past + s);
     const bool in_order = t.row0 >= 0 && r1 >= t.row0 && r1 <= a.total_new && r1 - t.row0 <= a.max_new;
     t.rows = in_order ? r1 - t.row0 : 0;
     const bool fits = t.past >= 0 && static_cast<long long>(t.past) + t.rows <= a.room;
@@ -78,7 +80,7 @@ __device__ __forceinline__ int tree_each(const TreeArgs& a, int total)
 // The work is counted in units: one key tile of one item, an item being a row tile of one
 // sequence and KV head.  Sequence by sequence, item by item, tile by tile they are one
 // long row, of which every block takes an equal stretch; a stretch is cut into segments
-// where items change.  The host has seen that the units are fewer than 2^31.
+// where items change.  The host has seen that the units are fewer than 2^30.
 template <int R, int KT>
 struct TreeCursor {
     TreeSeq t;

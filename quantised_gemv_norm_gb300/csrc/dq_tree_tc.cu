@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
             int node = c.rt * a.nodes + (PAIR ? t * tokens : 0) + token;
             bool live = token < tokens && node < c.t.rows;
             int row = c.t.row0 + node;
-            uint64_t seen = !live || c.t.keys == 0 ? 0ull : a.seen ? __ldg(a.seen + row) : (2ull << node) - 1;
+            uint64_t seen = !live || c.t.keys == 0 ? 0ull : a.seen ? __ldcg(a.seen + row) : (2ull << node) - 1;
             if (c.t.rows < 64)
                 seen &= (1ull << c.t.rows) - 1;
             const bool any = __any_sync(0xffffffffu, live);
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                         // new tokens' infinities and NaNs, which the products left out, to the rows that see them
                         const int last = min(c.t.keys, end * TT_KEYS);
                         for (int key = max(c.t.past, c.tile * TT_KEYS); key < last; ++key) {
-                            const int page = __ldg(a.pages + static_cast<size_t>(c.s) * a.max_pages + key / a.s.page_rows);
+                            const int page = __ldcg(a.pages + static_cast<size_t>(c.s) * a.max_pages + key / a.s.page_rows);
                             if (page < 0 || page >= a.s.n_pages || !(seen >> (key - c.t.past) & 1))
                                 continue;
                             const uint4* vp = reinterpret_cast<const uint4*>(
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(TT_THREADS, 1) tree_tc_kernel(const __grid_con
                 const int* pages = a.pages + static_cast<size_t>(c.s) * a.max_pages;
                 // lane i has the page of box `first + i`, and of box `first + 32 + i`
                 auto page_of = [&](int x) {
-                    return static_cast<long long>(x) * box < c.t.keys ? __ldg(pages + fast_div(x, a.by_boxes)) : 0;
+                    return static_cast<long long>(x) * box < c.t.keys ? __ldcg(pages + fast_div(x, a.by_boxes)) : 0;
                 };
                 const int from_new = c.t.keys ? c.t.past / TT_KEYS : 0;
                 int first = c.tile, now = page_of(first * boxes + lane), then = page_of((first + ahead) * boxes + lane);

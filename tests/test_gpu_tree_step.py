@@ -259,7 +259,8 @@ def test_attention(dq, case, dtype):
 
 
 @pytest.mark.parametrize("n_seq,max_new,n_q,n_kv,page,longest", [(70, 1, 8, 2, 32, 400), (40, 5, 4, 2, 16, 300),
-                                                                 (300, 2, 2, 1, 16, 40), (9, 64, 4, 1, 64, 500)])
+                                                                 (300, 2, 2, 1, 16, 40), (9, 64, 4, 1, 64, 500),
+                                                                 (150, 20, 4, 2, 16, 60), (40, 40, 8, 2, 32, 200)])
 def test_attention_of_batches(dq, n_seq, max_new, n_q, n_kv, page, longest):
     rng = random.Random(n_seq)
     new = [rng.randint(0, max_new) for _ in range(n_seq)]
@@ -355,28 +356,53 @@ def test_rows_of_no_sequence_and_strides(dq):
     assert torch.equal(again, out[1:6])
 
 
-def test_bad_tables_are_reported(dq):
+@pytest.mark.parametrize("new", [1, 8, 40])  # the kernels of few rows, of one and of two query tiles
+def test_bad_tables_are_reported(dq, new):
     g = gen(31)
     page = 16
-    pool = randn(g, 8, 2, 1, page, HD, dtype=F16)
-    pages = i32([[0, 1, 2], [3, 99, 4], [5, 6, 7]])
-    q = randn(g, 3, 4, HD, dtype=F16)
-    ref, mag = reference(q, pool, pages, [40, 40, 40], [1, 1, 1], [1, 1, 1])
-    out = dq.attention_tree(q, pool, pages, i32([40, 40, 40]))
+    past, rows = 200 - new, 3 * new
+    n_pages = 40
+    pool = randn(g, n_pages, 2, 1, page, HD, dtype=F16)
+    order = torch.randperm(39, device="cuda", generator=g).int()
+    good = order.reshape(3, 13)
+    bad = good.clone()
+    bad[1, 1], bad[1, 9], bad[2, 4] = 99, -2, 2 ** 31 - 1
+    pool[39] = float("nan")  # a page of nobody
+    q = randn(g, rows, 4, HD, dtype=F16)
+    ref, mag = reference(q, pool, bad, [past] * 3, [new] * 3, chain_masks([new] * 3))
+    out = dq.attention_tree(q, pool, bad, i32([past] * 3))
     assert dq.device_error() == BAD_ARG
     within(out, ref, (U[F16] + 4e-5) * mag)  # a bad page's keys take no part
-    for past in ([40, -1, 40], [40, 48, 40], [40, 2 ** 31 - 1, 40]):
-        out = dq.attention_tree(q, pool, i32([[0, 1, 2], [3, 0, 4], [5, 6, 7]]), i32(past))
+    ref, mag = reference(q, pool, good, [past] * 3, [new] * 3, chain_masks([new] * 3))
+    for value in (-1, 13 * page - new + 1, 2 ** 31 - 1, -2 ** 31):
+        out = dq.attention_tree(q, pool, good, i32([past, value, past]))
         assert dq.device_error() == BAD_ARG
-        assert bool((out[1] == 0).all())
-        within(out[[0, 2]], ref[[0, 2]], (U[F16] + 4e-5) * mag[[0, 2]])
-    for cu in ([0, 5, 2, 3], [-1, 1, 2, 3], [0, 1, 2, 2 ** 31 - 1], [2, 1, 0, 3]):
+        assert bool((out[new:2 * new] == 0).all())
+        others = torch.cat([torch.arange(new), torch.arange(2 * new, rows)]).cuda()
+        within(out[others], ref[others], (U[F16] + 4e-5) * mag[others])
+    for cu in ([0, 5 * new, 2 * new, rows], [-1, new, 2 * new, rows], [0, new, 2 * new, 2 ** 31 - 1], [2 * new, new, 0, rows]):
         keep = torch.full_like(q, 3.0)
-        dq.attention_tree(q, pool, i32([[0, 1, 2], [3, 0, 4], [5, 6, 7]]), i32([40, 40, 40]), cu_new=i32(cu), max_new=2, out=keep)
+        dq.attention_tree(q, pool, good, i32([past] * 3), cu_new=i32(cu), max_new=new, out=keep)
         assert dq.device_error() == BAD_ARG
-        for s, (a, b) in enumerate(zip(cu, cu[1:])):
-            if a == s and b == s + 1:
-                within(keep[s:s + 1], ref[s:s + 1], (U[F16] + 4e-5) * mag[s:s + 1]) if s != 1 else None
+        for s in range(3):
+            if cu[s] == s * new and cu[s + 1] == cu[s] + new:
+                at = slice(cu[s], cu[s + 1])
+                within(keep[at], ref[at], (U[F16] + 4e-5) * mag[at])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_with_whole_segments_of_absent_pages(dq, dtype):
+    """Sequences all of whose past pages are outside the pool, beside healthy ones."""
+    g = gen(33)
+    page, new, past = 32, 20, 416
+    pool = randn(g, 30, 2, 2, page, HD, dtype=dtype)
+    pages = torch.arange(28, device="cuda", dtype=torch.int32).reshape(2, 14)
+    pages[1, :13] = 1000
+    q = randn(g, 2 * new, 8, HD, dtype=dtype)
+    out = dq.attention_tree(q, pool, pages, i32([past, past]))
+    assert dq.device_error() == BAD_ARG
+    ref, mag = reference(q, pool, pages, [past, past], [new, new], chain_masks([new, new]))
+    within(out, ref, (U[dtype] + 4e-5) * mag)
 
 
 def test_a_pool_past_32_bit_offsets(dq):
