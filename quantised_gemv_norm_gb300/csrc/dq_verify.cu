@@ -489,13 +489,22 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
     const float z = static_cast<float>(sh.sum[last]);
     const uint64_t minus = f2(-top.v, -top.v);
     const bool infinite = isinf(top.v);
+    const bool vec = !((reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) | (reinterpret_cast<uintptr_t>(noise) & 15) |
+                       (reinterpret_cast<uintptr_t>(draft) & 15));
+    const int v4 = vec ? v0 + (max(0, v1 - v0) & ~3) : v0;
+    // whether a rejected token is among this thread's places: few threads have to look each place up
+    bool careful = false;
+    for (int k = 0; k < n_gone; ++k) {
+        const int v = sh.gone[k];
+        careful |= v >= v0 && v < v1 && (v < v4 ? (v - v0) / 4 % VF_PICK == tid : (v - v4) % VF_PICK == tid);
+    }
     Best best{0.f, -1};
     auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int v) {
         float2 p = un2(verify_exp2(f2(x, y), minus, c));
         if (infinite)
             p = make_float2(x == top.v ? 1.f : 0.f, y == top.v ? 1.f : 0.f);
         const float sx = __fdividef(fmaf(-z, qx, p.x), ex), sy = __fdividef(fmaf(-z, qy, p.y), ey);
-        if (n_gone) {
+        if (careful) {
             for (int e = 0; e < 2; ++e) {
                 if (!((e ? sy : sx) > best.v))
                     continue;
@@ -512,9 +521,6 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
             best.v = fmaxf(sy, best.v);
         }
     };
-    const bool vec = !((reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) | (reinterpret_cast<uintptr_t>(noise) & 15) |
-                       (reinterpret_cast<uintptr_t>(draft) & 15));
-    const int v4 = vec ? v0 + (max(0, v1 - v0) & ~3) : v0;
     constexpr int N = VF_BATCH / 4;
     for (int b0 = v0 + 4 * tid; b0 < v4; b0 += 4 * VF_PICK * N) {
         float4 x[N], e[N], d[N];
