@@ -335,25 +335,66 @@ def test_scores_far_from_zero(dq, dtype, size, new):
         within(out, ref, (U[dtype] + 4e-5 + 4 * off) * mag)
 
 
-def test_rows_of_no_sequence_and_strides(dq):
+@pytest.mark.parametrize("new", [[3, 2], [20, 9], [64, 33]])
+def test_rows_of_no_sequence_and_strides(dq, new):
     g = gen(21)
     page, n_kv, n_q = 32, 2, 8
-    past, new = [40, 7], [3, 2]
-    pages, total = tables([43, 9], page)
-    pool = randn(g, total, 2, n_kv, page, HD, dtype=BF16)
-    wide = randn(g, 8, n_q + 4, 2 * HD, dtype=BF16)
+    total = sum(new) + 3
+    past = [160 - new[0], 7]  # the first sequence fills its pages to the last row
+    pages, n_pages = tables([a + b for a, b in zip(past, new)], page)
+    assert pages.shape[1] * page == past[0] + new[0]
+    pool = randn(g, n_pages, 2, n_kv, page, HD, dtype=BF16)
+    wide = randn(g, total, n_q + 4, 2 * HD, dtype=BF16)
     q = wide[:, 2:2 + n_q, :HD]
-    out_wide = randn(g, 8, n_q, HD + 8, dtype=BF16)
+    out_wide = randn(g, total, n_q, HD + 8, dtype=BF16)
     before = out_wide.clone()
     out = out_wide[..., :HD]
-    dq.attention_tree(q, pool, pages, i32(past), cu_new=i32([1, 4, 6]), max_new=4, out=out)
-    ref, mag = reference(q[1:6], pool, pages, past, new, chain_masks(new))
-    within(out[1:6], ref, (U[BF16] + 4e-5) * mag)
-    assert torch.equal(out_wide[0], before[0]) and torch.equal(out_wide[6:], before[6:])
+    first, last = 1, 1 + sum(new)
+    dq.attention_tree(q, pool, pages, i32(past), cu_new=i32([1, 1 + new[0], last]), max_new=max(new), out=out)
+    ref, mag = reference(q[first:last], pool, pages, past, new, chain_masks(new))
+    within(out[first:last], ref, (U[BF16] + 4e-5) * mag)
+    assert torch.equal(out_wide[0], before[0]) and torch.equal(out_wide[last:], before[last:])
     assert torch.equal(out_wide[..., HD:], before[..., HD:])
-    again = q[1:6].contiguous()  # in place
-    dq.attention_tree(again, pool, pages, i32(past), cu_new=i32([0, 3, 5]), max_new=4, out=again)
-    assert torch.equal(again, out[1:6])
+    again = q[first:last].contiguous()  # in place
+    dq.attention_tree(again, pool, pages, i32(past), cu_new=i32([0, new[0], sum(new)]), max_new=max(new), out=again)
+    assert torch.equal(again, out[first:last])
+
+
+@pytest.mark.parametrize("new", [1, 8, 40])
+def test_a_captured_step_after_copies(dq, new):
+    """Lengths and queries written by a copy and by a kernel of the same graph directly before the attention, the output
+    read by one directly after it."""
+    g = gen(23)
+    page, n_kv, n_q, n_seq = 32, 2, 8, 3
+    pages, total = tables([300] * n_seq, page)
+    pool = randn(g, total, 2, n_kv, page, HD, dtype=F16)
+    given_q, given_past = randn(g, n_seq * new, n_q, HD, dtype=F16), i32([0, 0, 0])
+    q, n_past = torch.empty_like(given_q), i32([0, 0, 0])
+    out, twice = torch.empty_like(q), torch.empty_like(q)
+    ws = dq.attention_tree_workspace(n_seq, new, n_q, n_kv)
+
+    def step():
+        torch.mul(given_q, 1.0, out=q)
+        n_past.copy_(given_past)
+        dq.attention_tree(q, pool, pages, n_past, workspace=ws, out=out)
+        torch.mul(out, 2.0, out=twice)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            step()
+    for past in ([5, 200, 0], [250, 1, 64], [0, 0, 259]):
+        given_past.copy_(i32(past))
+        given_q.copy_(randn(g, *q.shape, dtype=F16))
+        graph.replay()
+        ref, mag = reference(given_q, pool, pages, past, [new] * n_seq, chain_masks([new] * n_seq))
+        within(out, ref, (U[F16] + 4e-5) * mag)
+        assert torch.equal(twice, out * 2)
 
 
 @pytest.mark.parametrize("new", [1, 8, 40])  # the kernels of few rows, of one and of two query tiles
@@ -686,9 +727,22 @@ def test_verify_reports_bad_trees(dq):
                 assert path[s].tolist() == [-1] * 4 and after[s].item() == -1
 
 
-def test_verify_strides_and_streams(dq):
+def test_verify_leaves_rows_of_no_sequence(dq):
+    """Logits before the first and after the last sequence have no part in anything, NaN or not."""
+    g, vocab = gen(10), 4100
+    logits = peaked(g, 9, vocab)
+    logits[0], logits[7:] = float("nan"), float("inf")
+    tokens, uniform, noise = logits.argmax(1).int(), torch.rand(9, device="cuda", generator=g), exponential(g, 2, vocab)
+    path, n_path, after = dq.verify_draft(logits, tokens, uniform, noise, cu_new=i32([1, 5, 7]), max_new=6)
+    paths, want = verify_reference(logits[1:7], tokens[1:7], uniform[1:7], noise, [4, 2])
+    assert after.tolist() == want and n_path.tolist() == [len(p) for p in paths]
+    assert path.tolist() == [p + [-1] * (6 - len(p)) for p in paths]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_verify_strides_and_streams(dq, dtype):
     g, vocab = gen(8), 10007
-    wide = peaked(g, 12, vocab + 9)
+    wide = peaked(g, 12, vocab + 9, dtype)
     logits = wide[:, 3:3 + vocab]  # rows of any alignment
     q = torch.softmax(randn(g, 12, vocab + 1), -1)[:, :vocab]
     tokens = torch.multinomial(q, 1, generator=g)[:, 0].int()
