@@ -98,6 +98,14 @@ __device__ __forceinline__ float verify_exp(float x, float m, const VerifyScale&
     return x == m ? 1.f : isinf(m) ? 0.f : fmaf(w, e * 0.6931471805599453f, w);
 }
 
+// The warp's largest, in one instruction.
+__device__ __forceinline__ float verify_warp_max(float x)
+{
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 struct Best {
     float v;
     int at;  // -1: none
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
 #pragma unroll
         for (int i = 0; i < VF_EACH; ++i)
             m4[i & 3] = fmaxf(m4[i & 3], x[i]);  // NaN is passed over
-        const float m = warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+        const float m = verify_warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         if (m > top.v) {  // the same in the whole warp
             int at = 0x7fffffff;
 #pragma unroll
@@ -642,18 +650,31 @@ static cudaError_t verify_prepare(K kernel, bool (&done)[64])
     return e;
 }
 
-// How the first kernel cuts a row: into pieces of so many steps that the card has two
-// rounds of blocks, five an SM, to do (a row may begin up to 7 elements into its first 16
-// bytes).
+// How the first kernel cuts a row (which may begin up to 7 elements into its first 16
+// bytes): into the number of pieces whose rounds of blocks, four an SM with 16-bit logits
+// and five with fp32 ones, take the fewest steps, a block's start and end counted as one and
+// a half of them (405 rows of 100003 in bf16: 24.5 us; 27.5 with pieces of six steps, whose
+// 2025 blocks are three rounds and a third).
 struct VerifyCut {
     int pieces, steps;
 };
-static VerifyCut verify_cut(int total_new, int vocab)
+static VerifyCut verify_cut(int total_new, int vocab, bool wide)
 {
     const int all = (vocab + 7 + dq::VF_STEP - 1) / dq::VF_STEP;
-    const long long steps = std::min<long long>(16, std::max(1ll, static_cast<long long>(total_new) * all / (10ll * sm_count())));
-    const int pieces = static_cast<int>((all + steps - 1) / steps);
-    return {pieces, (all + pieces - 1) / pieces};
+    const long long slots = (wide ? 5ll : 4ll) * sm_count();
+    VerifyCut best{1, all};
+    double least = 0.0;
+    for (int p = 1; p <= std::min(all, 64); ++p) {
+        const int steps = (all + p - 1) / p;
+        if ((all + steps - 1) / steps != p)
+            continue;  // as many steps as with fewer pieces
+        const double cost = static_cast<double>((total_new * static_cast<long long>(p) + slots - 1) / slots) * (steps + 1.5);
+        if (p == 1 || cost < least) {
+            least = cost;
+            best = {p, steps};
+        }
+    }
+    return best;
 }
 
 }  // namespace dqhost
@@ -664,7 +685,8 @@ DQ_API size_t dq_verify_draft_workspace_bytes(int total_new, int vocab)
 {
     if (total_new < 1 || vocab < 1 || total_new > (1 << 24) || vocab > (1 << 24))
         return 0;
-    return static_cast<size_t>(total_new) * dqhost::verify_cut(total_new, vocab).pieces * sizeof(float4);
+    const int pieces = std::max(dqhost::verify_cut(total_new, vocab, false).pieces, dqhost::verify_cut(total_new, vocab, true).pieces);
+    return static_cast<size_t>(total_new) * pieces * sizeof(float4);
 }
 
 DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
@@ -691,7 +713,7 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
         return DQ_ERR_ALIGN;
     if (v->workspace_bytes < dq_verify_draft_workspace_bytes(v->total_new, v->vocab))
         return DQ_ERR_SHAPE;
-    const dqhost::VerifyCut cut = dqhost::verify_cut(v->total_new, v->vocab);
+    const dqhost::VerifyCut cut = dqhost::verify_cut(v->total_new, v->vocab, v->type == DQ_TYPE_F32);
     const dq::VerifyArgs a{v->logits, v->logits_stride, v->draft_probs, v->draft_stride, v->noise, v->noise_stride,
                            v->tokens, v->parents, v->uniform, v->temperature, v->cu_new, v->path, v->n_path, v->next,
                            v->n_seq, v->total_new, v->max_new, v->vocab, cut.pieces, cut.steps, static_cast<float4*>(v->workspace),

@@ -129,7 +129,9 @@ def test_workspace_sizes(lib):
     assert lib.dq_attention_tree_workspace_bytes(1, 4, 32, 8) > 0
     assert lib.dq_verify_draft_workspace_bytes(0, 100) == 0
     assert lib.dq_verify_draft_workspace_bytes(3, 0) == 0
-    assert lib.dq_verify_draft_workspace_bytes(3, 8193) >= 3 * 2 * 16
+    n = lib.dq_verify_draft_workspace_bytes(3, 8193)
+    assert n >= 3 * 16 and n % 48 == 0
+    assert lib.dq_verify_draft_workspace_bytes(6, 8193) <= 2 * n
 
 
 def test_binding_refuses_shapes_and_types():
