@@ -8,7 +8,18 @@
 // by four warps, a row a thread, back over S in 16 bits, O += P V in tensor memory.  Two
 // such chains t = 0, 1 run side by side, so that the products of one meet the exponentials
 // of the other: with two query tiles (PAIR) a chain each, on the same keys; with one, the
-// even and the odd key tiles, whose sums meet at the end of a segment.
+// even and the odd key tiles, whose sums meet at the end of a segment.  A tile of 128 keys is
+// 64 KB, 2900 clocks of a SM's share of the memory's rate; its products take 1024 clocks for
+// one query tile, 2048 for two: the memory bounds both while the ring has enough on its way.
+//
+// One sequence of 16 tokens after 100001 keys, 410 MB: 73 us (floor 61: 4 us until the first
+// scores, 3 for partial sums, 4 for their join); 32 sequences of up to 8 after up to 12000, 769
+// MB: 137 us (115); 8 of 64 after up to 16000, 371 MB, 92 GFLOP: 86 us (56), DRAM 58% and
+// matrix pipe 47% busy.  Beside starts and ends, each segment costs two query tiles a drain
+// of the chains and 2.4 us to hand over partial sums (128 KB a block).  Tried and not kept:
+// keys and values asked into L2 four tiles ahead (8 of 64: 93 -> 107 us), the next item's
+// tiles copied before its queries (32 sequences 136 -> 138 us), ring tiles of one query tile in
+// the order K0 V0 K1 V1 (84 us for the first case, 78 in the order of their use).
 #include <mutex>
 
 #include "dq_tc.cuh"

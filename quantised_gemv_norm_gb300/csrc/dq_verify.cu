@@ -1,18 +1,26 @@
 // dq_verify.cu -- drafted tokens against the target's logits (dq_verify_draft).
 //
-// Two kernels.  The first reads every node's logits once, in pieces of 8192: a piece's
+// Two kernels.  The first reads every node's logits once, in pieces of a row: a piece's
 // largest logit with its lowest place, and the sum of exp((l - largest) / temperature).
-// The second, a cluster of eight blocks a sequence, joins the pieces, walks the tree
-// over numbers that are all in shared memory by then (a node's probability needs its
-// parent's logits at one place and their sum), and looks for the next token: one pass
-// over one node's logits, the random numbers and, for a rejected token of a chain, the
-// draft's probabilities.
+// The second, a cluster of up to 16 blocks a sequence, joins the pieces, tests every node as
+// if its turn came (a node's probability needs its parent's logits at one place and their
+// sum; all its siblings before it were rejected then), walks from the root along the nodes
+// that passed, and looks for the next token: one pass over one node's logits, the random
+// numbers and, for a rejected token of a chain, the draft's probabilities.
 //
 // The next token is the largest r(v) / noise(v) instead of the place where a cumulated
 // sum passes one random number: of 10^5 such places some lie within the rounding of any
 // 32-bit sum, where two ratios are seldom that close.  The pass runs in fp32; every
 // thread whose best is within 1e-5 of the largest computes that one ratio again in
-// 64 bits, and those decide.
+// 64 bits, and those decide (where only one is near, nothing is computed again).
+//
+// 64 sequences of up to 9 nodes, 151936 fp32 logits each, 193 MB and 78 MB of random numbers
+// and draft probabilities: 52 us (floor 40): 32 us the first kernel (6.0 TB/s), the rest the
+// pass (13 us, the same memory) and the second kernel's steps.  405 nodes of 100003 bf16
+// logits in 16 trees: 39 us (13): the first kernel 24 us, 3.4 TB/s, bound by a step's chain of
+// instructions at four blocks an SM (about 8 instructions a logit; issue 0.5 of its rate).
+// One sequence of 6: 11.6 us: 2.5 the first kernel, then waits for memory in a row (lengths,
+// tokens, their logits; sums; two rounds of the pass) and two meetings of the cluster.
 #include <cooperative_groups.h>
 
 #include <algorithm>
