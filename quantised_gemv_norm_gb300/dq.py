@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -678,6 +679,15 @@ class _Tree(ctypes.Structure):
                 + [("workspace", P), ("workspace_bytes", SZ)])
 
 
+def _packer(cls):
+    """The description as bytes, which cost half of what filling the structure does; a null pointer is 0."""
+    code = {P: "P", LL: "q", I: "i", SZ: "N"}
+    return struct.Struct("@" + "".join(code[t] for _, t in cls._fields_)).pack
+
+
+_pack_tree = _packer(_Tree)
+
+
 def attention_tree_workspace(n_seq: int, max_new: int, n_q: int, n_kv: int, device=None):
     """Scratch for attention_tree calls of these counts, whatever the lengths."""
     n = load().dq_attention_tree_workspace_bytes(n_seq, max_new, n_q, n_kv)
@@ -727,10 +737,10 @@ def attention_tree(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tensor, n_p
         _device(seen)
     need = _size("dq_attention_tree_workspace_bytes", dev, n_seq, max_new, n_q, n_kv) if workspace is None else 0
     pw, nw, workspace = _scratch(workspace, need, q.device)
-    d = _Tree(q.data_ptr(), out.data_ptr(), q_row, q_head, o_row, o_head, pool.data_ptr(), pages.data_ptr(),
-              n_past.data_ptr(), None if cu_new is None else cu_new.data_ptr(), None if seen is None else seen.data_ptr(),
-              _TYPES[dtype], n_seq, total, max_new, n_q, n_kv, 128, n_pages, page, max_pages, pw, nw)
-    st = lib.dq_attention_tree(ctypes.addressof(d), _raw_stream(dev))
+    d = _pack_tree(q.data_ptr(), out.data_ptr(), q_row, q_head, o_row, o_head, pool.data_ptr(), pages.data_ptr(),
+                   n_past.data_ptr(), 0 if cu_new is None else cu_new.data_ptr(), 0 if seen is None else seen.data_ptr(),
+                   _TYPES[dtype], n_seq, total, max_new, n_q, n_kv, 128, n_pages, page, max_pages, pw or 0, nw)
+    st = lib.dq_attention_tree(d, _raw_stream(dev))
     if st:
         raise DQError("dq_attention_tree", st)
     return out
@@ -742,6 +752,9 @@ class _Verify(ctypes.Structure):
                 + [(n, P) for n in ("tokens", "parents", "uniform", "temperature", "cu_new", "path", "n_path", "next")]
                 + [(n, I) for n in ("type", "n_seq", "total_new", "max_new", "vocab")]
                 + [("workspace", P), ("workspace_bytes", SZ)])
+
+
+_pack_verify = _packer(_Verify)
 
 
 def verify_draft_workspace(total_new: int, vocab: int, device=None):
@@ -810,13 +823,12 @@ def verify_draft(logits: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tens
     need = _size("dq_verify_draft_workspace_bytes", dev, total, vocab) if workspace is None else 0
     pw, nw, workspace = _scratch(workspace, need, logits.device)
 
-    def ptr(x):
-        return None if x is None else x.data_ptr()
-
-    d = _Verify(logits.data_ptr(), logits.stride(0) if total > 1 else vocab, ptr(draft_probs), draft_stride,
-                noise.data_ptr(), noise_stride, tokens.data_ptr(), ptr(parents), uniform.data_ptr(), ptr(temperature),
-                ptr(cu_new), path.data_ptr(), n_path.data_ptr(), after.data_ptr(), t, n_seq, total, max_new, vocab, pw, nw)
-    st = lib.dq_verify_draft(ctypes.addressof(d), _raw_stream(dev))
+    d = _pack_verify(logits.data_ptr(), logits.stride(0) if total > 1 else vocab,
+                     0 if draft_probs is None else draft_probs.data_ptr(), draft_stride, noise.data_ptr(), noise_stride,
+                     tokens.data_ptr(), 0 if parents is None else parents.data_ptr(), uniform.data_ptr(),
+                     0 if temperature is None else temperature.data_ptr(), 0 if cu_new is None else cu_new.data_ptr(),
+                     path.data_ptr(), n_path.data_ptr(), after.data_ptr(), t, n_seq, total, max_new, vocab, pw or 0, nw)
+    st = lib.dq_verify_draft(d, _raw_stream(dev))
     if st:
         raise DQError("dq_verify_draft", st)
     return path, n_path, after

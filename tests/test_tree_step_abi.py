@@ -176,6 +176,16 @@ def test_binding_refuses_shapes_and_types():
             dq.kv16_keep(**a)
 
 
+@pytest.mark.parametrize("name", ["_Tree", "_Verify"])
+def test_packed_descriptions_are_the_structures(name):
+    from quantised_gemv_norm_gb300 import dq
+
+    cls, pack = getattr(dq, name), {"_Tree": dq._pack_tree, "_Verify": dq._pack_verify}[name]
+    values = [1000 + 7 * i for i in range(len(cls._fields_))]
+    made = cls.from_buffer_copy(pack(*values).ljust(ctypes.sizeof(cls), b"\0"))
+    assert [getattr(made, f) for f, _ in cls._fields_] == values
+
+
 def test_structs_match_the_header(tmp_path):
     from quantised_gemv_norm_gb300 import dq
 
