@@ -579,8 +579,8 @@ typedef struct {
 
 /* Errors: NULL -> DQ_ERR_NULL; a count < 1, the type, a stride below vocab, total_new !=
  * n_seq * max_new without cu_new, a workspace too small -> DQ_ERR_SHAPE; max_new > 64,
- * draft_probs with parents, vocab or total_new > 2^24, more than 2^30 pieces of 8192
- * logits -> DQ_ERR_UNSUPPORTED; a pointer not aligned to its elements (workspace: 16
+ * draft_probs with parents, vocab, total_new or n_seq > 2^24, more than 2^30 steps of
+ * 4096 logits -> DQ_ERR_UNSUPPORTED; a pointer not aligned to its elements (workspace: 16
  * bytes) -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
 DQ_API size_t dq_verify_draft_workspace_bytes(int total_new, int vocab);
 DQ_API int dq_verify_draft(const dq_verify* v, void* stream);
