@@ -17,8 +17,9 @@
 // 64 sequences of up to 9 nodes, 151936 fp32 logits each, 193 MB and 78 MB of random numbers
 // and draft probabilities: 52 us (floor 40): 32 us the first kernel (6.0 TB/s), the rest the
 // pass (13 us, the same memory) and the second kernel's steps.  405 nodes of 100003 bf16
-// logits in 16 trees: 39 us (13): the first kernel 24 us, 3.4 TB/s, bound by a step's chain of
-// instructions at four blocks an SM (about 8 instructions a logit; issue 0.5 of its rate).
+// logits in 16 trees: 38 us (13): the first kernel 24 us, 3.4 TB/s, two rounds of four blocks
+// an SM: a block's start and the chain of each of its nine steps, 9.7 instructions a logit
+// counted, issue 0.5 of its rate (10.8 before 16-bit logits were widened in pairs: 0.8 us more).
 // One sequence of 6: 11.6 us: 2.5 the first kernel, then waits for memory in a row (lengths,
 // tokens, their logits; sums; two rounds of the pass) and two meetings of the cluster.
 #include <cooperative_groups.h>
@@ -131,16 +132,24 @@ __device__ __forceinline__ Best warp_best(Best x)
     return x;
 }
 
-// The sequence that a row belongs to, by one warp; -1: none.
-__device__ __forceinline__ int verify_seq(const VerifyArgs& a, int row, int lane)
+// The sequence that a row belongs to, by one warp; -1: none.  Its temperature comes with the
+// sequences' ends, not after them.
+__device__ __forceinline__ int verify_seq(const VerifyArgs& a, int row, int lane, float& temp)
 {
-    if (!a.cu)
-        return row / a.max_new;
+    temp = 1.f;
+    if (!a.cu) {
+        const int s = row / a.max_new;
+        if (a.temperature)
+            temp = __ldg(a.temperature + s);
+        return s;
+    }
     for (int s0 = 0; s0 < a.n_seq; s0 += 128) {
         unsigned hit[4];
+        float each[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int s = s0 + 32 * e + lane;
+            each[e] = a.temperature && s < a.n_seq ? __ldg(a.temperature + s) : 1.f;
             bool ok = false;
             int2 n = make_int2(0, 0);
             if (s < a.n_seq)
@@ -149,8 +158,10 @@ __device__ __forceinline__ int verify_seq(const VerifyArgs& a, int row, int lane
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (hit[e])
+            if (hit[e]) {
+                temp = __shfl_sync(0xffffffffu, each[e], __ffs(hit[e]) - 1);
                 return s0 + 32 * e + __ffs(hit[e]) - 1;
+            }
     }
     return -1;
 }
@@ -185,13 +196,50 @@ struct VerifyStep {
             }
         }
     }
+    // the largest, NaN passed over; 16-bit logits in pairs
+    __device__ __forceinline__ float top() const
+    {
+        float m = -INFINITY;
+        if constexpr (sizeof(T) == 4) {
+            float m4[4] = {m, m, m, m};
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    m4[i] = fmaxf(m4[i], reinterpret_cast<const float*>(&u[k])[i]);
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        } else {
+            using P = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+            const P* p = reinterpret_cast<const P*>(u);
+            P m2[2] = {p[0], p[1]};
+#pragma unroll
+            for (int i = 2; i < VF_EACH / 2; ++i)
+                m2[i & 1] = __hmax2(m2[i & 1], p[i]);
+            m2[0] = __hmax2(m2[0], m2[1]);
+            return fmaxf(m, fmaxf(verify_one(&m2[0].x), verify_one(&m2[0].y)));
+        }
+    }
     __device__ __forceinline__ void get(float (&x)[VF_EACH]) const
     {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(u);
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
 #pragma unroll
-        for (int k = 0; k < N; ++k)
+            for (int i = 0; i < VF_EACH / 2; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else if constexpr (std::is_same_v<T, __half>) {
 #pragma unroll
-            for (int i = 0; i < W; ++i)
-                x[W * k + i] = verify_one(reinterpret_cast<const T*>(&u[k]) + i);
+            for (int i = 0; i < VF_EACH / 2; ++i) {
+                const float2 f = __half22float2(reinterpret_cast<const __half2*>(w)[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < VF_EACH; ++i)
+                x[i] = __uint_as_float(w[i]);
+        }
     }
 };
 
@@ -222,9 +270,10 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
         if (d == 0 || d < steps)
             next[d].load(src, base + d * VF_STEP + W * tid, a.vocab, whole(base + d * VF_STEP));
     if (warp == 0) {
-        const int s = verify_seq(a, row, lane);
+        float t;
+        const int s = verify_seq(a, row, lane, t);
         if (lane == 0) {
-            row_temp = s < 0 ? -1.f : a.temperature ? __ldg(a.temperature + s) : 1.f;
+            row_temp = t;
             row_seq = s;
             row_scale = verify_scale(row_temp > 0.f ? row_temp : 1.f);
         }
@@ -239,16 +288,12 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
     for (int k = 0; k < steps; ++k, base += VF_STEP) {
         float x[VF_EACH];
         next[0].get(x);
+        const float m = verify_warp_max(next[0].top());
 #pragma unroll
         for (int d = 0; d + 1 < DEPTH; ++d)
             next[d] = next[d + 1];
         if (k + DEPTH < steps)
             next[DEPTH - 1].load(src, base + DEPTH * VF_STEP + W * tid, a.vocab, whole(base + DEPTH * VF_STEP));
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < VF_EACH; ++i)
-            m4[i & 3] = fmaxf(m4[i & 3], x[i]);  // NaN is passed over
-        const float m = verify_warp_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
         if (m > top.v) {  // the same in the whole warp
             int at = 0x7fffffff;
 #pragma unroll
