@@ -10,9 +10,12 @@
 //
 // The next token is the largest r(v) / noise(v) instead of the place where a cumulated
 // sum passes one random number: of 10^5 such places some lie within the rounding of any
-// 32-bit sum, where two ratios are seldom that close.  The pass runs in fp32; every
-// thread whose best is within 1e-5 of the largest computes that one ratio again in
-// 64 bits, and those decide (where only one is near, nothing is computed again).
+// 32-bit sum, where two ratios are seldom that close.  The pass runs in fp32 and has for
+// every place what its ratio is at least and at most, by a bound on all that fp32 may have
+// rounded (slack below; what a draft's probability cancels counts in full).  The places whose most
+// reaches the largest least can be the best: where that is one, it is; else they are compared in
+// 64 bits, with the sum of weights that a draft is multiplied by taken again to 2^-38.  That
+// happens about once in 10^4 calls a sequence.
 //
 // 64 sequences of up to 9 nodes, 151936 fp32 logits each, 193 MB and 78 MB of random numbers
 // and draft probabilities: 52 us (floor 40): 32 us the first kernel (6.0 TB/s), the rest the
@@ -56,6 +59,7 @@ struct VerifyArgs {
     int* next;
     int n_seq, total_new, max_new, vocab, pieces, steps;  // pieces of a row, a block each; steps a piece
     float4* part;  // [total_new][pieces]: largest logit, its place, sum
+    float slack;   // relative error of a node's sum and of a weight, at most (VerifyCut)
     int* err;
 };
 
@@ -98,6 +102,27 @@ __device__ __forceinline__ uint64_t verify_exp2(uint64_t x, uint64_t minus_m, co
     const uint64_t d = f2(fmaxf(d0.x, c.least), fmaxf(d0.y, c.least));
     const float2 t = un2(fma2(d, f2(c.lo, c.lo), mul2(d, f2(c.hi, c.hi))));
     return f2(ex2(t.x), ex2(t.y));
+}
+// The same with the exponent's own rounding put right: off by the difference's, 2^-24 of an
+// exponent of at most 126, and ex2's, 6e-6 in all; below 2^-126 it is 0.
+__device__ __forceinline__ uint64_t verify_exp2_close(uint64_t x, uint64_t minus_m, const VerifyScale& c)
+{
+    const float2 d0 = un2(add2(x, minus_m));
+    const uint64_t d = f2(fmaxf(d0.x, c.least), fmaxf(d0.y, c.least));
+    const uint64_t t = mul2(d, f2(c.hi, c.hi));
+    const uint64_t e = fma2(d, f2(-c.lo, -c.lo), fma2(d, f2(-c.hi, -c.hi), t));  // the error, negated
+    const float2 t2 = un2(t);
+    const uint64_t w = f2(ex2(t2.x), ex2(t2.y));
+    return fma2(w, mul2(e, f2(-0.6931471805599453f, -0.6931471805599453f)), w);
+}
+// In 64 bits, of one that is no NaN.
+__device__ __forceinline__ double verify_exp64(float x, float m, double temperature)
+{
+    return x == m ? 1.0 : exp((static_cast<double>(x) - m) / temperature);
+}
+__device__ __forceinline__ double verify_temperature64(float t)
+{
+    return fmin(fmax(static_cast<double>(t), 8.673617379884035e-19), 1.152921504606847e18);
 }
 // The same of one, 1 at m even where m is infinite; the product's rounding error goes back
 // in as a factor 1 + e ln 2.
@@ -343,11 +368,13 @@ struct VerifyShared {
     int path[VF_MAX_NEW], len;
     int gone[VF_MAX_NEW], n_gone;  // rejected tokens at the last node
     int last, turned_down;         // the rejected node of a chain, or 0
-    Best warp[VF_PICK / 32];
-    double exact_v[VF_PICK / 32];
-    int exact_at[VF_PICK / 32];
-    float best;  // the block's
-    int near[VF_PICK * VF_CLUSTER], n_near;  // in the first block: places near the cluster's best
+    float warp[VF_PICK / 32];
+    float sure;        // of the block's places: the largest of what their ratios are at least
+    int near, n_near;  // a place that may be the cluster's best, and how many there are
+    // the exact pass
+    float2 powers[128];  // 2^(k / 128) in two parts
+    double part, warp64[VF_PICK / 32], best64;
+    int warp_at[VF_PICK / 32], best_at;
 };
 
 // Four consecutive logits from an address that is a multiple of their size.
@@ -355,6 +382,140 @@ template <typename T>
 __device__ __forceinline__ float4 verify_four(const T* p)
 {
     return load4(p);
+}
+
+// The sum of a row's weights exp((x - m) / temperature) to 2^-38 of itself, by a cluster whose
+// blocks have the places v0 .. v1 - 1 each; the same number in all of its threads.
+// 2^t = 2^(k / 128) e^z with k = rint(128 t), |z| <= ln 2 / 256 (P. Tang's table method, 1989), where t,
+// the table and the sums are pairs of fp32, whose sums and products are exact up to 2^-41 of a
+// weight: 64-bit arithmetic has a sixty-fourth of fp32's rate here.
+template <typename T>
+__device__ __noinline__ double verify_sum64(VerifyShared& sh, const T* row, float m, double temperature, int v0, int v1)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x;
+    if (tid < 128) {
+        const double p = exp2(tid / 128.0);
+        sh.powers[tid].x = static_cast<float>(p);
+        sh.powers[tid].y = static_cast<float>(p - static_cast<float>(p));
+    }
+    __syncthreads();
+    const double scale = 1.4426950408889634074 / temperature;
+    const float ch = static_cast<float>(scale), cl = static_cast<float>(scale - ch);
+    const bool infinite = isinf(m);
+    double total = 0.0;
+    for (int b0 = v0 + tid; b0 < v1; b0 += VF_PICK * VF_EACH) {
+        float hi = 0.f, lo = 0.f;
+        auto add = [&](float x) {  // and its rounding
+            const float t = hi + x, z = t - hi;
+            lo += (hi - (t - z)) + (x - z);
+            hi = t;
+        };
+#pragma unroll 4
+        for (int i = 0; i < VF_EACH; ++i) {
+            const int v = b0 + i * VF_PICK;
+            if (v >= v1)
+                break;
+            const float x = verify_one(row + v);
+            if (infinite) {
+                hi += x == m ? 1.f : 0.f;
+                continue;
+            }
+            const float dh = x - m, back = dh - x, dl = (x - (dh - back)) - (m + back);
+            const float ph = dh * ch;
+            if (!(ph > -125.f))
+                continue;  // less than 2^-125, or a NaN
+            const float pl = fmaf(dl, ch, fmaf(dh, cl, fmaf(dh, ch, -ph)));
+            const float k = rintf(128.f * ph), h = fmaf(k, -1.f / 128.f, ph);
+            constexpr float LN2 = 0.6931471805599453f, REST = static_cast<float>(0.6931471805599453 - static_cast<double>(LN2));
+            const float zh = h * LN2, zl = fmaf(pl, LN2, fmaf(h, REST, fmaf(h, LN2, -zh)));
+            const float more = fmaf(zh * zh, fmaf(zh, fmaf(zh, 1.f / 24.f, 1.f / 6.f), 0.5f), zl);  // e^z - 1 - zh
+            const int n = static_cast<int>(k);
+            const float2 p = sh.powers[n & 127];
+            const float power = __int_as_float(((n >> 7) + 127) << 23), w = p.x * power, wz = w * zh;
+            add(w);
+            add(wz);
+            lo += fmaf(w, more, fmaf(w, zh, -wz)) + p.y * power * (1.f + zh);
+        }
+        total += static_cast<double>(hi) + lo;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    if ((tid & 31) == 0)
+        sh.warp64[tid >> 5] = total;
+    __syncthreads();
+    if (tid == 0) {
+        total = 0.0;
+        for (int w = 0; w < VF_PICK / 32; ++w)
+            total += sh.warp64[w];
+        sh.part = total;
+    }
+    cluster.sync();
+    total = 0.0;
+    for (int k = 0; k < static_cast<int>(cluster.num_blocks()); ++k)
+        total += *cluster.map_shared_rank(&sh.part, k);
+    cluster.sync();  // before a block writes its part again, or ends
+    return total;
+}
+
+// The next token by 64-bit ratios, of the places that fp32 left open: `near` of this thread's,
+// one of which is `at`, or all of a cluster's if none was near.  z: the weights' sum, where a
+// draft is subtracted.
+template <typename T>
+__device__ __noinline__ void verify_pick64(int* next, VerifyShared& sh, const T* row, const float* draft,
+                                           const float* noise, Best top, double temperature, double z, int near, int at,
+                                           int v0, int v1, int v4)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    double v64 = 0.0;
+    int at64 = -1;
+    auto larger = [&](double v, int place) {
+        if (v > v64 || (v == v64 && place >= 0 && place < at64)) {
+            v64 = v;
+            at64 = place;
+        }
+    };
+    auto look = [&](int v) {
+        for (int k = 0; k < sh.n_gone; ++k)
+            if (sh.gone[k] == v)
+                return;
+        const double w = verify_exp64(verify_clean(verify_one(row + v)), top.v, temperature);
+        larger((draft ? fma(-z, static_cast<double>(draft[v]), w) : w) / noise[v], v);
+    };
+    if (near == 1) {
+        look(at);
+    } else if (near > 1 || sh.n_near == 0) {
+        for (int b0 = v0 + 4 * tid; b0 < v4; b0 += 4 * VF_PICK)
+            for (int i = 0; i < 4; ++i)
+                look(b0 + i);
+        for (int v = v4 + tid; v < v1; v += VF_PICK)
+            look(v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        larger(__shfl_xor_sync(0xffffffffu, v64, o), __shfl_xor_sync(0xffffffffu, at64, o));
+    if (lane == 0) {
+        sh.warp64[warp] = v64;
+        sh.warp_at[warp] = at64;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < VF_PICK / 32; ++w)
+            larger(sh.warp64[w], sh.warp_at[w]);
+        sh.best64 = v64;
+        sh.best_at = at64;
+    }
+    cluster.sync();
+    if (cluster.block_rank() == 0 && tid == 0) {
+        for (int k = 1; k < static_cast<int>(cluster.num_blocks()); ++k)
+            larger(*cluster.map_shared_rank(&sh.best64, k), *cluster.map_shared_rank(&sh.best_at, k));
+        *next = at64 >= 0 ? at64 : top.at;  // nothing above 0: the largest logit
+    }
+    cluster.sync();  // no block ends while the first one reads
 }
 
 template <typename T>
@@ -559,37 +720,49 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
         const int v = sh.gone[k];
         careful |= v >= v0 && v < v1 && (v < v4 ? (v - v0) / 4 % VF_PICK == tid : (v - v4) % VF_PICK == tid);
     }
-    Best best{0.f, -1};
-    auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int v) {
-        float2 p = un2(verify_exp2(f2(x, y), minus, c));
+    // of this thread's places: the largest and the second largest of what a ratio may be, the
+    // first one's place, and the largest of what a ratio is at least
+    float first = 0.f, second = 0.f, sure = 0.f;
+    int at = -1;
+    auto place = [&](float most, float least, int v) {
+        if (careful && (most > second || least > sure))
+            for (int k = 0; k < n_gone; ++k)
+                if (sh.gone[k] == v)
+                    return;
+        second = fmaxf(second, fminf(first, most));
+        at = most > first ? v : at;
+        first = fmaxf(first, most);
+        sure = fmaxf(sure, least);
+    };
+    // Places that may not reach what one of the warp's is at least (bar) are passed over by a
+    // cheap bound first: three of four pairs are.
+    float bar = 0.f;
+    constexpr float TINY = 1.1754944e-38f;  // 2^-126: weights that fp32 has as 0
+    const float coarse = a.slack + 1.2e-5f, by_p = 1.f + coarse, by_q = -z * (1.f - coarse);
+    auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int vx, int vy) {
+        const uint64_t q = f2(qx, qy), inv = f2(__fdividef(1.f, ex), __fdividef(1.f, ey));
+        const float2 u = un2(mul2(fma2(q, f2(by_q, by_q), fma2(verify_exp2(f2(x, y), minus, c), f2(by_p, by_p), f2(TINY, TINY))), inv));
+        if (fmaxf(u.x, u.y) < bar && !infinite)
+            return;
+        uint64_t p = verify_exp2_close(f2(x, y), minus, c);
         if (infinite)
-            p = make_float2(x == top.v ? 1.f : 0.f, y == top.v ? 1.f : 0.f);
-        const float sx = __fdividef(fmaf(-z, qx, p.x), ex), sy = __fdividef(fmaf(-z, qy, p.y), ey);
-        if (careful) {
-            for (int e = 0; e < 2; ++e) {
-                if (!((e ? sy : sx) > best.v))
-                    continue;
-                bool out = false;
-                for (int k = 0; k < n_gone; ++k)
-                    out |= sh.gone[k] == v + e;
-                if (!out)
-                    best = Best{e ? sy : sx, v + e};
-            }
-        } else {
-            best.at = sx > best.v ? v : best.at;
-            best.v = fmaxf(sx, best.v);
-            best.at = sy > best.v ? v + 1 : best.at;
-            best.v = fmaxf(sy, best.v);
-        }
+            p = f2(x == top.v ? 1.f : 0.f, y == top.v ? 1.f : 0.f);
+        // r, and all that its numbers may be off by
+        const uint64_t r = fma2(q, f2(-z, -z), p);
+        const uint64_t off = fma2(fma2(q, f2(z, z), p), f2(a.slack, a.slack), f2(TINY, TINY));
+        const float2 most = un2(mul2(add2(r, off), inv)), least = un2(mul2(fma2(off, f2(-1.f, -1.f), r), inv));
+        place(most.x, least.x, vx);
+        place(most.y, least.y, vy);
     };
     constexpr int N = VF_BATCH / 4;
-    for (int b0 = v0 + 4 * tid; b0 < v4; b0 += 4 * VF_PICK * N) {
+    for (int b = v0; b < v4; b += 4 * VF_PICK * N) {
+        const int b0 = b + 4 * tid;
         float4 x[N], e[N], d[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int v = b0 + 4 * VF_PICK * i;
             x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            e[i] = make_float4(1.f, 1.f, 1.f, 1.f);
+            e[i] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);  // a ratio of 0 is never taken
             d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (v < v4) {
                 x[i] = verify_four(row + v);
@@ -601,84 +774,57 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int v = b0 + 4 * VF_PICK * i;
-            look(x[i].x, x[i].y, d[i].x, d[i].y, e[i].x, e[i].y, v);
-            look(x[i].z, x[i].w, d[i].z, d[i].w, e[i].z, e[i].w, v + 2);
+            look(x[i].x, x[i].y, d[i].x, d[i].y, e[i].x, e[i].y, v, v + 1);
+            look(x[i].z, x[i].w, d[i].z, d[i].w, e[i].z, e[i].w, v + 2, v + 3);
+            bar = verify_warp_max(sure);
         }
     }
     // rows that do not begin alike, and what four do not divide
-    for (int b0 = v4 + tid; b0 < v1; b0 += VF_PICK * VF_BATCH) {
+    for (int b = v4; b < v1; b += VF_PICK * VF_BATCH) {
+        const int b0 = b + tid;
         float x[VF_BATCH], d[VF_BATCH], e[VF_BATCH];
 #pragma unroll
         for (int i = 0; i < VF_BATCH; ++i) {
             const int v = b0 + i * VF_PICK;
             x[i] = v < v1 ? verify_one(row + v) : -INFINITY;
-            e[i] = v < v1 ? __ldcs(noise + v) : 1.f;
+            e[i] = v < v1 ? __ldcs(noise + v) : INFINITY;
             d[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < VF_BATCH; ++i)
-            look(x[i], -INFINITY, d[i], 0.f, e[i], 1.f, b0 + i * VF_PICK);
+        for (int i = 0; i < VF_BATCH; i += 2)
+            look(x[i], x[i + 1], d[i], d[i + 1], e[i], e[i + 1], b0 + i * VF_PICK, b0 + (i + 1) * VF_PICK);
+        bar = verify_warp_max(sure);
     }
-    // the numbers that the best's r is a difference of, over its noise
-    float size = 0.f;
-    if (best.at >= 0)
-        size = best.v + 2.f * (draft ? z * draft[best.at] : 0.f) / noise[best.at];
-    Best b = warp_best(best);
+    sure = verify_warp_max(sure);
     if (lane == 0)
-        sh.warp[warp] = b;
+        sh.warp[warp] = sure;
     __syncthreads();
     if (warp == 0) {
-        b = warp_best(lane < VF_PICK / 32 ? sh.warp[lane] : Best{0.f, -1});
+        sure = verify_warp_max(lane < VF_PICK / 32 ? sh.warp[lane] : 0.f);
         if (lane == 0) {
-            sh.best = b.at < 0 ? 0.f : b.v;
+            sh.sure = sure;
             sh.n_near = 0;
         }
     }
     cluster.sync();
     float most = 0.f;
     for (int k = 0; k < blocks; ++k)
-        most = fmaxf(most, *cluster.map_shared_rank(&sh.best, k));
-    if (best.at >= 0 && best.v + 1e-5f * size >= most * (1.f - 1e-5f)) {
-        VerifyShared* head = cluster.map_shared_rank(&sh, 0);
-        head->near[atomicAdd(&head->n_near, 1)] = best.at;
-    }
-    cluster.sync();
-    if (rank)
-        return;
-    const int near = sh.n_near;
-    if (near <= 1) {
-        if (tid == 0)
-            a.next[s] = near ? sh.near[0] : top.at;
-        return;
-    }
-    double v64 = 0.0;
-    int at64 = -1;
-    auto larger = [&](double v, int at) {
-        if (at >= 0 && (at64 < 0 || v > v64 || (v == v64 && at < at64))) {
-            v64 = v;
-            at64 = at;
+        most = fmaxf(most, *cluster.map_shared_rank(&sh.sure, k));
+    const int near = (first > 0.f && first >= most) + (second > 0.f && second >= most);
+    if (near)
+        for (int k = 0; k < blocks; ++k) {
+            VerifyShared* to = cluster.map_shared_rank(&sh, k);
+            atomicAdd(&to->n_near, near);
+            to->near = at;
         }
-    };
-    for (int k = tid; k < near; k += VF_PICK) {
-        const int at = sh.near[k];
-        const float x = verify_one(row + at);
-        const double t = fmin(fmax(static_cast<double>(temp), 8.673617379884035e-19), 1.152921504606847e18);
-        const double w = x == top.v ? 1.0 : exp((static_cast<double>(x) - top.v) / t);
-        larger((w - (draft ? sh.sum[last] * draft[at] : 0.0)) / noise[at], at);
+    cluster.sync();
+    if (sh.n_near == 1 && most > 0.f) {
+        if (rank == 0 && tid == 0)
+            a.next[s] = sh.near;
+        return;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        larger(__shfl_xor_sync(0xffffffffu, v64, o), __shfl_xor_sync(0xffffffffu, at64, o));
-    if (lane == 0) {
-        sh.exact_v[warp] = v64;
-        sh.exact_at[warp] = at64;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < VF_PICK / 32; ++w)
-            larger(sh.exact_v[w], sh.exact_at[w]);
-        a.next[s] = at64;
-    }
+    const double t64 = verify_temperature64(temp), z64 = draft ? verify_sum64(sh, row, top.v, t64, v0, v1) : 0.0;
+    verify_pick64(a.next + s, sh, row, draft, noise, top, t64, z64, near, at, v0, v1, v4);
 }
 
 }  // namespace dq
@@ -710,6 +856,12 @@ static cudaError_t verify_prepare(K kernel, bool (&done)[64])
 // 2025 blocks are three rounds and a third).
 struct VerifyCut {
     int pieces, steps;
+    // What the fp32 sum of a row's weights, and a weight, may be off by, relative to themselves.  A
+    // weight 2^-t: ex2's 2^-22 and, of t, the three roundings of verify_exp2, 3 t 2^-24 ln 2, where t
+    // averaged over a sum's weights is at most log2(vocab) <= 24: 3.3e-6; or the one of
+    // verify_exp2_close, 126 2^-24 ln 2: 5.5e-6.  The joins of lanes, warps and pieces: 2e-6.
+    // A step: an addition, and another maximum's factor and its product: 6 2^-24.
+    float slack() const { return 8e-6f + 3.6e-7f * static_cast<float>(steps); }
 };
 static VerifyCut verify_cut(int total_new, int vocab, bool wide)
 {
@@ -770,7 +922,7 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream)
     const dq::VerifyArgs a{v->logits, v->logits_stride, v->draft_probs, v->draft_stride, v->noise, v->noise_stride,
                            v->tokens, v->parents, v->uniform, v->temperature, v->cu_new, v->path, v->n_path, v->next,
                            v->n_seq, v->total_new, v->max_new, v->vocab, cut.pieces, cut.steps, static_cast<float4*>(v->workspace),
-                           dqhost::device_error_flag()};
+                           cut.slack(), dqhost::device_error_flag()};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = dqhost::with_type(v->type, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
