@@ -539,12 +539,14 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream);
  *   uniform[x] * (1 - p(rejected)) < p(token)         where it is NULL: candidates that
  *                     were chosen without chance; p(rejected) is the sum over the tokens
  *                     of the node's children before, each counted once and never taken
- *                     a second time
+ *                     a second time; the difference is kept at or above 0
  * and an accepted child is the new current node.  Where none is left, the next token is
  *   argmax_v r(v) / noise[s][v],  ties to the lowest v,
  * with r = max(p - draft_probs[x], 0) for the rejected x, else p without the rejected
  * tokens.  With uniform from [0, 1) and noise from the exponential distribution the
- * tokens are distributed as if drawn from p one by one.  Where r is zero everywhere, and
+ * tokens are distributed as if drawn from p one by one.  What fp32 leaves open of an
+ * acceptance or of the argmax is decided from 64-bit weights and a sum good to 2^-38.
+ * Where r is zero everywhere, and
  * where temperature[s] is not above 0 (a child is then accepted if its token is it), the
  * token of the largest logit (the lowest of equal ones).  temperature NULL: 1.
  * A NaN among the logits counts as -infinity, the weight of a -infinity is 0, the

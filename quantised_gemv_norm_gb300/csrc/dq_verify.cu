@@ -14,8 +14,10 @@
 // every place what its ratio is at least and at most, by a bound on all that fp32 may have
 // rounded (slack below; what a draft's probability cancels counts in full).  The places whose most
 // reaches the largest least can be the best: where that is one, it is; else they are compared in
-// 64 bits, with the sum of weights that a draft is multiplied by taken again to 2^-38.  That
-// happens about once in 10^4 calls a sequence.
+// 64 bits, with the sum of weights that a draft is multiplied by taken again to 2^-38.  The
+// acceptance of a token is open within the same bound of its border, and is then decided again
+// like that when its turn comes (what rejected siblings leave of 1 may be small).  Either happens
+// about once in 10^4 tokens, and costs 16 us for one sequence of 151936 logits.
 //
 // 64 sequences of up to 9 nodes, 151936 fp32 logits each, 193 MB and 78 MB of random numbers
 // and draft probabilities: 52 us (floor 40): 32 us the first kernel (6.0 TB/s), the rest the
@@ -103,18 +105,15 @@ __device__ __forceinline__ uint64_t verify_exp2(uint64_t x, uint64_t minus_m, co
     const float2 t = un2(fma2(d, f2(c.lo, c.lo), mul2(d, f2(c.hi, c.hi))));
     return f2(ex2(t.x), ex2(t.y));
 }
-// The same with the exponent's own rounding put right: off by the difference's, 2^-24 of an
-// exponent of at most 126, and ex2's, 6e-6 in all; below 2^-126 it is 0.
-__device__ __forceinline__ uint64_t verify_exp2_close(uint64_t x, uint64_t minus_m, const VerifyScale& c)
+// The same of one, 1 at m even where m is infinite; the product's rounding error goes back
+// in as a factor 1 + e ln 2, which leaves the difference's, 2^-24 of an exponent of at most 126,
+// and ex2's: 5.5e-6 in all.  Below 2^-126 it is 0.
+__device__ __forceinline__ float verify_exp(float x, float m, const VerifyScale& c)
 {
-    const float2 d0 = un2(add2(x, minus_m));
-    const uint64_t d = f2(fmaxf(d0.x, c.least), fmaxf(d0.y, c.least));
-    const uint64_t t = mul2(d, f2(c.hi, c.hi));
-    const uint64_t e = fma2(d, f2(-c.lo, -c.lo), fma2(d, f2(-c.hi, -c.hi), t));  // the error, negated
-    const float2 t2 = un2(t);
-    const uint64_t w = f2(ex2(t2.x), ex2(t2.y));
-    return fma2(w, mul2(e, f2(-0.6931471805599453f, -0.6931471805599453f)), w);
+    const float d = fmaxf(x - m, c.least), t = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -t)), w = ex2(t);
+    return x == m ? 1.f : isinf(m) ? 0.f : fmaf(w, e * 0.6931471805599453f, w);
 }
+
 // In 64 bits, of one that is no NaN.
 __device__ __forceinline__ double verify_exp64(float x, float m, double temperature)
 {
@@ -123,13 +122,6 @@ __device__ __forceinline__ double verify_exp64(float x, float m, double temperat
 __device__ __forceinline__ double verify_temperature64(float t)
 {
     return fmin(fmax(static_cast<double>(t), 8.673617379884035e-19), 1.152921504606847e18);
-}
-// The same of one, 1 at m even where m is infinite; the product's rounding error goes back
-// in as a factor 1 + e ln 2.
-__device__ __forceinline__ float verify_exp(float x, float m, const VerifyScale& c)
-{
-    const float d = fmaxf(x - m, c.least), t = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -t)), w = ex2(t);
-    return x == m ? 1.f : isinf(m) ? 0.f : fmaf(w, e * 0.6931471805599453f, w);
 }
 
 // The warp's largest, in one instruction.
@@ -361,11 +353,14 @@ __global__ void __launch_bounds__(VF_THREADS) verify_stats_kernel(const VerifyAr
 
 struct VerifyShared {
     Best top[VF_MAX_NEW];        // a node's largest logit
-    double sum[VF_MAX_NEW];      // of its weights
+    float sum[VF_MAX_NEW];       // of its weights
     float w[VF_MAX_NEW];         // the weight of a node's token at its parent
-    int parent[VF_MAX_NEW], token[VF_MAX_NEW];
-    unsigned long long taken[VF_MAX_NEW];  // the children of a node that are accepted if their turn comes
-    int path[VF_MAX_NEW], len;
+    int token[VF_MAX_NEW];
+    // a node's children, a bit each: all whose token is in the vocabulary, those whose token no
+    // sibling before them has, those accepted if their turn comes, those that fp32 leaves open
+    unsigned long long kids[VF_MAX_NEW], fresh[VF_MAX_NEW], taken[VF_MAX_NEW], open[VF_MAX_NEW];
+    double w64[VF_MAX_NEW];
+    int path[VF_MAX_NEW], len, stop;
     int gone[VF_MAX_NEW], n_gone;  // rejected tokens at the last node
     int last, turned_down;         // the rejected node of a chain, or 0
     float warp[VF_PICK / 32];
@@ -460,17 +455,32 @@ __device__ __noinline__ double verify_sum64(VerifyShared& sh, const T* row, floa
     return total;
 }
 
+// A node into a set in shared memory, by its half: 64-bit ones are loops that 63 children of a
+// node take turns in.
+__device__ __forceinline__ void verify_put(unsigned long long& set, int node)
+{
+    atomicOr(reinterpret_cast<unsigned*>(&set) + (node >> 5), 1u << (node & 31));
+}
+// f of each node in `set`, ascending.
+template <typename F>
+__device__ __forceinline__ void verify_each(unsigned long long set, F f)
+{
+    for (; set; set &= set - 1)
+        f(__ffsll(static_cast<long long>(set)) - 1);
+}
+
 // The next token by 64-bit ratios, of the places that fp32 left open: `near` of this thread's,
-// one of which is `at`, or all of a cluster's if none was near.  z: the weights' sum, where a
-// draft is subtracted.
+// one of which is `at`, or all of a cluster's if none was near.
 template <typename T>
 __device__ __noinline__ void verify_pick64(int* next, VerifyShared& sh, const T* row, const float* draft,
-                                           const float* noise, Best top, double temperature, double z, int near, int at,
-                                           int v0, int v1, int v4)
+                                           const float* noise, Best top, float temp, int near, int at, int v0, int v1,
+                                           int v4)
 {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const double temperature = verify_temperature64(temp);
+    const double z = draft ? verify_sum64(sh, row, top.v, temperature, v0, v1) : 0.0;
     double v64 = 0.0;
     int at64 = -1;
     auto larger = [&](double v, int place) {
@@ -518,15 +528,219 @@ __device__ __noinline__ void verify_pick64(int* next, VerifyShared& sh, const T*
     cluster.sync();  // no block ends while the first one reads
 }
 
+// From the last node that is known to be on the path as far as it is known; whether that is its end.
+__device__ __forceinline__ bool verify_walk(VerifyShared& sh)
+{
+    if (threadIdx.x == 0) {
+        int cur = sh.last, len = sh.len;
+        unsigned long long next;
+        while ((next = sh.taken[cur] | sh.open[cur]) != 0 && !(sh.open[cur] & next & (0ull - next))) {
+            cur = __ffsll(static_cast<long long>(next)) - 1;
+            sh.path[len++] = cur;
+        }
+        sh.last = cur;
+        sh.len = len;
+        sh.stop = next == 0;
+    }
+    __syncthreads();
+    return sh.stop;
+}
+
+// The path is known: it and the next token.
 template <typename T>
-__global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArgs a)
+__device__ __forceinline__ void verify_finish(const VerifyArgs& a, VerifyShared& sh, int s, int row0, int parent, int token,
+                                              float temp, const VerifyScale& c, int v0, int v1)
+{
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int last = sh.last;
+    if (parent == last) {  // the last node's children were all rejected
+        if (a.draft)
+            sh.turned_down = tid;  // a chain's one
+        else if (token >= 0)
+            sh.gone[atomicAdd(&sh.n_gone, 1)] = token;
+    }
+    if (rank == 0) {
+        if (tid < a.max_new)
+            a.path[static_cast<size_t>(s) * a.max_new + tid] = tid < sh.len ? sh.path[tid] : -1;
+        if (tid == 0)
+            a.n_path[s] = sh.len;
+    }
+    const Best top = sh.top[last];
+    if (!(temp > 0.f) || top.at < 0) {
+        if (rank == 0 && tid == 0)
+            a.next[s] = top.at;
+        return;
+    }
+    __syncthreads();
+    const int n_gone = sh.n_gone, down = sh.turned_down;
+
+    // ---- the next token
+    const T* row = static_cast<const T*>(a.logits) + (row0 + last) * a.ld;
+    const float* noise = a.noise + s * a.noise_ld;
+    const float* draft = down ? a.draft + (row0 + down) * a.draft_ld : nullptr;
+    const float z = sh.sum[last];
+    const uint64_t minus = f2(-top.v, -top.v);
+    const bool vec = !((reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) | (reinterpret_cast<uintptr_t>(noise) & 15) |
+                       (reinterpret_cast<uintptr_t>(draft) & 15));
+    const int v4 = vec ? v0 + (max(0, v1 - v0) & ~3) : v0;
+    // whether a rejected token is among this thread's places: few threads have to look each place up
+    bool careful = false;
+    for (int k = 0; k < n_gone; ++k) {
+        const int v = sh.gone[k];
+        careful |= v >= v0 && v < v1 && (v < v4 ? (v - v0) / 4 % VF_PICK == tid : (v - v4) % VF_PICK == tid);
+    }
+    // of this thread's places: the largest and the second largest of what a ratio may be, the
+    // first one's place, and the largest of what a ratio is at least
+    float first = 0.f, second = 0.f, sure = 0.f;
+    int at = -1;
+    auto place = [&](float most, float least, int v) {
+        if (careful && (most > second || least > sure))
+            for (int k = 0; k < n_gone; ++k)
+                if (sh.gone[k] == v)
+                    return;
+        second = fmaxf(second, fminf(first, most));
+        at = most > first ? v : at;
+        first = fmaxf(first, most);
+        sure = fmaxf(sure, least);
+    };
+    // Places that may not reach what one of the warp's is at least (bar) are passed over by a
+    // cheap bound first: three of four pairs are.  Not with an infinite logit, whose weights that
+    // bound does not have.
+    float bar = isinf(top.v) ? -INFINITY : 0.f;
+    constexpr float TINY = 1.1754944e-38f;  // 2^-126: weights that fp32 has as 0
+    const float coarse = a.slack + 1.2e-5f, by_p = 1.f + coarse, by_q = -z * (1.f - coarse);
+    auto close = [&](float x, float q, float inv, int v) {
+        // r, and all that its numbers may be off by
+        const float p = verify_exp(verify_clean(x), top.v, c), r = fmaf(-z, q, p), off = fmaf(fmaf(z, q, p), a.slack, TINY);
+        place((r + off) * inv, (r - off) * inv, v);
+    };
+    auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int vx, int vy) {
+        const uint64_t q = f2(qx, qy), inv = f2(__fdividef(1.f, ex), __fdividef(1.f, ey));
+        const float2 u = un2(mul2(fma2(q, f2(by_q, by_q), fma2(verify_exp2(f2(x, y), minus, c), f2(by_p, by_p), f2(TINY, TINY))), inv));
+        if (fmaxf(u.x, u.y) < bar)
+            return;
+        if (!(u.x < bar))
+            close(x, qx, un2(inv).x, vx);
+        if (!(u.y < bar))
+            close(y, qy, un2(inv).y, vy);
+    };
+    constexpr int N = VF_BATCH / 4;
+    for (int b = v0; b < v4; b += 4 * VF_PICK * N) {
+        const int b0 = b + 4 * tid;
+        float4 x[N], e[N], d[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = b0 + 4 * VF_PICK * i;
+            x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            e[i] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);  // a ratio of 0 is never taken
+            d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (v < v4) {
+                x[i] = verify_four(row + v);
+                e[i] = __ldcs(reinterpret_cast<const float4*>(noise + v));
+                if (draft)
+                    d[i] = __ldcs(reinterpret_cast<const float4*>(draft + v));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = b0 + 4 * VF_PICK * i;
+            look(x[i].x, x[i].y, d[i].x, d[i].y, e[i].x, e[i].y, v, v + 1);
+            look(x[i].z, x[i].w, d[i].z, d[i].w, e[i].z, e[i].w, v + 2, v + 3);
+            bar = isinf(top.v) ? bar : verify_warp_max(sure);
+        }
+    }
+    // rows that do not begin alike, and what four do not divide
+    for (int b = v4; b < v1; b += VF_PICK * VF_BATCH) {
+        const int b0 = b + tid;
+        float x[VF_BATCH], d[VF_BATCH], e[VF_BATCH];
+#pragma unroll
+        for (int i = 0; i < VF_BATCH; ++i) {
+            const int v = b0 + i * VF_PICK;
+            x[i] = v < v1 ? verify_one(row + v) : -INFINITY;
+            e[i] = v < v1 ? __ldcs(noise + v) : INFINITY;
+            d[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < VF_BATCH; i += 2)
+            look(x[i], x[i + 1], d[i], d[i + 1], e[i], e[i + 1], b0 + i * VF_PICK, b0 + (i + 1) * VF_PICK);
+        bar = isinf(top.v) ? bar : verify_warp_max(sure);
+    }
+    sure = verify_warp_max(sure);
+    if (lane == 0)
+        sh.warp[warp] = sure;
+    __syncthreads();
+    if (warp == 0) {
+        sure = verify_warp_max(lane < VF_PICK / 32 ? sh.warp[lane] : 0.f);
+        if (lane == 0) {
+            sh.sure = sure;
+            sh.n_near = 0;
+        }
+    }
+    cluster.sync();
+    float most = 0.f;
+    for (int k = 0; k < blocks; ++k)
+        most = fmaxf(most, *cluster.map_shared_rank(&sh.sure, k));
+    const int near = (first > 0.f && first >= most) + (second > 0.f && second >= most);
+    if (near)
+        for (int k = 0; k < blocks; ++k) {
+            VerifyShared* to = cluster.map_shared_rank(&sh, k);
+            atomicAdd(&to->n_near, near);
+            to->near = at;
+        }
+    cluster.sync();
+    if (sh.n_near == 1 && most > 0.f) {
+        if (rank == 0 && tid == 0)
+            a.next[s] = sh.near;
+        return;
+    }
+    verify_pick64(a.next + s, sh, row, draft, noise, top, temp, near, at, v0, v1, v4);
+}
+
+// The walk came to an open test, and does again: the last node's children once more, from the
+// sum to 2^-38 and weights in 64 bits.  All blocks of the cluster have the same numbers, so they
+// come here together.  A function of its own, which nothing follows, so that it takes no registers
+// from the usual way.
+template <typename T>
+__device__ __noinline__ void verify_open(const VerifyArgs& a, VerifyShared& sh, int s, int row0, int parent, int token, bool mine,
+                                         float own, float u, float q, float temp, int v0, int v1)
+{
+    const int tid = threadIdx.x;
+    const unsigned long long me = 1ull << (tid & 63);
+    const double temperature = verify_temperature64(temp);
+    do {
+        const int cur = sh.last;
+        const float top = sh.top[cur].v;
+        const double z = verify_sum64(sh, static_cast<const T*>(a.logits) + (row0 + cur) * a.ld, top, temperature, v0, v1);
+        if (tid < VF_MAX_NEW && (sh.fresh[cur] & me))
+            sh.w64[tid] = verify_exp64(own, top, temperature);
+        if (tid == 0) {
+            sh.sum[cur] = static_cast<float>(z);
+            sh.taken[cur] = sh.open[cur] = 0ull;
+        }
+        __syncthreads();
+        if (mine && parent == cur) {
+            double left = z;
+            verify_each(sh.fresh[cur] & (me - 1), [&](int i) { left -= sh.w64[i]; });
+            if (static_cast<double>(u) * q * fmax(left, 0.0) < sh.w64[tid])
+                verify_put(sh.taken[cur], tid);
+        }
+        __syncthreads();
+    } while (!verify_walk(sh));
+    verify_finish<T>(a, sh, s, row0, parent, token, temp, verify_scale(temp), v0, v1);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const __grid_constant__ VerifyArgs a)
 {
     namespace cg = cooperative_groups;
     __shared__ VerifyShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int s = blockIdx.x / blocks;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const float temp = a.temperature ? __ldg(a.temperature + s) : 1.f;
     bool ok;
     const int2 nodes = verify_nodes(a, s, ok);
@@ -550,6 +764,8 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
     const bool greedy = !(temp > 0.f);
     const VerifyScale c = verify_scale(greedy ? 1.f : temp);
 
+    if (tid < VF_MAX_NEW)
+        sh.kids[tid] = sh.fresh[tid] = sh.taken[tid] = sh.open[tid] = 0ull;
     // the tree's numbers and the random ones are on their way while the sums are still made
     int parent = -1, token = -1;
     float u = 0.f, q = 1.f;
@@ -563,6 +779,7 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
     if (!greedy)
         for (int v = v0 + 32 * tid; v < v1; v += 32 * VF_PICK)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(noise + v));
+    __syncthreads();
     pdl_wait();
     // eight threads a node join its pieces: the largest logit first, then the sums in two
     // parts (the second has what the first loses)
@@ -588,13 +805,12 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
         if (token < 0 || token >= a.vocab)
             token = -1;
         if (parent >= 0 && token >= 0) {
+            verify_put(sh.kids[parent], tid);
             own = verify_clean(verify_one(logits + (row0 + parent) * a.ld + token));
             if (a.draft)
                 q = __ldg(a.draft + (row0 + tid) * a.draft_ld + token);
         }
-        sh.parent[tid] = parent;
         sh.token[tid] = token;
-        sh.taken[tid] = 0ull;
     }
     if (warp < 4 * ((n + 15) / 16)) {
         Best top{-INFINITY, -1};
@@ -633,198 +849,57 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const VerifyArg
         }
         if (node < n && (tid & 7) == 0) {
             sh.top[node] = top;
-            sh.sum[node] = static_cast<double>(hi) + lo;
+            sh.sum[node] = hi + lo;
         }
     }
     __syncthreads();
     const Best above = parent >= 0 ? sh.top[parent] : Best{-INFINITY, -1};
     const float w = parent < 0 || token < 0 || above.at < 0 || greedy ? 0.f : verify_exp(own, above.v, c);
+    const unsigned long long me = 1ull << (tid & 63);
+    bool mine = parent >= 0 && token >= 0;  // may be accepted
+    if (mine)
+        verify_each(sh.kids[parent] & (me - 1), [&](int i) { mine = mine && sh.token[i] != token; });
+    if (mine)
+        verify_put(sh.fresh[parent], tid);
     if (tid < n)
         sh.w[tid] = w;
     __syncthreads();
 
     // ---- each node's test, should its turn come: the children of a node are tried in ascending
     // order, so all its siblings before it were rejected; probabilities in units of 1 / the
-    // node's sum
-    if (parent >= 0 && token >= 0) {
-        bool take;
+    // node's sum.  Where the two sides are nearer than what fp32 may have rounded (rejected
+    // siblings leave a difference of large numbers), the test is open.
+    mine = mine && above.at >= 0 && own > -INFINITY;  // a weight of 0 is never accepted
+    if (mine) {
+        bool take, open = false;
         if (greedy) {
             take = token == above.at;
         } else {
-            double left = sh.sum[parent];
-            bool again = false;
-            if (a.parents && !a.draft) {
-                for (int i = parent + 1; i < tid; ++i) {
-                    if (sh.parent[i] != parent || sh.token[i] < 0)
-                        continue;
-                    again |= sh.token[i] == token;
-                    bool counted = false;  // a token counts once
-                    for (int k = parent + 1; k < i; ++k)
-                        counted |= sh.parent[k] == parent && sh.token[k] == sh.token[i];
-                    if (!counted)
-                        left -= sh.w[i];
-                }
-            }
-            take = !again && static_cast<double>(u) * q * left < w;
+            const float sum = sh.sum[parent], by = u * q;
+            float left = sum;
+            verify_each(sh.fresh[parent] & (me - 1), [&](int i) { left -= sh.w[i]; });
+            left = by * fmaxf(left, 0.f);
+            // the sum's and the weights' errors, and 64 roundings; 2^-126 for what fp32 has as 0
+            const float off = fmaf(a.slack + 4e-6f, fmaf(2.f * by, sum, w), 1.1754944e-38f);
+            take = left + off < w;
+            open = !take && !(left - off >= w);
         }
         if (take)
-            atomicOr(&sh.taken[parent], 1ull << tid);
+            verify_put(sh.taken[parent], tid);
+        if (open)
+            verify_put(sh.open[parent], tid);
     }
-    __syncthreads();
     if (tid == 0) {
-        int cur = 0, len = 1;
-        sh.path[0] = 0;
-        while (sh.taken[cur]) {
-            cur = __ffsll(static_cast<long long>(sh.taken[cur])) - 1;
-            sh.path[len++] = cur;
-        }
-        sh.last = cur;
-        sh.len = len;
+        sh.last = sh.path[0] = 0;
+        sh.len = 1;
         sh.n_gone = sh.turned_down = 0;
     }
     __syncthreads();
-    const int last = sh.last;
-    if (parent == last && tid < n) {  // the last node's children were all rejected
-        if (a.draft)
-            sh.turned_down = tid;  // a chain's one
-        else if (token >= 0)
-            sh.gone[atomicAdd(&sh.n_gone, 1)] = token;
-    }
-    if (rank == 0) {
-        if (tid < a.max_new)
-            path[tid] = tid < sh.len ? sh.path[tid] : -1;
-        if (tid == 0)
-            a.n_path[s] = sh.len;
-    }
-    const Best top = sh.top[last];
-    if (greedy || top.at < 0) {
-        if (rank == 0 && tid == 0)
-            a.next[s] = top.at;
+    if (!verify_walk(sh)) {
+        verify_open<T>(a, sh, s, row0, parent, token, mine, own, u, q, temp, v0, v1);
         return;
     }
-    __syncthreads();
-    const int n_gone = sh.n_gone, down = sh.turned_down;
-
-    // ---- the next token
-    const T* row = logits + (row0 + last) * a.ld;
-    const float* draft = down ? a.draft + (row0 + down) * a.draft_ld : nullptr;
-    const float z = static_cast<float>(sh.sum[last]);
-    const uint64_t minus = f2(-top.v, -top.v);
-    const bool infinite = isinf(top.v);
-    const bool vec = !((reinterpret_cast<uintptr_t>(row) & (4 * sizeof(T) - 1)) | (reinterpret_cast<uintptr_t>(noise) & 15) |
-                       (reinterpret_cast<uintptr_t>(draft) & 15));
-    const int v4 = vec ? v0 + (max(0, v1 - v0) & ~3) : v0;
-    // whether a rejected token is among this thread's places: few threads have to look each place up
-    bool careful = false;
-    for (int k = 0; k < n_gone; ++k) {
-        const int v = sh.gone[k];
-        careful |= v >= v0 && v < v1 && (v < v4 ? (v - v0) / 4 % VF_PICK == tid : (v - v4) % VF_PICK == tid);
-    }
-    // of this thread's places: the largest and the second largest of what a ratio may be, the
-    // first one's place, and the largest of what a ratio is at least
-    float first = 0.f, second = 0.f, sure = 0.f;
-    int at = -1;
-    auto place = [&](float most, float least, int v) {
-        if (careful && (most > second || least > sure))
-            for (int k = 0; k < n_gone; ++k)
-                if (sh.gone[k] == v)
-                    return;
-        second = fmaxf(second, fminf(first, most));
-        at = most > first ? v : at;
-        first = fmaxf(first, most);
-        sure = fmaxf(sure, least);
-    };
-    // Places that may not reach what one of the warp's is at least (bar) are passed over by a
-    // cheap bound first: three of four pairs are.
-    float bar = 0.f;
-    constexpr float TINY = 1.1754944e-38f;  // 2^-126: weights that fp32 has as 0
-    const float coarse = a.slack + 1.2e-5f, by_p = 1.f + coarse, by_q = -z * (1.f - coarse);
-    auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int vx, int vy) {
-        const uint64_t q = f2(qx, qy), inv = f2(__fdividef(1.f, ex), __fdividef(1.f, ey));
-        const float2 u = un2(mul2(fma2(q, f2(by_q, by_q), fma2(verify_exp2(f2(x, y), minus, c), f2(by_p, by_p), f2(TINY, TINY))), inv));
-        if (fmaxf(u.x, u.y) < bar && !infinite)
-            return;
-        uint64_t p = verify_exp2_close(f2(x, y), minus, c);
-        if (infinite)
-            p = f2(x == top.v ? 1.f : 0.f, y == top.v ? 1.f : 0.f);
-        // r, and all that its numbers may be off by
-        const uint64_t r = fma2(q, f2(-z, -z), p);
-        const uint64_t off = fma2(fma2(q, f2(z, z), p), f2(a.slack, a.slack), f2(TINY, TINY));
-        const float2 most = un2(mul2(add2(r, off), inv)), least = un2(mul2(fma2(off, f2(-1.f, -1.f), r), inv));
-        place(most.x, least.x, vx);
-        place(most.y, least.y, vy);
-    };
-    constexpr int N = VF_BATCH / 4;
-    for (int b = v0; b < v4; b += 4 * VF_PICK * N) {
-        const int b0 = b + 4 * tid;
-        float4 x[N], e[N], d[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int v = b0 + 4 * VF_PICK * i;
-            x[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            e[i] = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);  // a ratio of 0 is never taken
-            d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (v < v4) {
-                x[i] = verify_four(row + v);
-                e[i] = __ldcs(reinterpret_cast<const float4*>(noise + v));
-                if (draft)
-                    d[i] = __ldcs(reinterpret_cast<const float4*>(draft + v));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int v = b0 + 4 * VF_PICK * i;
-            look(x[i].x, x[i].y, d[i].x, d[i].y, e[i].x, e[i].y, v, v + 1);
-            look(x[i].z, x[i].w, d[i].z, d[i].w, e[i].z, e[i].w, v + 2, v + 3);
-            bar = verify_warp_max(sure);
-        }
-    }
-    // rows that do not begin alike, and what four do not divide
-    for (int b = v4; b < v1; b += VF_PICK * VF_BATCH) {
-        const int b0 = b + tid;
-        float x[VF_BATCH], d[VF_BATCH], e[VF_BATCH];
-#pragma unroll
-        for (int i = 0; i < VF_BATCH; ++i) {
-            const int v = b0 + i * VF_PICK;
-            x[i] = v < v1 ? verify_one(row + v) : -INFINITY;
-            e[i] = v < v1 ? __ldcs(noise + v) : INFINITY;
-            d[i] = draft && v < v1 ? __ldcs(draft + v) : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < VF_BATCH; i += 2)
-            look(x[i], x[i + 1], d[i], d[i + 1], e[i], e[i + 1], b0 + i * VF_PICK, b0 + (i + 1) * VF_PICK);
-        bar = verify_warp_max(sure);
-    }
-    sure = verify_warp_max(sure);
-    if (lane == 0)
-        sh.warp[warp] = sure;
-    __syncthreads();
-    if (warp == 0) {
-        sure = verify_warp_max(lane < VF_PICK / 32 ? sh.warp[lane] : 0.f);
-        if (lane == 0) {
-            sh.sure = sure;
-            sh.n_near = 0;
-        }
-    }
-    cluster.sync();
-    float most = 0.f;
-    for (int k = 0; k < blocks; ++k)
-        most = fmaxf(most, *cluster.map_shared_rank(&sh.sure, k));
-    const int near = (first > 0.f && first >= most) + (second > 0.f && second >= most);
-    if (near)
-        for (int k = 0; k < blocks; ++k) {
-            VerifyShared* to = cluster.map_shared_rank(&sh, k);
-            atomicAdd(&to->n_near, near);
-            to->near = at;
-        }
-    cluster.sync();
-    if (sh.n_near == 1 && most > 0.f) {
-        if (rank == 0 && tid == 0)
-            a.next[s] = sh.near;
-        return;
-    }
-    const double t64 = verify_temperature64(temp), z64 = draft ? verify_sum64(sh, row, top.v, t64, v0, v1) : 0.0;
-    verify_pick64(a.next + s, sh, row, draft, noise, top, t64, z64, near, at, v0, v1, v4);
+    verify_finish<T>(a, sh, s, row0, parent, token, temp, c, v0, v1);
 }
 
 }  // namespace dq
@@ -859,7 +934,7 @@ struct VerifyCut {
     // What the fp32 sum of a row's weights, and a weight, may be off by, relative to themselves.  A
     // weight 2^-t: ex2's 2^-22 and, of t, the three roundings of verify_exp2, 3 t 2^-24 ln 2, where t
     // averaged over a sum's weights is at most log2(vocab) <= 24: 3.3e-6; or the one of
-    // verify_exp2_close, 126 2^-24 ln 2: 5.5e-6.  The joins of lanes, warps and pieces: 2e-6.
+    // verify_exp, 126 2^-24 ln 2: 5.5e-6.  The joins of lanes, warps and pieces: 2e-6.
     // A step: an addition, and another maximum's factor and its product: 6 2^-24.
     float slack() const { return 8e-6f + 3.6e-7f * static_cast<float>(steps); }
 };

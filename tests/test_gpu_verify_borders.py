@@ -144,3 +144,124 @@ def test_residual_below_the_normal_range(dq):
                                           draft_probs=draft)
     assert n_path.tolist() == [1] * n_seq
     assert after.tolist() == want
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gap", [6, 12])
+def test_a_child_after_a_likely_one(dq, dtype, gap):
+    """A first child of probability 1 - 2^-gap is rejected; the second's random number is 2^-20 beside p / (1 - p(first))."""
+    g, vocab, n_seq = gen(400 + gap), 1000, 64
+    logits = randn(g, 3 * n_seq, vocab).to(dtype)
+    uniform = torch.full((3 * n_seq,), 1 - 2.0 ** -24, device="cuda")
+    tokens, want = [], []
+    for s in range(n_seq):
+        row = logits[3 * s]
+        rest = torch.logsumexp(row.double(), 0)
+        row[500] = float(rest) + gap * math.log(2.0)
+        row[10 + s] = row[:500].float().max() + 2
+        w = weights(row)
+        p = w / w.sum()
+        border = float(w[10 + s] / (w.sum() - w[500]))
+        assert border < 0.9 and float(p[500]) < 1 - 2.0 ** -14
+        u = torch.tensor(border * (1 + 2.0 ** -20 * (-1) ** s)).float()
+        uniform[3 * s + 2] = u
+        assert (float(u) < border) == (s % 2 == 1) and abs(float(u) / border - 1) > 2.0 ** -21
+        tokens += [0, 500, 10 + s]
+        want.append(2 if float(u) < border else 1)
+    noise = exponential(g, n_seq, vocab)
+    path, n_path, after = dq.verify_draft(logits, i32(tokens), uniform, noise, parents=i32([-1, 0, 0] * n_seq))
+    assert n_path.tolist() == want
+    assert path.tolist() == [[0, 2, -1] if n == 2 else [0, -1, -1] for n in want]
+
+
+def test_chain_tokens_beside_their_border(dq):
+    """uniform * q is 2^-23 beside p, for the second and the third node of chains."""
+    g, vocab, n_seq = gen(500), 4000, 64
+    logits = spread(g, 3 * n_seq, vocab, F32)
+    draft = torch.softmax(spread(g, 3 * n_seq, vocab, F32), -1)
+    uniform, tokens, want = torch.zeros(3 * n_seq, device="cuda"), [], []
+    for s in range(n_seq):
+        tokens.append(0)
+        taken = []
+        for j in (1, 2):
+            w = weights(logits[3 * s + j - 1])
+            x = int(w.topk(20).indices[(s + j) % 20])
+            p = float(w[x] / w.sum())
+            u = torch.tensor(0.25 + 0.5 * ((s * 7 + j) % 11) / 11).float()
+            draft[3 * s + j, x] = p / float(u) * (1 + 2.0 ** -23 * (1 if s * (2 * j - 1) // 2 % 2 else -1))
+            q = float(draft[3 * s + j, x])
+            if float(u) * q == p:
+                q = 0.0
+            uniform[3 * s + j] = u
+            tokens.append(x)
+            taken.append(float(u) * q < p)
+        want.append(1 + taken[0] + (taken[0] and taken[1]))
+    assert len(set(want)) == 3
+    noise = exponential(g, n_seq, vocab)
+    assert dq.verify_draft(logits, i32(tokens), uniform, noise, draft_probs=draft)[1].tolist() == want
+
+
+def test_rejected_mass_of_everything(dq):
+    """A random number of 2 rejects whatever it is asked about: where the rejected tokens have all of the probability, the
+    last child, whose weight is 0, is not accepted for a rounding of what is left."""
+    g, vocab, n_seq = gen(600), 64, 2000
+    logits = torch.full((8 * n_seq, vocab), -float("inf"), device="cuda")
+    logits[:, 1:7] = 2 * randn(g, 8 * n_seq, 6)
+    tokens = i32([0, 1, 2, 3, 4, 5, 6, 7] * n_seq)
+    noise = exponential(g, n_seq, vocab)
+    path, n_path, after = dq.verify_draft(logits, tokens, torch.full((8 * n_seq,), 2.0, device="cuda"), noise,
+                                          parents=i32([-1] + [0] * 7).repeat(n_seq))
+    assert n_path.tolist() == [1] * n_seq
+    assert after.tolist() == logits[::8].argmax(1).tolist()  # nothing is left: the largest logit
+
+
+def wide_trees():
+    star = [-1] + [0] * 63
+    breadth4 = [-1] + [(i - 1) // 4 for i in range(1, 64)]
+    breadth8 = [-1] + [(i - 1) // 8 for i in range(1, 64)]
+    chains = [-1] + [0] * 10 + list(range(1, 54))  # ten children, a chain below each
+    return {"star": star, "breadth4": breadth4, "breadth8": breadth8, "chains": chains}
+
+
+@pytest.mark.parametrize("name", ["star", "breadth4", "breadth8", "chains"])
+def test_wide_trees(dq, name):
+    """Nodes with many children, some of them with a sibling's token or none of the vocabulary."""
+    parents, n, n_seq, vocab = wide_trees()[name], 64, 24, 3001
+    g = gen(len(name))
+    logits = spread(g, n * n_seq, vocab, F32)
+    uniform, noise = torch.rand(n * n_seq, device="cuda", generator=g), exponential(g, n_seq, vocab)
+    uniform[: n * n_seq // 2] = 0.99 + 0.0099 * uniform[: n * n_seq // 2]
+    tokens, paths, after = [], [], []
+    for s in range(n_seq):
+        rows = logits[n * s:n * (s + 1)]
+        top = rows.float().topk(40).indices.tolist()
+        count, mine = [0] * n, [0]
+        for i in range(1, n):
+            k = count[parents[i]]
+            count[parents[i]] += 1
+            mine.append(-1 if k % 11 == 10 else top[parents[i]][k % 9 + k // 2 % 31])
+        u = uniform[n * s:n * (s + 1)].tolist()
+        cur, path = 0, [0]
+        while True:
+            w = weights(rows[cur])
+            p, gone, step = w / w.sum(), [], None
+            for j in range(cur + 1, n):
+                x = mine[j]
+                if parents[j] != cur or x < 0 or x in gone:
+                    continue
+                if u[j] * (1.0 - sum(float(p[k]) for k in gone)) < float(p[x]):
+                    step = j
+                    break
+                gone.append(x)
+            if step is None:
+                break
+            cur = step
+            path.append(cur)
+        p = p.clone()
+        p[gone] = 0
+        tokens += mine
+        paths.append(path + [-1] * (n - len(path)))
+        after.append(best(p / noise[s].double()))
+    got = dq.verify_draft(logits, i32(tokens), uniform, noise, parents=i32(parents * n_seq))
+    assert got[0].tolist() == paths
+    assert got[2].tolist() == after
