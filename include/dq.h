@@ -521,9 +521,12 @@ typedef struct {
  * multiple of 16, a stride < 128 where its count exceeds 1, total_new != n_seq * max_new
  * without cu_new, a workspace too small -> DQ_ERR_SHAPE; head_dim != 128, max_new > 64,
  * n_q / n_kv > 64, total_new or max_pages * page_size > 2^30, n_seq * n_kv >= 2^24, 2^30
- * tiles of work or more (n_seq * n_kv * max_pages * page_size / 64 and the like), a
- * pool as in dq_kv16_append -> DQ_ERR_UNSUPPORTED; strides not multiples of 8, a pointer
- * not 16-byte aligned -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
+ * tiles of work or more, a pool as in dq_kv16_append -> DQ_ERR_UNSUPPORTED; strides not
+ * multiples of 8, a pointer not 16-byte aligned -> DQ_ERR_ALIGN; a CUDA error ->
+ * DQ_ERR_CUDA.  Tiles of work: n_seq * n_kv * the tiles of max_pages * page_size keys * the
+ * row tiles of max_new tokens: up to 16 rows of max_new * n_q / n_kv one of them and 64 keys
+ * a tile; else 128 keys, and as many whole tokens as fit 128 rows, or twice as many where
+ * one of these does not hold max_new. */
 DQ_API size_t dq_attention_tree_workspace_bytes(int n_seq, int max_new, int n_q, int n_kv);
 DQ_API int dq_attention_tree(const dq_tree* t, void* stream);
 

@@ -579,6 +579,12 @@ namespace dqhost {
 struct TreeCut {
     int rows, blocks;
     bool tc() const { return rows >= 128; }
+    // tokens an item where it has whole ones, else 0; row tiles of that many new tokens
+    int nodes(int group) const { return tc() ? 128 / group * (rows / 128) : 0; }
+    int row_tiles(int n, int group) const
+    {
+        return tc() ? (n + nodes(group) - 1) / nodes(group) : (n * group + rows - 1) / rows;
+    }
 };
 
 static TreeCut tree_cut(int max_new, int group)
@@ -627,7 +633,7 @@ static cudaError_t tree_launch(const dq::TreeArgs& a, const TreeCut& cut, cudaSt
 template <typename T, int R, int KT>
 static cudaError_t tree_join(const dq::TreeArgs& a, const TreeCut& cut, cudaStream_t s)
 {
-    const int per_seq = a.s.n_kv * (a.nodes ? (a.max_new + a.nodes - 1) / a.nodes : (a.max_new * a.group + R - 1) / R);
+    const int per_seq = a.s.n_kv * cut.row_tiles(a.max_new, a.group);
     const long long items = static_cast<long long>(a.n_seq) * per_seq;
     // warps a unit: an item has about blocks / items blocks' sums
     int parts = 1;
@@ -684,15 +690,14 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         (reinterpret_cast<uintptr_t>(t->n_past) & 3) || (reinterpret_cast<uintptr_t>(t->cu_new) & 3) ||
         (reinterpret_cast<uintptr_t>(t->seen) & 7))
         return DQ_ERR_ALIGN;
-    if (t->workspace_bytes < dq_attention_tree_workspace_bytes(t->n_seq, t->max_new, t->n_q, t->n_kv))
-        return DQ_ERR_SHAPE;
     const int group = t->n_q / t->n_kv;
     const dqhost::TreeCut cut = dqhost::tree_cut(t->max_new, group);
-    // units of work, at most: they are counted in 32 bits
+    // units of work, at most, as the kernels count them in 32 bits
     const long long tile = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS, tiles = (static_cast<long long>(t->max_pages) * t->page_size + tile - 1) / tile;
-    const long long row_tiles = (static_cast<long long>(t->max_new) * group + cut.rows - 1) / cut.rows + 1;
-    if (tiles * row_tiles > (1 << 30) / (static_cast<long long>(t->n_seq) * t->n_kv))
+    if (tiles * cut.row_tiles(t->max_new, group) * t->n_seq * t->n_kv >= (1 << 30))
         return DQ_ERR_UNSUPPORTED;
+    if (t->workspace_bytes < dq_attention_tree_workspace_bytes(t->n_seq, t->max_new, t->n_q, t->n_kv))
+        return DQ_ERR_SHAPE;
     int box = cut.tc() ? dqhost::TREE_TC_KEYS : dq::TM_KEYS;  // rows of a copy: what divides a tile and a page
     while (t->page_size % box)
         box /= 2;
@@ -702,7 +707,7 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream)
         return DQ_ERR_UNSUPPORTED;
     if (cut.tc()) {
         const int tokens = 128 / group;
-        a.nodes = tokens * (cut.rows / 128);
+        a.nodes = cut.nodes(group);
         // a stride of a dimension of one is never used, but has to be one that the encoder takes
         if (!dqhost::tree_map(&a.tq, t->type, t->q, {dq::ATT_HD, t->n_q, t->total_new},
                               {2 * (t->n_q > 1 ? heads[0] : dq::ATT_HD), 2 * (t->total_new > 1 ? rows[0] : dq::ATT_HD)}, group,
