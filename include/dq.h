@@ -475,8 +475,9 @@ DQ_API int dq_attention_decode_kv4(const void* q, int type, const void* pool, co
  * Errors: NULL -> DQ_ERR_NULL; a count < 1, a type (the cache's has 16 bits), an
  * epsilon, page_size not a multiple of 16, row_stride < the heads -> DQ_ERR_SHAPE;
  * head_dim != 128, n_q or n_kv > 65536, n_pages * page_size >= 2^31 or that times
- * 2 n_kv >= 2^31 -> DQ_ERR_UNSUPPORTED; a pointer not 16-byte aligned (positions and
- * slots: 4), row_stride not a multiple of 8 (fp32: 4) -> DQ_ERR_ALIGN. */
+ * 2 n_kv >= 2^31, rows * ceil((n_q + 2 n_kv) / 4) > 2^31 - 256 -> DQ_ERR_UNSUPPORTED; a
+ * pointer not 16-byte aligned (positions and slots: 4), row_stride not a multiple of 8
+ * (fp32: 4) -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
 DQ_API int dq_kv16_append(const void* qkv, int in_type, long long row_stride, const int* positions, const int* slots,
                           const float* q_norm, const float* k_norm, const float* rope_table, float eps, int rows,
                           int n_q, int n_kv, int head_dim, int max_ctx, int type, void* q_out, void* pool, int n_pages,
@@ -600,8 +601,9 @@ DQ_API int dq_verify_draft(const dq_verify* v, void* stream);
  * moved; n_path outside 0 .. max_new or a negative n_past the same for the sequence.
  * Errors: NULL -> DQ_ERR_NULL; a count < 1, the type, page_size not a multiple of 16,
  * layer_stride smaller than a pool -> DQ_ERR_SHAPE; max_new > 64, head_dim != 128, a
- * pool as in dq_kv16_append, 2^31 or more (sequence, layer, head) triples ->
- * DQ_ERR_UNSUPPORTED; DQ_ERR_ALIGN. */
+ * pool as in dq_kv16_append, 2^31 or more (sequence, layer, KV head) triples, n_layers >
+ * 2^16, n_seq > 2^29 -> DQ_ERR_UNSUPPORTED; the pool not 16-byte aligned, layer_stride not a
+ * multiple of 16 -> DQ_ERR_ALIGN; a CUDA error -> DQ_ERR_CUDA. */
 DQ_API int dq_kv16_keep(void* pool, int type, const int* pages, const int* n_past, const int* path, const int* n_path,
                         int n_layers, long long layer_stride, int n_seq, int max_new, int n_kv, int head_dim,
                         int n_pages, int page_size, int max_pages, void* stream);

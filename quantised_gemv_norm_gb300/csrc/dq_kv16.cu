@@ -262,14 +262,14 @@ DQ_API int dq_kv16_append(const void* qkv, int in_type, long long row_stride, co
     const long long heads = n_q + 2ll * n_kv;
     if (row_stride < heads * dq::ATT_HD)
         return DQ_ERR_SHAPE;
-    if (row_stride % (in_type == DQ_TYPE_F32 ? 4 : 8) || !dqhost::aligned16(qkv) || !dqhost::aligned16(rope_table) ||
-        !dqhost::aligned16(q_out) || !dqhost::aligned16(pool) || !dqhost::aligned16(q_norm) ||
-        !dqhost::aligned16(k_norm) || (reinterpret_cast<uintptr_t>(positions) & 3) || (reinterpret_cast<uintptr_t>(slots) & 3))
-        return DQ_ERR_ALIGN;
     const int chunks = static_cast<int>((heads + 2 * dq::KV16_PAIRS - 1) / (2 * dq::KV16_PAIRS));
     const long long items = static_cast<long long>(rows) * chunks, blocks = (items + dq::KV16_WARPS - 1) / dq::KV16_WARPS;
     if (items > 0x7fffff00ll)
         return DQ_ERR_UNSUPPORTED;
+    if (row_stride % (in_type == DQ_TYPE_F32 ? 4 : 8) || !dqhost::aligned16(qkv) || !dqhost::aligned16(rope_table) ||
+        !dqhost::aligned16(q_out) || !dqhost::aligned16(pool) || !dqhost::aligned16(q_norm) ||
+        !dqhost::aligned16(k_norm) || (reinterpret_cast<uintptr_t>(positions) & 3) || (reinterpret_cast<uintptr_t>(slots) & 3))
+        return DQ_ERR_ALIGN;
     const dq::Kv16AppendArgs a{qkv,  row_stride, positions, slots, q_norm, k_norm, reinterpret_cast<const float2*>(rope_table),
                                q_out, pool, eps, rows, n_q, max_ctx, {n_kv, n_pages, page_size}, dqhost::fast_divisor(chunks),
                                dqhost::fast_divisor(page_size), dqhost::device_error_flag()};
@@ -299,8 +299,9 @@ DQ_API int dq_kv16_keep(void* pool, int type, const int* pages, const int* n_pas
     const long long bytes = static_cast<long long>(n_pages) * page_size * 2 * n_kv * dq::ATT_HD * 2;
     if (n_layers > 1 && layer_stride < bytes)
         return DQ_ERR_SHAPE;
-    if (max_new > dq::KV16_MAX_NEW || n_layers > (1 << 16) ||
-        static_cast<long long>(n_seq) * n_layers > 0x7fffffffll / (2 * n_kv))
+    // the grid, two blocks a sequence and group of layers, stays below 2^31
+    if (max_new > dq::KV16_MAX_NEW || n_layers > (1 << 16) || n_seq > (1 << 29) ||
+        static_cast<long long>(n_seq) * n_layers > 0x7fffffffll / n_kv)
         return DQ_ERR_UNSUPPORTED;
     if (!dqhost::aligned16(pool) || (n_layers > 1 && layer_stride % 16) || (reinterpret_cast<uintptr_t>(pages) & 3) ||
         (reinterpret_cast<uintptr_t>(n_past) & 3) || (reinterpret_cast<uintptr_t>(path) & 3) ||

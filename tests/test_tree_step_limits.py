@@ -37,3 +37,24 @@ def test_attention_tiles(lib, kw, status):
              head_dim=128, n_pages=10, page_size=64, max_pages=5, workspace=4096, workspace_bytes=16)
     d.update(kw)
     assert lib.dq_attention_tree(ctypes.byref(dq._Tree(**d)), None) == status
+
+
+@pytest.mark.parametrize("layers,n_seq,n_kv,status", [
+    (1 << 16, 1 << 12, 8, UNSUPPORTED), (1 << 16, (1 << 12) - 1, 8, ALIGN), (1, 1 << 27, 16, UNSUPPORTED),
+    (1, (1 << 27) - 1, 16, ALIGN), (1, 1 << 29, 1, ALIGN), (1, (1 << 29) + 1, 1, UNSUPPORTED), ((1 << 16) + 1, 1, 1, UNSUPPORTED),
+    (1 << 16, 1, 1, ALIGN),
+])
+def test_kept_rows(lib, layers, n_seq, n_kv, status):
+    """2^31 (sequence, layer, head) triples, 2^16 layers, 2^29 sequences."""
+    assert lib.dq_kv16_keep(ODD, 1, A, A, A, A, layers, 4 * 64 * n_kv * 512, n_seq, 8, n_kv, 128, 4, 64, 2, None) == status
+
+
+@pytest.mark.parametrize("n_q,n_kv,rows,status", [
+    (2, 1, (1 << 31) - 1, UNSUPPORTED), (2, 1, (1 << 31) - 256, ALIGN), (2, 1, (1 << 31) - 255, UNSUPPORTED),
+    (32, 8, 178956949, ALIGN), (32, 8, 178956950, UNSUPPORTED),  # 12 fours of heads a row: 2^31 - 256 = 12 x 178956949.3
+])
+def test_appended_rows(lib, n_q, n_kv, rows, status):
+    """2^31 - 256 fours of heads."""
+    heads = n_q + 2 * n_kv
+    assert lib.dq_kv16_append(ODD, 0, heads * 128, A, A, None, None, A, 1e-6, rows, n_q, n_kv, 128, 64, 1, A, A, 4, 64,
+                              None) == status
