@@ -23,9 +23,10 @@
 // copy rate; matrix pipe 18%, issue 15%.  One token after 100000 keys 68 us (floor 61), after
 // 2000 keys 9.3 us, of which the start (lengths, pages, first keys: four waits for memory in a
 // row) is three, a tile 0.6, the meeting and the join three.  On the 5th-generation tensor
-// cores (dq_tree_tc.cu) the same three took 262, 71 and 12.3 us; from 17 rows on those win:
-// 8 tokens after 100000 keys 73 us there, 76 with 32 rows a block here; 32 sequences of 5 after
-// up to 4000 keys 67 and 73; 64 of 8 after 1000 58 and 56.  64 rows here: 97 and 82 us.
+// cores (dq_tree_tc.cu) the same three took 262, 71 and 12.3 us.  From 17 rows on those are
+// used: a variant of this kernel with 32 rows a block, since removed, took 76 us for 8 tokens
+// after 100000 keys where they take 73, 73 for 32 sequences of 5 after up to 4000 (67), 56 for
+// 64 of 8 after 1000 (58).
 #include <algorithm>
 #include <mutex>
 
@@ -84,7 +85,7 @@ template <typename T>
 __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const __grid_constant__ TreeArgs a)
 {
     constexpr int R = TM_ROWS, NK = TM_KEYS / TM_WARPS;  // keys a warp
-    static_assert(NK == 16, "one step of the matrix instruction");
+    static_assert(NK == 16, "one step of the second product, two blocks of eight keys of the first");
     constexpr float TOP = std::is_same<T, __half>::value ? 7.f : 0.f;
     extern __shared__ __align__(1024) uint8_t ring[];
     float2* meet = reinterpret_cast<float2*>(ring + TM_SLOTS * TM_SLOT);
@@ -185,13 +186,9 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
         } else {
             const int wk = warp, r8 = lane >> 2, q4 = lane & 3;
             const uint32_t panel = static_cast<uint32_t>(a.box) * 128;
-            // byte offset of key block i (16 keys, from the warp's first) in a slot
-            uint32_t block_at[NK / 16];
-#pragma unroll
-            for (int i = 0; i < NK / 16; ++i) {
-                const int key = wk * NK + 16 * i, b = key / a.box;
-                block_at[i] = static_cast<uint32_t>(b * a.box * 256 + (key - b * a.box) * 128);
-            }
+            // byte offset of the warp's 16 keys in a slot
+            const int box_of = wk * NK / a.box;
+            const uint32_t keys_at = static_cast<uint32_t>(box_of * a.box * 256 + (wk * NK - box_of * a.box) * 128);
             // this lane's row and 16-byte piece of the four 8 x 8 matrices: of keys (two runs of 8,
             // two of dims), of values (the same, transposed)
             const uint32_t sw = lane & 7;
@@ -238,15 +235,13 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                         s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
                     const uint32_t kb = base + slot * TM_SLOT;
 #pragma unroll
-                    for (int d = 0; d < 8; ++d)
-#pragma unroll
-                        for (int i = 0; i < NK / 16; ++i) {
-                            uint32_t b[4];
-                            ldsm4(b, ((kb + block_at[i] + k_at) ^ ((d & 3) * 32)) + (d >> 2) * panel);
-                            tree_mma<T>(s[2 * i], q[d], b[0], b[1]);
-                            tree_mma<T>(s[2 * i + 1], q[d], b[2], b[3]);
-                        }
-                    const uint32_t absent = !TAIL ? 0u : t.keys ? sh.absent[slot] : 0xfu;
+                    for (int d = 0; d < 8; ++d) {
+                        uint32_t b[4];
+                        ldsm4(b, ((kb + keys_at + k_at) ^ ((d & 3) * 32)) + (d >> 2) * panel);
+                        tree_mma<T>(s[0], q[d], b[0], b[1]);
+                        tree_mma<T>(s[1], q[d], b[2], b[3]);
+                    }
+                    const bool absent = TAIL && (!t.keys || (sh.absent[slot] >> wk & 1));  // the warp's 16 keys
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&sh.freed[slot]);
@@ -259,10 +254,9 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int node = node0 + 8 * i + e;
-                                const bool gone = absent >> ((wk * NK + 8 * i) / 16) & 1;
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
-                                    if (gone || node >= 64 || (node >= 0 && !(seen[h] >> (node & 63) & 1)))
+                                    if (absent || node >= 64 || (node >= 0 && !(seen[h] >> (node & 63) & 1)))
                                         s[i][2 * h + e] = -INFINITY;
                             }
                     }
@@ -290,7 +284,7 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                             }
                         }
                     }
-                    uint32_t p[NK / 16][4];
+                    uint32_t p[4];
                     const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
                     for (int i = 0; i < NK / 8; ++i)
@@ -298,49 +292,44 @@ __global__ void __launch_bounds__(TM_THREADS, TM_RESIDENT) tree_mma_kernel(const
                         for (int h = 0; h < 2; ++h) {
                             const float x = ex2(fmaf(s[i][2 * h] - ref[h], TR_C, TOP)), y = ex2(fmaf(s[i][2 * h + 1] - ref[h], TR_C, TOP));
                             l[h] += x + y;
-                            p[i >> 1][(i & 1) * 2 + h] = pack2(x, y, static_cast<const T*>(nullptr));
+                            p[2 * i + h] = pack2(x, y, static_cast<const T*>(nullptr));
                         }
                     wait(&sh.full[slot], phase, DEVERR_TIMEOUT_FULL);
                     __syncwarp();
                     const uint32_t vb = base + slot * TM_SLOT;
                     bool poison = false;
+                    uint32_t keep[2], fresh[2];  // keys 2 q4, + 1 and 8 more: those that exist, those that are new
+                    if (TAIL) {
 #pragma unroll
-                    for (int i = 0; i < NK / 16; ++i) {
-                        uint32_t keep[2], fresh[2];  // keys 2 q4, + 1 and 8 more: those that exist, those that are new
+                        for (int e = 0; e < 2; ++e) {
+                            const int node = node0 + 8 * e;
+                            keep[e] = absent ? 0u : (node < t.rows ? 0xffffu : 0u) | (node + 1 < t.rows ? 0xffff0000u : 0u);
+                            fresh[e] = (node >= 0 ? 0xffffu : 0u) | (node + 1 >= 0 ? 0xffff0000u : 0u);
+                        }
+                    }
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) {
+                        uint32_t b[4];
+                        ldsm4_trans(b, ((vb + keys_at + v_at) ^ ((d & 3) * 32)) + (d >> 2) * panel);
                         if (TAIL) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int node = node0 + 16 * i + 8 * e;
-                                const bool gone = absent >> ((wk * NK + 16 * i) / 16) & 1;
-                                keep[e] = gone ? 0u : (node < t.rows ? 0xffffu : 0u) | (node + 1 < t.rows ? 0xffff0000u : 0u);
-                                fresh[e] = (node >= 0 ? 0xffffu : 0u) | (node + 1 >= 0 ? 0xffff0000u : 0u);
+                            for (int e = 0; e < 4; ++e) {
+                                b[e] &= keep[e & 1];
+                                const uint32_t nf = tree_non_finite<T>(b[e]) & fresh[e & 1];
+                                poison |= nf != 0;
+                                b[e] &= ~nf;
                             }
                         }
-#pragma unroll
-                        for (int d = 0; d < 8; ++d) {
-                            uint32_t b[4];
-                            ldsm4_trans(b, ((vb + block_at[i] + v_at) ^ ((d & 3) * 32)) + (d >> 2) * panel);
-                            if (TAIL) {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    b[e] &= keep[e & 1];
-                                    const uint32_t nf = tree_non_finite<T>(b[e]) & fresh[e & 1];
-                                    poison |= nf != 0;
-                                    b[e] &= ~nf;
-                                }
-                            }
-                            tree_mma<T>(o[2 * d], p[i], b[0], b[1]);
-                            tree_mma<T>(o[2 * d + 1], p[i], b[2], b[3]);
-                        }
+                        tree_mma<T>(o[2 * d], p, b[0], b[1]);
+                        tree_mma<T>(o[2 * d + 1], p, b[2], b[3]);
                     }
                     if (TAIL && __any_sync(0xffffffffu, poison)) {
                         // new tokens' infinities and NaNs, which the products left out: to the rows that see them
                         for (int key = 0; key < NK; ++key) {
                             const int node = k * TM_KEYS + wk * NK + key - t.past;
-                            if (node < 0 || node >= t.rows || (absent >> ((wk * NK + key) / 16) & 1))
+                            if (node < 0 || node >= t.rows || absent)
                                 continue;
-                            const int first = (wk * NK + key) & ~15, b = first / a.box;
-                            const uint32_t at = b * a.box * 256 + (first - b * a.box + (key & 15)) * 128;
+                            const uint32_t at = keys_at + key * 128;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const uint32_t w = *reinterpret_cast<const uint32_t*>(
