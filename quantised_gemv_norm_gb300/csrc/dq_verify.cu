@@ -615,7 +615,8 @@ __device__ __forceinline__ void verify_finish(const VerifyArgs& a, VerifyShared&
     auto close = [&](float x, float q, float inv, int v) {
         // r, and all that its numbers may be off by
         const float p = verify_exp(verify_clean(x), top.v, c), r = fmaf(-z, q, p), off = fmaf(fmaf(z, q, p), a.slack, TINY);
-        place((r + off) * inv, (r - off) * inv, v);
+        // inv is infinite for a noise below 2^-128
+        place((r + off) * inv, (r - off) * fminf(inv, 8.5070592e37f), v);
     };
     auto look = [&](float x, float y, float qx, float qy, float ex, float ey, int vx, int vy) {
         const uint64_t q = f2(qx, qy), inv = f2(__fdividef(1.f, ex), __fdividef(1.f, ey));

@@ -146,6 +146,19 @@ def test_residual_below_the_normal_range(dq):
     assert after.tolist() == want
 
 
+@pytest.mark.parametrize("small", [2.0 ** -127, 2.0 ** -130, 2.0 ** -149])
+def test_noise_below_the_normal_range(dq, small):
+    """A token of weight 2^-115 and less with the smallest noise: its ratio is as large as another's, not infinite."""
+    vocab, n_seq = 1000, 24
+    logits = torch.full((n_seq, vocab), -float("inf"), device="cuda")
+    noise = torch.ones((n_seq, vocab), device="cuda")
+    logits[:, 10], noise[:, 10] = 0.0, 2.0 ** -10
+    logits[:, 900], noise[:, 900] = -80.0 - 0.25 * torch.arange(n_seq, device="cuda"), small
+    want = [best(weights(r) / e.double()) for r, e in zip(logits, noise)]
+    after = dq.verify_draft(logits, i32([0] * n_seq), torch.zeros(n_seq, device="cuda"), noise)[2]
+    assert after.tolist() == want
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("gap", [6, 12])
 def test_a_child_after_a_likely_one(dq, dtype, gap):
@@ -265,3 +278,28 @@ def test_wide_trees(dq, name):
     got = dq.verify_draft(logits, i32(tokens), uniform, noise, parents=i32(parents * n_seq))
     assert got[0].tolist() == paths
     assert got[2].tolist() == after
+
+
+def test_tokens_after_candidates_are_distributed_as_drawn(dq):
+    """20000 sequences of a root and three fixed candidates for its successor, the last of them after the second: the first
+    two tokens have the target's distribution, whatever was accepted (each count within five deviations)."""
+    g, vocab, n = gen(700), 8, 20000
+    rows = randn(g, 4, vocab)
+    p = torch.softmax(rows.double(), -1)
+    uniform, noise = torch.rand(4 * n, device="cuda", generator=g), exponential(g, n, vocab)
+    path, n_path, after = dq.verify_draft(rows.repeat(n, 1), i32([0, 3, 5, 6] * n), uniform, noise,
+                                          parents=i32([-1, 0, 0, 2] * n))
+    one, two = path[:, 1] == 1, path[:, 1] == 2
+    first = torch.where(one, 3, torch.where(two, 5, after)).long()
+    assert bool((n_path[~two] == 1 + one[~two].int()).all())
+
+    def drawn(tokens, p):
+        n = len(tokens)
+        count = torch.bincount(tokens.long(), minlength=vocab).double()
+        assert bool(((count - n * p).abs() <= 5 * torch.sqrt(n * p * (1 - p)) + 1).all())
+
+    drawn(first, p[0])
+    drawn(after[one], p[1])
+    both = two & (path[:, 2] == 3)
+    drawn(torch.where(both, 6, after)[two], p[2])
+    drawn(after[both], p[3])
