@@ -11,13 +11,13 @@
 // The next token is the largest r(v) / noise(v) instead of the place where a cumulated
 // sum passes one random number: of 10^5 such places some lie within the rounding of any
 // 32-bit sum, where two ratios are seldom that close.  The pass runs in fp32 and has for
-// every place what its ratio is at least and at most, by a bound on all that fp32 may have
-// rounded (slack below; what a draft's probability cancels counts in full).  The places whose most
+// every place what its ratio is at least and at most, by bounds on all that fp32 may have
+// rounded (slack, verify_exp_off; before a draft's part cancels).  The places whose most
 // reaches the largest least can be the best: where that is one, it is; else they are compared in
 // 64 bits, with the sum of weights that a draft is multiplied by taken again to 2^-38.  The
 // acceptance of a token is open within the same bound of its border, and is then decided again
 // like that when its turn comes (what rejected siblings leave of 1 may be small).  Either happens
-// about once in 10^4 tokens, and costs 16 us for one sequence of 151936 logits.
+// about once in 10^4 tokens, and costs 10 us for one sequence of 151936 logits.
 //
 // 64 sequences of up to 9 nodes, 151936 fp32 logits each, 193 MB and 78 MB of random numbers
 // and draft probabilities: 52 us (floor 40): 32 us the first kernel (6.0 TB/s), the rest the
@@ -61,7 +61,7 @@ struct VerifyArgs {
     int* next;
     int n_seq, total_new, max_new, vocab, pieces, steps;  // pieces of a row, a block each; steps a piece
     float4* part;  // [total_new][pieces]: largest logit, its place, sum
-    float slack;   // relative error of a node's sum and of a weight, at most (VerifyCut)
+    float slack;   // relative error of a node's sum, at most, and of a weight (VerifyCut)
     int* err;
 };
 
@@ -107,13 +107,19 @@ __device__ __forceinline__ uint64_t verify_exp2(uint64_t x, uint64_t minus_m, co
 }
 // The same of one, 1 at m even where m is infinite; the product's rounding error goes back
 // in as a factor 1 + e ln 2, which leaves the difference's, 2^-24 of an exponent of at most 126,
-// and ex2's: 5.5e-6 in all.  Below 2^-126 it is 0.
+// and ex2's (verify_exp_off).  Below 2^-126 it is 0.
 __device__ __forceinline__ float verify_exp(float x, float m, const VerifyScale& c)
 {
     const float d = fmaxf(x - m, c.least), t = d * c.hi, e = fmaf(d, c.lo, fmaf(d, c.hi, -t)), w = ex2(t);
     return x == m ? 1.f : isinf(m) ? 0.f : fmaf(w, e * 0.6931471805599453f, w);
 }
 
+// What that is off by, at most, relative to itself: the rounding of the difference, ex2's 2^-22, and
+// 4.6e-7 for the product with it, a division by the noise (2^-22) and a rounding.
+__device__ __forceinline__ float verify_exp_off(float x, float m, const VerifyScale& c)
+{
+    return fmaf(fmaxf((x - m) * c.hi, -130.f), -4.2e-8f, 7e-7f);
+}
 // In 64 bits, of one that is no NaN.
 __device__ __forceinline__ double verify_exp64(float x, float m, double temperature)
 {
@@ -367,8 +373,8 @@ struct VerifyShared {
     float sure;        // of the block's places: the largest of what their ratios are at least
     int near, n_near;  // a place that may be the cluster's best, and how many there are
     // the exact pass
-    float2 powers[128];  // 2^(k / 128) in two parts
-    double part, warp64[VF_PICK / 32], best64;
+    float2 powers[128], scale;  // 2^(k / 128) and log2(e) / temperature, in two parts
+    double part, total, warp64[VF_PICK / 32], best64;
     int warp_at[VF_PICK / 32], best_at;
 };
 
@@ -395,32 +401,35 @@ __device__ __noinline__ double verify_sum64(VerifyShared& sh, const T* row, floa
         sh.powers[tid].x = static_cast<float>(p);
         sh.powers[tid].y = static_cast<float>(p - static_cast<float>(p));
     }
+    if (tid == 128) {
+        const double scale = 1.4426950408889634074 / temperature;
+        sh.scale.x = static_cast<float>(scale);
+        sh.scale.y = static_cast<float>(scale - static_cast<float>(scale));
+    }
     __syncthreads();
-    const double scale = 1.4426950408889634074 / temperature;
-    const float ch = static_cast<float>(scale), cl = static_cast<float>(scale - ch);
+    const float ch = sh.scale.x, cl = sh.scale.y;
     const bool infinite = isinf(m);
-    double total = 0.0;
-    for (int b0 = v0 + tid; b0 < v1; b0 += VF_PICK * VF_EACH) {
-        float hi = 0.f, lo = 0.f;
-        auto add = [&](float x) {  // and its rounding
-            const float t = hi + x, z = t - hi;
-            lo += (hi - (t - z)) + (x - z);
-            hi = t;
-        };
-#pragma unroll 4
-        for (int i = 0; i < VF_EACH; ++i) {
-            const int v = b0 + i * VF_PICK;
-            if (v >= v1)
-                break;
-            const float x = verify_one(row + v);
-            if (infinite) {
-                hi += x == m ? 1.f : 0.f;
+    constexpr int N = 8;  // places on their way
+    float hi = 0.f, lo = 0.f;
+    auto add = [&](float y) {  // and its rounding
+        const float t = hi + y, z = t - hi;
+        lo += (hi - (t - z)) + (y - z);
+        hi = t;
+    };
+    for (int b0 = v0 + tid; b0 < v1; b0 += VF_PICK * N) {
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[i] = b0 + i * VF_PICK < v1 ? verify_one(row + b0 + i * VF_PICK) : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float dh = x[i] - m, back = dh - x[i], dl = (x[i] - (dh - back)) - (m + back);
+            const float ph = dh * ch;
+            if (!(ph > -125.f)) {  // less than 2^-125, or a NaN
+                if (infinite && x[i] == m)
+                    hi += 1.f;
                 continue;
             }
-            const float dh = x - m, back = dh - x, dl = (x - (dh - back)) - (m + back);
-            const float ph = dh * ch;
-            if (!(ph > -125.f))
-                continue;  // less than 2^-125, or a NaN
             const float pl = fmaf(dl, ch, fmaf(dh, cl, fmaf(dh, ch, -ph)));
             const float k = rintf(128.f * ph), h = fmaf(k, -1.f / 128.f, ph);
             constexpr float LN2 = 0.6931471805599453f, REST = static_cast<float>(0.6931471805599453 - static_cast<double>(LN2));
@@ -433,26 +442,34 @@ __device__ __noinline__ double verify_sum64(VerifyShared& sh, const T* row, floa
             add(wz);
             lo += fmaf(w, more, fmaf(w, zh, -wz)) + p.y * power * (1.f + zh);
         }
-        total += static_cast<double>(hi) + lo;
+        const float rest = lo;  // the second part stays a rounding of the first
+        lo = 0.f;
+        add(rest);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        const float h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        add(h2);
+    }
     if ((tid & 31) == 0)
-        sh.warp64[tid >> 5] = total;
+        sh.warp64[tid >> 5] = static_cast<double>(hi) + lo;
     __syncthreads();
     if (tid == 0) {
-        total = 0.0;
+        double part = 0.0;
         for (int w = 0; w < VF_PICK / 32; ++w)
-            total += sh.warp64[w];
-        sh.part = total;
+            part += sh.warp64[w];
+        sh.part = part;
     }
     cluster.sync();
-    total = 0.0;
-    for (int k = 0; k < static_cast<int>(cluster.num_blocks()); ++k)
-        total += *cluster.map_shared_rank(&sh.part, k);
+    if (tid == 0) {
+        double total = 0.0;
+        for (int k = 0; k < static_cast<int>(cluster.num_blocks()); ++k)
+            total += *cluster.map_shared_rank(&sh.part, k);
+        sh.total = total;
+    }
     cluster.sync();  // before a block writes its part again, or ends
-    return total;
+    return sh.total;
 }
 
 // A node into a set in shared memory, by its half: 64-bit ones are loops that 63 children of a
@@ -614,7 +631,8 @@ __device__ __forceinline__ void verify_finish(const VerifyArgs& a, VerifyShared&
     const float coarse = a.slack + 1.2e-5f, by_p = 1.f + coarse, by_q = -z * (1.f - coarse);
     auto close = [&](float x, float q, float inv, int v) {
         // r, and all that its numbers may be off by
-        const float p = verify_exp(verify_clean(x), top.v, c), r = fmaf(-z, q, p), off = fmaf(fmaf(z, q, p), a.slack, TINY);
+        const float p = verify_exp(verify_clean(x), top.v, c), r = fmaf(-z, q, p);
+        const float off = fmaf(p, verify_exp_off(x, top.v, c), fmaf(z * q, a.slack, TINY));
         // inv is infinite for a noise below 2^-128
         place((r + off) * inv, (r - off) * fminf(inv, 8.5070592e37f), v);
     };
@@ -879,9 +897,11 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const __grid_co
             const float sum = sh.sum[parent], by = u * q;
             float left = sum;
             verify_each(sh.fresh[parent] & (me - 1), [&](int i) { left -= sh.w[i]; });
+            const float gone = sum - left;
             left = by * fmaxf(left, 0.f);
-            // the sum's and the weights' errors, and 64 roundings; 2^-126 for what fp32 has as 0
-            const float off = fmaf(a.slack + 4e-6f, fmaf(2.f * by, sum, w), 1.1754944e-38f);
+            // the sum's and the weights' errors, and a rounding for each rejected one; 2^-126 for what
+            // fp32 has as 0
+            const float off = fmaf(a.slack, fmaf(by, sum + gone, w), fmaf(gone > 0.f ? 4e-6f : 0.f, by * sum, 1.1754944e-38f));
             take = left + off < w;
             open = !take && !(left - off >= w);
         }
@@ -932,11 +952,11 @@ static cudaError_t verify_prepare(K kernel, bool (&done)[64])
 // 2025 blocks are three rounds and a third).
 struct VerifyCut {
     int pieces, steps;
-    // What the fp32 sum of a row's weights, and a weight, may be off by, relative to themselves.  A
-    // weight 2^-t: ex2's 2^-22 and, of t, the three roundings of verify_exp2, 3 t 2^-24 ln 2, where t
-    // averaged over a sum's weights is at most log2(vocab) <= 24: 3.3e-6; or the one of
-    // verify_exp, 126 2^-24 ln 2: 5.5e-6.  The joins of lanes, warps and pieces: 2e-6.
-    // A step: an addition, and another maximum's factor and its product: 6 2^-24.
+    // What the fp32 sum of a row's weights may be off by, at most, relative to itself; more than a
+    // weight of 2^-126 and up (verify_exp_off).  A weight 2^-t: ex2's 2^-22 and, of t, the three
+    // roundings of verify_exp2, 3 t 2^-24 ln 2, where t averaged over a sum's weights is at most
+    // log2(vocab) <= 24: 3.3e-6.  The joins of lanes, warps and pieces: 2e-6.  A step: an addition,
+    // and another maximum's factor and its product: 6 2^-24.
     float slack() const { return 8e-6f + 3.6e-7f * static_cast<float>(steps); }
 };
 static VerifyCut verify_cut(int total_new, int vocab, bool wide)
