@@ -364,7 +364,7 @@ struct VerifyShared {
     int token[VF_MAX_NEW];
     // a node's children, a bit each: all whose token is in the vocabulary, those whose token no
     // sibling before them has, those accepted if their turn comes, those that fp32 leaves open
-    unsigned long long kids[VF_MAX_NEW], fresh[VF_MAX_NEW], taken[VF_MAX_NEW], open[VF_MAX_NEW];
+    uint2 kids[VF_MAX_NEW], fresh[VF_MAX_NEW], taken[VF_MAX_NEW], open[VF_MAX_NEW];
     double w64[VF_MAX_NEW];
     int path[VF_MAX_NEW], len, stop;
     int gone[VF_MAX_NEW], n_gone;  // rejected tokens at the last node
@@ -472,11 +472,12 @@ __device__ __noinline__ double verify_sum64(VerifyShared& sh, const T* row, floa
     return sh.total;
 }
 
-// A node into a set in shared memory, by its half: 64-bit ones are loops that 63 children of a
-// node take turns in.
-__device__ __forceinline__ void verify_put(unsigned long long& set, int node)
+// A set of nodes in shared memory: a node into it, by its half (64-bit atomics are loops that 63
+// children of a node take turns in), and all of it.
+__device__ __forceinline__ void verify_put(uint2& set, int node) { atomicOr(node < 32 ? &set.x : &set.y, 1u << (node & 31)); }
+__device__ __forceinline__ unsigned long long verify_set(const uint2& set)
 {
-    atomicOr(reinterpret_cast<unsigned*>(&set) + (node >> 5), 1u << (node & 31));
+    return static_cast<unsigned long long>(set.y) << 32 | set.x;
 }
 // f of each node in `set`, ascending.
 template <typename F>
@@ -551,7 +552,7 @@ __device__ __forceinline__ bool verify_walk(VerifyShared& sh)
     if (threadIdx.x == 0) {
         int cur = sh.last, len = sh.len;
         unsigned long long next;
-        while ((next = sh.taken[cur] | sh.open[cur]) != 0 && !(sh.open[cur] & next & (0ull - next))) {
+        while ((next = verify_set(sh.taken[cur]) | verify_set(sh.open[cur])) != 0 && !(verify_set(sh.open[cur]) & next & (0ull - next))) {
             cur = __ffsll(static_cast<long long>(next)) - 1;
             sh.path[len++] = cur;
         }
@@ -733,16 +734,16 @@ __device__ __noinline__ void verify_open(const VerifyArgs& a, VerifyShared& sh, 
         const int cur = sh.last;
         const float top = sh.top[cur].v;
         const double z = verify_sum64(sh, static_cast<const T*>(a.logits) + (row0 + cur) * a.ld, top, temperature, v0, v1);
-        if (tid < VF_MAX_NEW && (sh.fresh[cur] & me))
+        if (tid < VF_MAX_NEW && (verify_set(sh.fresh[cur]) & me))
             sh.w64[tid] = verify_exp64(own, top, temperature);
         if (tid == 0) {
             sh.sum[cur] = static_cast<float>(z);
-            sh.taken[cur] = sh.open[cur] = 0ull;
+            sh.taken[cur] = sh.open[cur] = make_uint2(0u, 0u);
         }
         __syncthreads();
         if (mine && parent == cur) {
             double left = z;
-            verify_each(sh.fresh[cur] & (me - 1), [&](int i) { left -= sh.w64[i]; });
+            verify_each(verify_set(sh.fresh[cur]) & (me - 1), [&](int i) { left -= sh.w64[i]; });
             if (static_cast<double>(u) * q * fmax(left, 0.0) < sh.w64[tid])
                 verify_put(sh.taken[cur], tid);
         }
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const __grid_co
     const VerifyScale c = verify_scale(greedy ? 1.f : temp);
 
     if (tid < VF_MAX_NEW)
-        sh.kids[tid] = sh.fresh[tid] = sh.taken[tid] = sh.open[tid] = 0ull;
+        sh.kids[tid] = sh.fresh[tid] = sh.taken[tid] = sh.open[tid] = make_uint2(0u, 0u);
     // the tree's numbers and the random ones are on their way while the sums are still made
     int parent = -1, token = -1;
     float u = 0.f, q = 1.f;
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const __grid_co
     const unsigned long long me = 1ull << (tid & 63);
     bool mine = parent >= 0 && token >= 0;  // may be accepted
     if (mine)
-        verify_each(sh.kids[parent] & (me - 1), [&](int i) { mine = mine && sh.token[i] != token; });
+        verify_each(verify_set(sh.kids[parent]) & (me - 1), [&](int i) { mine = mine && sh.token[i] != token; });
     if (mine)
         verify_put(sh.fresh[parent], tid);
     if (tid < n)
@@ -896,7 +897,7 @@ __global__ void __launch_bounds__(VF_PICK, 2) verify_pick_kernel(const __grid_co
         } else {
             const float sum = sh.sum[parent], by = u * q;
             float left = sum;
-            verify_each(sh.fresh[parent] & (me - 1), [&](int i) { left -= sh.w[i]; });
+            verify_each(verify_set(sh.fresh[parent]) & (me - 1), [&](int i) { left -= sh.w[i]; });
             const float gone = sum - left;
             left = by * fmaxf(left, 0.f);
             // the sum's and the weights' errors, and a rounding for each rejected one; 2^-126 for what
