@@ -550,9 +550,9 @@ DQ_API int dq_attention_tree(const dq_tree* t, void* stream);
  * tokens.  With uniform from [0, 1) and noise from the exponential distribution the
  * tokens are distributed as if drawn from p one by one.  What fp32 leaves open of an
  * acceptance or of the argmax is decided from 64-bit weights and a sum good to 2^-38.
- * Where r is zero everywhere, and
- * where temperature[s] is not above 0 (a child is then accepted if its token is it), the
- * token of the largest logit (the lowest of equal ones).  temperature NULL: 1.
+ * Where r is zero everywhere, and where temperature[s] is not above 0 (a child is then
+ * accepted if its token is it), the token of the largest logit (the lowest of equal
+ * ones).  temperature NULL: 1.
  * A NaN among the logits counts as -infinity, the weight of a -infinity is 0, the
  * largest one's 1 even where it is infinite; a row of none but those accepts nothing and
  * gives the token -1.  uniform and draft_probs are >= 0, noise > 0, none NaN; a

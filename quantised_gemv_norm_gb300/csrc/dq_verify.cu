@@ -22,11 +22,13 @@
 // 64 sequences of up to 9 nodes, 151936 fp32 logits each, 193 MB and 78 MB of random numbers
 // and draft probabilities: 52 us (floor 40): 32 us the first kernel (6.0 TB/s), the rest the
 // pass (13 us, the same memory) and the second kernel's steps.  405 nodes of 100003 bf16
-// logits in 16 trees: 38 us (13): the first kernel 24 us, 3.4 TB/s, two rounds of four blocks
+// logits in 16 trees: 36 us (13): the first kernel 24 us, 3.4 TB/s, two rounds of four blocks
 // an SM: a block's start and the chain of each of its nine steps, 9.7 instructions a logit
 // counted, issue 0.5 of its rate (10.8 before 16-bit logits were widened in pairs: 0.8 us more).
 // One sequence of 6: 11.6 us: 2.5 the first kernel, then waits for memory in a row (lengths,
-// tokens, their logits; sums; two rounds of the pass) and two meetings of the cluster.
+// tokens, their logits; sums; two rounds of the pass) and two meetings of the cluster.  64 nodes
+// of one sequence, 5000 logits: a chain 9.4 us, breadth first with 4 children each 10.0, with 8
+// 11.6, a root with 63 children 28.6: siblings are gone through one by one.
 #include <cooperative_groups.h>
 
 #include <algorithm>

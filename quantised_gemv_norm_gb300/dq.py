@@ -700,7 +700,9 @@ def attention_tree(q: torch.Tensor, pool: torch.Tensor, pages: torch.Tensor, n_p
     the pool's dtype (any row and head strides), pages int32 [n_seq, max_pages], n_past int32 [n_seq] (rows before the
     new ones), cu_new int32 [n_seq + 1] (None: as many rows in every sequence), seen int64 [total_new], bit t of a row's:
     it sees its sequence's new token t (None: those up to itself).  ``max_new``: a bound on a sequence's rows known to
-    the host, at most 64 (where it is not given: 64, or total_new if that is less).  -> [total_new, n_q, 128]."""
+    the host, at most 64 (where it is not given: 64, or total_new if that is less; the kernel and its row tiles are chosen
+    by it, not by the lengths, so give what is known: a batch of single tokens is slower under 64).  -> [total_new, n_q,
+    128]."""
     lib = _lib or load()
     n_pages, n_kv, page = _kv16(pool)
     dtype = pool.dtype
